@@ -73,6 +73,10 @@ typedef int pmn_status;
 #define PMN_GROUP_M 0
 #define PMN_GROUP_K 1
 
+/* states of pmn_adamw_step */
+#define PMN_STATE_F32 0
+#define PMN_STATE_MXFP8 1
+
 /* device error bits (pmn_get_device_error) */
 #define PMN_DEVERR_WAIT_TIMEOUT 1
 #define PMN_DEVERR_BAD_OFFSETS 2
@@ -421,6 +425,102 @@ PMN_API pmn_status pmn_gemm_mxfp8(const uint8_t *a, const uint8_t *a_scales, con
                           const uint8_t *b_scales, const int32_t *offsets, int num_groups,
                           int group_mode, int64_t m, int64_t n, int64_t k, int out_kind, void *out,
                           void *stream);
+
+/*
+ * The operators around the MXFP8 layers ([Cost]: the last 16.6 % of layers),
+ * which the pages leave out: what makes the rows that those layers quantise
+ * from the residual stream, and the optimiser step that consumes its weight gradients.
+ */
+
+/*
+ * Residual addition, root-mean-square norm and MXFP8 rows:
+ *   r = x + residual, rounded to the residual's type and written to res_out
+ *       (r = x without a residual)
+ *   rstd = 1 / sqrt(mean_c(r^2) + eps);  y = (r * rstd) * weight   (float32)
+ *   out, out_scales = MXFP8(y) along the row (the rule of pmn_mxfp8_quantize)
+ * The norm reads the rounded r, so the backward pass can start from res_out.
+ * A NaN in a row makes the whole row's codes NaN; an infinity makes its own
+ * code NaN and the others 0 (rstd = 0).  r beyond 1.8e19 overflows the float32
+ * sum of squares and counts as infinite.
+ *  x        bf16 [rows, ldx] (the first `cols` of each row); ldx % 8 == 0.
+ *  residual NULL, or [rows, ldr] of residual_kind PMN_OUT_BF16 (ldr % 8 == 0)
+ *           or PMN_OUT_F32 (ldr % 4 == 0).
+ *  weight   bf16 [cols];  eps > 0.
+ *  rows     >= 0 and < 2^31;  cols % 32 == 0, cols <= 16384.
+ *  res_out  [rows, cols] of residual_kind; NULL exactly where residual is.
+ *           May be `residual` itself where ldr == cols.
+ *  out      uint8 [rows, cols] (E4M3);  out_scales uint8 [rows, cols / 32].
+ *  y_out    NULL, or bf16 [rows, cols]: y rounded to nearest even.
+ *  rstd     NULL, or float32 [rows] (4-byte aligned).
+ * One kernel on `stream`.
+ */
+PMN_API pmn_status pmn_add_rmsnorm_mxfp8(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                         int residual_kind, const void *weight, int64_t rows, int64_t cols, float eps,
+                                         void *res_out, uint8_t *out, uint8_t *out_scales, void *y_out, float *rstd,
+                                         void *stream);
+
+/*
+ * Gradients of pmn_add_rmsnorm_mxfp8's y (its quantisation passes them through):
+ *   xh = r * rstd;  g = dy * weight;
+ *   dr = rstd * (g - xh * mean_c(g * xh)) + dres;   dw = sum_rows dy * xh
+ * dr is the gradient of x and of the residual alike.
+ *  dy       bf16 [rows, cols];  r [rows, cols] of residual_kind (res_out, or a
+ *           bf16 x where there was no residual);  rstd float32 [rows].
+ *  dres     NULL, or [rows, cols] of residual_kind: the gradient that reaches r
+ *           by the residual path.
+ *  dr       [rows, cols] of residual_kind (may be dres itself).
+ *  dx       NULL, or (PMN_OUT_F32 only) bf16 [rows, cols]: dr rounded for the
+ *           bf16 branch.
+ *  dw       float32 [cols]; written, not added to (zeros where rows == 0).
+ *  workspace  device scratch, 16-byte aligned, of at least
+ *           pmn_add_rmsnorm_backward_workspace_bytes(rows, cols) bytes.
+ * Two kernels on `stream`; the sums' order depends on the sizes alone.
+ */
+PMN_API pmn_status pmn_add_rmsnorm_backward(const void *dy, const void *r, int residual_kind, const float *rstd,
+                                            const void *weight, const void *dres, int64_t rows, int64_t cols, void *dr,
+                                            void *dx, float *dw, void *workspace, int64_t workspace_bytes,
+                                            void *stream);
+
+/* Workspace bytes of pmn_add_rmsnorm_backward; -1 for invalid sizes.  Host only. */
+PMN_API int64_t pmn_add_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* One tensor of an AdamW step: device pointers, 16-byte aligned except the
+ * scales; n elements. */
+typedef struct pmn_adamw_tensor {
+    void *param;         /* [n] of param_kind, updated */
+    void *copy;          /* NULL, or bf16 [n]: the updated float32 parameter, rounded */
+    const void *grad;    /* [n] of grad_kind */
+    void *m, *v;         /* PMN_STATE_F32: float32 [n]; PMN_STATE_MXFP8: E4M3 uint8 [n] of m and of sqrt(v) */
+    uint8_t *m_scales, *v_scales; /* PMN_STATE_MXFP8: E8M0 uint8 [ceil(n / 32)] */
+    int64_t n;
+} pmn_adamw_tensor;
+
+/*
+ * One AdamW step (decoupled weight decay) over many tensors:
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;
+ *   v = beta2 v + (1 - beta2) g^2;
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32.  MXFP8 states hold m and sqrt(v) (E8M0 per 32 elements, the rule
+ * of pmn_mxfp8_quantize), rounded stochastically; a nonzero sqrt(v) takes at
+ * least the smallest code, never 0.  bf16 parameters are rounded stochastically
+ * too: 16 random bits are added below the last place.  Random bits: Philox as
+ * in pmn_requant_transpose_sr_mxfp8, with counter (j lo, j hi, 4 * index of the
+ * tensor + stream, step), j = element / 16, stream 0 = param, 1 = m, 2 = v.
+ * A NaN or infinite gradient makes its own element's param and m NaN or infinite.
+ *  tensors  HOST array [num_tensors], copied by the call.
+ *  param_kind, grad_kind  PMN_OUT_BF16 or PMN_OUT_F32;  state_kind PMN_STATE_*.
+ *  beta1, beta2 in [0, 1);  eps > 0;  step >= 1 (its low 32 bits are used as the
+ *           counter word).
+ *  grad_scale  NULL (1), or a DEVICE float32: a clipping factor or the inverse of
+ *           a loss scale, read by the kernel.
+ * One kernel per 440 tensors on `stream`; the arguments are fixed in a captured
+ * graph (lr and step included).
+ */
+PMN_API pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_tensors, int param_kind, int grad_kind,
+                                  int state_kind, double lr, double beta1, double beta2, double eps,
+                                  double weight_decay, int64_t step, const float *grad_scale, uint64_t seed,
+                                  void *stream);
 
 #ifdef __cplusplus
 }

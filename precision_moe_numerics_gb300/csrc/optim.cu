@@ -1,0 +1,362 @@
+// optim.cu -- pmn_adamw_step: one AdamW step over many tensors, with float32
+// or MXFP8 states.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/pmn.h"
+#include "numerics.cuh"
+
+using namespace pmn;
+
+namespace {
+
+constexpr int CTA = 256;
+constexpr int WARP_ELEMS = 512;                    // 2 groups of 8 elements per thread
+constexpr int CHUNK = CTA / 32 * WARP_ELEMS;       // elements of one CTA
+
+// The tensors travel as a kernel argument (no table in device memory that a
+// caller would have to keep alive): up to MAXT per launch.
+template <int MAXT>
+struct Table {
+    pmn_adamw_tensor t[MAXT];
+    int first[MAXT + 1];  // first chunk (CTA) of each tensor
+    int count;
+    uint32_t base;        // index of t[0] among the call's tensors
+};
+
+struct Hyper {
+    float beta1, omb1, beta2, omb2;  // omb: 1 - beta
+    float decay;                     // 1 - lr * weight_decay
+    float lr1;                       // lr / (1 - beta1^step)
+    float rbc2;                      // 1 / sqrt(1 - beta2^step)
+    float eps;
+    uint32_t step;
+    uint64_t seed;
+    const float *grad_scale;
+};
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Eight consecutive values at element i of a bf16 or float32 array; `left`
+// counts the elements from i to the array's end (8 or more: vector access).
+template <bool F32>
+__device__ __forceinline__ void load8(const void *p, int64_t i, int64_t left, float (&v)[8])
+{
+    if (left >= 8) {
+        if (F32) {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+            const float4 a = __ldcs(q), b = __ldcs(q + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(u4_word(q, k) << 16);
+                v[2 * k + 1] = __uint_as_float(u4_word(q, k) & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = 0.0f;
+            if (k < left)
+                v[k] = F32 ? static_cast<const float *>(p)[i + k]
+                           : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i + k] << 16);
+        }
+    }
+}
+
+__device__ __forceinline__ void store8_f32(void *p, int64_t i, int64_t left, const float (&v)[8])
+{
+    float *o = static_cast<float *>(p) + i;
+    if (left >= 8) {
+        reinterpret_cast<float4 *>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) o[k] = v[k];
+    }
+}
+
+__device__ __forceinline__ void store8_b16(void *p, int64_t i, int64_t left, const uint32_t (&w)[4])
+{
+    uint16_t *o = static_cast<uint16_t *>(p) + i;
+    if (left >= 8) {
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) o[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
+}
+
+// Eight E4M3 codes (a word pair) times 2^(b - 127).
+__device__ __forceinline__ void load8_mx(const uint8_t *q, const uint8_t *sc, int64_t i, int64_t left, float (&v)[8])
+{
+    uint32_t w[2] = {0u, 0u};
+    float s = 0.0f;
+    if (left > 0) s = e8m0_to_f32(sc[i / 32]);
+    if (left >= 8) {
+        const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(q + i));
+        w[0] = u.x;
+        w[1] = u.y;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) w[k >> 2] |= (uint32_t)q[i + k] << (8 * (k & 3));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t h2;  // two codes as f16x2 (exact)
+        const uint16_t b16 = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b16));
+        v[2 * k] = __fmul_rn(h2_lo_to_f32(h2), s);
+        v[2 * k + 1] = __fmul_rn(h2_hi_to_f32(h2), s);
+    }
+}
+
+// MXFP8 of the thread's eight values, its block being the 32 values of four
+// adjacent lanes, rounded stochastically with the words r0 (values 0..3) and r1
+// (4..7).  keep: a nonzero value takes the smallest code instead of 0.
+template <bool KEEP>
+__device__ __forceinline__ void store8_mx(uint8_t *q, uint8_t *sc, int64_t i, int64_t left, const float (&v)[8],
+                                          uint32_t r0, uint32_t r1)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const int e = mx_exponent_448(amax);
+    const float s = exp2_neg(e);
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(v[k], s);
+    uint32_t w[2] = {cvt_e4m3x4_rs(y[0], y[1], y[2], y[3], r0), cvt_e4m3x4_rs(y[4], y[5], y[6], y[7], r1)};
+    if (KEEP) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (v[k] > 0.0f && ((w[k >> 2] >> (8 * (k & 3))) & 0xFFu) == 0u) w[k >> 2] |= 1u << (8 * (k & 3));
+    }
+    if (left >= 8) {
+        *reinterpret_cast<uint2 *>(q + i) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) q[i + k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    }
+    if (left > 0 && (threadIdx.x & 3) == 0) sc[i / 32] = (uint8_t)(e + 127);
+}
+
+// The random words of the thread's two groups of 8 elements, at elements
+// i and i + 256 of the tensor.  One Philox call serves 16 elements: the call of
+// the even lane covers the first group of a lane pair, the odd lane's the second
+// one, and the pair exchanges the halves (words 0, 1 go to the even lane).
+__device__ __forceinline__ void pair_words(uint64_t seed, uint32_t tag, uint32_t step, int64_t i, uint32_t (&r)[2][2])
+{
+    const bool odd = threadIdx.x & 1;
+    const uint64_t j = (uint64_t)(odd ? i + 256 : i) >> 4;
+    const uint4 c = philox4x32_10(make_uint4((uint32_t)j, (uint32_t)(j >> 32), tag, step), (uint32_t)seed,
+                                  (uint32_t)(seed >> 32));
+    const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? c.x : c.z, 1);
+    const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? c.y : c.w, 1);
+    r[0][0] = odd ? a : c.x;
+    r[0][1] = odd ? b : c.y;
+    r[1][0] = odd ? c.z : a;
+    r[1][1] = odd ? c.w : b;
+}
+
+// The 16 random bits of element k (0..3) of a word, as the hardware's
+// stochastic conversion takes them: low half, low half reversed, high half,
+// high half reversed.
+__device__ __forceinline__ uint32_t bits16(uint32_t w, int k)
+{
+    if (k == 0) return w & 0xFFFFu;
+    if (k == 1) return __brev(w) >> 16;
+    if (k == 2) return w >> 16;
+    return __brev(w) & 0xFFFFu;
+}
+
+// One AdamW step.  Memory-bound: each value is read and written once, 16 elements
+// a thread in two groups of 8 so that both groups' loads are in flight together.
+//   g = grad_scale grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+// MXFP8 states hold m and sqrt(v): the root halves the range of exponents that
+// one block's scale has to serve.  Both are rounded stochastically: a step moves
+// v by about 1 - b2 of itself, far less than half a step of E4M3, and rounding to
+// nearest would never move it.  p is updated from the unrounded m and v.
+template <bool PF32, bool GF32, bool MX, int MAXT>
+__global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Table<MAXT> tab, const Hyper h)
+{
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {  // the last tensor whose first chunk is at or before this one
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= (int)blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
+    const pmn_adamw_tensor &t = tab.t[lo];
+    const int64_t n = t.n;
+    const int64_t i0 = (int64_t)((int)blockIdx.x - tab.first[lo]) * CHUNK + (threadIdx.x >> 5) * WARP_ELEMS +
+                       8 * (threadIdx.x & 31);
+    const uint32_t tag = 4u * (tab.base + (uint32_t)lo);
+    float p[2][8], g[2][8], m[2][8], v[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t i = i0 + 256 * u, left = n - i;
+        load8<PF32>(t.param, i, left, p[u]);
+        load8<GF32>(t.grad, i, left, g[u]);
+        if (MX) {
+            load8_mx(static_cast<const uint8_t *>(t.m), t.m_scales, i, left, m[u]);
+            load8_mx(static_cast<const uint8_t *>(t.v), t.v_scales, i, left, v[u]);
+        } else {
+            load8<true>(t.m, i, left, m[u]);
+            load8<true>(t.v, i, left, v[u]);
+        }
+    }
+    const float gs = h.grad_scale ? __ldg(h.grad_scale) : 1.0f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float gr = __fmul_rn(g[u][k], gs);
+            if (MX) v[u][k] = __fmul_rn(v[u][k], v[u][k]);
+            m[u][k] = fmaf(h.beta1, m[u][k], __fmul_rn(h.omb1, gr));
+            v[u][k] = fmaf(h.beta2, v[u][k], __fmul_rn(h.omb2, __fmul_rn(gr, gr)));
+            const float root = __fsqrt_rn(v[u][k]);
+            const float d = __fdiv_rn(m[u][k], fmaf(root, h.rbc2, h.eps));
+            p[u][k] = fmaf(-h.lr1, d, __fmul_rn(p[u][k], h.decay));
+            if (MX) v[u][k] = root;
+        }
+    uint32_t r[2][2];
+    if (!PF32) pair_words(h.seed, tag, h.step, i0, r);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t i = i0 + 256 * u, left = n - i;
+        uint32_t w[4];
+        if (PF32) {
+            store8_f32(t.param, i, left, p[u]);
+            if (t.copy) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(p[u][2 * k], p[u][2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                store8_b16(t.copy, i, left, w);
+            }
+        } else {
+            // bf16 without a master: the step is often below half a place, so the
+            // rounding is stochastic (16 bits added below the last place)
+            uint32_t b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                b[k] = __float_as_uint(p[u][k]) + bits16(r[u][k >> 2], k & 3);
+                if (p[u][k] != p[u][k]) b[k] = 0x7FC00000u;  // the addition may carry a NaN's bits into the sign
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __byte_perm(b[2 * k], b[2 * k + 1], 0x7632);
+            store8_b16(t.param, i, left, w);
+        }
+        if (!MX) {
+            store8_f32(t.m, i, left, m[u]);
+            store8_f32(t.v, i, left, v[u]);
+        }
+    }
+    if (MX) {
+        pair_words(h.seed, tag + 1u, h.step, i0, r);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            store8_mx<false>(static_cast<uint8_t *>(t.m), t.m_scales, i0 + 256 * u, n - i0 - 256 * u, m[u], r[u][0],
+                             r[u][1]);
+        pair_words(h.seed, tag + 2u, h.step, i0, r);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            store8_mx<true>(static_cast<uint8_t *>(t.v), t.v_scales, i0 + 256 * u, n - i0 - 256 * u, v[u], r[u][0],
+                            r[u][1]);
+    }
+}
+
+template <int MAXT>
+pmn_status launch_adamw(const pmn_adamw_tensor *t, int count, uint32_t base, int kinds, const Hyper &h, cudaStream_t s)
+{
+    static thread_local Table<MAXT> tab;
+    int64_t chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        tab.t[i] = t[i];
+        tab.first[i] = (int)chunks;
+        chunks += (t[i].n + CHUNK - 1) / CHUNK;
+        if (chunks >= (int64_t(1) << 31)) return PMN_ERR_UNSUPPORTED;
+    }
+    tab.first[count] = (int)chunks;
+    tab.count = count;
+    tab.base = base;
+    if (chunks == 0) return PMN_OK;
+    const unsigned grid = (unsigned)chunks;
+#define PMN_ADAMW(P, G, M) adamw_kernel<P, G, M, MAXT><<<grid, CTA, 0, s>>>(tab, h)
+    switch (kinds) {
+        case 0: PMN_ADAMW(false, false, false); break;
+        case 1: PMN_ADAMW(true, false, false); break;
+        case 2: PMN_ADAMW(false, true, false); break;
+        case 3: PMN_ADAMW(true, true, false); break;
+        case 4: PMN_ADAMW(false, false, true); break;
+        case 5: PMN_ADAMW(true, false, true); break;
+        case 6: PMN_ADAMW(false, true, true); break;
+        default: PMN_ADAMW(true, true, true); break;
+    }
+#undef PMN_ADAMW
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+constexpr int SMALL_TABLE = 48, LARGE_TABLE = 440;  // 3.3 KB and 30 KB of kernel arguments (limit 32 764 bytes)
+
+}  // namespace
+
+extern "C" pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_tensors, int param_kind, int grad_kind,
+                                     int state_kind, double lr, double beta1, double beta2, double eps,
+                                     double weight_decay, int64_t step, const float *grad_scale, uint64_t seed,
+                                     void *stream)
+{
+    if (num_tensors < 0 || num_tensors > (1 << 28) || (num_tensors > 0 && !tensors)) return PMN_ERR_INVALID_ARG;
+    const auto two = [](int k) { return k == PMN_OUT_BF16 || k == PMN_OUT_F32; };
+    if (!two(param_kind) || !two(grad_kind) || (state_kind != PMN_STATE_F32 && state_kind != PMN_STATE_MXFP8))
+        return PMN_ERR_INVALID_ARG;
+    // NaN fails every comparison
+    if (!(std::isfinite(lr) && beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps > 0.0 &&
+          std::isfinite(eps) && std::isfinite(weight_decay)) || step < 1 || ((uintptr_t)grad_scale & 3u))
+        return PMN_ERR_INVALID_ARG;
+    for (int i = 0; i < num_tensors; ++i) {
+        const pmn_adamw_tensor &t = tensors[i];
+        if (t.n < 0 || (t.copy && param_kind != PMN_OUT_F32)) return PMN_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v) return PMN_ERR_INVALID_ARG;
+        if (!aligned16(t.param) || !aligned16(t.copy) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v))
+            return PMN_ERR_INVALID_ARG;
+        if (state_kind == PMN_STATE_MXFP8 && (!t.m_scales || !t.v_scales)) return PMN_ERR_INVALID_ARG;
+    }
+    Hyper h;
+    h.beta1 = (float)beta1;
+    h.omb1 = (float)(1.0 - beta1);
+    h.beta2 = (float)beta2;
+    h.omb2 = (float)(1.0 - beta2);
+    h.decay = (float)(1.0 - lr * weight_decay);
+    h.lr1 = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    h.rbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    h.eps = (float)eps;
+    h.step = (uint32_t)step;
+    h.seed = seed;
+    h.grad_scale = grad_scale;
+    const int kinds = (param_kind == PMN_OUT_F32 ? 1 : 0) | (grad_kind == PMN_OUT_F32 ? 2 : 0) |
+                      (state_kind == PMN_STATE_MXFP8 ? 4 : 0);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    for (int at = 0; at < num_tensors; at += LARGE_TABLE) {
+        const int count = num_tensors - at < LARGE_TABLE ? num_tensors - at : LARGE_TABLE;
+        const pmn_status st = count <= SMALL_TABLE ? launch_adamw<SMALL_TABLE>(tensors + at, count, at, kinds, h, s)
+                                                   : launch_adamw<LARGE_TABLE>(tensors + at, count, at, kinds, h, s);
+        if (st != PMN_OK) return st;
+    }
+    return PMN_OK;
+}

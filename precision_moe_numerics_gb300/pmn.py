@@ -21,6 +21,7 @@ OUTER_PER_ROW, OUTER_PER_GROUP = 0, 1
 ROUND_SR, ROUND_RN = 0, 1
 OUT_BF16, OUT_F32, OUT_RHT_S2F6, OUT_SWIGLU_BF16 = 0, 1, 2, 3
 GROUP_M, GROUP_K = 0, 1
+STATE_F32, STATE_MXFP8 = 0, 1
 DEVERR_WAIT_TIMEOUT = 1
 DEVERR_BAD_OFFSETS = 2
 
@@ -28,6 +29,14 @@ DEVERR_BAD_OFFSETS = 2
 TAG_X, TAG_H, TAG_W1, TAG_W2 = 1, 2, 3, 4
 
 _P, _I64, _U64, _U32, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
+_F, _D = ctypes.c_float, ctypes.c_double
+
+
+class AdamWTensor(ctypes.Structure):
+    """pmn_adamw_tensor"""
+    _fields_ = [("param", _P), ("copy", _P), ("grad", _P), ("m", _P), ("v", _P), ("m_scales", _P), ("v_scales", _P),
+                ("n", _I64)]
+
 
 SIGNATURES = {
     "pmn_version": ([], _I),
@@ -49,6 +58,10 @@ SIGNATURES = {
     "pmn_rht_s2f6_quantize": ([_P, _I64, _I64, _U64, _P, _P, _P], _I),
     "pmn_combine_receive_s2f6": ([_P, _P, _I64, _I64, _U64, _P, _P, _I64, _I, _I, _P, _P], _I),
     "pmn_gemm_mxfp8": ([_P, _P, _P, _P, _P, _I, _I, _I64, _I64, _I64, _I, _P, _P], _I),
+    "pmn_add_rmsnorm_mxfp8": ([_P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _P, _P, _P, _P, _P], _I),
+    "pmn_add_rmsnorm_backward": ([_P, _P, _I, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P], _I),
+    "pmn_add_rmsnorm_backward_workspace_bytes": ([_I64, _I64], _I64),
+    "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
 _lib = None
@@ -388,3 +401,185 @@ def gemm_mxfp8(a, a_sc, b, b_sc, offsets, group_mode, out_dtype=torch.float32, o
                               _ptr(out), _stream(stream))
     _check(st, "gemm_mxfp8")
     return out
+
+
+# ------------------------------------------------------------------ around the MXFP8 layers
+_KINDS = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _kind(t, what):
+    k = _KINDS.get(t.dtype)
+    if k is None:
+        raise PmnError("%s must be bfloat16 or float32, got %s" % (what, t.dtype))
+    return k
+
+
+def _rows(t, what, dtype=None):
+    """2-D GPU tensor whose rows are contiguous (any row pitch); returns its pitch in elements"""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise PmnError("%s must be a 2-D GPU tensor with contiguous rows" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise PmnError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shaped(t, shape, dtype, what):
+    """a dense GPU tensor of this shape and type (an output or operand that the kernels index by it)"""
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise PmnError("%s must be a dense %s GPU tensor of shape %s" % (what, dtype, (shape,)))
+    return t
+
+
+def _mxfp8_out(out, rows, cols, device, what="out"):
+    if out is None:
+        return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                torch.empty((rows, cols // 32), dtype=torch.uint8, device=device))
+    _shaped(out[0], (rows, cols), torch.uint8, what)
+    _shaped(out[1], (rows, cols // 32), torch.uint8, what + " scales")
+    return out
+
+
+def add_rmsnorm_mxfp8(x, residual, weight, eps=1e-6, out=None, res_out=None, y=None, rstd=None, want_y=False,
+                      want_rstd=False, stream=None):
+    """r = x + residual (in the residual's type; r = x where residual is None), y = r * rstd * weight, MXFP8 of y.
+
+    x bf16 [rows, cols], residual None or bf16 / float32 [rows, cols] (both may be row-strided views), weight
+    bf16 [cols].  Returns ((u8 values, u8 E8M0 scales), r or None, y or None, rstd or None); y (bf16) and rstd
+    (float32) are written where they are passed in or wanted."""
+    ldx = _rows(x, "x", torch.bfloat16)
+    rows, cols = x.shape
+    dev = x.device
+    _shaped(weight, (cols,), torch.bfloat16, "weight")
+    ldr, kind = 0, OUT_BF16
+    if residual is not None:
+        ldr, kind = _rows(residual, "residual"), _kind(residual, "residual")
+        if residual.shape != x.shape:
+            raise PmnError("residual must have x's shape")
+        if res_out is None:
+            res_out = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
+        else:
+            _shaped(res_out, (rows, cols), residual.dtype, "res_out")
+    elif res_out is not None:
+        raise PmnError("res_out without a residual")
+    out = _mxfp8_out(out, rows, cols, dev)
+    if y is not None:
+        _shaped(y, (rows, cols), torch.bfloat16, "y")
+    elif want_y:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    if rstd is not None:
+        _shaped(rstd, (rows,), torch.float32, "rstd")
+    elif want_rstd:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    _check(lib().pmn_add_rmsnorm_mxfp8(_ptr(x), ldx, _ptr(residual), ldr, kind, _ptr(weight), rows, cols, eps,
+                                       _ptr(res_out), _ptr(out[0]), _ptr(out[1]), _ptr(y), _ptr(rstd),
+                                       _stream(stream)),
+           "add_rmsnorm_mxfp8")
+    return out, res_out, y, rstd
+
+
+def add_rmsnorm_backward_workspace_bytes(rows, cols):
+    n = lib().pmn_add_rmsnorm_backward_workspace_bytes(rows, cols)
+    if n < 0:
+        raise PmnError("add_rmsnorm_backward_workspace_bytes: invalid arguments")
+    return n
+
+
+def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=None, want_dx=False, workspace=None,
+                         stream=None):
+    """Gradients of add_rmsnorm_mxfp8's y: (dr in r's type, dx bf16 or None, dw float32 [cols]).
+
+    dy bf16 [rows, cols]; r bf16 or float32 [rows, cols]; dres (r's type) is added to dr, which is the gradient of
+    x and of the residual.  dx: dr rounded to bf16 (float32 r only).  workspace: uint8 device tensor of at least
+    add_rmsnorm_backward_workspace_bytes(rows, cols) bytes, allocated here when None."""
+    rows, cols = dy.shape
+    dev = dy.device
+    _shaped(dy, (rows, cols), torch.bfloat16, "dy")
+    kind = _kind(r, "r")
+    _shaped(r, (rows, cols), r.dtype, "r")
+    _shaped(rstd, (rows,), torch.float32, "rstd")
+    _shaped(weight, (cols,), torch.bfloat16, "weight")
+    if dres is not None:
+        _shaped(dres, (rows, cols), r.dtype, "dres")
+    dr = torch.empty_like(r) if dr is None else _shaped(dr, (rows, cols), r.dtype, "dr")
+    if dx is not None:
+        _shaped(dx, (rows, cols), torch.bfloat16, "dx")
+    elif want_dx:
+        dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    dw = torch.empty((cols,), dtype=torch.float32, device=dev) if dw is None else _shaped(dw, (cols,), torch.float32, "dw")
+    if workspace is None:
+        workspace = torch.empty((add_rmsnorm_backward_workspace_bytes(rows, cols),), dtype=torch.uint8, device=dev)
+    _dev(workspace)
+    _check(lib().pmn_add_rmsnorm_backward(_ptr(dy), _ptr(r), kind, _ptr(rstd), _ptr(weight), _ptr(dres), rows, cols,
+                                          _ptr(dr), _ptr(dx), _ptr(dw), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+           "add_rmsnorm_backward")
+    return dr, dx, dw
+
+
+class AdamWTensors:
+    """The tensors of adamw_step, checked and laid out once.
+
+    params: GPU tensors, all bf16 or all float32; grads: all bf16 or all float32, of the same lengths; m, v: float32
+    tensors, or (uint8 E4M3, uint8 E8M0 per 32) pairs of m and of sqrt(v) -- adamw_states() makes zero ones; copies:
+    bf16 tensors that receive the updated float32 params, or None.  Any shapes; the kernels see flat tensors.  The
+    object keeps references to the tensors, and their storage must stay where it is."""
+
+    def __init__(self, params, grads, m, v, copies=None):
+        params, grads, m, v = list(params), list(grads), list(m), list(v)
+        copies = [None] * len(params) if copies is None else list(copies)
+        if len({len(params), len(grads), len(m), len(v), len(copies)}) != 1:
+            raise PmnError("AdamWTensors: lists of different lengths")
+        kinds = {(_kind(p, "param"), _kind(g, "grad"), isinstance(a, (tuple, list)), isinstance(b, (tuple, list)))
+                 for p, g, a, b in zip(params, grads, m, v)}
+        if len(kinds) > 1 or any(a != b for _, _, a, b in kinds):
+            raise PmnError("AdamWTensors: one type of params, one of grads and one of states")
+        self.param_kind, self.grad_kind, eight, _ = next(iter(kinds), (OUT_F32, OUT_F32, False, False))
+        self.state_kind = STATE_MXFP8 if eight else STATE_F32
+        self.table = (AdamWTensor * max(1, len(params)))()
+        self.count = len(params)
+        self.tensors = (params, grads, m, v, copies)
+        for t, p, g, a, b, c in zip(self.table, params, grads, m, v, copies):
+            n = p.numel()
+            q = list(a) + list(b) if eight else [a, b]
+            sizes = [n, (n + 31) // 32, n, (n + 31) // 32] if eight else [n, n]
+            if len(q) != len(sizes):
+                raise PmnError("AdamWTensors: an MXFP8 state is a (values, scales) pair")
+            for x, k in zip(q, sizes):
+                _dev(x, torch.uint8 if eight else torch.float32)
+                if x.numel() != k:
+                    raise PmnError("AdamWTensors: a state has %d elements, expected %d" % (x.numel(), k))
+            _dev(p), _dev(g)
+            if g.numel() != n or (c is not None and (_dev(c, torch.bfloat16).numel() != n or p.dtype != torch.float32)):
+                raise PmnError("AdamWTensors: grads and copies have their params' lengths, copies are of float32 params")
+            if len({x.device for x in [p, g] + q}) != 1:
+                raise PmnError("AdamWTensors: tensors of one step on one GPU")
+            t.param, t.grad, t.n = p.data_ptr(), g.data_ptr(), n
+            t.copy = None if c is None else c.data_ptr()
+            if eight:
+                t.m, t.m_scales, t.v, t.v_scales = [x.data_ptr() for x in q]
+            else:
+                t.m, t.v = [x.data_ptr() for x in q]
+
+
+def adamw_states(params, mxfp8=False):
+    """Zero states (m, v) for AdamWTensors: float32, or (E4M3, E8M0) pairs (byte 0 is the value 0)."""
+    def one(p):
+        n = p.numel()
+        if not mxfp8:
+            return torch.zeros((n,), dtype=torch.float32, device=p.device)
+        return (torch.zeros((n,), dtype=torch.uint8, device=p.device),
+                torch.zeros(((n + 31) // 32,), dtype=torch.uint8, device=p.device))
+    return [one(p) for p in params], [one(p) for p in params]
+
+
+def adamw_step(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, seed=0, grad_scale=None,
+               stream=None):
+    """One AdamW step (decoupled weight decay) over the tensors of an AdamWTensors object, in place; step counts
+    from 1.  grad_scale: None, or a float32 GPU tensor of one element that the gradients are multiplied by.  bf16
+    params and MXFP8 states are rounded stochastically with bits that follow from seed, step and position."""
+    if grad_scale is not None and _dev(grad_scale, torch.float32).numel() != 1:
+        raise PmnError("grad_scale must have one element")
+    _check(lib().pmn_adamw_step(tensors.table, tensors.count, tensors.param_kind, tensors.grad_kind,
+                                tensors.state_kind, lr, beta1, beta2, eps, weight_decay, step, _ptr(grad_scale),
+                                seed, _stream(stream)),
+           "adamw_step")
