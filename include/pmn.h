@@ -429,7 +429,8 @@ PMN_API pmn_status pmn_gemm_mxfp8(const uint8_t *a, const uint8_t *a_scales, con
 /*
  * The operators around the MXFP8 layers ([Cost]: the last 16.6 % of layers),
  * which the pages leave out: what makes the rows that those layers quantise
- * from the residual stream, and the optimiser step that consumes its weight gradients.
+ * from the residual stream, the gated block in one kernel with its backward
+ * pass, and the optimiser step that consumes its weight gradients.
  */
 
 /*
@@ -483,6 +484,51 @@ PMN_API pmn_status pmn_add_rmsnorm_backward(const void *dy, const void *r, int r
 
 /* Workspace bytes of pmn_add_rmsnorm_backward; -1 for invalid sizes.  Host only. */
 PMN_API int64_t pmn_add_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * The gated projection of an MXFP8 expert in one kernel: both projections, the
+ * activation, the product and the quantisation of h.
+ *   y = A . B_e^T (gate = its first f columns, up = the last f; float32)
+ *   h = silu(gate) * up;  out = MXFP8(h) along the row,
+ *   out_t = MXFP8(h^T) along the routed rows (what the K-grouped GEMM of dW2
+ *   contracts); both from the float32 h.
+ *  a, a_scales  MXFP8 [total_rows, k];  b, b_scales  MXFP8 [num_experts, 2 f, k].
+ *  offsets  DEVICE int32 [num_experts + 1], non-decreasing, within
+ *           [0, total_rows]; multiples of 32 where out_t is written.  Checked on
+ *           the device: bad offsets run nothing and latch PMN_DEVERR_BAD_OFFSETS.
+ *  f        multiple of 128;  k multiple of 512;  num_experts <= 1024.
+ *  out      uint8 [total_rows, f];  out_scales uint8 [total_rows, f / 32].
+ *  out_t, out_t_scales  both NULL, or uint8 [f, total_rows] and
+ *           [f, total_rows / 32] (total_rows % 32 == 0).
+ *  y_out    NULL, or bf16 [total_rows, 2 f]: y rounded to nearest even, for
+ *           pmn_dh_gemm_swiglu_backward_mxfp8.
+ * Rows outside every expert's segment are not written.
+ */
+PMN_API pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
+                                            const uint8_t *b_scales, const int32_t *offsets, int num_experts,
+                                            int64_t total_rows, int64_t f, int64_t k, uint8_t *out,
+                                            uint8_t *out_scales, uint8_t *out_t, uint8_t *out_t_scales, void *y_out,
+                                            void *stream);
+
+/*
+ * Backward of the gated projection as far as its pre-activations, in one kernel:
+ *   dh = A . B_e^T  (A = MXFP8 of dY [total_rows, k], B = MXFP8 of W2^T
+ *        [num_experts, f, k]; k = d_model; float32)
+ *   s = 1 / (1 + e^-gate);  dup = dh * gate * s;
+ *   dgate = dh * up * s * (1 + gate * (1 - s));   dY1 = [dgate | dup]
+ *   out = MXFP8(dY1) along the row (for dX), out_t = MXFP8(dY1^T) along the
+ *   routed rows (for dW1); both from the float32 dY1.
+ *  y        bf16 [total_rows, 2 f]: gate | up as the forward wrote them.
+ *  offsets  as above, multiples of 32.  f % 128 == 0, k % 512 == 0.
+ *  out      uint8 [total_rows, 2 f];  out_scales uint8 [total_rows, 2 f / 32];
+ *  out_t    uint8 [2 f, total_rows];  out_t_scales uint8 [2 f, total_rows / 32];
+ *           total_rows % 32 == 0.
+ */
+PMN_API pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
+                                                     const uint8_t *b_scales, const void *y, const int32_t *offsets,
+                                                     int num_experts, int64_t total_rows, int64_t f, int64_t k,
+                                                     uint8_t *out, uint8_t *out_scales, uint8_t *out_t,
+                                                     uint8_t *out_t_scales, void *stream);
 
 /* One tensor of an AdamW step: device pointers, 16-byte aligned except the
  * scales; n elements. */

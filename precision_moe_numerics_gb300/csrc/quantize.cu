@@ -1556,9 +1556,13 @@ pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fo
 
 // Reads and clears the quantisation kernels' device error bits (called by
 // pmn_get_device_error, which owns the stream synchronisation).
+pmn_status pmn_take_gated_device_error(cudaStream_t s, int *bits);  // gated.cu
+
+// The error bits of this file's kernels and of the gated block's.
 pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits)
 {
-    int host = 0;
+    int host = 0, gated = 0;
+    if (pmn_take_gated_device_error(s, &gated) != PMN_OK) return PMN_ERR_CUDA;
     if (cudaMemcpyFromSymbolAsync(&host, g_pmn_quant_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return PMN_ERR_CUDA;
@@ -1569,7 +1573,7 @@ pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits)
             cudaStreamSynchronize(s) != cudaSuccess)
             return PMN_ERR_CUDA;
     }
-    *bits = host;
+    *bits = host | gated;
     return PMN_OK;
 }
 

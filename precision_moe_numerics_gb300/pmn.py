@@ -61,6 +61,8 @@ SIGNATURES = {
     "pmn_add_rmsnorm_mxfp8": ([_P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _P, _P, _P, _P, _P], _I),
     "pmn_add_rmsnorm_backward": ([_P, _P, _I, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P], _I),
     "pmn_add_rmsnorm_backward_workspace_bytes": ([_I64, _I64], _I64),
+    "pmn_w1_gemm_swiglu_mxfp8": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P], _I),
+    "pmn_dh_gemm_swiglu_backward_mxfp8": ([_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P], _I),
     "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
@@ -514,6 +516,62 @@ def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=No
                                           workspace.numel() * workspace.element_size(), _stream(stream)),
            "add_rmsnorm_backward")
     return dr, dx, dw
+
+
+def _gated_operands(a, b, offsets, what):
+    """checks of the operands both directions share; (rows, k, experts, rows of B per expert)"""
+    aq, asc = a
+    bq, bsc = b
+    if aq.dim() != 2 or bq.dim() != 3 or aq.shape[1] != bq.shape[2]:
+        raise PmnError("%s: a is [rows, k], b is [experts, n, k]" % what)
+    rows, k = aq.shape
+    experts, n = bq.shape[0], bq.shape[1]
+    for t, shape in ((aq, (rows, k)), (asc, (rows, k // 32)), (bq, (experts, n, k)), (bsc, (experts, n, k // 32))):
+        _shaped(t, shape, torch.uint8, what + ": an operand")
+    _shaped(offsets, (experts + 1,), torch.int32, what + ": offsets")
+    return rows, k, experts, n
+
+
+def w1_gemm_swiglu_mxfp8(a, b, offsets, out=None, out_t=None, y=None, want_t=False, want_y=False, stream=None):
+    """The gated projection in one kernel: MXFP8 of h = silu(X . Wg^T) * (X . Wu^T).
+
+    a = MXFP8 rows (u8 [T, K], u8 [T, K/32]); b = MXFP8 W1 (u8 [E, 2F, K], u8 [E, 2F, K/32]), gate rows first;
+    offsets int32 [E+1] on the device.  Returns (h, h_t or None, y or None): h = (u8 [T, F], u8 [T, F/32]); h_t =
+    MXFP8 of h^T along the rows (u8 [F, T], u8 [F, T/32]; offsets and T multiples of 32), y = bf16 [T, 2F], both
+    written where they are passed in or wanted (a training step's backward pass needs them)."""
+    rows, k, experts, f2 = _gated_operands(a, b, offsets, "w1_gemm_swiglu_mxfp8")
+    f, dev = f2 // 2, a[0].device
+    out = _mxfp8_out(out, rows, f, dev)
+    if out_t is not None or want_t:
+        out_t = _mxfp8_out(out_t, f, rows, dev, "out_t")
+    if y is not None:
+        _shaped(y, (rows, f2), torch.bfloat16, "y")
+    elif want_y:
+        y = torch.empty((rows, f2), dtype=torch.bfloat16, device=dev)
+    t, tsc = out_t if out_t is not None else (None, None)
+    _check(lib().pmn_w1_gemm_swiglu_mxfp8(_ptr(a[0]), _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), _ptr(offsets), experts,
+                                          rows, f, k, _ptr(out[0]), _ptr(out[1]), _ptr(t), _ptr(tsc), _ptr(y),
+                                          _stream(stream)),
+           "w1_gemm_swiglu_mxfp8")
+    return out, out_t, y
+
+
+def dh_gemm_swiglu_backward_mxfp8(a, b, y, offsets, out=None, out_t=None, stream=None):
+    """Backward of the gated projection as far as its pre-activations: dH = dY . W2, then MXFP8 of dY1 =
+    [dgate | dup] and of dY1^T.
+
+    a = MXFP8 dY (u8 [T, D], u8 [T, D/32]); b = MXFP8 W2^T (u8 [E, F, D], u8 [E, F, D/32]); y = bf16 [T, 2F] of the
+    forward.  Returns ((u8 [T, 2F], u8 [T, 2F/32]), (u8 [2F, T], u8 [2F, T/32])): the operands of the dX and dW1
+    GEMMs.  offsets and T are multiples of 32."""
+    rows, k, experts, f = _gated_operands(a, b, offsets, "dh_gemm_swiglu_backward_mxfp8")
+    _shaped(y, (rows, 2 * f), torch.bfloat16, "y")
+    dev = a[0].device
+    out, out_t = _mxfp8_out(out, rows, 2 * f, dev), _mxfp8_out(out_t, 2 * f, rows, dev, "out_t")
+    _check(lib().pmn_dh_gemm_swiglu_backward_mxfp8(_ptr(a[0]), _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), _ptr(y),
+                                                   _ptr(offsets), experts, rows, f, k, _ptr(out[0]), _ptr(out[1]),
+                                                   _ptr(out_t[0]), _ptr(out_t[1]), _stream(stream)),
+           "dh_gemm_swiglu_backward_mxfp8")
+    return out, out_t
 
 
 class AdamWTensors:

@@ -27,20 +27,23 @@ def blocks(v):
 
 
 def check_rn(q, sc, v, rel, what=""):
-    """q, sc: bytes of MXFP8 (round to nearest) of values that are within `rel` of the 64-bit v.
+    """q, sc: bytes of MXFP8 (round to nearest) of values that are within `rel` (relative) of the 64-bit v"""
+    check_rn_abs(q, sc, v, rel * np.abs(v), what)
 
-    The scale must be the definition's, except where amax is within `rel` of a power-of-two boundary; each element
-    must be within half a step of its neighbourhood (2^-4 of the value, 2^-10 of the scale below E4M3's normal
-    range) plus what `rel` allows."""
-    b = blocks(v)
-    amax = np.abs(b).max(-1)
-    lo, hi = exponent(amax * (1 - rel)), exponent(amax * (1 + rel))
+
+def check_rn_abs(q, sc, v, err, what=""):
+    """q, sc: bytes of MXFP8 (round to nearest) of values that are within `err` (absolute, per element) of v.
+
+    The scale must be the definition's, except where the block's largest value is within its error of a boundary
+    between two scales; each element must be within half a step of its neighbourhood (2^-4 of the value, 2^-10 of the
+    scale below E4M3's normal range) plus what `err` allows."""
+    b, d = blocks(np.abs(v)), blocks(err)
+    lo, hi = exponent(np.maximum(b - d, 0).max(-1)), exponent((b + d).max(-1))
     e = sc.astype(np.int64) - 127
     bad = (e < lo) | (e > hi)
     assert not bad.any(), "%s: %d scales off" % (what, bad.sum())
-    d = decode(q, sc)
     step = np.maximum(np.abs(v) * 2.0 ** -4, np.repeat(np.ldexp(1.0, e - 10), 32, axis=-1)[..., :v.shape[-1]])
-    over = np.abs(d - v) - step - 2 * rel * np.abs(v)
+    over = np.abs(decode(q, sc) - v) - step - 2 * err
     assert over.max(initial=-1.0) <= 0, "%s: %d of %d elements beyond half a step" % (what, (over > 0).sum(), v.size)
 
 
