@@ -33,8 +33,10 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int EW = 8;                       // epilogue warps, two per TMEM lane quadrant
 constexpr int THREADS = 128 + 32 * EW;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int TP = 17;                      // row pitch (floats) of a warp's transposition buffer
-constexpr int TP_BYTES = 32 * TP * 4;
+// An epilogue warp's shared memory: 32 rows x 32 columns of bf16 gate and up
+// (2 x 2 KB), and 2 KB through which blocks are transposed and codes are staged
+// for TMA stores.
+constexpr int Y_BYTES = 4096, T_BYTES = 2048, WARP_BYTES = Y_BYTES + T_BYTES;
 
 // One tile: 128 routed rows of an expert times TBN rows of its weight.  Forward:
 // TBN / 2 gate rows and the TBN / 2 up rows of the same columns of h; backward:
@@ -48,12 +50,12 @@ struct Cfg {
     static constexpr int RB = (TBN + 127) / 128;    // 128-row scale blocks of B
     static constexpr int A_BYTES = BM * 128, B_BYTES = TBN * 128, SF_BYTES = 512 * (1 + RB);
     static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SF_BYTES + 1023) / 1024 * 1024;
-    static constexpr int STAGES = TBN == 256 ? 4 : TBN == 128 ? 5 : 7;
+    static constexpr int STAGES = TBN >= 192 ? 4 : TBN == 128 ? 5 : 7;
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
     static constexpr int NR = 4 + TBN / 32;         // scale rows per lane
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * TP_BYTES + 1024 + (MAX_GROUPS + 1) * 4;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * WARP_BYTES + 1024 + (MAX_GROUPS + 1) * 4;
     static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -112,54 +114,91 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, f
     return cvt_e4m3x2_rn(__fmul_rn(a, s), __fmul_rn(b, s)) | (cvt_e4m3x2_rn(__fmul_rn(c, s), __fmul_rn(d, s)) << 16);
 }
 
+// Largest magnitude of the thread's values -> E8M0 exponent and 2^-e.
+__device__ __forceinline__ float block_scale(float amax, uint8_t &byte)
+{
+    const int e = mx_exponent_448(amax);
+    byte = (uint8_t)(e + 127);
+    return exp2_neg(e);
+}
+
 // MXFP8 of one row's 32 columns held by this thread.
-__device__ __forceinline__ void store_row_block(const float (&v)[32], uint8_t *q, uint8_t *sc)
+__device__ __forceinline__ void row_block(const float (&v)[32], uint4 (&q)[2], uint8_t &sc)
 {
     float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    const int e = mx_exponent_448(amax);
-    const float s = exp2_neg(e);
+    const float s = block_scale(amax, sc);
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = e4m3x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s);
-    uint4 *o = reinterpret_cast<uint4 *>(q);
-    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    *sc = (uint8_t)(e + 127);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// MXFP8 along the rows of a warp's 32 x 32 block (lane = row, v[j] = column j),
-// in two halves of 16 columns through shared memory: lane l takes column l % 16
-// and rows 16 (l / 16) .. + 15, so a column's block lies in lanes l and l + 16.
-// q, sc: the block's first column in the transposed tensor, at its first row.
-__device__ __forceinline__ void store_col_blocks(const float (&v)[32], float *buf, uint8_t *q, uint8_t *sc,
-                                                 int64_t pitch, int lane)
+// 16-byte piece `i` of row `r` in a box of 32 rows x 32 bytes (TMA's 32-byte
+// swizzle) or x 64 bytes (64-byte swizzle): eight lanes that access one piece of
+// eight consecutive rows meet eight different bank groups.
+__device__ __forceinline__ int box32(int r, int i) { return 32 * r + 16 * (i ^ ((r >> 2) & 1)); }
+__device__ __forceinline__ int box64(int r, int i) { return 64 * r + 16 * (i ^ ((r >> 1) & 3)); }
+
+// Largest magnitude over the warp's lanes (NaN ignored, as fmaxf does).
+__device__ __forceinline__ uint32_t warp_absmax(float v)
 {
-    const int c = lane & 15, hi = lane >> 4;
+    float m;
+    asm("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return __float_as_uint(m);
+}
+
+// MXFP8 along the rows of a warp's 32 x 32 block (lane = row, v[j] = column j).
+// A column's maximum is one reduction over the lanes, so the values are scaled
+// and converted where they are and only bytes are transposed: through shared
+// memory (rows 36 bytes apart: conflict-free both ways), lane 4 k + r then holds
+// columns 4 k .. 4 k + 3, rows 8 r .. 8 r + 7.
+// The exponent rule of mx_exponent_448 on the bits M of the maximum: with
+// t = (M + 0x1FFFFF) >> 23 (a carry where M's fraction is above 1.75) and t >= 8,
+// e = t - 135, so the scale byte is t - 8 and 2^-e has the exponent field 262 - t.
+// q: the block's first column at its first row; pitch: bytes between columns.
+__device__ __forceinline__ void col_blocks(const float (&v)[32], uint8_t *buf, uint8_t *q, int64_t pitch, uint8_t &sc,
+                                           int lane)
+{
+    uint32_t sb[8];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        __syncwarp();
+    for (int k = 0; k < 8; ++k) {
+        float y[4];
+        uint32_t t[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) buf[lane * TP + j] = v[16 * half + j];
-        __syncwarp();
-        float u[16];
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            u[i] = buf[(16 * hi + i) * TP + c];
-            amax = fmaxf(amax, fabsf(u[i]));
+        for (int i = 0; i < 4; ++i) {
+            t[i] = max(min(warp_absmax(v[4 * k + i]), 0x7F800000u), 0x04000000u) + 0x1FFFFFu;  // (all NaN: as infinity)
+            y[i] = __fmul_rn(v[4 * k + i], __uint_as_float(0x83000000u - (t[i] & 0xFF800000u)));
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 16));
-        const int e = mx_exponent_448(amax);
-        const float s = exp2_neg(e);
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = e4m3x4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3], s);
-        const int64_t col = 16 * half + c;
-        *reinterpret_cast<uint4 *>(q + col * pitch + 16 * hi) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (hi == 0) sc[col * (pitch / 32)] = (uint8_t)(e + 127);
+        *reinterpret_cast<uint32_t *>(buf + 36 * lane + 4 * k) =
+            cvt_e4m3x2_rn(y[0], y[1]) | (cvt_e4m3x2_rn(y[2], y[3]) << 16);
+        sb[k] = __byte_perm(__byte_perm(t[0] << 1, t[1] << 1, 0x0073), __byte_perm(t[2] << 1, t[3] << 1, 0x0073), 0x5410) -
+                0x08080808u;
     }
+    __syncwarp();
+    const int k = lane >> 2, r = lane & 3;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t *>(buf + 36 * (8 * r + i) + 4 * k);
+    __syncwarp();
+    uint2 o[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 4 x 4 bytes each
+        const uint32_t a = __byte_perm(w[4 * h], w[4 * h + 1], 0x5140), b = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x5140);
+        const uint32_t c = __byte_perm(w[4 * h], w[4 * h + 1], 0x7362), d = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x7362);
+        (h ? o[0].y : o[0].x) = __byte_perm(a, b, 0x5410);
+        (h ? o[1].y : o[1].x) = __byte_perm(a, b, 0x7632);
+        (h ? o[2].y : o[2].x) = __byte_perm(c, d, 0x5410);
+        (h ? o[3].y : o[3].x) = __byte_perm(c, d, 0x7632);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2 *>(q + (4 * k + i) * pitch + 8 * r) = o[i];
+    const uint32_t s01 = k & 1 ? sb[1] : sb[0], s23 = k & 1 ? sb[3] : sb[2], s45 = k & 1 ? sb[5] : sb[4],
+                   s67 = k & 1 ? sb[7] : sb[6];
+    const uint32_t lo = k & 2 ? s23 : s01, hi = k & 2 ? s67 : s45;
+    sc = (uint8_t)((k & 4 ? hi : lo) >> (8 * r));
 }
 
 // One persistent kernel per call, one CTA per SM:
@@ -174,19 +213,20 @@ __device__ __forceinline__ void store_col_blocks(const float (&v)[32], float *bu
 // down.
 template <bool BWD, int TBN>
 __global__ void __launch_bounds__(THREADS, 1)
-    gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args p)
+    gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmY, const Args p)
 {
     using C = Cfg<BWD, TBN>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *stages = smem;
-    float *tbuf = reinterpret_cast<float *>(smem + STAGES * C::STAGE_BYTES);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES + EW * TP_BYTES);
+    uint8_t *wbuf = smem + STAGES * C::STAGE_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES + EW * WARP_BYTES);
     const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * STAGES, bar_sfr = bar_empty + 8 * STAGES;
     const uint32_t bar_acc_full = bar_sfr + 8 * STAGES, bar_acc_empty = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_empty + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 5);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 5 + EW);
     int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
     int *s_total = s_abort + 1;
     int *s_cum = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 1024);
@@ -203,6 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(bar_acc_empty + 8 * b, EW);
         }
         mbar_init(bar_drain, 1);
+        for (int w = 0; w < EW; ++w) mbar_init(bar_drain + 8 + 8 * w, 1);
         *s_abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
@@ -420,103 +461,186 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
         // Warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31 and every
-        // second 32-column chunk.
+        // second 32-column chunk.  Its global accesses are TMA boxes of 32 rows x
+        // 32 columns (a row-per-thread access would touch 32 lines per
+        // instruction); only the rows of a 32-row slice that an expert's end cuts
+        // are stored one by one.
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        float *buf = tbuf + (warp - 4) * (32 * TP);
-        uint32_t abuf = 0, aphase = 0;
+        uint8_t *ybuf = wbuf + (warp - 4) * WARP_BYTES, *tb = ybuf + Y_BYTES;
+        const uint32_t yb = smem_u32(ybuf), tbs = smem_u32(tb), bar_y = bar_drain + 8 + 8 * (warp - 4);
+        uint32_t abuf = 0, aphase = 0, yphase = 0;
         int gc = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        bool ok = true;
+        // backward: gate and up of the next chunk are on their way while a chunk
+        // is worked on
+        int yt = blockIdx.x, yc = half, ygc = 0;
+        bool pending = false;
+        Tile yti;
+        if (BWD && yt < total) yti = get_tile<BWD, TBN>(yt, p, s_cum, ygc);
+        auto fetch_y = [&]() {
+            if (yt >= total) return;
+            if (yti.m0 + 32 * quad < yti.row_end && yti.h0 + 32 * yc < p.f) {
+                pending = true;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar_y, Y_BYTES);
+                    tma_load_2d(yb, &tmY, bar_y, yti.h0 + 32 * yc, (int32_t)yti.m0 + 32 * quad);
+                    tma_load_2d(yb + Y_BYTES / 2, &tmY, bar_y, (int32_t)p.f + yti.h0 + 32 * yc, (int32_t)yti.m0 + 32 * quad);
+                }
+            }
+            yc += 2;
+            if (yc >= C::NCH) {
+                yc = half;
+                yt += gridDim.x;
+                if (yt < total) yti = get_tile<BWD, TBN>(yt, p, s_cum, ygc);
+            }
+        };
+        // shared memory that TMA stores still read may be written again
+        auto stores_read = [&]() {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+        };
+        auto publish = [&]() {  // written by all lanes -> visible to TMA
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        // one output's row codes into a staging box, and its scale bytes
+        auto put_row = [&](const float (&v)[32], int box, int64_t row, int64_t col, int64_t width, bool valid, bool full) {
+            uint4 q[2];
+            uint8_t sc;
+            row_block(v, q, sc);
+            if (full) {
+                *reinterpret_cast<uint4 *>(tb + 1024 * box + box32(lane, 0)) = q[0];
+                *reinterpret_cast<uint4 *>(tb + 1024 * box + box32(lane, 1)) = q[1];
+            } else if (valid) {
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + row * width + col);
+                o[0] = q[0];
+                o[1] = q[1];
+            }
+            if (valid) p.out_sc[row * (width / 32) + col / 32] = sc;
+        };
+        // one output's column blocks
+        auto put_cols = [&](const float (&v)[32], int64_t row0, int64_t col) {
+            uint8_t sc;
+            col_blocks(v, tb, p.out_t + col * p.m + row0, p.m, sc, lane);
+            p.out_t_sc[(col + lane) * (p.m / 32) + row0 / 32] = sc;
+        };
+        if (BWD) fetch_y();
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             const Tile ti = get_tile<BWD, TBN>(t, p, s_cum, gc);
             const int64_t row0 = ti.m0 + 32 * quad, row = row0 + lane;
-            const bool valid = row < ti.row_end;
-            const bool any = row0 < ti.row_end;  // with column blocks: all 32 rows or none
-            if (!warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns)) {
-                if (lane == 0) {
-                    *(volatile int *)s_abort = 1;
-                    latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-                }
-                break;
-            }
+            const bool valid = row < ti.row_end, any = row0 < ti.row_end, full = row0 + 32 <= ti.row_end;
+            ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
+            if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * TBN;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
+            };
+            if (half >= C::NCH) release();
 #pragma unroll 1
             for (int c = half; c < C::NCH; c += 2) {
                 const int64_t col = ti.h0 + 32 * c;
                 const bool on = any && col < p.f;
-                float v[32];
+                float v[32], u[32];
                 if constexpr (!BWD) {
-                    float u[32];
                     tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_32x32b_x32(acc + C::HB + 32 * c, reinterpret_cast<uint32_t(&)[32]>(u));
                     tmem_ld_wait();
-                    if (on) {
-                        if (p.y && valid) {
+                    if (c + 2 >= C::NCH) release();
+                    if (!on) continue;
+                    stores_read();
+                    if (p.y) {  // y in bf16 for the backward pass
 #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                uint4 *o = reinterpret_cast<uint4 *>(p.y + row * 2 * p.f + part * p.f + col);
+                        for (int part = 0; part < 2; ++part)
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint32_t w[4];
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t w[4];
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float *x = (part ? u : v) + 8 * j + 2 * i;
-                                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
-                                        w[i] = *reinterpret_cast<const uint32_t *>(&b2);
-                                    }
-                                    o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int i = 0; i < 4; ++i) {
+                                    const float *x = (part ? u : v) + 8 * j + 2 * i;
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
+                                    w[i] = *reinterpret_cast<const uint32_t *>(&b2);
                                 }
+                                const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (full) *reinterpret_cast<uint4 *>(ybuf + part * (Y_BYTES / 2) + box64(lane, j)) = q;
+                                else if (valid) *reinterpret_cast<uint4 *>(p.y + row * 2 * p.f + part * p.f + col + 8 * j) = q;
                             }
-                        }
+                    }
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = silu_mul(v[j], u[j]);
-                        if (valid) store_row_block(v, p.out + row * p.f + col, p.out_sc + row * (p.f / 32) + col / 32);
-                        if (p.out_t)
-                            store_col_blocks(v, buf, p.out_t + col * p.m + row0, p.out_t_sc + col * (p.m / 32) + row0 / 32,
-                                             p.m, lane);
+                    for (int j = 0; j < 32; ++j) v[j] = silu_mul(v[j], u[j]);
+                    put_row(v, 0, row, col, p.f, valid, full);
+                    if (full) {
+                        publish();
+                        if (lane == 0) {
+                            tma_store_2d(&tmO, tbs, (int32_t)col, (int32_t)row0);
+                            if (p.y) {
+                                tma_store_2d(&tmY, yb, (int32_t)col, (int32_t)row0);
+                                tma_store_2d(&tmY, yb + Y_BYTES / 2, (int32_t)(p.f + col), (int32_t)row0);
+                            }
+                            bulk_commit_group();
+                        }
+                    }
+                    if (p.out_t) {
+                        stores_read();
+                        put_cols(v, row0, col);
                     }
                 } else {
                     uint4 gw[4], uw[4];
                     if (on) {
-                        const uint4 *yg = reinterpret_cast<const uint4 *>(p.y + row * 2 * p.f + col);
-                        const uint4 *yu = reinterpret_cast<const uint4 *>(p.y + row * 2 * p.f + p.f + col);
+                        ok = warp_wait(bar_y, yphase, p.wait_ns);
+                        if (!ok) break;
+                        pending = false;
+                        yphase ^= 1;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            gw[j] = __ldg(yg + j);
-                            uw[j] = __ldg(yu + j);
+                            gw[j] = *reinterpret_cast<const uint4 *>(ybuf + box64(lane, j));
+                            uw[j] = *reinterpret_cast<const uint4 *>(ybuf + Y_BYTES / 2 + box64(lane, j));
                         }
+                        __syncwarp();
                     }
+                    fetch_y();
                     tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_wait();
-                    if (on) {
-                        float du[32];
+                    if (c + 2 >= C::NCH) release();
+                    if (!on) continue;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const uint32_t a = u4_word(gw[j >> 3], (j >> 1) & 3), b = u4_word(uw[j >> 3], (j >> 1) & 3);
-                            const float g = __uint_as_float((j & 1) ? (a & 0xFFFF0000u) : (a << 16));
-                            const float u = __uint_as_float((j & 1) ? (b & 0xFFFF0000u) : (b << 16));
-                            const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g)));
-                            const float ds = __fmul_rn(v[j], s);
-                            du[j] = __fmul_rn(ds, g);
-                            v[j] = __fmul_rn(__fmul_rn(ds, u), fmaf(g, __fsub_rn(1.0f, s), 1.0f));
-                        }
-                        const int64_t f2 = 2 * p.f;
-                        store_row_block(v, p.out + row * f2 + col, p.out_sc + row * (f2 / 32) + col / 32);
-                        store_row_block(du, p.out + row * f2 + p.f + col, p.out_sc + row * (f2 / 32) + (p.f + col) / 32);
-                        store_col_blocks(v, buf, p.out_t + col * p.m + row0, p.out_t_sc + col * (p.m / 32) + row0 / 32,
-                                         p.m, lane);
-                        store_col_blocks(du, buf, p.out_t + (p.f + col) * p.m + row0,
-                                         p.out_t_sc + (p.f + col) * (p.m / 32) + row0 / 32, p.m, lane);
+                    for (int j = 0; j < 32; ++j) {
+                        const uint32_t a = u4_word(gw[j >> 3], (j >> 1) & 3), b = u4_word(uw[j >> 3], (j >> 1) & 3);
+                        const float gt = __uint_as_float((j & 1) ? (a & 0xFFFF0000u) : (a << 16));
+                        const float up = __uint_as_float((j & 1) ? (b & 0xFFFF0000u) : (b << 16));
+                        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gt)));
+                        const float ds = __fmul_rn(v[j], s);
+                        u[j] = __fmul_rn(ds, gt);
+                        v[j] = __fmul_rn(__fmul_rn(ds, up), fmaf(gt, __fsub_rn(1.0f, s), 1.0f));
                     }
+                    stores_read();
+                    put_row(v, 0, row, col, 2 * p.f, true, true);
+                    put_row(u, 1, row, p.f + col, 2 * p.f, true, true);
+                    publish();
+                    if (lane == 0) {
+                        tma_store_2d(&tmO, tbs, (int32_t)col, (int32_t)row0);
+                        tma_store_2d(&tmO, tbs + 1024, (int32_t)(p.f + col), (int32_t)row0);
+                        bulk_commit_group();
+                    }
+                    stores_read();
+                    put_cols(v, row0, col);
+                    put_cols(u, row0, p.f + col);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
             if (++abuf == C::ACC) {
                 abuf = 0;
                 aphase ^= 1;
             }
         }
+        if (!ok && lane == 0) {
+            *(volatile int *)s_abort = 1;
+            latch_error(PMN_DEVERR_WAIT_TIMEOUT);
+        }
+        if (BWD && pending) (void)warp_wait(bar_y, yphase, 1000000000ull);  // a copy may still be landing
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -545,16 +669,17 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// E4M3 bytes [rows, k] in boxes of 128 bytes x box_rows, 128-byte swizzle; rows
-// past the end read as zeros.
-bool make_map(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint32_t box_rows)
+// A row-major tensor [rows, width] of bytes or bf16 values; out-of-range elements of
+// a loaded box read as zeros, of a stored box are not written.
+bool make_map(CUtensorMap *m, const void *base, bool bf16, uint64_t width, uint64_t rows, uint32_t box_w,
+              uint32_t box_rows, CUtensorMapSwizzle swizzle)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {k, rows}, strides[1] = {k};
-    cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t dims[2] = {width, rows}, strides[1] = {width * (bf16 ? 2 : 1)};
+    cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -564,10 +689,15 @@ template <bool BWD, int TBN>
 pmn_status launch(const uint8_t *a, const uint8_t *b, const Args &args, cudaStream_t s)
 {
     using C = Cfg<BWD, TBN>;
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, a, (uint64_t)args.k, (uint64_t)args.m, BM) ||
-        !make_map(&mb, b, (uint64_t)args.k, (uint64_t)args.b_rows, BWD ? TBN : TBN / 2))
+    const uint64_t m = (uint64_t)args.m, f = (uint64_t)args.f, k = (uint64_t)args.k, w = BWD ? 2 * f : f;
+    const auto S32 = CU_TENSOR_MAP_SWIZZLE_32B, S64 = CU_TENSOR_MAP_SWIZZLE_64B, S128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap ma, mb, mo, my;
+    if (!make_map(&ma, a, false, k, m, 128, BM, S128) ||
+        !make_map(&mb, b, false, k, (uint64_t)args.b_rows, 128, BWD ? TBN : TBN / 2, S128) ||
+        !make_map(&mo, args.out, false, w, m, 32, 32, S32))
         return PMN_ERR_CUDA;
+    my = mo;  // without y: not used
+    if (args.y && !make_map(&my, args.y, true, 2 * f, m, 32, 32, S64)) return PMN_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
@@ -575,7 +705,7 @@ pmn_status launch(const uint8_t *a, const uint8_t *b, const Args &args, cudaStre
     auto kern = gated_kernel<BWD, TBN>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return PMN_ERR_CUDA;
-    kern<<<(unsigned)sms, THREADS, C::SMEM_BYTES, s>>>(ma, mb, args);
+    kern<<<(unsigned)sms, THREADS, C::SMEM_BYTES, s>>>(ma, mb, mo, my, args);
     return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
@@ -627,7 +757,7 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
     if (!out || !out_scales || !aligned16(out) || !aligned16(out_t) || !aligned16(y_out)) return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * 2 * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), pmn_wait_limit_ns()};
-    return launch<false, 256>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+    return launch<false, 192>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
@@ -644,5 +774,5 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const 
     const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)),
                     pmn_wait_limit_ns()};
-    return launch<true, 256>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+    return launch<true, 192>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
 }
