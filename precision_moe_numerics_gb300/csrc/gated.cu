@@ -28,34 +28,154 @@ namespace {
 
 __device__ int g_gated_error = 0;
 
-constexpr int BM = 128;
+// ---------------------------------------------------------------- CTA pairs
+// tcgen05 with cta_group::2: two CTAs of a cluster compute one 256-row tile, each
+// with its own 128 rows of A and half of B's rows; the leader (rank 0) issues.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The leader's copy of a shared-memory address of this CTA.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrives on the leader's copy of a barrier.  CTA scope: what the arrival stands
+// for lies in this CTA's own shared memory or TMEM, was put in order before it
+// (fence.proxy.async, tcgen05.wait) and is read there by tensor instructions.  A
+// release at cluster scope takes ~1000 clocks here (measured: a pair's stage
+// 1200-1700 clocks, bound by that).
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+
+// A tile load whose bytes are counted on a barrier of the pair's leader.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+template <int CT>
+__device__ __forceinline__ void tmem_alloc_ct(uint32_t dst_smem, uint32_t ncols)
+{
+    if (CT == 1) {
+        tmem_alloc(dst_smem, ncols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CT>
+__device__ __forceinline__ void tmem_dealloc_ct(uint32_t taddr, uint32_t ncols)
+{
+    if (CT == 1) tmem_dealloc(taddr, ncols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Arrives on `bar` (in both CTAs of a pair) once this thread's tcgen05 operations
+// so far have completed.
+template <int CT>
+__device__ __forceinline__ void tc_commit_ct(uint32_t bar)
+{
+    if (CT == 1) tc_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// The same in this CTA alone.
+template <int CT>
+__device__ __forceinline__ void tc_commit_own(uint32_t bar)
+{
+    if (CT == 1) tc_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int CT>
+__device__ __forceinline__ void tc_cp_ct(uint32_t taddr, uint64_t sdesc)
+{
+    if (CT == 1) tc_cp_32x128b_warpx4(taddr, sdesc);
+    else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+template <int CT>
+__device__ __forceinline__ void mma_mxfp8_ct(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    if (CT == 1) mma_mxfp8(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+}
+
+constexpr int BM = 128;  // rows per CTA
 constexpr int MAX_GROUPS = 1024;
-constexpr int EW = 8;                       // epilogue warps, two per TMEM lane quadrant
+constexpr int EW = 12;                      // epilogue warps, three per TMEM lane quadrant
 constexpr int THREADS = 128 + 32 * EW;
 constexpr uint32_t TMEM_COLS = 512;
 // An epilogue warp's shared memory: 32 rows x 32 columns of bf16 gate and up
-// (2 x 2 KB), and 2 KB through which blocks are transposed and codes are staged
-// for TMA stores.
-constexpr int Y_BYTES = 4096, T_BYTES = 2048, WARP_BYTES = Y_BYTES + T_BYTES;
+// (2 x 2 KB), and, once those are in registers, two blocks that are being
+// transposed (32 rows of 36 bytes each).
+constexpr int WARP_BYTES = 4096, COL_BYTES = 32 * 36;
 
-// One tile: 128 routed rows of an expert times TBN rows of its weight.  Forward:
+// One tile: 128 routed rows of an expert (256 on a CTA pair) times TBN rows of its weight.  Forward:
 // TBN / 2 gate rows and the TBN / 2 up rows of the same columns of h; backward:
 // TBN columns of dH.  A stage holds 128 bytes of K of both operands (TMA,
 // 128-byte swizzle) and their scale factors in the 32 x 128-bit form that
 // tcgen05.cp copies into TMEM.
-template <bool BWD, int TBN>
+template <bool BWD, int TBN, int CT>
 struct Cfg {
     static constexpr int HB = BWD ? TBN : TBN / 2;  // columns of h (dH) per tile
     static constexpr int NCH = HB / 32;             // 32-column chunks (MX blocks) of the epilogue
+    static constexpr int CPW = (NCH + 2) / 3;       // consecutive chunks per epilogue warp
     static constexpr int RB = (TBN + 127) / 128;    // 128-row scale blocks of B
-    static constexpr int A_BYTES = BM * 128, B_BYTES = TBN * 128, SF_BYTES = 512 * (1 + RB);
-    static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SF_BYTES + 1023) / 1024 * 1024;
-    static constexpr int STAGES = TBN >= 192 ? 4 : TBN == 128 ? 5 : 7;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = TBN / CT * 128;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, SF_BYTES = 512 * (1 + RB);
+    static constexpr int STAGES = CT == 2 ? 5 : 4;
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
-    static constexpr int NR = 4 + TBN / 32;         // scale rows per lane
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * WARP_BYTES + 1024 + (MAX_GROUPS + 1) * 4;
+    static constexpr int NR = 2 * (1 + RB);         // scale rows per lane of a scale-factor warp
+    static constexpr int SF_OFF = STAGES * STAGE_BYTES, WARP_OFF = SF_OFF + STAGES * SF_BYTES,
+                         BAR_OFF = WARP_OFF + EW * WARP_BYTES, SCALE_OFF = BAR_OFF + 256,
+                         CUM_OFF = SCALE_OFF + 3 * 2 * 512;
+    static constexpr int SMEM_BYTES = 1024 + CUM_OFF + (MAX_GROUPS + 1) * 4;
+    static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
+    static_assert(8 * (2 * STAGES + 8) + 16 <= 256, "barrier space");
     static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -68,6 +188,8 @@ struct Args {
     int64_t b_rows;          // rows of B of all experts
     uint8_t *out, *out_sc, *out_t, *out_t_sc;
     uint16_t *y;             // forward: written (or NULL); backward: read
+    bool wide;               // out is 32-byte aligned
+    bool pairs, words;       // alignment lets two row scales, four column scales be stored at once
     uint64_t wait_ns;
 };
 
@@ -77,16 +199,16 @@ struct Tile {
     int h0;  // first column of h
 };
 
-template <bool BWD, int TBN>
+template <bool BWD, int TBN, int CT>
 __device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int &gc)
 {
     while (gc + 1 < p.groups && s_cum[gc + 1] <= t) ++gc;  // every role walks its tiles upwards
-    constexpr int HB = Cfg<BWD, TBN>::HB;
+    constexpr int HB = Cfg<BWD, TBN, CT>::HB;
     const int nt = (int)((p.f + HB - 1) / HB);
     const int local = t - s_cum[gc], mi = local / nt;
     Tile ti;
     ti.g = gc;
-    ti.m0 = __ldg(p.offsets + gc) + (int64_t)mi * BM;
+    ti.m0 = __ldg(p.offsets + gc) + (int64_t)mi * (CT * BM);  // of the tile
     ti.row_end = __ldg(p.offsets + gc + 1);
     ti.h0 = (local - mi * nt) * HB;
     return ti;
@@ -101,17 +223,20 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 }
 
 // Instruction descriptor of the block-scaled MMA: E4M3 operands, E8M0 scales,
-// M = 128, N = TBN; sf_id selects the scale byte of the 32-deep K step.
-template <int TBN>
+// M = 128 per CTA, N = TBN; sf_id selects the scale byte of the 32-deep K step.
+template <int TBN, int CT>
 __device__ __forceinline__ uint32_t make_idesc(uint32_t sf_id)
 {
-    return (sf_id << 4) | ((uint32_t)(TBN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 4) << 24) | (sf_id << 29);
+    return (sf_id << 4) | ((uint32_t)(TBN >> 3) << 17) | (1u << 23) | ((uint32_t)(CT * BM >> 4) << 24) | (sf_id << 29);
 }
 
-// Four values times 2^-e -> four E4M3 bytes, nearest even.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float s)
+// Four values times their scales -> four E4M3 bytes, nearest even.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float sa, float sb, float sc, float sd)
 {
-    return cvt_e4m3x2_rn(__fmul_rn(a, s), __fmul_rn(b, s)) | (cvt_e4m3x2_rn(__fmul_rn(c, s), __fmul_rn(d, s)) << 16);
+    float x[4];
+    mul2(a, b, sa, sb, x[0], x[1]);
+    mul2(c, d, sc, sd, x[2], x[3]);
+    return cvt_e4m3x2_rn(x[0], x[1]) | (cvt_e4m3x2_rn(x[2], x[3]) << 16);
 }
 
 // Largest magnitude of the thread's values -> E8M0 exponent and 2^-e.
@@ -131,16 +256,34 @@ __device__ __forceinline__ void row_block(const float (&v)[32], uint4 (&q)[2], u
     const float s = block_scale(amax, sc);
     uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = e4m3x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s);
+    for (int j = 0; j < 8; ++j) w[j] = e4m3x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s, s, s, s);
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     q[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// 16-byte piece `i` of row `r` in a box of 32 rows x 32 bytes (TMA's 32-byte
-// swizzle) or x 64 bytes (64-byte swizzle): eight lanes that access one piece of
-// eight consecutive rows meet eight different bank groups.
-__device__ __forceinline__ int box32(int r, int i) { return 32 * r + 16 * (i ^ ((r >> 2) & 1)); }
-__device__ __forceinline__ int box64(int r, int i) { return 64 * r + 16 * (i ^ ((r >> 1) & 3)); }
+// 16-byte piece i of row r in 32 rows of 64 bytes: eight lanes that access one
+// piece of eight consecutive rows, or the four pieces of two rows, meet eight
+// different bank groups.
+__device__ __forceinline__ int piece64(int r, int i) { return 64 * r + 16 * (i ^ ((r >> 1) & 3)); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 32 bytes of one row: a whole sector in one store where the tensor is 32-byte aligned.
+__device__ __forceinline__ void store32(uint8_t *o, const uint4 (&q)[2], bool wide)
+{
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(q[0].x), "r"(q[0].y),
+                     "r"(q[0].z), "r"(q[0].w), "r"(q[1].x), "r"(q[1].y), "r"(q[1].z), "r"(q[1].w)
+                     : "memory");
+    else {
+        reinterpret_cast<uint4 *>(o)[0] = q[0];
+        reinterpret_cast<uint4 *>(o)[1] = q[1];
+    }
+}
+
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Largest magnitude over the warp's lanes (NaN ignored, as fmaxf does).
 __device__ __forceinline__ uint32_t warp_absmax(float v)
@@ -159,46 +302,58 @@ __device__ __forceinline__ uint32_t warp_absmax(float v)
 // t = (M + 0x1FFFFF) >> 23 (a carry where M's fraction is above 1.75) and t >= 8,
 // e = t - 135, so the scale byte is t - 8 and 2^-e has the exponent field 262 - t.
 // q: the block's first column at its first row; pitch: bytes between columns.
-__device__ __forceinline__ void col_blocks(const float (&v)[32], uint8_t *buf, uint8_t *q, int64_t pitch, uint8_t &sc,
-                                           int lane)
+// NB blocks are worked on side by side, as each step waits on the one before.
+template <int NB>
+__device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], uint8_t *buf, uint8_t *const (&q)[NB],
+                                           int64_t pitch, uint8_t (&sc)[NB], int lane)
 {
-    uint32_t sb[8];
+    uint32_t sb[NB][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float y[4];
-        uint32_t t[4];
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            t[i] = max(min(warp_absmax(v[4 * k + i]), 0x7F800000u), 0x04000000u) + 0x1FFFFFu;  // (all NaN: as infinity)
-            y[i] = __fmul_rn(v[4 * k + i], __uint_as_float(0x83000000u - (t[i] & 0xFF800000u)));
+        for (int n = 0; n < NB; ++n) {
+            float x[4], m[4];
+            uint32_t t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = (*v[n])[4 * k + i];
+                t[i] = max(min(warp_absmax(x[i]), 0x7F800000u), 0x04000000u) + 0x1FFFFFu;  // (all NaN: as infinity)
+                m[i] = __uint_as_float(0x83000000u - (t[i] & 0xFF800000u));
+            }
+            *reinterpret_cast<uint32_t *>(buf + n * COL_BYTES + 36 * lane + 4 * k) =
+                e4m3x4(x[0], x[1], x[2], x[3], m[0], m[1], m[2], m[3]);
+            sb[n][k] = __byte_perm(__byte_perm(t[0] << 1, t[1] << 1, 0x0073), __byte_perm(t[2] << 1, t[3] << 1, 0x0073),
+                                   0x5410) - 0x08080808u;
         }
-        *reinterpret_cast<uint32_t *>(buf + 36 * lane + 4 * k) =
-            cvt_e4m3x2_rn(y[0], y[1]) | (cvt_e4m3x2_rn(y[2], y[3]) << 16);
-        sb[k] = __byte_perm(__byte_perm(t[0] << 1, t[1] << 1, 0x0073), __byte_perm(t[2] << 1, t[3] << 1, 0x0073), 0x5410) -
-                0x08080808u;
-    }
     __syncwarp();
     const int k = lane >> 2, r = lane & 3;
-    uint32_t w[8];
+    uint32_t w[NB][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t *>(buf + 36 * (8 * r + i) + 4 * k);
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[n][i] = *reinterpret_cast<const uint32_t *>(buf + n * COL_BYTES + 36 * (8 * r + i) + 4 * k);
     __syncwarp();
-    uint2 o[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // 4 x 4 bytes each
-        const uint32_t a = __byte_perm(w[4 * h], w[4 * h + 1], 0x5140), b = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x5140);
-        const uint32_t c = __byte_perm(w[4 * h], w[4 * h + 1], 0x7362), d = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x7362);
-        (h ? o[0].y : o[0].x) = __byte_perm(a, b, 0x5410);
-        (h ? o[1].y : o[1].x) = __byte_perm(a, b, 0x7632);
-        (h ? o[2].y : o[2].x) = __byte_perm(c, d, 0x5410);
-        (h ? o[3].y : o[3].x) = __byte_perm(c, d, 0x7632);
+    for (int n = 0; n < NB; ++n) {
+        uint2 o[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 4 x 4 bytes each
+            const uint32_t w0 = w[n][4 * h], w1 = w[n][4 * h + 1], w2 = w[n][4 * h + 2], w3 = w[n][4 * h + 3];
+            const uint32_t a = __byte_perm(w0, w1, 0x5140), b = __byte_perm(w2, w3, 0x5140);
+            const uint32_t c = __byte_perm(w0, w1, 0x7362), d = __byte_perm(w2, w3, 0x7362);
+            (h ? o[0].y : o[0].x) = __byte_perm(a, b, 0x5410);
+            (h ? o[1].y : o[1].x) = __byte_perm(a, b, 0x7632);
+            (h ? o[2].y : o[2].x) = __byte_perm(c, d, 0x5410);
+            (h ? o[3].y : o[3].x) = __byte_perm(c, d, 0x7632);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2 *>(q[n] + (4 * k + i) * pitch + 8 * r) = o[i];
+        const uint32_t s01 = k & 1 ? sb[n][1] : sb[n][0], s23 = k & 1 ? sb[n][3] : sb[n][2],
+                       s45 = k & 1 ? sb[n][5] : sb[n][4], s67 = k & 1 ? sb[n][7] : sb[n][6];
+        const uint32_t lo = k & 2 ? s23 : s01, hi = k & 2 ? s67 : s45;
+        sc[n] = (uint8_t)((k & 4 ? hi : lo) >> (8 * r));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2 *>(q + (4 * k + i) * pitch + 8 * r) = o[i];
-    const uint32_t s01 = k & 1 ? sb[1] : sb[0], s23 = k & 1 ? sb[3] : sb[2], s45 = k & 1 ? sb[5] : sb[4],
-                   s67 = k & 1 ? sb[7] : sb[6];
-    const uint32_t lo = k & 2 ? s23 : s01, hi = k & 2 ? s67 : s45;
-    sc = (uint8_t)((k & 4 ? hi : lo) >> (8 * r));
 }
 
 // One persistent kernel per call, one CTA per SM:
@@ -211,39 +366,38 @@ __device__ __forceinline__ void col_blocks(const float (&v)[32], uint8_t *buf, u
 //   warps 4..  epilogue, one row per thread and 32 columns at a time
 // Every wait is bounded: on a timeout an error bit is latched and the CTA winds
 // down.
-template <bool BWD, int TBN>
+template <bool BWD, int TBN, int CT>
 __global__ void __launch_bounds__(THREADS, 1)
     gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmY, const Args p)
+                 const Args p)
 {
-    using C = Cfg<BWD, TBN>;
+    using C = Cfg<BWD, TBN, CT>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *stages = smem;
-    uint8_t *wbuf = smem + STAGES * C::STAGE_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES + EW * WARP_BYTES);
-    const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * STAGES, bar_sfr = bar_empty + 8 * STAGES;
-    const uint32_t bar_acc_full = bar_sfr + 8 * STAGES, bar_acc_empty = bar_acc_full + 16;
-    const uint32_t bar_drain = bar_acc_empty + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 5 + EW);
+    const uint32_t stages = smem_u32(smem);
+    const uint32_t bar_full = stages + C::BAR_OFF, bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16;
+    const uint32_t bar_drain = bar_acc_empty + 16, bar_group = bar_drain + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * (2 * STAGES + 8));
     int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
     int *s_total = s_abort + 1;
-    int *s_cum = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 1024);
+    int *s_cum = reinterpret_cast<int *>(smem + C::CUM_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CT == 2 ? (int)cluster_rank() : 0;
+    const int tile0 = blockIdx.x / CT, tstep = gridDim.x / CT;  // tiles of this CTA (pair)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_full + 8 * s, 1 + 2 * CT);  // the code tiles' bytes, each CTA's two scale-factor warps
             mbar_init(bar_empty + 8 * s, 1);
-            mbar_init(bar_sfr + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, EW);
+            mbar_init(bar_acc_empty + 8 * b, CT * EW);
         }
         mbar_init(bar_drain, 1);
-        for (int w = 0; w < EW; ++w) mbar_init(bar_drain + 8 + 8 * w, 1);
+        for (int g = 0; g < 3; ++g) mbar_init(bar_group + 8 * g, 4);
         *s_abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
@@ -251,8 +405,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (warp == 0) {
         __syncwarp();
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc_ct<CT>(smem_u32(tmem_slot), TMEM_COLS);
     }
     if (warp == 1) {
         // tiles of each group and their running sum, 32 groups at a time; offsets
@@ -272,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             good = __all_sync(0xFFFFFFFFu, good);
             if (!good) break;
-            int n = (hi - lo + BM - 1) / BM * nt, sum = n;
+            int n = (hi - lo + CT * BM - 1) / (CT * BM) * nt, sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -289,157 +442,180 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (CT == 2) cluster_sync();  // the pair's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = *s_total;
+    const int total = __shfl_sync(0xFFFFFFFFu, *s_total, 0);
     const int nks = (int)(p.k / 128);
+    auto give_up = [&]() {  // a wait ran out: every role winds down
+        if (lane == 0) {
+            *(volatile int *)s_abort = 1;
+            latch_error(PMN_DEVERR_WAIT_TIMEOUT);
+        }
+    };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            uint32_t stage = 0, phase = 0, issued = 0, last = 0;
-            int gc = 0;
-            for (int t = blockIdx.x; t < total && !*(volatile int *)s_abort; t += gridDim.x) {
-                const Tile ti = get_tile<BWD, TBN>(t, p, s_cum, gc);
-                const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
-                for (int ks = 0; ks < nks; ++ks) {
-                    if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns)) {
-                        *(volatile int *)s_abort = 1;
-                        latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-                        break;
-                    }
-                    uint8_t *st = stages + stage * C::STAGE_BYTES;
-                    const uint32_t fb = bar_full + 8 * stage;
-                    mbar_arrive_expect_tx(fb, C::A_BYTES + C::B_BYTES);
-                    tma_load_2d(smem_u32(st), &tmA, fb, ks * 128, (int32_t)ti.m0);
-                    tma_load_2d(smem_u32(st + C::A_BYTES), &tmB, fb, ks * 128, (int32_t)brow);
-                    if (!BWD)
-                        tma_load_2d(smem_u32(st + C::A_BYTES + C::B_BYTES / 2), &tmB, fb, ks * 128, (int32_t)(brow + p.f));
-                    issued |= 1u << stage;
-                    last = (last & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            // no copy may still be landing when the CTA ends
-            for (int s = 0; s < STAGES; ++s)
-                if (issued & (1u << s)) (void)mbar_wait(bar_full + 8 * s, (last >> s) & 1u, 1000000000ull);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---------------------------------------------------- scale factors
-        // Block b (A, then the 128-row blocks of B), lane r, word j: the four
-        // scale bytes of row 32 j + r of the stage's 128-deep K range.
-        const int64_t pitch = p.k / 32;
-        const int groups4 = nks / 4;  // k is a multiple of 512
-        int t = blockIdx.x, q = 0, gc = 0;
-        Tile ti;
-        if (t < total) ti = get_tile<BWD, TBN>(t, p, s_cum, gc);
-        auto fetch = [&](uint4 (&v)[C::NR]) {
-            if (t >= total) return;
-            const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
-#pragma unroll
-            for (int j = 0; j < C::NR; ++j) {
-                int64_t row;
-                const uint8_t *base;
-                bool ok;
-                if (j < 4) {
-                    row = ti.m0 + 32 * j + lane;
-                    base = p.sa;
-                    ok = row < p.m;
-                } else {
-                    const int n = 32 * (j - 4);  // row of B within the tile
-                    row = brow + n + lane + (!BWD && n >= C::HB ? p.f - C::HB : 0);
-                    base = p.sb;
-                    ok = row < p.b_rows;
-                }
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (ok) v[j] = __ldg(reinterpret_cast<const uint4 *>(base + row * pitch + 16 * q));
-            }
-            if (++q == groups4) {
-                q = 0;
-                t += gridDim.x;
-                if (t < total) ti = get_tile<BWD, TBN>(t, p, s_cum, gc);
-            }
-        };
-        uint32_t stage = 0, phase = 0;
+        // ---------------------------------------------------- TMA producer
+        uint32_t stage = 0, phase = 0, issued = 0, last = 0;
+        int gc = 0;
         bool ok = true;
-        auto put = [&](const uint4 (&v)[C::NR]) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                ok = ok && warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+        for (int t = tile0; t < total && ok; t += tstep) {
+            const Tile ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+            const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+            for (int ks = 0; ks < nks; ++ks) {
+                ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
                 if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
-                    if (!ok && lane == 0) {
-                        *(volatile int *)s_abort = 1;
-                        latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-                    }
+                    if (!ok) give_up();
                     ok = false;
-                    return;
+                    break;
                 }
-                uint4 *sf = reinterpret_cast<uint4 *>(stages + stage * C::STAGE_BYTES + C::A_BYTES + C::B_BYTES) + lane;
-                sf[0] = make_uint4(u4_word(v[0], s), u4_word(v[1], s), u4_word(v[2], s), u4_word(v[3], s));
-#pragma unroll
-                for (int b = 0; b < C::RB; ++b) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = 4 + 4 * b + j < C::NR ? u4_word(v[4 + 4 * b + j], s) : 0u;
-                    sf[32 * (1 + b)] = make_uint4(w[0], w[1], w[2], w[3]);
+                const uint32_t st = stages + stage * C::STAGE_BYTES, fb = bar_full + 8 * stage;
+                const int32_t x = ks * 128;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(fb, CT * (C::A_BYTES + C::B_BYTES));
+                    if constexpr (CT == 2) {
+                        // forward: the leader holds the gate rows, its peer the up rows
+                        const int64_t br = rank == 0 ? brow : BWD ? brow + TBN / 2 : brow + p.f;
+                        tma_load_2d_pair(st, &tmA, leader_addr(fb), x, (int32_t)ti.m0 + BM * rank);
+                        tma_load_2d_pair(st + C::A_BYTES, &tmB, leader_addr(fb), x, (int32_t)br);
+                    } else {
+                        tma_load_2d(st, &tmA, fb, x, (int32_t)ti.m0);
+                        tma_load_2d(st + C::A_BYTES, &tmB, fb, x, (int32_t)brow);
+                        if (!BWD) tma_load_2d(st + C::A_BYTES + C::B_BYTES / 2, &tmB, fb, x, (int32_t)(brow + p.f));
+                    }
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfr + 8 * stage);
+                issued |= 1u << stage;
+                last = (last & ~(1u << stage)) | (phase << stage);
                 if (++stage == STAGES) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
+        }
+        // no copy may still be landing when the CTA ends; a pair's copies are
+        // counted by its leader, and both CTAs end together
+        for (int s = 0; s < STAGES; ++s)
+            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, (last >> s) & 1u, 1000000000ull);
+        if (CT == 2 && *(volatile int *)s_abort) {  // one side may have given up before the other: let copies land
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 10000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2 || warp == 3) {
+        // ---------------------------------------------------- scale factors
+        // Block b (A, then the 128-row blocks of B), lane r, word j: the four
+        // scale bytes of row 32 j + r of the stage's 128-deep K range.  Words 0, 1
+        // are warp 2's, words 2, 3 warp 3's; both take part in every stage, as a
+        // wait tells one phase of a barrier from the next alone.  16 bytes of a row
+        // cover a group of four stages; two groups are read ahead of the one being
+        // written.
+        const int64_t pitch = p.k / 32;
+        const int groups4 = nks / 4;  // k is a multiple of 512
+        const int w0 = 2 * (warp - 2);
+        int t = tile0, q = 0, gc = 0;
+        Tile ti;
+        if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+        auto fetch = [&](uint4 (&v)[C::NR]) {
+            if (t >= total) return;
+            const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+#pragma unroll
+            for (int j = 0; j < C::NR; ++j) {
+                const int n = 128 * (j / 2 - 1) + 32 * (w0 + (j & 1));  // row of B within the tile (j >= 2)
+                int64_t row;
+                bool ok;
+                if (j < 2) {
+                    row = ti.m0 + BM * rank + 32 * (w0 + j) + lane;
+                    ok = row < p.m;
+                } else {
+                    row = brow + n + lane + (!BWD && n >= C::HB ? p.f - C::HB : 0);
+                    ok = n < TBN && row < p.b_rows;
+                }
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (ok) v[j] = __ldg(reinterpret_cast<const uint4 *>((j < 2 ? p.sa : p.sb) + row * pitch + 16 * q));
+            }
+            if (++q == groups4) {
+                q = 0;
+                t += tstep;
+                if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+            }
         };
-        int64_t left = 0;  // groups of four stages of this CTA
-        for (int u = blockIdx.x; u < total; u += gridDim.x) left += groups4;
-        uint4 v0[C::NR], v1[C::NR];
+        uint32_t stage = 0, phase = 0;
+        const int64_t tiles = tile0 < total ? (total - 1 - tile0) / tstep + 1 : 0;
+        int64_t left = tiles * groups4;
+        auto put = [&](const uint4 (&v)[C::NR]) {  // false: no more, or winding down
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const bool ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
+                    if (!ok) give_up();
+                    return false;
+                }
+                uint2 *sf = reinterpret_cast<uint2 *>(smem + C::SF_OFF + stage * C::SF_BYTES) + 2 * lane + w0 / 2;
+#pragma unroll
+                for (int b = 0; b < 1 + C::RB; ++b) sf[64 * b] = make_uint2(u4_word(v[2 * b], s), u4_word(v[2 * b + 1], s));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CT == 2) mbar_arrive_leader(bar_full + 8 * stage);
+                    else mbar_arrive(bar_full + 8 * stage);
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            return --left > 0;
+        };
+        uint4 v0[C::NR], v1[C::NR], v2[C::NR];
         fetch(v0);
-        while (ok && left > 0) {
-            fetch(v1);
-            put(v0);
-            if (--left <= 0 || !ok) break;
+        fetch(v1);
+        while (left > 0) {
+            fetch(v2);
+            if (!put(v0)) break;
             fetch(v0);
-            put(v1);
-            --left;
+            if (!put(v1)) break;
+            fetch(v1);
+            if (!put(v2)) break;
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        // The whole warp walks the loop, so that the operands of the tensor
+        // instructions are warp-uniform values; one elected lane issues.
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                if (!mbar_wait(bar_acc_empty + 8 * abuf, aphase ^ 1, p.wait_ns) || *(volatile int *)s_abort) {
-                    ok = false;
+            for (int t = tile0; t < total && ok; t += tstep) {
+                ok = warp_wait(bar_acc_empty + 8 * abuf, aphase ^ 1, p.wait_ns);
+                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
+                    if (!ok) give_up();
                     break;
                 }
-                tc_fence_after();
-                const uint32_t d = tmem + abuf * TBN;
+                const uint32_t d = tm + abuf * TBN;
                 for (int ks = 0; ks < nks; ++ks) {
-                    if (!mbar_wait(bar_full + 8 * stage, phase, p.wait_ns) ||
-                        !mbar_wait(bar_sfr + 8 * stage, phase, p.wait_ns)) {
-                        ok = false;
+                    ok = warp_wait(bar_full + 8 * stage, phase, p.wait_ns);
+                    if (!ok) {
+                        give_up();
                         break;
                     }
                     tc_fence_after();
-                    uint8_t *st = stages + stage * C::STAGE_BYTES;
-                    const uint32_t sf = smem_u32(st + C::A_BYTES + C::B_BYTES);
-                    const uint32_t sfa = tmem + C::SF_COL0 + stage * C::SF_COLS, sfb = sfa + 4;
+                    const uint32_t a = stages + stage * C::STAGE_BYTES, b = a + C::A_BYTES;
+                    const uint32_t sf = stages + C::SF_OFF + stage * C::SF_BYTES;
+                    const uint32_t sfa = tm + C::SF_COL0 + stage * C::SF_COLS, sfb = sfa + 4;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int b = 0; b < 1 + C::RB; ++b)
-                        tc_cp_32x128b_warpx4(sfa + 4 * b, smem_desc(sf + 512 * b, 0, 128, 0));
-                    const uint32_t a = smem_u32(st), b = smem_u32(st + C::A_BYTES);
+                        for (int i = 0; i < 1 + C::RB; ++i)
+                            tc_cp_ct<CT>(sfa + 4 * i, smem_desc(sf + 512 * i, 0, 128, 0));
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)  // 32 of K per MMA inside the 128-byte swizzled rows
-                        mma_mxfp8(d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2),
-                                  make_idesc<TBN>((uint32_t)s), sfa, sfb, (ks > 0 || s > 0) ? 1u : 0u);
-                    tc_commit(bar_empty + 8 * stage);
-                    if (ks == nks - 1) tc_commit(bar_acc_full + 8 * abuf);
+                        for (int s = 0; s < 4; ++s)  // 32 of K per MMA inside the 128-byte swizzled rows
+                            mma_mxfp8_ct<CT>(d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2),
+                                             make_idesc<TBN, CT>((uint32_t)s), sfa, sfb, (ks > 0 || s > 0) ? 1u : 0u);
+                        tc_commit_ct<CT>(bar_empty + 8 * stage);
+                        if (ks == nks - 1) tc_commit_ct<CT>(bar_acc_full + 8 * abuf);
+                    }
+                    __syncwarp();
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -450,85 +626,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                     aphase ^= 1;
                 }
             }
-            if (!ok && !*(volatile int *)s_abort) {
-                *(volatile int *)s_abort = 1;
-                latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-            }
-            tc_commit(bar_drain);  // every tcgen05 operation of this thread has completed
-            (void)mbar_wait(bar_drain, 0, 1000000000ull);
+            if (elect_one()) tc_commit_own<CT>(bar_drain);  // every tcgen05 operation of this warp has completed
+            __syncwarp();
+            (void)warp_wait(bar_drain, 0, 1000000000ull);
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
-        // Warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31 and every
-        // second 32-column chunk.  Its global accesses are TMA boxes of 32 rows x
-        // 32 columns (a row-per-thread access would touch 32 lines per
-        // instruction); only the rows of a 32-row slice that an expert's end cuts
-        // are stored one by one.
-        const int quad = warp & 3, half = (warp - 4) >> 2;
-        uint8_t *ybuf = wbuf + (warp - 4) * WARP_BYTES, *tb = ybuf + Y_BYTES;
-        const uint32_t yb = smem_u32(ybuf), tbs = smem_u32(tb), bar_y = bar_drain + 8 + 8 * (warp - 4);
-        uint32_t abuf = 0, aphase = 0, yphase = 0;
+        // Warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31 of CPW chunks of
+        // 32 columns in a row.
+        const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0);  // warp-uniform, and known to be
+        const int quad = wu & 3, c0 = ((wu - 4) >> 2) * C::CPW, c1 = min(c0 + C::CPW, C::NCH);
+        uint8_t *buf = smem + C::WARP_OFF + (wu - 4) * WARP_BYTES;
+        const uint32_t bufs = stages + C::WARP_OFF + (wu - 4) * WARP_BYTES;
+        const int pr = lane >> 2, pi = lane & 3;  // four lanes cover a row's 64 bytes of y
+        // The four warps that hold a chunk's 128 rows collect its column scales, so
+        // that a column's four bytes leave in one store: two buffers in turn, one
+        // barrier per tile.
+        const int group = (wu - 4) >> 2;
+        uint8_t *const sscale0 = smem + C::SCALE_OFF + group * 1024;
+        uint32_t collected = 0;
+        uint32_t rsc[2] = {0u, 0u};
+        uint32_t abuf = 0, aphase = 0;
         int gc = 0;
         bool ok = true;
-        // backward: gate and up of the next chunk are on their way while a chunk
-        // is worked on
-        int yt = blockIdx.x, yc = half, ygc = 0;
-        bool pending = false;
-        Tile yti;
-        if (BWD && yt < total) yti = get_tile<BWD, TBN>(yt, p, s_cum, ygc);
-        auto fetch_y = [&]() {
-            if (yt >= total) return;
-            if (yti.m0 + 32 * quad < yti.row_end && yti.h0 + 32 * yc < p.f) {
-                pending = true;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar_y, Y_BYTES);
-                    tma_load_2d(yb, &tmY, bar_y, yti.h0 + 32 * yc, (int32_t)yti.m0 + 32 * quad);
-                    tma_load_2d(yb + Y_BYTES / 2, &tmY, bar_y, (int32_t)p.f + yti.h0 + 32 * yc, (int32_t)yti.m0 + 32 * quad);
-                }
-            }
-            yc += 2;
-            if (yc >= C::NCH) {
-                yc = half;
-                yt += gridDim.x;
-                if (yt < total) yti = get_tile<BWD, TBN>(yt, p, s_cum, ygc);
+        // backward: copies gate and up of 32 rows x 32 columns into the buffer
+        auto fetch_y = [&](int64_t row0, int64_t col) {
+            const uint16_t *g = p.y + (row0 + pr) * 2 * p.f + col + 8 * pi;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t d = bufs + piece64(pr + 8 * i, pi);
+                cp_async16(d, g + 16 * i * p.f);
+                cp_async16(d + WARP_BYTES / 2, g + 16 * i * p.f + p.f);
             }
         };
-        // shared memory that TMA stores still read may be written again
-        auto stores_read = [&]() {
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-        };
-        auto publish = [&]() {  // written by all lanes -> visible to TMA
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        // one output's row codes into a staging box, and its scale bytes
-        auto put_row = [&](const float (&v)[32], int box, int64_t row, int64_t col, int64_t width, bool valid, bool full) {
-            uint4 q[2];
-            uint8_t sc;
-            row_block(v, q, sc);
-            if (full) {
-                *reinterpret_cast<uint4 *>(tb + 1024 * box + box32(lane, 0)) = q[0];
-                *reinterpret_cast<uint4 *>(tb + 1024 * box + box32(lane, 1)) = q[1];
-            } else if (valid) {
-                uint4 *o = reinterpret_cast<uint4 *>(p.out + row * width + col);
-                o[0] = q[0];
-                o[1] = q[1];
-            }
-            if (valid) p.out_sc[row * (width / 32) + col / 32] = sc;
-        };
-        // one output's column blocks
-        auto put_cols = [&](const float (&v)[32], int64_t row0, int64_t col) {
-            uint8_t sc;
-            col_blocks(v, tb, p.out_t + col * p.m + row0, p.m, sc, lane);
-            p.out_t_sc[(col + lane) * (p.m / 32) + row0 / 32] = sc;
-        };
-        if (BWD) fetch_y();
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile ti = get_tile<BWD, TBN>(t, p, s_cum, gc);
-            const int64_t row0 = ti.m0 + 32 * quad, row = row0 + lane;
-            const bool valid = row < ti.row_end, any = row0 < ti.row_end, full = row0 + 32 <= ti.row_end;
+        for (int t = tile0; t < total && ok; t += tstep) {
+            const Tile ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+            const int64_t row0 = ti.m0 + BM * rank + 32 * quad, row = row0 + lane;
+            const bool valid = row < ti.row_end, any = row0 < ti.row_end;
+            const int64_t tile_row = ti.m0 + BM * rank;
+            const bool words = p.words && tile_row % 128 == 0 && tile_row + BM <= ti.row_end;
+            uint8_t *const sscale = sscale0 + 512 * (collected & 1u);
+            if (BWD && any && ti.h0 + 32 * c0 < p.f) fetch_y(row0, ti.h0 + 32 * c0);  // lands while the MMAs run
             ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
@@ -536,22 +675,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
+                if (lane == 0) {
+                    if (CT == 2) mbar_arrive_leader(bar_acc_empty + 8 * abuf);
+                    else mbar_arrive(bar_acc_empty + 8 * abuf);
+                }
             };
-            if (half >= C::NCH) release();
+            if (c0 >= c1) release();
 #pragma unroll 1
-            for (int c = half; c < C::NCH; c += 2) {
+            for (int c = c0; c < c1; ++c) {
                 const int64_t col = ti.h0 + 32 * c;
-                const bool on = any && col < p.f;
+                const bool on = any && col < p.f;  // (with column blocks: all 32 rows are valid)
                 float v[32], u[32];
+                uint4 q[2];
+                uint8_t sc;
                 if constexpr (!BWD) {
                     tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_32x32b_x32(acc + C::HB + 32 * c, reinterpret_cast<uint32_t(&)[32]>(u));
                     tmem_ld_wait();
-                    if (c + 2 >= C::NCH) release();
+                    if (c == c1 - 1) release();
                     if (!on) continue;
-                    stores_read();
-                    if (p.y) {  // y in bf16 for the backward pass
+                    if (p.y) {  // y in bf16 for the backward pass, through shared memory: four lanes store a row's 64 bytes
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -563,90 +706,115 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
                                     w[i] = *reinterpret_cast<const uint32_t *>(&b2);
                                 }
-                                const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
-                                if (full) *reinterpret_cast<uint4 *>(ybuf + part * (Y_BYTES / 2) + box64(lane, j)) = q;
-                                else if (valid) *reinterpret_cast<uint4 *>(p.y + row * 2 * p.f + part * p.f + col + 8 * j) = q;
+                                *reinterpret_cast<uint4 *>(buf + part * (WARP_BYTES / 2) + piece64(lane, j)) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
                             }
+                        __syncwarp();
+                        uint16_t *o = p.y + (row0 + pr) * 2 * p.f + col + 8 * pi;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (row0 + pr + 8 * i < ti.row_end) {
+                                const uint8_t *b8 = buf + piece64(pr + 8 * i, pi);
+                                *reinterpret_cast<uint4 *>(o + 16 * i * p.f) = *reinterpret_cast<const uint4 *>(b8);
+                                *reinterpret_cast<uint4 *>(o + 16 * i * p.f + p.f) =
+                                    *reinterpret_cast<const uint4 *>(b8 + WARP_BYTES / 2);
+                            }
+                        __syncwarp();
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = silu_mul(v[j], u[j]);
-                    put_row(v, 0, row, col, p.f, valid, full);
-                    if (full) {
-                        publish();
-                        if (lane == 0) {
-                            tma_store_2d(&tmO, tbs, (int32_t)col, (int32_t)row0);
-                            if (p.y) {
-                                tma_store_2d(&tmY, yb, (int32_t)col, (int32_t)row0);
-                                tma_store_2d(&tmY, yb + Y_BYTES / 2, (int32_t)(p.f + col), (int32_t)row0);
-                            }
-                            bulk_commit_group();
-                        }
+                    row_block(v, q, sc);
+                    if (valid) {
+                        store32(p.out + row * p.f + col, q, p.wide);
+                        p.out_sc[row * (p.f / 32) + col / 32] = sc;
                     }
                     if (p.out_t) {
-                        stores_read();
-                        put_cols(v, row0, col);
+                        uint8_t st[1];
+                        col_blocks<1>({&v}, buf, {p.out_t + col * p.m + row0}, p.m, st, lane);
+                        if (words) sscale[128 * (c - c0) + 4 * lane + quad] = st[0];
+                        else p.out_t_sc[(col + lane) * (p.m / 32) + row0 / 32] = st[0];
                     }
                 } else {
-                    uint4 gw[4], uw[4];
-                    if (on) {
-                        ok = warp_wait(bar_y, yphase, p.wait_ns);
-                        if (!ok) break;
-                        pending = false;
-                        yphase ^= 1;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            gw[j] = *reinterpret_cast<const uint4 *>(ybuf + box64(lane, j));
-                            uw[j] = *reinterpret_cast<const uint4 *>(ybuf + Y_BYTES / 2 + box64(lane, j));
-                        }
-                        __syncwarp();
-                    }
-                    fetch_y();
                     tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
+                    cp_async_wait();
+                    __syncwarp();
                     tmem_ld_wait();
-                    if (c + 2 >= C::NCH) release();
+                    if (c == c1 - 1) release();
                     if (!on) continue;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const uint32_t a = u4_word(gw[j >> 3], (j >> 1) & 3), b = u4_word(uw[j >> 3], (j >> 1) & 3);
-                        const float gt = __uint_as_float((j & 1) ? (a & 0xFFFF0000u) : (a << 16));
-                        const float up = __uint_as_float((j & 1) ? (b & 0xFFFF0000u) : (b << 16));
-                        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gt)));
-                        const float ds = __fmul_rn(v[j], s);
-                        u[j] = __fmul_rn(ds, gt);
-                        v[j] = __fmul_rn(__fmul_rn(ds, up), fmaf(gt, __fsub_rn(1.0f, s), 1.0f));
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 gw = *reinterpret_cast<const uint4 *>(buf + piece64(lane, i));
+                        const uint4 uw = *reinterpret_cast<const uint4 *>(buf + WARP_BYTES / 2 + piece64(lane, i));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int j = 8 * i + k;
+                            const uint32_t a = u4_word(gw, k >> 1), b = u4_word(uw, k >> 1);
+                            const float gt = __uint_as_float((k & 1) ? (a & 0xFFFF0000u) : (a << 16));
+                            const float up = __uint_as_float((k & 1) ? (b & 0xFFFF0000u) : (b << 16));
+                            const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gt)));
+                            const float ds = __fmul_rn(v[j], s);
+                            u[j] = __fmul_rn(ds, gt);
+                            v[j] = __fmul_rn(__fmul_rn(ds, up), fmaf(gt, __fsub_rn(1.0f, s), 1.0f));
+                        }
                     }
-                    stores_read();
-                    put_row(v, 0, row, col, 2 * p.f, true, true);
-                    put_row(u, 1, row, p.f + col, 2 * p.f, true, true);
-                    publish();
-                    if (lane == 0) {
-                        tma_store_2d(&tmO, tbs, (int32_t)col, (int32_t)row0);
-                        tma_store_2d(&tmO, tbs + 1024, (int32_t)(p.f + col), (int32_t)row0);
-                        bulk_commit_group();
+                    const int64_t f2 = 2 * p.f;
+                    uint8_t *os = p.out_sc + row * (f2 / 32) + col / 32;
+                    row_block(v, q, sc);
+                    store32(p.out + row * f2 + col, q, p.wide);
+                    rsc[0] = (rsc[0] >> 8) | ((uint32_t)sc << 8);
+                    row_block(u, q, sc);
+                    store32(p.out + row * f2 + p.f + col, q, p.wide);
+                    rsc[1] = (rsc[1] >> 8) | ((uint32_t)sc << 8);
+                    if (!p.pairs) {
+                        os[0] = (uint8_t)(rsc[0] >> 8);
+                        os[p.f / 32] = (uint8_t)(rsc[1] >> 8);
+                    } else if (c > c0) {  // (c0 and f / 32 are even)
+                        *reinterpret_cast<uint16_t *>(os - 1) = (uint16_t)rsc[0];
+                        *reinterpret_cast<uint16_t *>(os + p.f / 32 - 1) = (uint16_t)rsc[1];
                     }
-                    stores_read();
-                    put_cols(v, row0, col);
-                    put_cols(u, row0, p.f + col);
+                    __syncwarp();  // every lane has read its gate and up values: they went into the codes above
+                    uint8_t st[2];
+                    uint8_t *qt = p.out_t + col * p.m + row0;
+                    col_blocks<2>({&v, &u}, buf, {qt, qt + p.f * p.m}, p.m, st, lane);
+                    if (words) {
+                        sscale[256 * (c - c0) + 4 * lane + quad] = st[0];
+                        sscale[256 * (c - c0) + 128 + 4 * lane + quad] = st[1];
+                    } else {
+                        uint8_t *ot = p.out_t_sc + (col + lane) * (p.m / 32) + row0 / 32;
+                        ot[0] = st[0];
+                        ot[p.f * (p.m / 32)] = st[1];
+                    }
+                    if (c + 1 < c1 && col + 32 < p.f) fetch_y(row0, col + 32);  // the blocks above have been read
                 }
+            }
+            if (words && c0 < C::NCH) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_group + 8 * group);
+                ok = warp_wait(bar_group + 8 * group, collected & 1u, p.wait_ns);
+                if (!ok) break;
+                ++collected;
+                constexpr int NOUT = BWD ? 2 : 1;  // slot: chunk and (backward) gate or up
+                const int64_t col = ti.h0 + 32 * (c0 + quad / NOUT) + lane;
+                if (quad < C::CPW * NOUT && col < p.f)
+                    *reinterpret_cast<uint32_t *>(p.out_t_sc + (col + (quad % NOUT) * p.f) * (p.m / 32) + tile_row / 32) =
+                        *reinterpret_cast<const uint32_t *>(sscale + 128 * quad + 4 * lane);
             }
             if (++abuf == C::ACC) {
                 abuf = 0;
                 aphase ^= 1;
             }
         }
-        if (!ok && lane == 0) {
-            *(volatile int *)s_abort = 1;
-            latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-        }
-        if (BWD && pending) (void)warp_wait(bar_y, yphase, 1000000000ull);  // a copy may still be landing
-        if (lane == 0) bulk_wait_group_all();
+        if (!ok) give_up();
+        if (BWD) cp_async_wait();
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
+    if (CT == 2) cluster_sync();  // neither CTA's memory is still in use by the other
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+    if (warp == 0) tmem_dealloc_ct<CT>(tmem, TMEM_COLS);
+    if (CT == 2) cluster_sync();
 }
 
 // ====================================================================== host
@@ -669,44 +837,49 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// A row-major tensor [rows, width] of bytes or bf16 values; out-of-range elements of
-// a loaded box read as zeros, of a stored box are not written.
-bool make_map(CUtensorMap *m, const void *base, bool bf16, uint64_t width, uint64_t rows, uint32_t box_w,
-              uint32_t box_rows, CUtensorMapSwizzle swizzle)
+// E4M3 bytes [rows, k] in boxes of 128 bytes x box_rows, 128-byte swizzle; rows
+// past the end read as zeros.
+bool make_map(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint32_t box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {width, rows}, strides[1] = {width * (bf16 ? 2 : 1)};
-    cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
-              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t dims[2] = {k, rows}, strides[1] = {k};
+    cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline bool aligned16(const void *p) { return aligned(p, 16); }
 
-template <bool BWD, int TBN>
+template <bool BWD, int TBN, int CT>
 pmn_status launch(const uint8_t *a, const uint8_t *b, const Args &args, cudaStream_t s)
 {
-    using C = Cfg<BWD, TBN>;
-    const uint64_t m = (uint64_t)args.m, f = (uint64_t)args.f, k = (uint64_t)args.k, w = BWD ? 2 * f : f;
-    const auto S32 = CU_TENSOR_MAP_SWIZZLE_32B, S64 = CU_TENSOR_MAP_SWIZZLE_64B, S128 = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap ma, mb, mo, my;
-    if (!make_map(&ma, a, false, k, m, 128, BM, S128) ||
-        !make_map(&mb, b, false, k, (uint64_t)args.b_rows, 128, BWD ? TBN : TBN / 2, S128) ||
-        !make_map(&mo, args.out, false, w, m, 32, 32, S32))
+    using C = Cfg<BWD, TBN, CT>;
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, a, (uint64_t)args.k, (uint64_t)args.m, BM) ||
+        !make_map(&mb, b, (uint64_t)args.k, (uint64_t)args.b_rows, BWD ? TBN / CT : TBN / 2))
         return PMN_ERR_CUDA;
-    my = mo;  // without y: not used
-    if (args.y && !make_map(&my, args.y, true, 2 * f, m, 32, 32, S64)) return PMN_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < CT)
         return PMN_ERR_CUDA;
-    auto kern = gated_kernel<BWD, TBN>;
+    auto kern = gated_kernel<BWD, TBN, CT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return PMN_ERR_CUDA;
-    kern<<<(unsigned)sms, THREADS, C::SMEM_BYTES, s>>>(ma, mb, mo, my, args);
-    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / CT * CT));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CT;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CT > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 // What both directions ask of their sizes and operands.
@@ -756,8 +929,10 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
     if ((out_t != nullptr) != (out_t_scales != nullptr) || (out_t && total_rows % 32 != 0)) return PMN_ERR_INVALID_ARG;
     if (!out || !out_scales || !aligned16(out) || !aligned16(out_t) || !aligned16(y_out)) return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * 2 * f,
-                    out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), pmn_wait_limit_ns()};
-    return launch<false, 192>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+                    out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), aligned(out, 32),
+                    aligned(out_scales, 2), out_t && total_rows % 128 == 0 && aligned(out_t_scales, 4),
+                    pmn_wait_limit_ns()};
+    return launch<false, 192, 2>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
@@ -772,7 +947,7 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const 
     if (!y || !out || !out_scales || !out_t || !out_t_scales || !aligned16(y) || !aligned16(out) || !aligned16(out_t))
         return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * f,
-                    out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)),
-                    pmn_wait_limit_ns()};
-    return launch<true, 192>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+                    out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)), aligned(out, 32),
+                    aligned(out_scales, 2), total_rows % 128 == 0 && aligned(out_t_scales, 4), pmn_wait_limit_ns()};
+    return launch<true, 192, 2>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
 }
