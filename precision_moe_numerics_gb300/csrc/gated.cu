@@ -169,13 +169,14 @@ struct Cfg {
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
-    static constexpr int NR = 2 * (1 + RB);         // scale rows per lane of a scale-factor warp
+    static constexpr int NR = 2 * (1 + RB);         // 32-row boxes of scales per scale-factor warp
+    static constexpr int RAW_SLOTS = 3, RAW_BYTES = NR * 512;  // groups of four stages in flight, per warp
     static constexpr int SF_OFF = STAGES * STAGE_BYTES, WARP_OFF = SF_OFF + STAGES * SF_BYTES,
-                         BAR_OFF = WARP_OFF + EW * WARP_BYTES, SCALE_OFF = BAR_OFF + 256,
-                         CUM_OFF = SCALE_OFF + 3 * 2 * 512;
+                         RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + 2 * RAW_SLOTS * RAW_BYTES,
+                         SCALE_OFF = BAR_OFF + 256, CUM_OFF = SCALE_OFF + 3 * 2 * 512;
     static constexpr int SMEM_BYTES = 1024 + CUM_OFF + (MAX_GROUPS + 1) * 4;
     static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
-    static_assert(8 * (2 * STAGES + 8) + 16 <= 256, "barrier space");
+    static_assert(8 * (2 * STAGES + 8 + 2 * RAW_SLOTS) + 16 <= 256, "barrier space");
     static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -184,7 +185,6 @@ struct Args {
     const int32_t *offsets;
     int groups;
     int64_t m, f, k;         // routed rows, columns of h, contraction length
-    const uint8_t *sa, *sb;  // scales, k / 32 bytes per row
     int64_t b_rows;          // rows of B of all experts
     uint8_t *out, *out_sc, *out_t, *out_t_sc;
     uint16_t *y;             // forward: written (or NULL); backward: read
@@ -369,7 +369,7 @@ __device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], ui
 template <bool BWD, int TBN, int CT>
 __global__ void __launch_bounds__(THREADS, 1)
     gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const Args p)
+                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p)
 {
     using C = Cfg<BWD, TBN, CT>;
     constexpr int STAGES = C::STAGES;
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t stages = smem_u32(smem);
     const uint32_t bar_full = stages + C::BAR_OFF, bar_empty = bar_full + 8 * STAGES;
     const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16;
-    const uint32_t bar_drain = bar_acc_empty + 16, bar_group = bar_drain + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * (2 * STAGES + 8));
+    const uint32_t bar_drain = bar_acc_empty + 16, bar_group = bar_drain + 8, bar_raw = bar_group + 24;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * (2 * STAGES + 8 + 2 * C::RAW_SLOTS));
     int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
     int *s_total = s_abort + 1;
     int *s_cum = reinterpret_cast<int *>(smem + C::CUM_OFF);
@@ -398,10 +398,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mbar_init(bar_drain, 1);
         for (int g = 0; g < 3; ++g) mbar_init(bar_group + 8 * g, 4);
+        for (int g = 0; g < 2 * C::RAW_SLOTS; ++g) mbar_init(bar_raw + 8 * g, 1);
         *s_abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
     }
     if (warp == 0) {
         __syncwarp();
@@ -509,48 +512,75 @@ __global__ void __launch_bounds__(THREADS, 1)
         // scale bytes of row 32 j + r of the stage's 128-deep K range.  Words 0, 1
         // are warp 2's, words 2, 3 warp 3's; both take part in every stage, as a
         // wait tells one phase of a barrier from the next alone.  16 bytes of a row
-        // cover a group of four stages; two groups are read ahead of the one being
-        // written.
-        const int64_t pitch = p.k / 32;
+        // cover a group of four stages and come by TMA, RAW_SLOTS groups ahead, in
+        // boxes of 32 rows.  (Plain loads of 16 bytes from 32 rows each queue behind
+        // the epilogue's stores and held the MMAs up: a stage then took 850 clocks
+        // beside the epilogue, 600 without.)
         const int groups4 = nks / 4;  // k is a multiple of 512
-        const int w0 = 2 * (warp - 2);
+        const int wr = __shfl_sync(0xFFFFFFFFu, warp, 0) - 2, w0 = 2 * wr;
+        const uint8_t *raw = smem + C::RAW_OFF + wr * C::RAW_SLOTS * C::RAW_BYTES;
+        const uint32_t raws = stages + C::RAW_OFF + wr * C::RAW_SLOTS * C::RAW_BYTES;
+        const uint32_t bar = bar_raw + 8 * C::RAW_SLOTS * wr;
+        constexpr auto in_tile = [](int j, int w) { return j < 2 || 128 * (j / 2 - 1) + 32 * (w + (j & 1)) < TBN; };
+        int boxes = 0;
+#pragma unroll
+        for (int j = 0; j < C::NR; ++j) boxes += in_tile(j, w0);
+        const int64_t tiles = tile0 < total ? (total - 1 - tile0) / tstep + 1 : 0, groups = tiles * groups4;
+        int64_t asked = 0;  // groups whose scales have been asked for
         int t = tile0, q = 0, gc = 0;
         Tile ti;
         if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
-        auto fetch = [&](uint4 (&v)[C::NR]) {
-            if (t >= total) return;
+        auto fetch = [&]() {
+            if (asked >= groups) return;
+            const int slot = (int)(asked % C::RAW_SLOTS);
+            const int32_t arow = (int32_t)ti.m0 + BM * rank;
             const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar + 8 * slot, 512 * boxes);
 #pragma unroll
-            for (int j = 0; j < C::NR; ++j) {
-                const int n = 128 * (j / 2 - 1) + 32 * (w0 + (j & 1));  // row of B within the tile (j >= 2)
-                int64_t row;
-                bool ok;
-                if (j < 2) {
-                    row = ti.m0 + BM * rank + 32 * (w0 + j) + lane;
-                    ok = row < p.m;
-                } else {
-                    row = brow + n + lane + (!BWD && n >= C::HB ? p.f - C::HB : 0);
-                    ok = n < TBN && row < p.b_rows;
+                for (int j = 0; j < C::NR; ++j) {
+                    const uint32_t d = raws + slot * C::RAW_BYTES + 512 * j;
+                    const int n = 128 * (j / 2 - 1) + 32 * (w0 + (j & 1));  // row of B within the tile (j >= 2)
+                    if (j < 2) tma_load_2d(d, &tmSA, bar + 8 * slot, 16 * q, arow + 32 * (w0 + j));
+                    else if (in_tile(j, w0))
+                        tma_load_2d(d, &tmSB, bar + 8 * slot, 16 * q, (int32_t)(brow + n + (!BWD && n >= C::HB ? p.f - C::HB : 0)));
                 }
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (ok) v[j] = __ldg(reinterpret_cast<const uint4 *>((j < 2 ? p.sa : p.sb) + row * pitch + 16 * q));
             }
+            __syncwarp();
+            ++asked;
             if (++q == groups4) {
                 q = 0;
                 t += tstep;
                 if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
             }
         };
-        uint32_t stage = 0, phase = 0;
-        const int64_t tiles = tile0 < total ? (total - 1 - tile0) / tstep + 1 : 0;
-        int64_t left = tiles * groups4;
-        auto put = [&](const uint4 (&v)[C::NR]) {  // false: no more, or winding down
+        for (int i = 0; i < C::RAW_SLOTS; ++i) fetch();
+        uint32_t stage = 0, phase = 0, rslot = 0, rphase = 0;
+        bool ok = true;
+        int64_t g = 0;
+        for (; g < groups && ok; ++g) {
+            ok = warp_wait(bar + 8 * rslot, rphase, p.wait_ns);
+            if (!ok) {
+                give_up();
+                break;
+            }
+            uint4 v[C::NR];
+#pragma unroll
+            for (int j = 0; j < C::NR; ++j) {
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (in_tile(j, w0)) v[j] = *reinterpret_cast<const uint4 *>(raw + rslot * C::RAW_BYTES + 512 * j + 16 * lane);
+            }
+            if (++rslot == C::RAW_SLOTS) {
+                rslot = 0;
+                rphase ^= 1;
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const bool ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+                ok = ok && warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
                 if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
                     if (!ok) give_up();
-                    return false;
+                    ok = false;
+                    break;
                 }
                 uint2 *sf = reinterpret_cast<uint2 *>(smem + C::SF_OFF + stage * C::SF_BYTES) + 2 * lane + w0 / 2;
 #pragma unroll
@@ -566,19 +596,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     phase ^= 1;
                 }
             }
-            return --left > 0;
-        };
-        uint4 v0[C::NR], v1[C::NR], v2[C::NR];
-        fetch(v0);
-        fetch(v1);
-        while (left > 0) {
-            fetch(v2);
-            if (!put(v0)) break;
-            fetch(v0);
-            if (!put(v1)) break;
-            fetch(v1);
-            if (!put(v2)) break;
+            // the slot may be refilled: what was read from it has been written on
+            if (ok) fetch();
         }
+        // copies that nobody will wait for may still be landing
+        for (; !ok && g < asked; ++g) (void)warp_wait(bar + 8 * (uint32_t)(g % C::RAW_SLOTS), (uint32_t)(g / C::RAW_SLOTS) & 1u, 1000000000ull);
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
         // The whole warp walks the loop, so that the operands of the tensor
@@ -837,29 +859,31 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// E4M3 bytes [rows, k] in boxes of 128 bytes x box_rows, 128-byte swizzle; rows
-// past the end read as zeros.
-bool make_map(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint32_t box_rows)
+// Bytes [rows, width] in boxes of box_w (128: with the 128-byte swizzle) x
+// box_rows; rows past the end read as zeros.
+bool make_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, uint32_t box_w, uint32_t box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {k, rows}, strides[1] = {k};
-    cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+    cuuint64_t dims[2] = {width, rows}, strides[1] = {width};
+    cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool aligned16(const void *p) { return aligned(p, 16); }
 
 template <bool BWD, int TBN, int CT>
-pmn_status launch(const uint8_t *a, const uint8_t *b, const Args &args, cudaStream_t s)
+pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
+                  const Args &args, cudaStream_t s)
 {
     using C = Cfg<BWD, TBN, CT>;
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, a, (uint64_t)args.k, (uint64_t)args.m, BM) ||
-        !make_map(&mb, b, (uint64_t)args.k, (uint64_t)args.b_rows, BWD ? TBN / CT : TBN / 2))
+    const uint64_t k = (uint64_t)args.k, m = (uint64_t)args.m, n = (uint64_t)args.b_rows;
+    CUtensorMap ma, mb, msa, msb;
+    if (!make_map(&ma, a, k, m, 128, BM) || !make_map(&mb, b, k, n, 128, BWD ? TBN / CT : TBN / 2) ||
+        !make_map(&msa, a_scales, k / 32, m, 16, 32) || !make_map(&msb, b_scales, k / 32, n, 16, 32))
         return PMN_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -879,7 +903,7 @@ pmn_status launch(const uint8_t *a, const uint8_t *b, const Args &args, cudaStre
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = CT > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, msa, msb, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 // What both directions ask of their sizes and operands.
@@ -928,11 +952,11 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
     if (st != PMN_OK || total_rows == 0) return st;
     if ((out_t != nullptr) != (out_t_scales != nullptr) || (out_t && total_rows % 32 != 0)) return PMN_ERR_INVALID_ARG;
     if (!out || !out_scales || !aligned16(out) || !aligned16(out_t) || !aligned16(y_out)) return PMN_ERR_INVALID_ARG;
-    const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * 2 * f,
+    const Args args{offsets, num_experts, total_rows, f, k, (int64_t)num_experts * 2 * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), aligned(out, 32),
                     aligned(out_scales, 2), out_t && total_rows % 128 == 0 && aligned(out_t_scales, 4),
                     pmn_wait_limit_ns()};
-    return launch<false, 192, 2>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+    return launch<false, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
@@ -946,8 +970,8 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const 
     if (total_rows % 32 != 0) return PMN_ERR_INVALID_ARG;
     if (!y || !out || !out_scales || !out_t || !out_t_scales || !aligned16(y) || !aligned16(out) || !aligned16(out_t))
         return PMN_ERR_INVALID_ARG;
-    const Args args{offsets, num_experts, total_rows, f, k, a_scales, b_scales, (int64_t)num_experts * f,
+    const Args args{offsets, num_experts, total_rows, f, k, (int64_t)num_experts * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)), aligned(out, 32),
                     aligned(out_scales, 2), total_rows % 128 == 0 && aligned(out_t_scales, 4), pmn_wait_limit_ns()};
-    return launch<true, 192, 2>(a, b, args, reinterpret_cast<cudaStream_t>(stream));
+    return launch<true, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
 }
