@@ -556,7 +556,7 @@ typedef struct pmn_adamw_tensor {
  * A NaN or infinite gradient makes its own element's param and m NaN or infinite.
  *  tensors  HOST array [num_tensors], copied by the call.
  *  param_kind, grad_kind  PMN_OUT_BF16 or PMN_OUT_F32;  state_kind PMN_STATE_*.
- *  beta1, beta2 in [0, 1);  eps > 0;  step >= 1 (its low 32 bits are used as the
+ *  beta1, beta2 in [0, 1);  eps >= 2^-126 (normal in float32);  step >= 1 (its low 32 bits are used as the
  *           counter word).
  *  grad_scale  NULL (1), or a DEVICE float32: a clipping factor or the inverse of
  *           a loss scale, read by the kernel.

@@ -40,35 +40,65 @@ struct Hyper {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Eight consecutive values at element i of a bf16 or float32 array; `left`
-// counts the elements from i to the array's end (8 or more: vector access).
-template <bool F32>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int64_t left, float (&v)[8])
-{
-    if (left >= 8) {
-        if (F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-            const float4 a = __ldcs(q), b = __ldcs(q + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// Eight consecutive elements of an array of B-byte elements as they lie in memory.
+// Loads and decoding are apart, so that all of a thread's loads are in flight
+// together; `left` counts the elements from i to the array's end.
+template <int B>
+struct Raw {
+    uint32_t w[2 * B];
+    __device__ __forceinline__ void load(const void *p, int64_t i)
+    {
+        const uint8_t *b = static_cast<const uint8_t *>(p) + i * B;
+        if (B == 1) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(b));
+            w[0] = q.x;
+            w[1] = q.y;
         } else {
-            const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(u4_word(q, k) << 16);
-                v[2 * k + 1] = __uint_as_float(u4_word(q, k) & 0xFFFF0000u);
+            for (int j = 0; j < B / 2; ++j) {
+                const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(b) + j);
+                w[4 * j] = q.x;
+                w[4 * j + 1] = q.y;
+                w[4 * j + 2] = q.z;
+                w[4 * j + 3] = q.w;
             }
         }
-    } else {
+    }
+    __device__ __forceinline__ void load_some(const void *p, int64_t i, int64_t left)
+    {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[k] = 0.0f;
-            if (k < left)
-                v[k] = F32 ? static_cast<const float *>(p)[i + k]
-                           : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i + k] << 16);
+        for (int j = 0; j < 2 * B; ++j) w[j] = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) {
+                if (B == 4) w[k] = static_cast<const uint32_t *>(p)[i + k];
+                else if (B == 2) w[k >> 1] |= (uint32_t) static_cast<const uint16_t *>(p)[i + k] << (16 * (k & 1));
+                else w[k >> 2] |= (uint32_t) static_cast<const uint8_t *>(p)[i + k] << (8 * (k & 3));
+            }
+    }
+    // float32, bf16, or E4M3 codes times `scale`
+    __device__ __forceinline__ void values(float (&v)[8], float scale = 1.0f) const
+    {
+        if constexpr (B == 4) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+        } else if constexpr (B == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t h2;  // two codes as f16x2 (exact)
+                const uint16_t b16 = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b16));
+                mul2(h2_lo_to_f32(h2), h2_hi_to_f32(h2), scale, scale, v[2 * k], v[2 * k + 1]);
+            }
         }
     }
-}
+};
 
 __device__ __forceinline__ void store8_f32(void *p, int64_t i, int64_t left, const float (&v)[8])
 {
@@ -95,34 +125,12 @@ __device__ __forceinline__ void store8_b16(void *p, int64_t i, int64_t left, con
     }
 }
 
-// Eight E4M3 codes (a word pair) times 2^(b - 127).
-__device__ __forceinline__ void load8_mx(const uint8_t *q, const uint8_t *sc, int64_t i, int64_t left, float (&v)[8])
-{
-    uint32_t w[2] = {0u, 0u};
-    float s = 0.0f;
-    if (left > 0) s = e8m0_to_f32(sc[i / 32]);
-    if (left >= 8) {
-        const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(q + i));
-        w[0] = u.x;
-        w[1] = u.y;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < left) w[k >> 2] |= (uint32_t)q[i + k] << (8 * (k & 3));
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t h2;  // two codes as f16x2 (exact)
-        const uint16_t b16 = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b16));
-        v[2 * k] = __fmul_rn(h2_lo_to_f32(h2), s);
-        v[2 * k + 1] = __fmul_rn(h2_hi_to_f32(h2), s);
-    }
-}
-
 // MXFP8 of the thread's eight values, its block being the 32 values of four
 // adjacent lanes, rounded stochastically with the words r0 (values 0..3) and r1
 // (4..7).  keep: a nonzero value takes the smallest code instead of 0.
+// (A value below the smallest code 2^-9 of its block becomes that code exactly,
+// whose rounding is certain; larger ones never round to 0.  Blocks that have such
+// a value are rare, so one comparison of the thread's minimum guards the work.)
 template <bool KEEP>
 __device__ __forceinline__ void store8_mx(uint8_t *q, uint8_t *sc, int64_t i, int64_t left, const float (&v)[8],
                                           uint32_t r0, uint32_t r1)
@@ -136,13 +144,18 @@ __device__ __forceinline__ void store8_mx(uint8_t *q, uint8_t *sc, int64_t i, in
     const float s = exp2_neg(e);
     float y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(v[k], s);
-    uint32_t w[2] = {cvt_e4m3x4_rs(y[0], y[1], y[2], y[3], r0), cvt_e4m3x4_rs(y[4], y[5], y[6], y[7], r1)};
+    for (int k = 0; k < 8; k += 2) mul2(v[k], v[k + 1], s, s, y[k], y[k + 1]);
     if (KEEP) {
+        float least = y[0];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (v[k] > 0.0f && ((w[k >> 2] >> (8 * (k & 3))) & 0xFFu) == 0u) w[k >> 2] |= 1u << (8 * (k & 3));
+        for (int k = 1; k < 8; ++k) least = fminf(least, y[k]);
+        if (least < 0.001953125f) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (y[k] > 0.0f) y[k] = fmaxf(y[k], 0.001953125f);
+        }
     }
+    const uint32_t w[2] = {cvt_e4m3x4_rs(y[0], y[1], y[2], y[3], r0), cvt_e4m3x4_rs(y[4], y[5], y[6], y[7], r1)};
     if (left >= 8) {
         *reinterpret_cast<uint2 *>(q + i) = make_uint2(w[0], w[1]);
     } else {
@@ -182,6 +195,51 @@ __device__ __forceinline__ uint32_t bits16(uint32_t w, int k)
     return __brev(w) & 0xFFFFu;
 }
 
+// a * b + c on two lanes, each rounded once.
+__device__ __forceinline__ void fma2v(float a0, float a1, float b0, float b1, float c0, float c1, float &r0, float &r1)
+{
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x)
+{
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Square root and quotient from the hardware's approximations and one Newton step
+// on the residual (x - r^2, n - q d are exact up to one rounding of a small
+// number): within one place of the correctly rounded values.  Subnormal arguments
+// and 0, whose reciprocal root the hardware takes as infinite, go the long way;
+// the root of infinity or NaN is itself.
+__device__ __forceinline__ float root(float x)
+{
+    const float y = rsqrt_approx(x), r = __fmul_rn(x, y);
+    const float f = fmaf(fmaf(-r, r, x), __fmul_rn(0.5f, y), r);
+    if (x < 1.17549435e-38f) return __fsqrt_rn(x);
+    return x > 3.4e38f ? x : f;
+}
+
+// d is positive and normal (at least eps or a root); where its reciprocal or the
+// product leaves the normal range the quotient is within a place of 0 or infinite.
+__device__ __forceinline__ float quotient(float n, float d)
+{
+    const float y = rcp_approx(d), q = __fmul_rn(n, y);
+    const float f = fmaf(fmaf(-q, d, n), y, q);
+    return fabsf(q) < 3.4e38f && fabsf(d) < 3.4e38f ? f : q;
+}
+
 // One AdamW step.  Memory-bound: each value is read and written once, 16 elements
 // a thread in two groups of 8 so that both groups' loads are in flight together.
 //   g = grad_scale grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
@@ -204,34 +262,65 @@ __global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Tabl
     const int64_t i0 = (int64_t)((int)blockIdx.x - tab.first[lo]) * CHUNK + (threadIdx.x >> 5) * WARP_ELEMS +
                        8 * (threadIdx.x & 31);
     const uint32_t tag = 4u * (tab.base + (uint32_t)lo);
-    float p[2][8], g[2][8], m[2][8], v[2][8];
+    Raw<PF32 ? 4 : 2> rp[2];
+    Raw<GF32 ? 4 : 2> rg[2];
+    Raw<MX ? 1 : 4> rm[2], rv[2];
+    uint32_t ms[2] = {0u, 0u}, vs[2] = {0u, 0u};
+    if (i0 - 8 * (threadIdx.x & 31) + WARP_ELEMS <= n) {  // the whole warp's elements lie inside
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int64_t i = i0 + 256 * u, left = n - i;
-        load8<PF32>(t.param, i, left, p[u]);
-        load8<GF32>(t.grad, i, left, g[u]);
-        if (MX) {
-            load8_mx(static_cast<const uint8_t *>(t.m), t.m_scales, i, left, m[u]);
-            load8_mx(static_cast<const uint8_t *>(t.v), t.v_scales, i, left, v[u]);
-        } else {
-            load8<true>(t.m, i, left, m[u]);
-            load8<true>(t.v, i, left, v[u]);
+        for (int u = 0; u < 2; ++u) {
+            const int64_t i = i0 + 256 * u;
+            rp[u].load(t.param, i);
+            rg[u].load(t.grad, i);
+            rm[u].load(t.m, i);
+            rv[u].load(t.v, i);
+            if (MX) {
+                ms[u] = t.m_scales[i / 32];
+                vs[u] = t.v_scales[i / 32];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t i = i0 + 256 * u, left = n - i;
+            rp[u].load_some(t.param, i, left);
+            rg[u].load_some(t.grad, i, left);
+            rm[u].load_some(t.m, i, left);
+            rv[u].load_some(t.v, i, left);
+            if (MX && left > 0) {
+                ms[u] = t.m_scales[i / 32];
+                vs[u] = t.v_scales[i / 32];
+            }
         }
     }
     const float gs = h.grad_scale ? __ldg(h.grad_scale) : 1.0f;
+    float p[2][8], g[2][8], m[2][8], v[2][8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+        rp[u].values(p[u]);
+        rg[u].values(g[u]);
+        rm[u].values(m[u], MX ? e8m0_to_f32(ms[u]) : 1.0f);
+        rv[u].values(v[u], MX ? e8m0_to_f32(vs[u]) : 1.0f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float gr = __fmul_rn(g[u][k], gs);
-            if (MX) v[u][k] = __fmul_rn(v[u][k], v[u][k]);
-            m[u][k] = fmaf(h.beta1, m[u][k], __fmul_rn(h.omb1, gr));
-            v[u][k] = fmaf(h.beta2, v[u][k], __fmul_rn(h.omb2, __fmul_rn(gr, gr)));
-            const float root = __fsqrt_rn(v[u][k]);
-            const float d = __fdiv_rn(m[u][k], fmaf(root, h.rbc2, h.eps));
-            p[u][k] = fmaf(-h.lr1, d, __fmul_rn(p[u][k], h.decay));
-            if (MX) v[u][k] = root;
+        for (int k = 0; k < 8; k += 2) {  // two elements at a time
+            float g0, g1, t0, t1;
+            mul2(g[u][k], g[u][k + 1], gs, gs, g0, g1);
+            mul2(g0, g1, h.omb1, h.omb1, t0, t1);
+            fma2v(h.beta1, h.beta1, m[u][k], m[u][k + 1], t0, t1, m[u][k], m[u][k + 1]);
+            if (MX) mul2(v[u][k], v[u][k + 1], v[u][k], v[u][k + 1], v[u][k], v[u][k + 1]);
+            mul2(g0, g1, g0, g1, t0, t1);
+            mul2(t0, t1, h.omb2, h.omb2, t0, t1);
+            fma2v(h.beta2, h.beta2, v[u][k], v[u][k + 1], t0, t1, v[u][k], v[u][k + 1]);
+            const float r0 = root(v[u][k]), r1 = root(v[u][k + 1]);
+            float d0, d1;
+            fma2v(r0, r1, h.rbc2, h.rbc2, h.eps, h.eps, d0, d1);
+            d0 = quotient(m[u][k], d0);
+            d1 = quotient(m[u][k + 1], d1);
+            mul2(p[u][k], p[u][k + 1], h.decay, h.decay, t0, t1);
+            fma2v(-h.lr1, -h.lr1, d0, d1, t0, t1, p[u][k], p[u][k + 1]);
+            if (MX) v[u][k] = r0, v[u][k + 1] = r1;
         }
+    }
     uint32_t r[2][2];
     if (!PF32) pair_words(h.seed, tag, h.step, i0, r);
 #pragma unroll
@@ -326,7 +415,7 @@ extern "C" pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_te
         return PMN_ERR_INVALID_ARG;
     // NaN fails every comparison
     if (!(std::isfinite(lr) && beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps > 0.0 &&
-          std::isfinite(eps) && std::isfinite(weight_decay)) || step < 1 || ((uintptr_t)grad_scale & 3u))
+          std::isfinite(weight_decay)) || !std::isfinite((float)eps) || (float)eps < 1.17549435e-38f || step < 1 || ((uintptr_t)grad_scale & 3u))
         return PMN_ERR_INVALID_ARG;
     for (int i = 0; i < num_tensors; ++i) {
         const pmn_adamw_tensor &t = tensors[i];
