@@ -218,26 +218,28 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// Square root and quotient from the hardware's approximations and one Newton step
-// on the residual (x - r^2, n - q d are exact up to one rounding of a small
-// number): within one place of the correctly rounded values.  Subnormal arguments
-// and 0, whose reciprocal root the hardware takes as infinite, go the long way;
-// the root of infinity or NaN is itself.
-__device__ __forceinline__ float root(float x)
+// Square roots and quotients of two pairs from the hardware's approximations and one
+// Newton step on the residual (x - r^2, n - q d are exact up to one rounding of a
+// small number): within one place of the correctly rounded values.  x is 0 or a
+// normal number (the root of 0 comes out as 0), d a normal one.
+__device__ __forceinline__ void root2(float x0, float x1, float &r0, float &r1)
 {
-    const float y = rsqrt_approx(x), r = __fmul_rn(x, y);
-    const float f = fmaf(fmaf(-r, r, x), __fmul_rn(0.5f, y), r);
-    if (x < 1.17549435e-38f) return __fsqrt_rn(x);
-    return x > 3.4e38f ? x : f;
+    const float least = 1.17549435e-38f;
+    const float y0 = rsqrt_approx(fmaxf(x0, least)), y1 = rsqrt_approx(fmaxf(x1, least));
+    float a0, a1, e0, e1, h0, h1;
+    mul2(x0, x1, y0, y1, a0, a1);
+    fma2v(-a0, -a1, a0, a1, x0, x1, e0, e1);
+    mul2(y0, y1, 0.5f, 0.5f, h0, h1);
+    fma2v(e0, e1, h0, h1, a0, a1, r0, r1);
 }
 
-// d is positive and normal (at least eps or a root); where its reciprocal or the
-// product leaves the normal range the quotient is within a place of 0 or infinite.
-__device__ __forceinline__ float quotient(float n, float d)
+__device__ __forceinline__ void quotient2(float n0, float n1, float d0, float d1, float &q0, float &q1)
 {
-    const float y = rcp_approx(d), q = __fmul_rn(n, y);
-    const float f = fmaf(fmaf(-q, d, n), y, q);
-    return fabsf(q) < 3.4e38f && fabsf(d) < 3.4e38f ? f : q;
+    const float y0 = rcp_approx(d0), y1 = rcp_approx(d1);
+    float a0, a1, e0, e1;
+    mul2(n0, n1, y0, y1, a0, a1);
+    fma2v(-a0, -a1, d0, d1, n0, n1, e0, e1);
+    fma2v(e0, e1, y0, y1, a0, a1, q0, q1);
 }
 
 // One AdamW step.  Memory-bound: each value is read and written once, 16 elements
@@ -249,7 +251,7 @@ __device__ __forceinline__ float quotient(float n, float d)
 // v by about 1 - b2 of itself, far less than half a step of E4M3, and rounding to
 // nearest would never move it.  p is updated from the unrounded m and v.
 template <bool PF32, bool GF32, bool MX, int MAXT>
-__global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Table<MAXT> tab, const Hyper h)
+__global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_constant__ Table<MAXT> tab, const Hyper h)
 {
     int lo = 0, hi = tab.count - 1;
     while (lo < hi) {  // the last tensor whose first chunk is at or before this one
@@ -301,6 +303,8 @@ __global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Tabl
         rg[u].values(g[u]);
         rm[u].values(m[u], MX ? e8m0_to_f32(ms[u]) : 1.0f);
         rv[u].values(v[u], MX ? e8m0_to_f32(vs[u]) : 1.0f);
+        int top = 0;                    // largest v's bits: infinity
+        uint32_t odd = 0xFFFFFFFFu;     // smallest v's bits - 1, 0 not counted: subnormal
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {  // two elements at a time
             float g0, g1, t0, t1;
@@ -311,11 +315,26 @@ __global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Tabl
             mul2(g0, g1, g0, g1, t0, t1);
             mul2(t0, t1, h.omb2, h.omb2, t0, t1);
             fma2v(h.beta2, h.beta2, v[u][k], v[u][k + 1], t0, t1, v[u][k], v[u][k + 1]);
-            const float r0 = root(v[u][k]), r1 = root(v[u][k + 1]);
-            float d0, d1;
+            top = max(max(top, __float_as_int(v[u][k])), __float_as_int(v[u][k + 1]));
+            odd = min(min(odd, __float_as_uint(v[u][k]) - 1u), __float_as_uint(v[u][k + 1]) - 1u);
+        }
+        const bool plain = top < 0x7F800000 && odd >= 0x007FFFFFu;  // every v is 0 or normal
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            float r0, r1, d0, d1, t0, t1;
+            if (plain) {
+                root2(v[u][k], v[u][k + 1], r0, r1);
+            } else {
+                r0 = __fsqrt_rn(v[u][k]);
+                r1 = __fsqrt_rn(v[u][k + 1]);
+            }
             fma2v(r0, r1, h.rbc2, h.rbc2, h.eps, h.eps, d0, d1);
-            d0 = quotient(m[u][k], d0);
-            d1 = quotient(m[u][k + 1], d1);
+            if (plain) {
+                quotient2(m[u][k], m[u][k + 1], d0, d1, d0, d1);
+            } else {
+                d0 = __fdiv_rn(m[u][k], d0);
+                d1 = __fdiv_rn(m[u][k + 1], d1);
+            }
             mul2(p[u][k], p[u][k + 1], h.decay, h.decay, t0, t1);
             fma2v(-h.lr1, -h.lr1, d0, d1, t0, t1, p[u][k], p[u][k + 1]);
             if (MX) v[u][k] = r0, v[u][k + 1] = r1;
@@ -341,10 +360,16 @@ __global__ void __launch_bounds__(CTA) adamw_kernel(const __grid_constant__ Tabl
             // bf16 without a master: the step is often below half a place, so the
             // rounding is stochastic (16 bits added below the last place)
             uint32_t b[8];
+            float any = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 b[k] = __float_as_uint(p[u][k]) + bits16(r[u][k >> 2], k & 3);
-                if (p[u][k] != p[u][k]) b[k] = 0x7FC00000u;  // the addition may carry a NaN's bits into the sign
+                any += p[u][k];
+            }
+            if (any != any) {  // the addition may carry a NaN's bits into the sign
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (p[u][k] != p[u][k]) b[k] = 0x7FC00000u;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = __byte_perm(b[2 * k], b[2 * k + 1], 0x7632);
