@@ -16,7 +16,8 @@ namespace {
 
 constexpr int RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2;
 constexpr int CTA = 256;
-constexpr int WARP_COLS = 1024;  // rows up to here: one warp each; longer ones: one CTA each
+constexpr int WARP_COLS = 1024;     // rows up to here: one warp each; longer ones: one CTA each
+constexpr int BWD_WARP_COLS = 512;  // the same in the backward pass, which holds more per column
 constexpr int MAX_COLS = 16384;
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -87,11 +88,11 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Sum over the threads of one row: a warp (T = 32) or the CTA (T = 256, one
+// Sum over the threads of one row: a warp (T = 32) or the whole CTA (one
 // barrier; `slot` alternates between calls so that a slot's readers are done
 // before its next writer: a barrier of the other slot lies between them).
 template <int T>
-__device__ __forceinline__ float row_sum(float v, float (*red)[CTA / 32], int slot)
+__device__ __forceinline__ float row_sum(float v, float (*red)[T / 32], int slot)
 {
     v = warp_sum(v);
     if (T == 32) return v;
@@ -99,7 +100,7 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[CTA / 32], int sl
     __syncthreads();
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < CTA / 32; ++w) s += red[slot][w];
+    for (int w = 0; w < T / 32; ++w) s += red[slot][w];
     return s;
 }
 
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_kernel(const uint16_t *__rest
                                                           uint8_t *__restrict__ out, uint8_t *__restrict__ out_sc,
                                                           uint16_t *__restrict__ y_out, float *__restrict__ rstd_out)
 {
-    __shared__ float red[2][CTA / 32];
+    __shared__ float red[2][T / 32];
     const int t = threadIdx.x & (T - 1);
     const int64_t row = T == 32 ? (int64_t)blockIdx.x * (CTA / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
     if (T == 32 && row >= rows) return;  // whole warps
@@ -198,14 +199,17 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_kernel(const uint16_t *__rest
 // threads walk the rows with the grid's stride; each keeps the dw sums of its
 // own columns in registers and writes them once, and a second kernel adds the
 // CTAs' partial sums in a fixed order (no atomics: the same bits every run).
+// AHEAD: the next row's loads are on their way while this one is reduced and
+// written; rows of more than 8192 columns have no registers for that.
 template <int T, int NP, int RK>
-__global__ void __launch_bounds__(CTA) add_rmsnorm_backward_kernel(
+__global__ void __launch_bounds__(T == 32 ? CTA : T, T == 512 ? 1 : 2) add_rmsnorm_backward_kernel(
     const uint16_t *__restrict__ dy, const void *__restrict__ r, const float *__restrict__ rstd,
     const uint16_t *__restrict__ weight, const void *__restrict__ dres, int64_t rows, int cols, void *__restrict__ dr,
     uint16_t *__restrict__ dx, float *__restrict__ partial)
 {
-    __shared__ float red[2][CTA / 32];
-    constexpr int RPC = CTA / T;  // rows of a CTA at a time
+    __shared__ float red[2][T / 32];
+    constexpr int RPC = T == 32 ? CTA / T : 1;  // rows of a CTA at a time
+    constexpr bool AHEAD = T * NP <= 1024;
     const int t = threadIdx.x & (T - 1);
     uint4 wv[NP];
     float acc[NP][8];
@@ -218,10 +222,10 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_backward_kernel(
         for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
     }
     int slot = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPC + (T == 32 ? threadIdx.x >> 5 : 0); row < rows;
-         row += (int64_t)gridDim.x * RPC, slot ^= 1) {
-        uint4 dv[NP];
-        Piece<RK> rv[NP], sv[NP];
+    uint4 dv[NP];
+    Piece<RK> rv[NP], sv[NP];
+    float rs = 0.0f;
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = 8 * (t + T * i);
@@ -231,40 +235,45 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_backward_kernel(
                 if (dres) sv[i].load(dres, row * cols + c);
             }
         }
-        const float rs = __ldg(rstd + row);
+        rs = __ldg(rstd + row);
+    };
+    const int64_t step = (int64_t)gridDim.x * RPC;
+    int64_t row = (int64_t)blockIdx.x * RPC + (T == 32 ? threadIdx.x >> 5 : 0);
+    if (AHEAD && row < rows) load(row);
+    for (; row < rows; row += step, slot ^= 1) {
+        if (!AHEAD) load(row);
+        // g = dy w and xh = r rstd take the loads' place
+        float g[NP][8], xh[NP][8], s8[NP][8];
+        const float rstd_row = rs;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             if (8 * (t + T * i) < cols) {
-                float d8[8], r8[8], w8[8];
+                float d8[8], w8[8];
                 unpack8(dv[i], d8);
-                rv[i].values(r8);
+                rv[i].values(xh[i]);
                 unpack8(wv[i], w8);
+                if (dres) sv[i].values(s8[i]);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float xh = __fmul_rn(r8[k], rs);
-                    acc[i][k] = fmaf(d8[k], xh, acc[i][k]);
-                    s = fmaf(__fmul_rn(d8[k], w8[k]), xh, s);
+                    xh[i][k] = __fmul_rn(xh[i][k], rstd_row);
+                    g[i][k] = __fmul_rn(d8[k], w8[k]);
+                    acc[i][k] = fmaf(d8[k], xh[i][k], acc[i][k]);
+                    s = fmaf(g[i][k], xh[i][k], s);
                 }
             }
         }
+        if (AHEAD && row + step < rows) load(row + step);
         const float c1 = __fdiv_rn(row_sum<T>(s, red, slot), (float)cols);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = 8 * (t + T * i);
             if (c < cols) {
-                float d8[8], r8[8], w8[8], o[8];
-                unpack8(dv[i], d8);
-                rv[i].values(r8);
-                unpack8(wv[i], w8);
+                float o[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    o[k] = __fmul_rn(rs, fmaf(-__fmul_rn(r8[k], rs), c1, __fmul_rn(d8[k], w8[k])));
-                if (dres) {
-                    float s8[8];
-                    sv[i].values(s8);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = __fadd_rn(o[k], s8[k]);
+                for (int k = 0; k < 8; ++k) {
+                    o[k] = __fmul_rn(rstd_row, fmaf(-xh[i][k], c1, g[i][k]));
+                    if (dres) o[k] = __fadd_rn(o[k], s8[i][k]);
                 }
                 Piece<RK>::store(dr, row * cols + c, o);
                 if (dx) *reinterpret_cast<uint4 *>(dx + row * cols + c) = pack8(o);
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_backward_kernel(
     }
     if constexpr (T == 32) {
         // the CTA's eight warps hold sums of the same columns
-        __shared__ float sums[CTA / 32][WARP_COLS];
+        __shared__ float sums[CTA / 32][BWD_WARP_COLS];
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -301,36 +310,40 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_backward_kernel(
     }
 }
 
-// dw[c] = sum of the CTAs' partial sums: 32 columns per CTA, 8 warps each take
-// every eighth partial row, then the warps' sums are added in order.
-__global__ void __launch_bounds__(CTA) add_rmsnorm_dw_kernel(const float *__restrict__ partial, int parts, int cols,
-                                                             float *__restrict__ dw)
+// dw[c] = sum of the CTAs' partial sums: 32 columns per CTA, each of its 32 warps
+// takes every 32nd partial row, then the warps' sums are added in order.
+constexpr int DW_WARPS = 32;
+__global__ void __launch_bounds__(32 * DW_WARPS) add_rmsnorm_dw_kernel(const float *__restrict__ partial, int parts,
+                                                                       int cols, float *__restrict__ dw)
 {
-    __shared__ float sums[CTA / 32][32];
+    __shared__ float sums[DW_WARPS][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // cols % 32 == 0
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the backward kernel still runs
     float v = 0.0f;
 #pragma unroll 8
-    for (int p = w; p < parts; p += CTA / 32) v += partial[(int64_t)p * cols + c];
+    for (int p = w; p < parts; p += DW_WARPS) v += partial[(int64_t)p * cols + c];
     sums[w][lane] = v;
     __syncthreads();
     if (w == 0) {
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < CTA / 32; ++k) s += sums[k][lane];
+        for (int k = 0; k < DW_WARPS; ++k) s += sums[k][lane];
         dw[c] = s;
     }
 }
 
-// CTAs of the backward kernel (rows of its partial sums): two for each of the
-// 152 SMs, fewer where there are fewer rows.  A constant, so that the
-// workspace's size and the sums' order depend on the sizes alone.
-constexpr int64_t BWD_CTAS = 304;
-
+// CTAs of the backward kernel (rows of its partial sums): as many as the 152 SMs
+// hold at once (one of 512 threads, two of 256, four of 128), fewer where there
+// are fewer rows.  More are slower: they run in turn, and each adds a row of partial
+// sums (16384 x 4096: 304 CTAs 93 us, 456 110 us, 608 97 us; 304 of 512 threads,
+// half of them waiting, 111 us).  A constant, so that the workspace's size and the sums' order
+// depend on the sizes alone.
 int64_t backward_parts(int64_t rows, int64_t cols)
 {
-    const int64_t per = cols <= WARP_COLS ? CTA / 32 : 1;
-    return std::min<int64_t>(BWD_CTAS, (rows + per - 1) / per);
+    const int64_t per = cols <= BWD_WARP_COLS ? CTA / 32 : 1;
+    const int64_t most = cols > 4096 ? 152 : cols > BWD_WARP_COLS && cols <= 1024 ? 608 : 304;
+    return std::min<int64_t>(most, (rows + per - 1) / per);
 }
 
 struct NormArgs {
@@ -378,7 +391,7 @@ template <int T, int NP>
 void launch_norm_bwd(int rk, int parts, const NormBwdArgs &a, cudaStream_t s)
 {
 #define PMN_NORM_BWD(RK)                                                                                              \
-    add_rmsnorm_backward_kernel<T, NP, RK><<<parts, CTA, 0, s>>>(a.dy, a.r, a.rstd, a.weight, a.dres, a.rows, a.cols, \
+    add_rmsnorm_backward_kernel<T, NP, RK><<<parts, T == 32 ? CTA : T, 0, s>>>(a.dy, a.r, a.rstd, a.weight, a.dres, a.rows, a.cols, \
                                                                  a.dr, a.dx, a.partial)
     if (rk == RES_BF16) PMN_NORM_BWD(RES_BF16);
     else PMN_NORM_BWD(RES_F32);
@@ -458,9 +471,24 @@ extern "C" pmn_status pmn_add_rmsnorm_backward(const void *dy, const void *r, in
     float *partial = static_cast<float *>(workspace);
     const NormBwdArgs a{static_cast<const uint16_t *>(dy), r, rstd, static_cast<const uint16_t *>(weight), dres, rows,
                         (int)cols, dr, static_cast<uint16_t *>(dx), partial};
-#define PMN_CALL(T, NP) launch_norm_bwd<T, NP>(rk, parts, a, s)
-    PMN_BY_COLS(cols, PMN_CALL);
-#undef PMN_CALL
-    add_rmsnorm_dw_kernel<<<(unsigned)(cols / 32), CTA, 0, s>>>(partial, parts, (int)cols, dw);
-    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    if (cols <= 256) launch_norm_bwd<32, 1>(rk, parts, a, s);
+    else if (cols <= BWD_WARP_COLS) launch_norm_bwd<32, 2>(rk, parts, a, s);
+    else if (cols <= 1024) launch_norm_bwd<128, 1>(rk, parts, a, s);
+    else if (cols <= 2048) launch_norm_bwd<256, 1>(rk, parts, a, s);
+    else if (cols <= 4096) launch_norm_bwd<256, 2>(rk, parts, a, s);
+    else if (cols <= 8192) launch_norm_bwd<512, 2>(rk, parts, a, s);
+    else launch_norm_bwd<512, 4>(rk, parts, a, s);
+    if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
+    // the second kernel's launch overlaps the first one's end; it waits for its writes
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(cols / 32));
+    cfg.blockDim = dim3(32 * DW_WARPS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, add_rmsnorm_dw_kernel, (const float *)partial, parts, (int)cols, dw) == cudaSuccess
+               ? PMN_OK : PMN_ERR_CUDA;
 }
