@@ -99,16 +99,28 @@ __device__ __forceinline__ void tmem_dealloc_ct(uint32_t taddr, uint32_t ncols)
     else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Arrives on `bar` (in both CTAs of a pair) once this thread's tcgen05 operations
-// so far have completed.
+// The tensor instructions are executed by whole warps in step and issued by one
+// lane, by a predicate inside the instruction (`el`: this is the lane): a branch
+// around them costs a reconvergence per stage, and a branch around the loop hides
+// from the compiler that their operands are warp-uniform (measured, clocks per
+// 128-deep stage that the issuing warp needs: loop in one lane 940, branch per stage
+// 510-600, this form see the kernel).
+
+// Arrives on `bar` (in both CTAs of a pair) once the issuing lane's tcgen05
+// operations so far have completed.
 template <int CT>
-__device__ __forceinline__ void tc_commit_ct(uint32_t bar)
+__device__ __forceinline__ void tc_commit_ct(uint32_t el, uint32_t bar)
 {
-    if (CT == 1) tc_commit(bar);
+    if (CT == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(el), "r"(bar)
+            : "memory");
     else
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"(el),
+            "r"(bar), "h"((uint16_t)3)
             : "memory");
 }
 
@@ -122,26 +134,57 @@ __device__ __forceinline__ void tc_commit_own(uint32_t bar)
 }
 
 template <int CT>
-__device__ __forceinline__ void tc_cp_ct(uint32_t taddr, uint64_t sdesc)
+__device__ __forceinline__ void tc_cp_ct(uint32_t el, uint32_t taddr, uint64_t sdesc)
 {
-    if (CT == 1) tc_cp_32x128b_warpx4(taddr, sdesc);
-    else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-template <int CT>
-__device__ __forceinline__ void mma_mxfp8_ct(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
-{
-    if (CT == 1) mma_mxfp8(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+    if (CT == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
+            : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
             : "memory");
 }
 
+template <int CT>
+__device__ __forceinline__ void mma_mxfp8_ct(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    if (CT == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(el)
+            : "memory");
+}
+
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+#ifndef PMN_SERVE_KERNEL
+#define PMN_SERVE_KERNEL 0
+#endif
 constexpr int BM = 128;  // rows per CTA
 constexpr int MAX_GROUPS = 1024;
 constexpr int EW = 12;                      // epilogue warps, three per TMEM lane quadrant
@@ -150,30 +193,36 @@ constexpr uint32_t TMEM_COLS = 512;
 // An epilogue warp's shared memory: 32 rows x 32 columns of bf16 gate and up
 // (2 x 2 KB), and, once those are in registers, two blocks that are being
 // transposed (32 rows of 36 bytes each).
-constexpr int WARP_BYTES = 4096, COL_BYTES = 32 * 36;
+constexpr int WARP_BUF = 4096, COL_BYTES = 32 * 36;
 
 // One tile: 128 routed rows of an expert (256 on a CTA pair) times TBN rows of its weight.  Forward:
 // TBN / 2 gate rows and the TBN / 2 up rows of the same columns of h; backward:
 // TBN columns of dH.  A stage holds 128 bytes of K of both operands (TMA,
 // 128-byte swizzle) and their scale factors in the 32 x 128-bit form that
 // tcgen05.cp copies into TMEM.
-template <bool BWD, int TBN, int CT>
+// Forward for serving (h alone), forward for training (h^T and y where wanted),
+// backward.
+constexpr int SERVE = 0, TRAIN = 1, BACKWARD = 2;
+
+template <int MODE, int TBN, int CT>
 struct Cfg {
+    static constexpr bool BWD = MODE == BACKWARD;
     static constexpr int HB = BWD ? TBN : TBN / 2;  // columns of h (dH) per tile
     static constexpr int NCH = HB / 32;             // 32-column chunks (MX blocks) of the epilogue
     static constexpr int CPW = (NCH + 2) / 3;       // consecutive chunks per epilogue warp
     static constexpr int RB = (TBN + 127) / 128;    // 128-row scale blocks of B
     static constexpr int A_BYTES = BM * 128, B_BYTES = TBN / CT * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, SF_BYTES = 512 * (1 + RB);
-    static constexpr int STAGES = CT == 2 ? 5 : 4;
+    static constexpr int STAGES = MODE != SERVE ? (CT == 2 ? 5 : 3) : CT == 2 ? 6 : TBN == 64 ? 8 : 5;
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
     static constexpr int NR = 2 * (1 + RB);         // 32-row boxes of scales per scale-factor warp
-    static constexpr int RAW_SLOTS = 3, RAW_BYTES = NR * 512;  // groups of four stages in flight, per warp
+    static constexpr int RAW_SLOTS = CT == 2 ? 3 : 2, RAW_BYTES = NR * 512;  // groups of four stages in flight, per warp
+    static constexpr int WARP_BYTES = MODE == SERVE ? 0 : WARP_BUF, GROUP_BYTES = MODE == SERVE ? 0 : 1024;
     static constexpr int SF_OFF = STAGES * STAGE_BYTES, WARP_OFF = SF_OFF + STAGES * SF_BYTES,
                          RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + 2 * RAW_SLOTS * RAW_BYTES,
-                         SCALE_OFF = BAR_OFF + 256, CUM_OFF = SCALE_OFF + 3 * 2 * 512;
+                         SCALE_OFF = BAR_OFF + 256, CUM_OFF = SCALE_OFF + 3 * GROUP_BYTES;
     static constexpr int SMEM_BYTES = 1024 + CUM_OFF + (MAX_GROUPS + 1) * 4;
     static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
     static_assert(8 * (2 * STAGES + 8 + 2 * RAW_SLOTS) + 16 <= 256, "barrier space");
@@ -199,11 +248,11 @@ struct Tile {
     int h0;  // first column of h
 };
 
-template <bool BWD, int TBN, int CT>
+template <int MODE, int TBN, int CT>
 __device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int &gc)
 {
     while (gc + 1 < p.groups && s_cum[gc + 1] <= t) ++gc;  // every role walks its tiles upwards
-    constexpr int HB = Cfg<BWD, TBN, CT>::HB;
+    constexpr int HB = Cfg<MODE, TBN, CT>::HB;
     const int nt = (int)((p.f + HB - 1) / HB);
     const int local = t - s_cum[gc], mi = local / nt;
     Tile ti;
@@ -366,12 +415,13 @@ __device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], ui
 //   warps 4..  epilogue, one row per thread and 32 columns at a time
 // Every wait is bounded: on a timeout an error bit is latched and the CTA winds
 // down.
-template <bool BWD, int TBN, int CT>
+template <int MODE, int TBN, int CT>
 __global__ void __launch_bounds__(THREADS, 1)
     gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p)
 {
-    using C = Cfg<BWD, TBN, CT>;
+    using C = Cfg<MODE, TBN, CT>;
+    constexpr bool BWD = MODE == BACKWARD;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -415,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // that are not monotone, in range and (with column blocks) multiples of
         // 32 run no tile
         const int nt = (int)((p.f + C::HB - 1) / C::HB);
-        const bool cols = p.out_t != nullptr;
+        const bool cols = MODE != SERVE && p.out_t != nullptr;
         int base = 0;
         bool good = true;
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
@@ -463,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int gc = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+            const Tile ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
             const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
             for (int ks = 0; ks < nks; ++ks) {
                 ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
@@ -529,7 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int64_t asked = 0;  // groups whose scales have been asked for
         int t = tile0, q = 0, gc = 0;
         Tile ti;
-        if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+        if (t < total) ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
         auto fetch = [&]() {
             if (asked >= groups) return;
             const int slot = (int)(asked % C::RAW_SLOTS);
@@ -551,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (++q == groups4) {
                 q = 0;
                 t += tstep;
-                if (t < total) ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+                if (t < total) ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
             }
         };
         for (int i = 0; i < C::RAW_SLOTS; ++i) fetch();
@@ -606,9 +656,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The whole warp walks the loop, so that the operands of the tensor
         // instructions are warp-uniform values; one elected lane issues.
         if (rank == 0) {
-            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), el = elect_one();
             uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
-            bool ok = true;
+            bool ok = true, ready = false;
             for (int t = tile0; t < total && ok; t += tstep) {
                 ok = warp_wait(bar_acc_empty + 8 * abuf, aphase ^ 1, p.wait_ns);
                 if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
@@ -617,32 +667,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const uint32_t d = tm + abuf * TBN;
                 for (int ks = 0; ks < nks; ++ks) {
-                    ok = warp_wait(bar_full + 8 * stage, phase, p.wait_ns);
-                    if (!ok) {
-                        give_up();
-                        break;
+                    // asked for a stage ahead, the answer is there when it is needed
+                    if (__all_sync(0xFFFFFFFFu, ready) == 0) {
+                        ok = warp_wait(bar_full + 8 * stage, phase, p.wait_ns);
+                        if (!ok) {
+                            give_up();
+                            break;
+                        }
                     }
                     tc_fence_after();
                     const uint32_t a = stages + stage * C::STAGE_BYTES, b = a + C::A_BYTES;
                     const uint32_t sf = stages + C::SF_OFF + stage * C::SF_BYTES;
-                    const uint32_t sfa = tm + C::SF_COL0 + stage * C::SF_COLS, sfb = sfa + 4;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int i = 0; i < 1 + C::RB; ++i)
-                            tc_cp_ct<CT>(sfa + 4 * i, smem_desc(sf + 512 * i, 0, 128, 0));
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)  // 32 of K per MMA inside the 128-byte swizzled rows
-                            mma_mxfp8_ct<CT>(d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2),
-                                             make_idesc<TBN, CT>((uint32_t)s), sfa, sfb, (ks > 0 || s > 0) ? 1u : 0u);
-                        tc_commit_ct<CT>(bar_empty + 8 * stage);
-                        if (ks == nks - 1) tc_commit_ct<CT>(bar_acc_full + 8 * abuf);
-                    }
-                    __syncwarp();
+                    const uint32_t sfa = tm + C::SF_COL0 + stage * C::SF_COLS, sfb = sfa + 4, done = bar_empty + 8 * stage;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
+                    ready = mbar_test(bar_full + 8 * stage, phase);
+#pragma unroll
+                    for (int i = 0; i < 1 + C::RB; ++i)
+                        tc_cp_ct<CT>(el, sfa + 4 * i, smem_desc(sf + 512 * i, 0, 128, 0));
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)  // 32 of K per MMA inside the 128-byte swizzled rows
+                        mma_mxfp8_ct<CT>(el, d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2),
+                                         make_idesc<TBN, CT>((uint32_t)s), sfa, sfb, (ks > 0 || s > 0) ? 1u : 0u);
+                    tc_commit_ct<CT>(el, done);
                 }
+                if (!ok) break;
+                tc_commit_ct<CT>(el, bar_acc_full + 8 * abuf);
                 if (++abuf == C::ACC) {
                     abuf = 0;
                     aphase ^= 1;
@@ -659,14 +711,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         // 32 columns in a row.
         const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0);  // warp-uniform, and known to be
         const int quad = wu & 3, c0 = ((wu - 4) >> 2) * C::CPW, c1 = min(c0 + C::CPW, C::NCH);
-        uint8_t *buf = smem + C::WARP_OFF + (wu - 4) * WARP_BYTES;
-        const uint32_t bufs = stages + C::WARP_OFF + (wu - 4) * WARP_BYTES;
+        uint8_t *buf = smem + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
+        const uint32_t bufs = stages + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
         const int pr = lane >> 2, pi = lane & 3;  // four lanes cover a row's 64 bytes of y
         // The four warps that hold a chunk's 128 rows collect its column scales, so
         // that a column's four bytes leave in one store: two buffers in turn, one
         // barrier per tile.
         const int group = (wu - 4) >> 2;
-        uint8_t *const sscale0 = smem + C::SCALE_OFF + group * 1024;
+        uint8_t *const sscale0 = smem + C::SCALE_OFF + group * C::GROUP_BYTES;
         uint32_t collected = 0;
         uint32_t rsc[2] = {0u, 0u};
         uint32_t abuf = 0, aphase = 0;
@@ -679,15 +731,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < 4; ++i) {
                 const uint32_t d = bufs + piece64(pr + 8 * i, pi);
                 cp_async16(d, g + 16 * i * p.f);
-                cp_async16(d + WARP_BYTES / 2, g + 16 * i * p.f + p.f);
+                cp_async16(d + WARP_BUF / 2, g + 16 * i * p.f + p.f);
             }
         };
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<BWD, TBN, CT>(t, p, s_cum, gc);
+            const Tile ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
             const int64_t row0 = ti.m0 + BM * rank + 32 * quad, row = row0 + lane;
             const bool valid = row < ti.row_end, any = row0 < ti.row_end;
             const int64_t tile_row = ti.m0 + BM * rank;
-            const bool words = p.words && tile_row % 128 == 0 && tile_row + BM <= ti.row_end;
+            const bool words = MODE != SERVE && p.words && tile_row % 128 == 0 && tile_row + BM <= ti.row_end;
             uint8_t *const sscale = sscale0 + 512 * (collected & 1u);
             if (BWD && any && ti.h0 + 32 * c0 < p.f) fetch_y(row0, ti.h0 + 32 * c0);  // lands while the MMAs run
             ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
@@ -716,7 +768,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_wait();
                     if (c == c1 - 1) release();
                     if (!on) continue;
-                    if (p.y) {  // y in bf16 for the backward pass, through shared memory: four lanes store a row's 64 bytes
+                    if (MODE == TRAIN && p.y) {  // y in bf16 for the backward pass, through shared memory: four lanes store a row's 64 bytes
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -728,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
                                     w[i] = *reinterpret_cast<const uint32_t *>(&b2);
                                 }
-                                *reinterpret_cast<uint4 *>(buf + part * (WARP_BYTES / 2) + piece64(lane, j)) =
+                                *reinterpret_cast<uint4 *>(buf + part * (WARP_BUF / 2) + piece64(lane, j)) =
                                     make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         __syncwarp();
@@ -739,7 +791,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 const uint8_t *b8 = buf + piece64(pr + 8 * i, pi);
                                 *reinterpret_cast<uint4 *>(o + 16 * i * p.f) = *reinterpret_cast<const uint4 *>(b8);
                                 *reinterpret_cast<uint4 *>(o + 16 * i * p.f + p.f) =
-                                    *reinterpret_cast<const uint4 *>(b8 + WARP_BYTES / 2);
+                                    *reinterpret_cast<const uint4 *>(b8 + WARP_BUF / 2);
                             }
                         __syncwarp();
                     }
@@ -750,7 +802,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         store32(p.out + row * p.f + col, q, p.wide);
                         p.out_sc[row * (p.f / 32) + col / 32] = sc;
                     }
-                    if (p.out_t) {
+                    if (MODE == TRAIN && p.out_t) {
                         uint8_t st[1];
                         col_blocks<1>({&v}, buf, {p.out_t + col * p.m + row0}, p.m, st, lane);
                         if (words) sscale[128 * (c - c0) + 4 * lane + quad] = st[0];
@@ -766,7 +818,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 gw = *reinterpret_cast<const uint4 *>(buf + piece64(lane, i));
-                        const uint4 uw = *reinterpret_cast<const uint4 *>(buf + WARP_BYTES / 2 + piece64(lane, i));
+                        const uint4 uw = *reinterpret_cast<const uint4 *>(buf + WARP_BUF / 2 + piece64(lane, i));
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int j = 8 * i + k;
@@ -839,6 +891,132 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (CT == 2) cluster_sync();
 }
 
+// ---------------------------------------------------------------- few rows
+// The forward for a handful of rows (single tokens of a serving loop): its time is
+// that of reading the weights, which 128-row tiles would spread over a dozen SMs.
+// A cluster of four CTAs takes 32 columns of h for up to RR rows of one expert, each
+// CTA a quarter of K in units of 512; a warp holds 8 of the 64 weight rows, a lane 16
+// consecutive codes of each (512 bytes per warp load), multiplied in float32 and
+// scaled once per 32.  The four partial sums meet in the leader's shared memory.
+constexpr int RR = 4, FEW_CTAS = 4, FEW_ROWS = 8;
+
+// 16 E4M3 codes -> float32
+__device__ __forceinline__ void decode16(const uint4 &q, float (&v)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t h2;
+        const uint16_t b16 = (uint16_t)(u4_word(q, i >> 1) >> (16 * (i & 1)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b16));
+        v[2 * i] = h2_lo_to_f32(h2);
+        v[2 * i + 1] = h2_hi_to_f32(h2);
+    }
+}
+
+__global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
+    gated_rows_kernel(const uint8_t *__restrict__ a, const uint8_t *__restrict__ sa, const uint8_t *__restrict__ b,
+                      const uint8_t *__restrict__ sb, const Args p)
+{
+    __shared__ float part[FEW_CTAS][RR][64];  // the leader's: gate sums 0 .. 31, up sums 32 .. 63
+    __shared__ int s_expert, s_lo, s_hi;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int64_t t = blockIdx.y;                       // a row; the rows of one expert go four by four
+    const int64_t col = 32 * (int64_t)(blockIdx.x / FEW_CTAS);
+    if (threadIdx.x == 0) s_expert = -1;
+    __syncthreads();
+    bool good = true;
+    for (int e = threadIdx.x; e < p.groups; e += 256) {
+        const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
+        if (lo < 0 || hi < lo || hi > p.m) good = false;
+        if (lo <= t && t < hi) s_expert = e, s_lo = lo, s_hi = hi;
+    }
+    good = __syncthreads_and(good) != 0;
+    if (!good) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
+        return;  // alike in every CTA
+    }
+    if (s_expert < 0 || (t - s_lo) % RR != 0) return;  // alike in the cluster
+    const int nr = (int)min((int64_t)RR, (int64_t)s_hi - t);
+    const int64_t wrow = (int64_t)s_expert * 2 * p.f + (warp >= 4 ? p.f : 0) + col + 8 * (warp & 3);
+    const int64_t pitch = p.k / 32;
+    float acc[8][RR];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 0; r < RR; ++r) acc[j][r] = 0.0f;
+    for (int64_t u = rank; u < p.k / 512; u += FEW_CTAS) {
+        const int64_t k0 = 512 * u + 16 * lane;
+        uint4 w[8], x[RR];
+        uint32_t ws[8], xs[RR];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = __ldcs(reinterpret_cast<const uint4 *>(b + (wrow + j) * p.k + k0));
+            ws[j] = __ldg(sb + (wrow + j) * pitch + k0 / 32);
+        }
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+            x[r] = make_uint4(0u, 0u, 0u, 0u);
+            xs[r] = 0u;
+            if (r < nr) {
+                x[r] = __ldg(reinterpret_cast<const uint4 *>(a + (t + r) * p.k + k0));
+                xs[r] = __ldg(sa + (t + r) * pitch + k0 / 32);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+            if (r < nr) {  // uniform
+                float xv[16];
+                decode16(x[r], xv);
+                const float s = e8m0_to_f32(xs[r]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float wv[16];
+                    decode16(w[j], wv);
+                    float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        d0 = fmaf(wv[i], xv[i], d0);
+                        d1 = fmaf(wv[i + 1], xv[i + 1], d1);
+                    }
+                    // the sum of one scale block's half: both scales are powers of two
+                    acc[j][r] = fmaf(__fadd_rn(d0, d1) * s, e8m0_to_f32(ws[j]), acc[j][r]);
+                }
+            }
+        }
+    }
+    // the lanes' sums, then the four CTAs'
+    const uint32_t base = leader_addr(smem_u32(&part[rank][0][0]));
+#pragma unroll
+    for (int r = 0; r < RR; ++r) {
+        if (r < nr) {
+            float mine = 0.0f;  // lane j keeps weight row j's sum
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = acc[j][r];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+                if (lane == j) mine = v;
+            }
+            if (lane < 8)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(base + 4u * (64 * r + 8 * warp + lane)), "f"(mine)
+                             : "memory");
+        }
+    }
+    cluster_sync();
+    if (rank != 0 || warp >= nr) return;
+    float g = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int c = 0; c < FEW_CTAS; ++c) {
+        g += part[c][warp][lane];
+        v += part[c][warp][32 + lane];
+    }
+    const float h = silu_mul(g, v);
+    const int e = mx_exponent_448(__uint_as_float(warp_absmax(h)));
+    p.out[(t + warp) * p.f + col + lane] = (uint8_t)cvt_e4m3x2_rn(__fmul_rn(h, exp2_neg(e)), 0.0f);
+    if (lane == 0) p.out_sc[(t + warp) * (p.f / 32) + col / 32] = (uint8_t)(e + 127);
+}
+
 // ====================================================================== host
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -875,11 +1053,12 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, u
 inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool aligned16(const void *p) { return aligned(p, 16); }
 
-template <bool BWD, int TBN, int CT>
+template <int MODE, int TBN, int CT>
 pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
                   const Args &args, cudaStream_t s)
 {
-    using C = Cfg<BWD, TBN, CT>;
+    using C = Cfg<MODE, TBN, CT>;
+    constexpr bool BWD = MODE == BACKWARD;
     const uint64_t k = (uint64_t)args.k, m = (uint64_t)args.m, n = (uint64_t)args.b_rows;
     CUtensorMap ma, mb, msa, msb;
     if (!make_map(&ma, a, k, m, 128, BM) || !make_map(&mb, b, k, n, 128, BWD ? TBN / CT : TBN / 2) ||
@@ -889,7 +1068,7 @@ pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, c
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < CT)
         return PMN_ERR_CUDA;
-    auto kern = gated_kernel<BWD, TBN, CT>;
+    auto kern = gated_kernel<MODE, TBN, CT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return PMN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -956,7 +1135,16 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), aligned(out, 32),
                     aligned(out_scales, 2), out_t && total_rows % 128 == 0 && aligned(out_t_scales, 4),
                     pmn_wait_limit_ns()};
-    return launch<false, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (out_t || y_out) return launch<TRAIN, 192, 2>(a, a_scales, b, b_scales, args, s);
+    switch (PMN_SERVE_KERNEL) {
+        case 3:
+            gated_rows_kernel<<<dim3((unsigned)(f / 32 * FEW_CTAS), (unsigned)total_rows), 256, 0, s>>>(a, a_scales, b, b_scales, args);
+            return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+        case 1: return launch<SERVE, 192, 2>(a, a_scales, b, b_scales, args, s);
+        case 2: return launch<SERVE, 64, 1>(a, a_scales, b, b_scales, args, s);
+        default: return launch<SERVE, 192, 1>(a, a_scales, b, b_scales, args, s);
+    }
 }
 
 extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
@@ -973,5 +1161,5 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const 
     const Args args{offsets, num_experts, total_rows, f, k, (int64_t)num_experts * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)), aligned(out, 32),
                     aligned(out_scales, 2), total_rows % 128 == 0 && aligned(out_t_scales, 4), pmn_wait_limit_ns()};
-    return launch<true, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
+    return launch<BACKWARD, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
 }
