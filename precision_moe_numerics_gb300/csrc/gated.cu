@@ -279,6 +279,30 @@ __device__ __forceinline__ uint32_t make_idesc(uint32_t sf_id)
     return (sf_id << 4) | ((uint32_t)(TBN >> 3) << 17) | (1u << 23) | ((uint32_t)(CT * BM >> 4) << 24) | (sf_id << 29);
 }
 
+// 1 / (1 + e^-g) on two lanes, from the hardware's exponential and reciprocal: a
+// relative error of a few 2^-23 and (the argument's rounding) |g| 2^-23; 0 and 1
+// where e^-g leaves float32's normal range.
+__device__ __forceinline__ void sigmoid2(float g0, float g1, float &s0, float &s1)
+{
+    float a0, a1, b0, b1;
+    mul2(g0, g1, -1.44269504f, -1.44269504f, a0, a1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b0) : "f"(a0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b1) : "f"(a1));
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}" : "=f"(a0), "=f"(a1) : "f"(b0), "f"(b1), "f"(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(a0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(a1));
+}
+
+// a * b + c on two lanes, each rounded once.
+__device__ __forceinline__ void fma2v(float a0, float a1, float b0, float b1, float c0, float c1, float &r0, float &r1)
+{
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
 // Four values times their scales -> four E4M3 bytes, nearest even.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float sa, float sb, float sc, float sd)
 {
@@ -348,7 +372,7 @@ __device__ __forceinline__ uint32_t warp_absmax(float v)
 // memory (rows 36 bytes apart: conflict-free both ways), lane 4 k + r then holds
 // columns 4 k .. 4 k + 3, rows 8 r .. 8 r + 7.
 // The exponent rule of mx_exponent_448 on the bits M of the maximum: with
-// t = (M + 0x1FFFFF) >> 23 (a carry where M's fraction is above 1.75) and t >= 8,
+// t = (max(M, 8 << 23) + 0x1FFFFF) >> 23 (a carry where M's fraction is above 1.75),
 // e = t - 135, so the scale byte is t - 8 and 2^-e has the exponent field 262 - t.
 // q: the block's first column at its first row; pitch: bytes between columns.
 // NB blocks are worked on side by side, as each step waits on the one before.
@@ -366,13 +390,13 @@ __device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], ui
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = (*v[n])[4 * k + i];
-                t[i] = max(min(warp_absmax(x[i]), 0x7F800000u), 0x04000000u) + 0x1FFFFFu;  // (all NaN: as infinity)
-                m[i] = __uint_as_float(0x83000000u - (t[i] & 0xFF800000u));
+                t[i] = max(warp_absmax(x[i]), 0x04000000u) - (0x04000000u - 0x1FFFFFu);  // byte in bits 23 .. 30
+                m[i] = __uint_as_float(0x7F000000u - (t[i] & 0x7F800000u));
             }
             *reinterpret_cast<uint32_t *>(buf + n * COL_BYTES + 36 * lane + 4 * k) =
                 e4m3x4(x[0], x[1], x[2], x[3], m[0], m[1], m[2], m[3]);
             sb[n][k] = __byte_perm(__byte_perm(t[0] << 1, t[1] << 1, 0x0073), __byte_perm(t[2] << 1, t[3] << 1, 0x0073),
-                                   0x5410) - 0x08080808u;
+                                   0x5410);
         }
     __syncwarp();
     const int k = lane >> 2, r = lane & 3;
@@ -796,7 +820,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         __syncwarp();
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = silu_mul(v[j], u[j]);
+                    for (int j = 0; j < 32; j += 2) {
+                        float s0, s1;
+                        sigmoid2(v[j], v[j + 1], s0, s1);
+                        mul2(v[j], v[j + 1], s0, s1, s0, s1);
+                        mul2(s0, s1, u[j], u[j + 1], v[j], v[j + 1]);
+                    }
                     row_block(v, q, sc);
                     if (valid) {
                         store32(p.out + row * p.f + col, q, p.wide);
@@ -820,15 +849,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint4 gw = *reinterpret_cast<const uint4 *>(buf + piece64(lane, i));
                         const uint4 uw = *reinterpret_cast<const uint4 *>(buf + WARP_BUF / 2 + piece64(lane, i));
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int j = 8 * i + k;
-                            const uint32_t a = u4_word(gw, k >> 1), b = u4_word(uw, k >> 1);
-                            const float gt = __uint_as_float((k & 1) ? (a & 0xFFFF0000u) : (a << 16));
-                            const float up = __uint_as_float((k & 1) ? (b & 0xFFFF0000u) : (b << 16));
-                            const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gt)));
-                            const float ds = __fmul_rn(v[j], s);
-                            u[j] = __fmul_rn(ds, gt);
-                            v[j] = __fmul_rn(__fmul_rn(ds, up), fmaf(gt, __fsub_rn(1.0f, s), 1.0f));
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = 8 * i + 2 * k;
+                            const uint32_t a = u4_word(gw, k), b = u4_word(uw, k);
+                            const float g0 = __uint_as_float(a << 16), g1 = __uint_as_float(a & 0xFFFF0000u);
+                            const float u0 = __uint_as_float(b << 16), u1 = __uint_as_float(b & 0xFFFF0000u);
+                            float s0, s1, d0, d1, k0, k1;
+                            sigmoid2(g0, g1, s0, s1);
+                            mul2(v[j], v[j + 1], s0, s1, d0, d1);             // dh s
+                            mul2(d0, d1, g0, g1, u[j], u[j + 1]);             // dup
+                            fma2v(s0, s1, -1.0f, -1.0f, 1.0f, 1.0f, k0, k1);  // 1 - s
+                            fma2v(g0, g1, k0, k1, 1.0f, 1.0f, k0, k1);        // 1 + gate (1 - s)
+                            mul2(d0, d1, u0, u1, d0, d1);
+                            mul2(d0, d1, k0, k1, v[j], v[j + 1]);             // dgate
                         }
                     }
                     const int64_t f2 = 2 * p.f;
