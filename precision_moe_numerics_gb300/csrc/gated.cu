@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -182,11 +183,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-#ifndef PMN_SERVE_KERNEL
-#define PMN_SERVE_KERNEL 0
-#endif
 constexpr int BM = 128;  // rows per CTA
 constexpr int MAX_GROUPS = 1024;
+constexpr int MAX_DEVICES = 64;
 constexpr int EW = 12;                      // epilogue warps, three per TMEM lane quadrant
 constexpr int THREADS = 128 + 32 * EW;
 constexpr uint32_t TMEM_COLS = 512;
@@ -213,7 +212,7 @@ struct Cfg {
     static constexpr int RB = (TBN + 127) / 128;    // 128-row scale blocks of B
     static constexpr int A_BYTES = BM * 128, B_BYTES = TBN / CT * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, SF_BYTES = 512 * (1 + RB);
-    static constexpr int STAGES = MODE != SERVE ? (CT == 2 ? 5 : 3) : CT == 2 ? 6 : TBN == 64 ? 8 : 5;
+    static constexpr int STAGES = MODE == SERVE && CT == 2 ? 6 : 5;
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
@@ -927,11 +926,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ---------------------------------------------------------------- few rows
 // The forward for a handful of rows (single tokens of a serving loop): its time is
 // that of reading the weights, which 128-row tiles would spread over a dozen SMs.
-// A cluster of four CTAs takes 32 columns of h for up to RR rows of one expert, each
-// CTA a quarter of K in units of 512; a warp holds 8 of the 64 weight rows, a lane 16
-// consecutive codes of each (512 bytes per warp load), multiplied in float32 and
-// scaled once per 32.  The four partial sums meet in the leader's shared memory.
-constexpr int RR = 4, FEW_CTAS = 4, FEW_ROWS = 8;
+// A cluster of four CTAs takes 32 columns of h for one row, each CTA a quarter of K
+// in units of 512; a warp holds 8 of the 64 weight rows, a lane 16 consecutive codes
+// of each (512 bytes per warp load), multiplied in float32 and scaled once per half
+// block.  The four partial sums meet in the leader's shared memory.  Rows of one
+// expert share its weights through L2 only.
+constexpr int FEW_CTAS = 4;
 
 // 16 E4M3 codes -> float32
 __device__ __forceinline__ void decode16(const uint4 &q, float (&v)[16])
@@ -950,11 +950,11 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
     gated_rows_kernel(const uint8_t *__restrict__ a, const uint8_t *__restrict__ sa, const uint8_t *__restrict__ b,
                       const uint8_t *__restrict__ sb, const Args p)
 {
-    __shared__ float part[FEW_CTAS][RR][64];  // the leader's: gate sums 0 .. 31, up sums 32 .. 63
-    __shared__ int s_expert, s_lo, s_hi;
+    __shared__ float part[FEW_CTAS][64];  // the leader's: gate sums 0 .. 31, up sums 32 .. 63
+    __shared__ int s_expert;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
-    const int64_t t = blockIdx.y;                       // a row; the rows of one expert go four by four
+    const int64_t t = blockIdx.y;
     const int64_t col = 32 * (int64_t)(blockIdx.x / FEW_CTAS);
     if (threadIdx.x == 0) s_expert = -1;
     __syncthreads();
@@ -962,92 +962,72 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
     for (int e = threadIdx.x; e < p.groups; e += 256) {
         const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
         if (lo < 0 || hi < lo || hi > p.m) good = false;
-        if (lo <= t && t < hi) s_expert = e, s_lo = lo, s_hi = hi;
+        if (lo <= t && t < hi) s_expert = e;
     }
     good = __syncthreads_and(good) != 0;
     if (!good) {
         if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         return;  // alike in every CTA
     }
-    if (s_expert < 0 || (t - s_lo) % RR != 0) return;  // alike in the cluster
-    const int nr = (int)min((int64_t)RR, (int64_t)s_hi - t);
+    if (s_expert < 0) return;  // a row outside the segments: alike in the cluster
     const int64_t wrow = (int64_t)s_expert * 2 * p.f + (warp >= 4 ? p.f : 0) + col + 8 * (warp & 3);
     const int64_t pitch = p.k / 32;
-    float acc[8][RR];
+    const uint8_t *wp = b + wrow * p.k + 16 * lane, *wsp = sb + wrow * pitch + lane / 2;
+    const uint8_t *xp = a + t * p.k + 16 * lane, *xsp = sa + t * pitch + lane / 2;
+    float acc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int r = 0; r < RR; ++r) acc[j][r] = 0.0f;
-    for (int64_t u = rank; u < p.k / 512; u += FEW_CTAS) {
-        const int64_t k0 = 512 * u + 16 * lane;
-        uint4 w[8], x[RR];
-        uint32_t ws[8], xs[RR];
+    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    const int units = (int)(p.k / 512);
+#pragma unroll 2
+    for (int u = rank; u < units; u += FEW_CTAS) {
+        uint4 w[8];
+        uint32_t ws[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            w[j] = __ldcs(reinterpret_cast<const uint4 *>(b + (wrow + j) * p.k + k0));
-            ws[j] = __ldg(sb + (wrow + j) * pitch + k0 / 32);
+            w[j] = __ldcs(reinterpret_cast<const uint4 *>(wp + j * p.k + 512 * u));
+            ws[j] = __ldg(wsp + j * pitch + 16 * u);
         }
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xp + 512 * u));
+        const float s = e8m0_to_f32(__ldg(xsp + 16 * u));
+        float xv[16];
+        decode16(x, xv);
 #pragma unroll
-        for (int r = 0; r < RR; ++r) {
-            x[r] = make_uint4(0u, 0u, 0u, 0u);
-            xs[r] = 0u;
-            if (r < nr) {
-                x[r] = __ldg(reinterpret_cast<const uint4 *>(a + (t + r) * p.k + k0));
-                xs[r] = __ldg(sa + (t + r) * pitch + k0 / 32);
+        for (int j = 0; j < 8; ++j) {
+            float wv[16];
+            decode16(w[j], wv);
+            float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                d0 = fmaf(wv[i], xv[i], d0);
+                d1 = fmaf(wv[i + 1], xv[i + 1], d1);
             }
-        }
-#pragma unroll
-        for (int r = 0; r < RR; ++r) {
-            if (r < nr) {  // uniform
-                float xv[16];
-                decode16(x[r], xv);
-                const float s = e8m0_to_f32(xs[r]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float wv[16];
-                    decode16(w[j], wv);
-                    float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        d0 = fmaf(wv[i], xv[i], d0);
-                        d1 = fmaf(wv[i + 1], xv[i + 1], d1);
-                    }
-                    // the sum of one scale block's half: both scales are powers of two
-                    acc[j][r] = fmaf(__fadd_rn(d0, d1) * s, e8m0_to_f32(ws[j]), acc[j][r]);
-                }
-            }
+            acc[j] = fmaf(__fadd_rn(d0, d1) * s, e8m0_to_f32(ws[j]), acc[j]);
         }
     }
-    // the lanes' sums, then the four CTAs'
-    const uint32_t base = leader_addr(smem_u32(&part[rank][0][0]));
+    float mine = 0.0f;  // lane j keeps weight row j's sum
 #pragma unroll
-    for (int r = 0; r < RR; ++r) {
-        if (r < nr) {
-            float mine = 0.0f;  // lane j keeps weight row j's sum
+    for (int j = 0; j < 8; ++j) {
+        float v = acc[j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = acc[j][r];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-                if (lane == j) mine = v;
-            }
-            if (lane < 8)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(base + 4u * (64 * r + 8 * warp + lane)), "f"(mine)
-                             : "memory");
-        }
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        if (lane == j) mine = v;
     }
+    if (lane < 8)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(leader_addr(smem_u32(&part[rank][8 * warp + lane]))), "f"(mine)
+                     : "memory");
     cluster_sync();
-    if (rank != 0 || warp >= nr) return;
-    float g = 0.0f, v = 0.0f;
+    if (rank != 0 || warp != 0) return;
+    float g = 0.0f, v = 0.0f, s0, s1;
 #pragma unroll
     for (int c = 0; c < FEW_CTAS; ++c) {
-        g += part[c][warp][lane];
-        v += part[c][warp][32 + lane];
+        g += part[c][lane];
+        v += part[c][32 + lane];
     }
-    const float h = silu_mul(g, v);
+    sigmoid2(g, 0.0f, s0, s1);
+    const float h = __fmul_rn(__fmul_rn(g, s0), v);
     const int e = mx_exponent_448(__uint_as_float(warp_absmax(h)));
-    p.out[(t + warp) * p.f + col + lane] = (uint8_t)cvt_e4m3x2_rn(__fmul_rn(h, exp2_neg(e)), 0.0f);
-    if (lane == 0) p.out_sc[(t + warp) * (p.f / 32) + col / 32] = (uint8_t)(e + 127);
+    p.out[t * p.f + col + lane] = (uint8_t)cvt_e4m3x2_rn(__fmul_rn(h, exp2_neg(e)), 0.0f);
+    if (lane == 0) p.out_sc[t * (p.f / 32) + col / 32] = (uint8_t)(e + 127);
 }
 
 // ====================================================================== host
@@ -1097,13 +1077,17 @@ pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, c
     if (!make_map(&ma, a, k, m, 128, BM) || !make_map(&mb, b, k, n, 128, BWD ? TBN / CT : TBN / 2) ||
         !make_map(&msa, a_scales, k / 32, m, 16, 32) || !make_map(&msb, b_scales, k / 32, n, 16, 32))
         return PMN_ERR_CUDA;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < CT)
-        return PMN_ERR_CUDA;
     auto kern = gated_kernel<MODE, TBN, CT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
-        return PMN_ERR_CUDA;
+    static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return PMN_ERR_CUDA;
+    int sms = dev < MAX_DEVICES ? sm_count[dev].load(std::memory_order_acquire) : 0;
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < CT ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+            return PMN_ERR_CUDA;
+        if (dev < MAX_DEVICES) sm_count[dev].store(sms, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms / CT * CT));
     cfg.blockDim = dim3(THREADS);
@@ -1170,14 +1154,19 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
                     pmn_wait_limit_ns()};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (out_t || y_out) return launch<TRAIN, 192, 2>(a, a_scales, b, b_scales, args, s);
-    switch (PMN_SERVE_KERNEL) {
-        case 3:
-            gated_rows_kernel<<<dim3((unsigned)(f / 32 * FEW_CTAS), (unsigned)total_rows), 256, 0, s>>>(a, a_scales, b, b_scales, args);
-            return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
-        case 1: return launch<SERVE, 192, 2>(a, a_scales, b, b_scales, args, s);
-        case 2: return launch<SERVE, 64, 1>(a, a_scales, b, b_scales, args, s);
-        default: return launch<SERVE, 192, 1>(a, a_scales, b, b_scales, args, s);
+    // Serving.  A few rows: one cluster per row and 32 columns (f 1536, k 4096: one
+    // row 4.7 us against 12.7 in 128-row tiles, four of one expert 10.9 against 12.7,
+    // eight 18.7 against 12.9, eight of eight experts 25.5 against 28.0).
+    if (total_rows <= 4 || (total_rows <= 8 && num_experts >= 8)) {
+        gated_rows_kernel<<<dim3((unsigned)(f / 32 * FEW_CTAS), (unsigned)total_rows), 256, 0, s>>>(a, a_scales, b,
+                                                                                                b_scales, args);
+        return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
     }
+    // 256-row tiles on CTA pairs load less per product, 128-row tiles waste less at
+    // the segments' ends (8192 rows of 8 experts 78 us paired, 83 single; of 24 experts
+    // 101 and 98).
+    if (total_rows >= 1024 * (int64_t)num_experts) return launch<SERVE, 192, 2>(a, a_scales, b, b_scales, args, s);
+    return launch<SERVE, 192, 1>(a, a_scales, b, b_scales, args, s);
 }
 
 extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
