@@ -224,6 +224,87 @@ class MXFP8Forward:
             f()
 
 
+class GatedBlockTrainStep:
+    """One training step of a pre-norm gated feed-forward block in MXFP8, from
+    the residual stream to the updated weights:
+      r = residual + x; xn = rmsnorm(r) * gamma          MXFP8 rows, bf16 xn for its transpose
+      h = silu(xn . Wg^T) * (xn . Wu^T)                   one kernel; MXFP8 of h and h^T, bf16 y
+      z = h . W2^T                                        the block's output (the next residual branch)
+      dY1 from dz, W2 and y                               one kernel; MXFP8 of dY1 and dY1^T
+      dW2 = dz^T . h, dW1 = dY1^T . xn, dxn = dY1 . W1    MXFP8 gradient GEMMs
+      dr, dgamma                                          norm backward; dr is also x's gradient
+      W1, W2, gamma                                       AdamW, states in 8 bits (or float32)
+    The weights are bf16 without float32 masters, updated with stochastic
+    rounding; they are quantised in both orientations every step.
+
+    residual [T, D] bf16 or float32 and x bf16 [T, D] are rows in expert order
+    (one expert: all tokens), w1 bf16 [E, 2F, D], w2 bf16 [E, D, F], gamma bf16
+    [D]; offsets device int32 [E+1], multiples of 128, 0 .. T.  T, D and F are
+    multiples of 512.  All buffers are allocated here; forward(), backward()
+    and update() only enqueue kernels on the current stream."""
+
+    def __init__(self, residual, w1, w2, gamma, offsets, mxfp8_states=True, lr=1e-3, weight_decay=0.1, seed=0):
+        E, F2, D = w1.shape
+        F, T, dev = F2 // 2, residual.shape[0], residual.device
+        if T % ALIGN_ROWS or D % 512 or F % 512 or w2.shape != (E, D, F) or residual.shape != (T, D):
+            raise ValueError("GatedBlockTrainStep: T, D and F are multiples of 512")
+        self.residual, self.w1, self.w2, self.gamma, self.offsets = residual, w1, w2, gamma, offsets
+        self.E, self.T, self.D, self.F = E, T, D, F
+        self.lr, self.weight_decay, self.seed, self.steps = lr, weight_decay, seed, 0
+        u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+
+        def e(*shape, dtype=u8):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        def mx(*shape):
+            return e(*shape), e(*shape[:-1], shape[-1] // 32)
+
+        self.w1q, self.w1t = mx(E, F2, D), mx(E, D, F2)
+        self.w2q, self.w2t = mx(E, D, F), mx(E, F, D)
+        self.r, self.xq, self.xn, self.rstd = torch.empty_like(residual), mx(T, D), e(T, D, dtype=bf16), e(T, dtype=f32)
+        self.xt = mx(D, T)
+        self.hq, self.ht, self.y = mx(T, F), mx(F, T), e(T, F2, dtype=bf16)
+        self.z = e(T, D, dtype=bf16)
+        self.dz_r, self.dz_t = mx(T, D), mx(D, T)
+        self.dy1, self.dy1_t = mx(T, F2), mx(F2, T)
+        self.dxn, self.dr = e(T, D, dtype=bf16), torch.empty_like(residual)
+        self.dx = e(T, D, dtype=bf16) if residual.dtype == f32 else None
+        self.dw1, self.dw2, self.dgamma = e(E, F2, D, dtype=f32), e(E, D, F, dtype=f32), e(D, dtype=f32)
+        self.ws = e(pmn.add_rmsnorm_backward_workspace_bytes(T, D))
+        params = [w1, w2, gamma]
+        self.m, self.v = pmn.adamw_states(params, mxfp8=mxfp8_states)
+        self.opt = pmn.AdamWTensors(params, [self.dw1, self.dw2, self.dgamma], self.m, self.v)
+
+    def forward(self, x):
+        """The block's output z (bf16 [T, D]) and the stream r that it is to be added to."""
+        P, E = pmn, self.E
+        for i in range(E):  # the transposes stay inside an expert's matrix
+            P.mxfp8_quantize_both(self.w1[i], out=(self.w1q[0][i], self.w1q[1][i]), out_t=(self.w1t[0][i], self.w1t[1][i]))
+            P.mxfp8_quantize_both(self.w2[i], out=(self.w2q[0][i], self.w2q[1][i]), out_t=(self.w2t[0][i], self.w2t[1][i]))
+        P.add_rmsnorm_mxfp8(x, self.residual, self.gamma, out=self.xq, res_out=self.r, y=self.xn, rstd=self.rstd)
+        P.w1_gemm_swiglu_mxfp8(self.xq, self.w1q, self.offsets, out=self.hq, out_t=self.ht, y=self.y)
+        P.gemm_mxfp8(self.hq[0], self.hq[1], self.w2q[0], self.w2q[1], self.offsets, P.GROUP_M, torch.bfloat16, out=self.z)
+        return self.z, self.r
+
+    def backward(self, dz, dres=None):
+        """Gradients from dz (bf16 [T, D], of z) and dres (of r): (dr, dW1, dW2, dgamma)."""
+        P = pmn
+        P.mxfp8_quantize_both(dz, out=self.dz_r, out_t=self.dz_t)
+        P.dh_gemm_swiglu_backward_mxfp8(self.dz_r, self.w2t, self.y, self.offsets, out=self.dy1, out_t=self.dy1_t)
+        P.gemm_mxfp8(self.dz_t[0], self.dz_t[1], self.ht[0], self.ht[1], self.offsets, P.GROUP_K, out=self.dw2)
+        P.gemm_mxfp8(self.dy1[0], self.dy1[1], self.w1t[0], self.w1t[1], self.offsets, P.GROUP_M, torch.bfloat16, out=self.dxn)
+        P.mxfp8_quantize(self.xn, transpose=True, out=self.xt)
+        P.gemm_mxfp8(self.dy1_t[0], self.dy1_t[1], self.xt[0], self.xt[1], self.offsets, P.GROUP_K, out=self.dw1)
+        P.add_rmsnorm_backward(self.dxn, self.r, self.rstd, self.gamma, dres=dres, dr=self.dr, dx=self.dx, dw=self.dgamma,
+                               workspace=self.ws)
+        return self.dr, self.dw1, self.dw2, self.dgamma
+
+    def update(self, grad_scale=None):
+        self.steps += 1
+        pmn.adamw_step(self.opt, self.lr, weight_decay=self.weight_decay, step=self.steps, seed=self.seed,
+                       grad_scale=grad_scale)
+
+
 def mxfp8_forward_algorithmic(real_rows, experts, d_model, d_ff):
     """(flops, algorithmic HBM bytes) of MXFP8Forward on the real routed rows:
     bf16 weights and X read once, their MXFP8 copies written and read once,
