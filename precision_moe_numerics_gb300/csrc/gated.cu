@@ -216,11 +216,20 @@ struct Cfg {
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
-    static constexpr int NR = 2 * (1 + RB);         // 32-row boxes of scales per scale-factor warp
-    static constexpr int RAW_SLOTS = CT == 2 ? 3 : 2, RAW_BYTES = NR * 512;  // groups of four stages in flight, per warp
+    // Scale-factor warp w has the boxes of 32 scale rows at words 2 w, 2 w + 1 of each
+    // block; a box holds RAW_W bytes of each row, a quarter as many stages' worth.
+    static constexpr int NR = 2 * (1 + RB);
+    static constexpr bool in_tile(int j, int w) { return j < 2 || 128 * (j / 2 - 1) + 32 * (2 * w + (j & 1)) < TBN; }
+    static constexpr int boxes(int w)
+    {
+        int n = 0;
+        for (int j = 0; j < NR; ++j) n += in_tile(j, w);
+        return n;
+    }
+    static constexpr int RAW_W = CT == 2 ? 32 : 16, RAW_SLOTS = 2, RAW_BOX = 32 * RAW_W;
     static constexpr int WARP_BYTES = MODE == SERVE ? 0 : WARP_BUF, GROUP_BYTES = MODE == SERVE ? 0 : 1024;
     static constexpr int SF_OFF = STAGES * STAGE_BYTES, WARP_OFF = SF_OFF + STAGES * SF_BYTES,
-                         RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + 2 * RAW_SLOTS * RAW_BYTES,
+                         RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + RAW_SLOTS * RAW_BOX * (boxes(0) + boxes(1)),
                          SCALE_OFF = BAR_OFF + 256, CUM_OFF = SCALE_OFF + 3 * GROUP_BYTES;
     static constexpr int SMEM_BYTES = 1024 + CUM_OFF + (MAX_GROUPS + 1) * 4;
     static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
@@ -535,9 +544,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, issued = 0, last = 0;
         int gc = 0;
         bool ok = true;
+        // first row of B that this CTA loads for a tile (single CTA: of the gate half)
+        auto b_row = [&](const Tile &ti) {
+            const int64_t br = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+            return CT == 1 || rank == 0 ? br : BWD ? br + TBN / 2 : br + p.f;
+        };
         for (int t = tile0; t < total && ok; t += tstep) {
             const Tile ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
-            const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+            const int32_t arow = (int32_t)ti.m0 + BM * rank, brow = (int32_t)b_row(ti);
             for (int ks = 0; ks < nks; ++ks) {
                 ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
                 if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
@@ -551,12 +565,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (rank == 0) mbar_arrive_expect_tx(fb, CT * (C::A_BYTES + C::B_BYTES));
                     if constexpr (CT == 2) {
                         // forward: the leader holds the gate rows, its peer the up rows
-                        const int64_t br = rank == 0 ? brow : BWD ? brow + TBN / 2 : brow + p.f;
-                        tma_load_2d_pair(st, &tmA, leader_addr(fb), x, (int32_t)ti.m0 + BM * rank);
-                        tma_load_2d_pair(st + C::A_BYTES, &tmB, leader_addr(fb), x, (int32_t)br);
+                        tma_load_2d_pair(st, &tmA, leader_addr(fb), x, arow);
+                        tma_load_2d_pair(st + C::A_BYTES, &tmB, leader_addr(fb), x, brow);
                     } else {
-                        tma_load_2d(st, &tmA, fb, x, (int32_t)ti.m0);
-                        tma_load_2d(st + C::A_BYTES, &tmB, fb, x, (int32_t)brow);
+                        tma_load_2d(st, &tmA, fb, x, arow);
+                        tma_load_2d(st + C::A_BYTES, &tmB, fb, x, brow);
                         if (!BWD) tma_load_2d(st + C::A_BYTES + C::B_BYTES / 2, &tmB, fb, x, (int32_t)(brow + p.f));
                     }
                 }
@@ -584,21 +597,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Block b (A, then the 128-row blocks of B), lane r, word j: the four
         // scale bytes of row 32 j + r of the stage's 128-deep K range.  Words 0, 1
         // are warp 2's, words 2, 3 warp 3's; both take part in every stage, as a
-        // wait tells one phase of a barrier from the next alone.  16 bytes of a row
-        // cover a group of four stages and come by TMA, RAW_SLOTS groups ahead, in
-        // boxes of 32 rows.  (Plain loads of 16 bytes from 32 rows each queue behind
-        // the epilogue's stores and held the MMAs up: a stage then took 850 clocks
-        // beside the epilogue, 600 without.)
-        const int groups4 = nks / 4;  // k is a multiple of 512
-        const int wr = __shfl_sync(0xFFFFFFFFu, warp, 0) - 2, w0 = 2 * wr;
-        const uint8_t *raw = smem + C::RAW_OFF + wr * C::RAW_SLOTS * C::RAW_BYTES;
-        const uint32_t raws = stages + C::RAW_OFF + wr * C::RAW_SLOTS * C::RAW_BYTES;
+        // wait tells one phase of a barrier from the next alone.  The rows come by TMA,
+        // two groups of RAW_W / 4 stages ahead, in boxes of 32 rows.  (Plain loads from
+        // 32 rows each queue behind the epilogue's stores and held the MMAs up; boxes of
+        // 16 bytes cost TMA as many requests per stage as B's tile, which a single CTA
+        // has no shared memory to avoid.)
+        const int per_tile = (nks + C::RAW_W / 4 - 1) / (C::RAW_W / 4);
+        const int wr = __shfl_sync(0xFFFFFFFFu, warp, 0) - 2;
+        const int boxes = wr ? C::boxes(1) : C::boxes(0), slot_bytes = boxes * C::RAW_BOX;
+        const int raw0 = C::RAW_OFF + wr * C::RAW_SLOTS * C::RAW_BOX * C::boxes(0);
         const uint32_t bar = bar_raw + 8 * C::RAW_SLOTS * wr;
-        constexpr auto in_tile = [](int j, int w) { return j < 2 || 128 * (j / 2 - 1) + 32 * (w + (j & 1)) < TBN; };
-        int boxes = 0;
-#pragma unroll
-        for (int j = 0; j < C::NR; ++j) boxes += in_tile(j, w0);
-        const int64_t tiles = tile0 < total ? (total - 1 - tile0) / tstep + 1 : 0, groups = tiles * groups4;
+        const int64_t tiles = tile0 < total ? (total - 1 - tile0) / tstep + 1 : 0, groups = tiles * per_tile;
         int64_t asked = 0;  // groups whose scales have been asked for
         int t = tile0, q = 0, gc = 0;
         Tile ti;
@@ -608,20 +617,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int slot = (int)(asked % C::RAW_SLOTS);
             const int32_t arow = (int32_t)ti.m0 + BM * rank;
             const int64_t brow = (int64_t)ti.g * (BWD ? p.f : 2 * p.f) + ti.h0;
+            uint32_t d = stages + raw0 + slot * slot_bytes;
             if (elect_one()) {
-                mbar_arrive_expect_tx(bar + 8 * slot, 512 * boxes);
+                mbar_arrive_expect_tx(bar + 8 * slot, slot_bytes);
 #pragma unroll
                 for (int j = 0; j < C::NR; ++j) {
-                    const uint32_t d = raws + slot * C::RAW_BYTES + 512 * j;
-                    const int n = 128 * (j / 2 - 1) + 32 * (w0 + (j & 1));  // row of B within the tile (j >= 2)
-                    if (j < 2) tma_load_2d(d, &tmSA, bar + 8 * slot, 16 * q, arow + 32 * (w0 + j));
-                    else if (in_tile(j, w0))
-                        tma_load_2d(d, &tmSB, bar + 8 * slot, 16 * q, (int32_t)(brow + n + (!BWD && n >= C::HB ? p.f - C::HB : 0)));
+                    const int n = 128 * (j / 2 - 1) + 32 * (2 * wr + (j & 1));  // row of B within the tile (j >= 2)
+                    if (j >= 2 && n >= TBN) continue;
+                    if (j < 2) tma_load_2d(d, &tmSA, bar + 8 * slot, C::RAW_W * q, arow + 32 * (2 * wr + j));
+                    else tma_load_2d(d, &tmSB, bar + 8 * slot, C::RAW_W * q, (int32_t)(brow + n + (!BWD && n >= C::HB ? p.f - C::HB : 0)));
+                    d += C::RAW_BOX;
                 }
             }
             __syncwarp();
             ++asked;
-            if (++q == groups4) {
+            if (++q == per_tile) {
                 q = 0;
                 t += tstep;
                 if (t < total) ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
@@ -631,42 +641,51 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, rslot = 0, rphase = 0;
         bool ok = true;
         int64_t g = 0;
+        int gq = 0;  // the group within its tile
         for (; g < groups && ok; ++g) {
             ok = warp_wait(bar + 8 * rslot, rphase, p.wait_ns);
             if (!ok) {
                 give_up();
                 break;
             }
-            uint4 v[C::NR];
-#pragma unroll
-            for (int j = 0; j < C::NR; ++j) {
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (in_tile(j, w0)) v[j] = *reinterpret_cast<const uint4 *>(raw + rslot * C::RAW_BYTES + 512 * j + 16 * lane);
-            }
+            const uint8_t *raw = smem + raw0 + rslot * slot_bytes + C::RAW_W * lane;
             if (++rslot == C::RAW_SLOTS) {
                 rslot = 0;
                 rphase ^= 1;
             }
+            const int halves = C::RAW_W == 16 || nks - 8 * gq == 4 ? 1 : 2;  // k is a multiple of 512
+            if (++gq == per_tile) gq = 0;
+            for (int half = 0; half < halves && ok; ++half) {
+                uint4 v[C::NR];
+                int box = 0;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                ok = ok && warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
-                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
-                    if (!ok) give_up();
-                    ok = false;
-                    break;
+                for (int j = 0; j < C::NR; ++j) {
+                    v[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j >= 2 && 128 * (j / 2 - 1) + 32 * (2 * wr + (j & 1)) >= TBN) continue;
+                    v[j] = *reinterpret_cast<const uint4 *>(raw + box * C::RAW_BOX + 16 * half);
+                    ++box;
                 }
-                uint2 *sf = reinterpret_cast<uint2 *>(smem + C::SF_OFF + stage * C::SF_BYTES) + 2 * lane + w0 / 2;
 #pragma unroll
-                for (int b = 0; b < 1 + C::RB; ++b) sf[64 * b] = make_uint2(u4_word(v[2 * b], s), u4_word(v[2 * b + 1], s));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CT == 2) mbar_arrive_leader(bar_full + 8 * stage);
-                    else mbar_arrive(bar_full + 8 * stage);
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                for (int s = 0; s < 4; ++s) {
+                    ok = ok && warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+                    if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
+                        if (!ok) give_up();
+                        ok = false;
+                        break;
+                    }
+                    uint2 *sf = reinterpret_cast<uint2 *>(smem + C::SF_OFF + stage * C::SF_BYTES) + 2 * lane + wr;
+#pragma unroll
+                    for (int b = 0; b < 1 + C::RB; ++b) sf[64 * b] = make_uint2(u4_word(v[2 * b], s), u4_word(v[2 * b + 1], s));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CT == 2) mbar_arrive_leader(bar_full + 8 * stage);
+                        else mbar_arrive(bar_full + 8 * stage);
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             // the slot may be refilled: what was read from it has been written on
@@ -1075,7 +1094,7 @@ pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, c
     const uint64_t k = (uint64_t)args.k, m = (uint64_t)args.m, n = (uint64_t)args.b_rows;
     CUtensorMap ma, mb, msa, msb;
     if (!make_map(&ma, a, k, m, 128, BM) || !make_map(&mb, b, k, n, 128, BWD ? TBN / CT : TBN / 2) ||
-        !make_map(&msa, a_scales, k / 32, m, 16, 32) || !make_map(&msb, b_scales, k / 32, n, 16, 32))
+        !make_map(&msa, a_scales, k / 32, m, C::RAW_W, 32) || !make_map(&msb, b_scales, k / 32, n, C::RAW_W, 32))
         return PMN_ERR_CUDA;
     auto kern = gated_kernel<MODE, TBN, CT>;
     static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
