@@ -8,6 +8,25 @@
 // float32 accumulators in TMEM); everything after them is done on the
 // accumulators, so y, h and dH never make a round trip through memory at a wider
 // type than the one they are kept in.
+//
+// Measured on one GB300 (d_model 4096, d_ff 1536; device time, weights and rows
+// larger than or streaming through L2), and what bounds it:
+//   forward, training, 8192 rows of 24 experts   102 us   2.0 PFLOP/s   62 us are HBM's; 8.2 rounds
+//                                                of 256-row tiles (6.7 without the segments' tails) take 9
+//   forward, training, 16384 rows of one expert  131 us   3.1 PFLOP/s   operand bytes into the SMs:
+//                                                28 KB per 128-deep stage at ~55 B a clock
+//   backward, 8192 rows of 24 experts             78 us   1.3 PFLOP/s   4.1 rounds take 5; as the next
+//   backward, 16384 rows of one expert           100 us   2.1 PFLOP/s   the epilogue beside the main loop:
+//                                                gate and up reads, code and scale stores and the
+//                                                column reduction cost 5 to 8 us each, together 25
+//   forward, serving, 512 rows of 24 experts      52 us   6.0 TB/s      HBM (46 us)
+//   forward, serving, one row                    4.7 us   2.8 TB/s      latency: a launch, two
+//                                                dependent reads, a cluster barrier
+// What the tiles and roles are for: 192 weight rows per tile leave TMEM room for two
+// accumulators beside the scale factors, so the epilogue of one tile runs while the
+// next is multiplied (256 rows with one accumulator: 143 / 112 / 206 us for the
+// training rows above but the second); two CTAs per 256-row tile load 28 KB per stage
+// and SM where one loads 40 KB (backward of 16384 rows 119 -> 101 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -103,9 +122,9 @@ __device__ __forceinline__ void tmem_dealloc_ct(uint32_t taddr, uint32_t ncols)
 // The tensor instructions are executed by whole warps in step and issued by one
 // lane, by a predicate inside the instruction (`el`: this is the lane): a branch
 // around them costs a reconvergence per stage, and a branch around the loop hides
-// from the compiler that their operands are warp-uniform (measured, clocks per
-// 128-deep stage that the issuing warp needs: loop in one lane 940, branch per stage
-// 510-600, this form see the kernel).
+// from the compiler that their operands are warp-uniform.  Clocks per 128-deep stage
+// that the issuing warp needs: the loop in one lane 940, a branch per stage 510 to
+// 600, this form 430 (the MMAs of a pair's stage take 384).
 
 // Arrives on `bar` (in both CTAs of a pair) once the issuing lane's tcgen05
 // operations so far have completed.
@@ -194,15 +213,15 @@ constexpr uint32_t TMEM_COLS = 512;
 // transposed (32 rows of 36 bytes each).
 constexpr int WARP_BUF = 4096, COL_BYTES = 32 * 36;
 
-// One tile: 128 routed rows of an expert (256 on a CTA pair) times TBN rows of its weight.  Forward:
-// TBN / 2 gate rows and the TBN / 2 up rows of the same columns of h; backward:
-// TBN columns of dH.  A stage holds 128 bytes of K of both operands (TMA,
-// 128-byte swizzle) and their scale factors in the 32 x 128-bit form that
-// tcgen05.cp copies into TMEM.
 // Forward for serving (h alone), forward for training (h^T and y where wanted),
 // backward.
 constexpr int SERVE = 0, TRAIN = 1, BACKWARD = 2;
 
+// One tile: 128 routed rows of an expert (CT = 2: 256 on a pair of CTAs) times TBN
+// rows of its weight.  Forward: TBN / 2 gate rows and the TBN / 2 up rows of the same
+// columns of h; backward: TBN columns of dH.  A stage holds 128 bytes of K of both
+// operands (TMA, 128-byte swizzle) and their scale factors in the 32 x 128-bit form
+// that tcgen05.cp copies into TMEM.
 template <int MODE, int TBN, int CT>
 struct Cfg {
     static constexpr bool BWD = MODE == BACKWARD;
@@ -272,6 +291,11 @@ __device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum,
 }
 
 __device__ __forceinline__ void latch_error(int bit) { atomicOr(&g_gated_error, bit); }
+
+// After a timeout a role still waits for its own copies and tensor operations in
+// flight, this long for each: they need microseconds, but a barrier that counts
+// another role's arrivals too may never complete.
+constexpr uint64_t DRAIN_NS = 100000000ull;
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
@@ -437,14 +461,13 @@ __device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], ui
     }
 }
 
-// One persistent kernel per call, one CTA per SM:
-//   warp 0     one lane loads the operands' code tiles by TMA
-//   warp 2     scale factors: 16 bytes of each row cover four stages; they are
-//              read a group of four stages ahead and written in the form that
-//              tcgen05.cp expects
-//   warp 1     one lane copies a stage's scale factors into TMEM and issues its
-//              MMAs (copies and MMAs of one thread execute in order)
-//   warps 4..  epilogue, one row per thread and 32 columns at a time
+// One persistent kernel per call, one CTA per SM (CT = 2: a pair per two SMs, whose
+// leader issues the MMAs of both):
+//   warp 0      loads the operands' code tiles by TMA
+//   warp 1      copies a stage's scale factors into TMEM and issues its MMAs (copies
+//               and MMAs of one lane execute in order)
+//   warps 2, 3  put the scale rows into the form that tcgen05.cp expects
+//   warps 4..   epilogue: a row per thread, 32 columns at a time
 // Every wait is bounded: on a timeout an error bit is latched and the CTA winds
 // down.
 template <int MODE, int TBN, int CT>
@@ -585,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // no copy may still be landing when the CTA ends; a pair's copies are
         // counted by its leader, and both CTAs end together
         for (int s = 0; s < STAGES; ++s)
-            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, (last >> s) & 1u, 1000000000ull);
+            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, (last >> s) & 1u, DRAIN_NS);
         if (CT == 2 && *(volatile int *)s_abort) {  // one side may have given up before the other: let copies land
             const uint64_t t0 = globaltimer();
             while (globaltimer() - t0 < 10000000ull) {
@@ -692,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (ok) fetch();
         }
         // copies that nobody will wait for may still be landing
-        for (; !ok && g < asked; ++g) (void)warp_wait(bar + 8 * (uint32_t)(g % C::RAW_SLOTS), (uint32_t)(g / C::RAW_SLOTS) & 1u, 1000000000ull);
+        for (; !ok && g < asked; ++g) (void)warp_wait(bar + 8 * (uint32_t)(g % C::RAW_SLOTS), (uint32_t)(g / C::RAW_SLOTS) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
         // The whole warp walks the loop, so that the operands of the tensor
@@ -744,7 +767,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (elect_one()) tc_commit_own<CT>(bar_drain);  // every tcgen05 operation of this warp has completed
             __syncwarp();
-            (void)warp_wait(bar_drain, 0, 1000000000ull);
+            (void)warp_wait(bar_drain, 0, DRAIN_NS);
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -810,7 +833,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_wait();
                     if (c == c1 - 1) release();
                     if (!on) continue;
-                    if (MODE == TRAIN && p.y) {  // y in bf16 for the backward pass, through shared memory: four lanes store a row's 64 bytes
+                    if (MODE == TRAIN && p.y) {
+                        // y in bf16 for the backward pass, through shared memory: four
+                        // lanes store a row's 64 bytes
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -862,6 +887,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_wait();
                     if (c == c1 - 1) release();
                     if (!on) continue;
+                    // The gate and up values leave the buffer before it is written again:
+                    // they are in the codes stored below.  (Copies by TMA overtook reads
+                    // that were still outstanding behind a warp barrier and even a
+                    // barrier's arrival; these copies are the lanes' own, in order.)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 gw = *reinterpret_cast<const uint4 *>(buf + piece64(lane, i));
@@ -897,7 +926,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         *reinterpret_cast<uint16_t *>(os - 1) = (uint16_t)rsc[0];
                         *reinterpret_cast<uint16_t *>(os + p.f / 32 - 1) = (uint16_t)rsc[1];
                     }
-                    __syncwarp();  // every lane has read its gate and up values: they went into the codes above
+                    __syncwarp();
                     uint8_t st[2];
                     uint8_t *qt = p.out_t + col * p.m + row0;
                     col_blocks<2>({&v, &u}, buf, {qt, qt + p.f * p.m}, p.m, st, lane);
@@ -989,6 +1018,8 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
         return;  // alike in every CTA
     }
     if (s_expert < 0) return;  // a row outside the segments: alike in the cluster
+    // the leader's memory is written below: every CTA of the cluster has to have begun
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int64_t wrow = (int64_t)s_expert * 2 * p.f + (warp >= 4 ? p.f : 0) + col + 8 * (warp & 3);
     const int64_t pitch = p.k / 32;
     const uint8_t *wp = b + wrow * p.k + 16 * lane, *wsp = sb + wrow * pitch + lane / 2;
@@ -1031,9 +1062,12 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         if (lane == j) mine = v;
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (lane < 8)
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(leader_addr(smem_u32(&part[rank][8 * warp + lane]))), "f"(mine)
                      : "memory");
+    __syncwarp();
     cluster_sync();
     if (rank != 0 || warp != 0) return;
     float g = 0.0f, v = 0.0f, s0, s1;
@@ -1079,7 +1113,8 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, u
     cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, box_w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              box_w == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

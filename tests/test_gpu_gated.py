@@ -130,6 +130,83 @@ def test_training_forward_and_backward(pmn, rows, offsets, f, d):
     check_backward(pmn, problem(rows, len(offsets) - 1, f, d, offsets, True, rows + 2))
 
 
+@pytest.mark.parametrize("rows,offsets", [(1, [0, 1]), (45, [0, 7, 45]), (300, [0, 0, 7, 135, 300]), (513, [0, 256, 256, 513])])
+def test_y_alone_on_ragged_segments(pmn, rows, offsets):
+    """y without h^T: any offsets, slices cut by a segment's end"""
+    a, b, _, off = problem(rows, len(offsets) - 1, 384, 512, offsets, False, rows + 5)
+    h, h_t, y = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(off).cuda(), want_y=True)
+    z, mass = product(a, b, off)
+    err = 512 * U * mass
+    assert h_t is None and (np.abs(f64(y) - z) <= 2.0 ** -8 * np.abs(z) + 2 * err).all()
+    g, u, eg, eu = z[:, :384], z[:, 384:], err[:, :384], err[:, 384:]
+    s = sigmoid(g)
+    eh = np.abs(u) * 1.1 * eg + np.abs(g * s) * eu + eg * eu + np.abs(g * s * u) * ((np.abs(g) + 8) * 2.0 ** -23 + 8 * U)
+    mx64.check_rn_abs(h[0].cpu().numpy(), h[1].cpu().numpy(), g * s * u, eh, "h")
+
+
+def test_outputs_at_every_alignment(pmn):
+    """16-byte aligned codes and byte-aligned scales: the wide stores give way to narrow ones, with the same bytes"""
+    off = [0, 128, 256]
+    fr, br = (problem(256, 2, 384, 512, off, bwd, 41 + bwd) for bwd in (False, True))
+    a, b, o = cuda(fr[0]), cuda(fr[1]), torch.from_numpy(fr[3]).cuda()
+    c, w, y = cuda(br[0]), cuda(br[1]), br[2].cuda()
+
+    def shifted(rows, cols):
+        q = torch.zeros((rows * cols + 64,), dtype=torch.uint8, device="cuda")[16:16 + rows * cols].view(rows, cols)
+        sc = torch.zeros((rows * cols // 32 + 8,), dtype=torch.uint8, device="cuda")[1:1 + rows * cols // 32]
+        return q, sc.view(rows, cols // 32)
+
+    want = pmn.w1_gemm_swiglu_mxfp8(a, b, o, want_t=True)
+    got = pmn.w1_gemm_swiglu_mxfp8(a, b, o, out=shifted(256, 384), out_t=shifted(384, 256))
+    wb = pmn.dh_gemm_swiglu_backward_mxfp8(c, w, y, o)
+    gb = pmn.dh_gemm_swiglu_backward_mxfp8(c, w, y, o, out=shifted(256, 768), out_t=shifted(768, 256))
+    for x, z in zip(want[:2] + wb, got[:2] + gb):
+        assert torch.equal(x[0], z[0]) and torch.equal(x[1], z[1])
+    assert pmn.get_device_error() == 0
+
+
+@pytest.mark.parametrize("which", ["serve", "train", "backward"])
+def test_a_wait_that_runs_out_is_reported(pmn, which):
+    """with no time to wait the call returns, latches the timeout at most, and the next call is right"""
+    off = [0, 256, 512]
+    a, b, y, o = problem(512, 2, 384, 512, off, which == "backward", 61)
+    a, b, o, y = cuda(a), cuda(b), torch.from_numpy(o).cuda(), y.cuda() if which == "backward" else None
+
+    def call():
+        if which == "backward":
+            return pmn.dh_gemm_swiglu_backward_mxfp8(a, b, y, o)
+        r = pmn.w1_gemm_swiglu_mxfp8(a, b, o, want_t=which == "train", want_y=which == "train")
+        return r[:2] if which == "train" else r[:1]
+
+    want = call()
+    assert pmn.get_device_error() == 0
+    limit = pmn.set_wait_limit_ns(0)
+    try:
+        call()
+        torch.cuda.synchronize()
+        assert pmn.get_device_error() in (0, pmn.DEVERR_WAIT_TIMEOUT)
+    finally:
+        pmn.set_wait_limit_ns(limit)
+    for x, z in zip(want, call()):
+        assert torch.equal(x[0], z[0]) and torch.equal(x[1], z[1])
+    assert pmn.get_device_error() == 0
+
+
+def test_a_few_rows_and_many_agree(pmn):
+    """the kernel for a handful of rows and the tiles: their float32 sums differ, their codes by one at most"""
+    a, b, _, _ = problem(8, 9, 256, 2048, [0] * 10, False, 51)
+    few = np.array([0, 1, 1, 3, 3, 4, 6, 6, 8, 8], np.int32)
+    h, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(few).cuda())
+    wide = (np.concatenate([a[0], np.zeros((8, 2048), np.uint8)]), np.concatenate([a[1], np.zeros((8, 64), np.uint8)]))
+    many, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(wide), cuda(b), torch.from_numpy(few).cuda())
+    same = (h[1] == many[1][:8]).cpu().numpy()
+    assert same.mean() > 0.99
+    d = np.abs(mx64.E4M3[h[0].cpu().numpy()] - mx64.E4M3[many[0][:8].cpu().numpy()])
+    v = np.abs(mx64.E4M3[h[0].cpu().numpy()])
+    assert (d <= np.maximum(v / 4, 2.0 ** -8))[np.repeat(same, 32, axis=1)].all()
+    assert pmn.get_device_error() == 0
+
+
 def test_long_contraction_and_many_tiles(pmn):
     """K = 4096 and more tiles than SMs, so every CTA runs several and both accumulators come round"""
     off = [0, 640, 640, 1536, 2688]
