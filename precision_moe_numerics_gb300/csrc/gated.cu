@@ -9,16 +9,17 @@
 // accumulators, so y, h and dH never make a round trip through memory at a wider
 // type than the one they are kept in.
 //
-// Measured on one GB300 (d_model 4096, d_ff 1536; device time, weights and rows
-// larger than or streaming through L2), and what bounds it:
-//   forward, training, 8192 rows of 24 experts   102 us   2.0 PFLOP/s   62 us are HBM's; 8.2 rounds
-//                                                of 256-row tiles (6.7 without the segments' tails) take 9
-//   forward, training, 16384 rows of one expert  131 us   3.1 PFLOP/s   operand bytes into the SMs:
-//                                                28 KB per 128-deep stage at ~55 B a clock
-//   backward, 8192 rows of 24 experts             78 us   1.3 PFLOP/s   4.1 rounds take 5; as the next
-//   backward, 16384 rows of one expert           100 us   2.1 PFLOP/s   the epilogue beside the main loop:
+// Measured on one GB300 (d_model 4096, d_ff 1536; device time, operands larger than L2
+// or streaming through it), and what bounds it:
+//   forward, training, 8192 rows of 24 experts    97 us   2.1 PFLOP/s   8.2 rounds of 256-row tiles
+//                                                (6.7 without the segments' ends) take 9;
+//                                                the bytes alone 62 us
+//   forward, serving, 16384 rows of one expert   120 us   3.4 PFLOP/s   the tensor pipe: 430 clocks a stage,
+//                                                of which 384 are MMAs, plus the ends of 14 rounds
+//   backward, 8192 rows of 24 experts             73 us   1.4 PFLOP/s   4.1 rounds take 5; as the next
+//   backward, 16384 rows of one expert            93 us   2.2 PFLOP/s   the epilogue beside the main loop:
 //                                                gate and up reads, code and scale stores and the
-//                                                column reduction cost 5 to 8 us each, together 25
+//                                                column reduction cost 4 to 7 us each
 //   forward, serving, 512 rows of 24 experts      52 us   6.0 TB/s      HBM (46 us)
 //   forward, serving, one row                    4.7 us   2.8 TB/s      latency: a launch, two
 //                                                dependent reads, a cluster barrier
@@ -205,12 +206,10 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 constexpr int BM = 128;  // rows per CTA
 constexpr int MAX_GROUPS = 1024;
 constexpr int MAX_DEVICES = 64;
-constexpr int EW = 12;                      // epilogue warps, three per TMEM lane quadrant
-constexpr int THREADS = 128 + 32 * EW;
 constexpr uint32_t TMEM_COLS = 512;
-// An epilogue warp's shared memory: 32 rows x 32 columns of bf16 gate and up
-// (2 x 2 KB), and, once those are in registers, two blocks that are being
-// transposed (32 rows of 36 bytes each).
+// An epilogue warp's shared memory.  Backward: 32 rows x 32 columns of bf16 gate and
+// up (2 x 2 KB), and, once those are in registers, two blocks that are being
+// transposed (32 rows of 36 bytes each).  Forward for training: one such block.
 constexpr int WARP_BUF = 4096, COL_BYTES = 32 * 36;
 
 // Forward for serving (h alone), forward for training (h^T and y where wanted),
@@ -226,17 +225,28 @@ template <int MODE, int TBN, int CT>
 struct Cfg {
     static constexpr bool BWD = MODE == BACKWARD;
     static constexpr int HB = BWD ? TBN : TBN / 2;  // columns of h (dH) per tile
-    static constexpr int NCH = HB / 32;             // 32-column chunks (MX blocks) of the epilogue
-    static constexpr int CPW = (NCH + 2) / 3;       // consecutive chunks per epilogue warp
+    // Epilogue warps: GR per quarter of the rows.  No more than keep up with the main
+    // loop, whose loads their stores get in the way of (training forward of 8192 rows:
+    // 12 warps 101.5 us, 4 warps 100.4; backward of 8192 and 16384 rows: 12 warps 77.3
+    // and 99.4, 8 warps 74.8 and 95.6).  Serving stores little, and with few tiles the
+    // epilogue's latency counts.
+    static constexpr int EW = BWD ? 8 : MODE == TRAIN ? 4 : 12, GR = EW / 4, THREADS = 128 + 32 * EW;
+    static constexpr int NCH = HB / 32;              // 32-column chunks (MX blocks) of the epilogue
+    static constexpr int CPW = NCH / GR;             // consecutive chunks per epilogue warp
     static constexpr int RB = (TBN + 127) / 128;    // 128-row scale blocks of B
     static constexpr int A_BYTES = BM * 128, B_BYTES = TBN / CT * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, SF_BYTES = 512 * (1 + RB);
-    static constexpr int STAGES = MODE == SERVE && CT == 2 ? 6 : 5;
+    // Stages in flight, as many as fit (training forward of 8192 rows: 4 stages 115 us,
+    // 5 101.5, 6 99.7; a seventh and sixth at the price of RAW_W = 16 lose more).
+    static constexpr int STAGES = CT == 2 && !BWD ? 6 : 5;
     static constexpr uint32_t SF_COLS = 4 * (1 + RB);
     static constexpr int ACC = 2 * TBN + STAGES * (int)SF_COLS <= (int)TMEM_COLS ? 2 : 1;  // accumulators
     static constexpr uint32_t SF_COL0 = ACC * TBN;
     // Scale-factor warp w has the boxes of 32 scale rows at words 2 w, 2 w + 1 of each
     // block; a box holds RAW_W bytes of each row, a quarter as many stages' worth.
+    // A row of a box costs TMA about as much as 128 bytes of a tile, so the boxes are as
+    // wide as fits (training forward of 8192 rows: 16 bytes 103 us, 32 98.0, 64 96.5;
+    // copied by the lanes with cp.async instead 101; with 512 rows 63 for 52).
     static constexpr int NR = 2 * (1 + RB);
     static constexpr bool in_tile(int j, int w) { return j < 2 || 128 * (j / 2 - 1) + 32 * (2 * w + (j & 1)) < TBN; }
     static constexpr int boxes(int w)
@@ -245,14 +255,18 @@ struct Cfg {
         for (int j = 0; j < NR; ++j) n += in_tile(j, w);
         return n;
     }
-    static constexpr int RAW_W = CT == 2 ? 32 : 16, RAW_SLOTS = 2, RAW_BOX = 32 * RAW_W;
-    static constexpr int WARP_BYTES = MODE == SERVE ? 0 : WARP_BUF, GROUP_BYTES = MODE == SERVE ? 0 : 1024;
+    static constexpr int RAW_W = CT == 2 ? 64 : 16, RAW_SLOTS = 2, RAW_BOX = 32 * RAW_W;
+    static constexpr int WARP_BYTES = BWD ? WARP_BUF : MODE == TRAIN ? COL_BYTES : 0;
+    // column scales that a group of four warps collects: two buffers of 128 bytes per
+    // block and chunk
+    static constexpr int GROUP_BYTES = MODE == SERVE ? 0 : 2 * 128 * CPW * (BWD ? 2 : 1);
     static constexpr int SF_OFF = STAGES * STAGE_BYTES, WARP_OFF = SF_OFF + STAGES * SF_BYTES,
                          RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + RAW_SLOTS * RAW_BOX * (boxes(0) + boxes(1)),
-                         SCALE_OFF = BAR_OFF + 256, CUM_OFF = SCALE_OFF + 3 * GROUP_BYTES;
-    static constexpr int SMEM_BYTES = 1024 + CUM_OFF + (MAX_GROUPS + 1) * 4;
+                         SCALE_OFF = BAR_OFF + 224, CUM_OFF = SCALE_OFF + GR * GROUP_BYTES;
+    static constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
+    static_assert(NCH % GR == 0 && HB % 32 == 0, "chunks per warp");
     static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
-    static_assert(8 * (2 * STAGES + 8 + 2 * RAW_SLOTS) + 16 <= 256, "barrier space");
+    static_assert(8 * (2 * STAGES + 8 + 2 * RAW_SLOTS) + 16 <= 224, "barrier space");
     static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -264,8 +278,8 @@ struct Args {
     int64_t b_rows;          // rows of B of all experts
     uint8_t *out, *out_sc, *out_t, *out_t_sc;
     uint16_t *y;             // forward: written (or NULL); backward: read
-    bool wide;               // out is 32-byte aligned
-    bool pairs, words;       // alignment lets two row scales, four column scales be stored at once
+    bool wide, wide_y;       // out, y are 32-byte aligned
+    bool words;              // alignment lets four column scales be stored at once
     uint64_t wait_ns;
 };
 
@@ -471,15 +485,18 @@ __device__ __forceinline__ void col_blocks(const float (*const (&v)[NB])[32], ui
 // Every wait is bounded: on a timeout an error bit is latched and the CTA winds
 // down.
 template <int MODE, int TBN, int CT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
     gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p)
 {
     using C = Cfg<MODE, TBN, CT>;
     constexpr bool BWD = MODE == BACKWARD;
     constexpr int STAGES = C::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // TMA and descriptors: 1024-byte swizzle atoms
+    // the compiler is kept from knowing the address: with it the MMA loop's operands are
+    // formed by a longer chain (forward of 16384 rows 123 -> 132 us)
+    uint8_t *smem = smem_raw;
+    asm volatile("" : "+l"(smem));
     const uint32_t stages = smem_u32(smem);
     const uint32_t bar_full = stages + C::BAR_OFF, bar_empty = bar_full + 8 * STAGES;
     const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16;
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, CT * EW);
+            mbar_init(bar_acc_empty + 8 * b, CT * C::EW);
         }
         mbar_init(bar_drain, 1);
         for (int g = 0; g < 3; ++g) mbar_init(bar_group + 8 * g, 4);
@@ -622,9 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // are warp 2's, words 2, 3 warp 3's; both take part in every stage, as a
         // wait tells one phase of a barrier from the next alone.  The rows come by TMA,
         // two groups of RAW_W / 4 stages ahead, in boxes of 32 rows.  (Plain loads from
-        // 32 rows each queue behind the epilogue's stores and held the MMAs up; boxes of
-        // 16 bytes cost TMA as many requests per stage as B's tile, which a single CTA
-        // has no shared memory to avoid.)
+        // 32 rows each queue behind the epilogue's stores and held the MMAs up.)
         const int per_tile = (nks + C::RAW_W / 4 - 1) / (C::RAW_W / 4);
         const int wr = __shfl_sync(0xFFFFFFFFu, warp, 0) - 2;
         const int boxes = wr ? C::boxes(1) : C::boxes(0), slot_bytes = boxes * C::RAW_BOX;
@@ -648,7 +663,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int n = 128 * (j / 2 - 1) + 32 * (2 * wr + (j & 1));  // row of B within the tile (j >= 2)
                     if (j >= 2 && n >= TBN) continue;
                     if (j < 2) tma_load_2d(d, &tmSA, bar + 8 * slot, C::RAW_W * q, arow + 32 * (2 * wr + j));
-                    else tma_load_2d(d, &tmSB, bar + 8 * slot, C::RAW_W * q, (int32_t)(brow + n + (!BWD && n >= C::HB ? p.f - C::HB : 0)));
+                    else
+                        tma_load_2d(d, &tmSB, bar + 8 * slot, C::RAW_W * q,
+                                    (int32_t)(brow + n + (!BWD && n >= C::HB ? p.f - C::HB : 0)));
                     d += C::RAW_BOX;
                 }
             }
@@ -676,16 +693,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 rslot = 0;
                 rphase ^= 1;
             }
-            const int halves = C::RAW_W == 16 || nks - 8 * gq == 4 ? 1 : 2;  // k is a multiple of 512
+            const int parts = min(C::RAW_W / 16, nks / 4 - C::RAW_W / 16 * gq);  // k is a multiple of 512
             if (++gq == per_tile) gq = 0;
-            for (int half = 0; half < halves && ok; ++half) {
+            for (int part = 0; part < parts && ok; ++part) {
                 uint4 v[C::NR];
                 int box = 0;
 #pragma unroll
                 for (int j = 0; j < C::NR; ++j) {
                     v[j] = make_uint4(0u, 0u, 0u, 0u);
                     if (j >= 2 && 128 * (j / 2 - 1) + 32 * (2 * wr + (j & 1)) >= TBN) continue;
-                    v[j] = *reinterpret_cast<const uint4 *>(raw + box * C::RAW_BOX + 16 * half);
+                    v[j] = *reinterpret_cast<const uint4 *>(raw + box * C::RAW_BOX + 16 * part);
                     ++box;
                 }
 #pragma unroll
@@ -715,7 +732,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (ok) fetch();
         }
         // copies that nobody will wait for may still be landing
-        for (; !ok && g < asked; ++g) (void)warp_wait(bar + 8 * (uint32_t)(g % C::RAW_SLOTS), (uint32_t)(g / C::RAW_SLOTS) & 1u, DRAIN_NS);
+        for (; !ok && g < asked; ++g)
+            (void)warp_wait(bar + 8 * (uint32_t)(g % C::RAW_SLOTS), (uint32_t)(g / C::RAW_SLOTS) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
         // The whole warp walks the loop, so that the operands of the tensor
@@ -775,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31 of CPW chunks of
         // 32 columns in a row.
         const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0);  // warp-uniform, and known to be
-        const int quad = wu & 3, c0 = ((wu - 4) >> 2) * C::CPW, c1 = min(c0 + C::CPW, C::NCH);
+        const int quad = wu & 3, c0 = ((wu - 4) >> 2) * C::CPW, c1 = c0 + C::CPW;
         uint8_t *buf = smem + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
         const uint32_t bufs = stages + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
         const int pr = lane >> 2, pi = lane & 3;  // four lanes cover a row's 64 bytes of y
@@ -785,10 +803,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int group = (wu - 4) >> 2;
         uint8_t *const sscale0 = smem + C::SCALE_OFF + group * C::GROUP_BYTES;
         uint32_t collected = 0;
-        uint32_t rsc[2] = {0u, 0u};
         uint32_t abuf = 0, aphase = 0;
         int gc = 0;
-        bool ok = true;
+        bool ok = true, have = false;  // have: the tile's first gate and up values have been asked for
         // backward: copies gate and up of 32 rows x 32 columns into the buffer
         auto fetch_y = [&](int64_t row0, int64_t col) {
             const uint16_t *g = p.y + (row0 + pr) * 2 * p.f + col + 8 * pi;
@@ -805,8 +822,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool valid = row < ti.row_end, any = row0 < ti.row_end;
             const int64_t tile_row = ti.m0 + BM * rank;
             const bool words = MODE != SERVE && p.words && tile_row % 128 == 0 && tile_row + BM <= ti.row_end;
-            uint8_t *const sscale = sscale0 + 512 * (collected & 1u);
-            if (BWD && any && ti.h0 + 32 * c0 < p.f) fetch_y(row0, ti.h0 + 32 * c0);  // lands while the MMAs run
+            uint8_t *const sscale = sscale0 + C::GROUP_BYTES / 2 * (collected & 1u);
+            // The next tile's first gate and up values are asked for once this tile's
+            // last ones have been used.
+            bool has_next = false;
+            int64_t next_row0 = 0, next_col = 0;
+            if (BWD) {
+                if (!have && any && ti.h0 + 32 * c0 < p.f) fetch_y(row0, ti.h0 + 32 * c0);
+                have = false;
+                if (t + tstep < total) {
+                    int g2 = gc;
+                    const Tile tn = get_tile<MODE, TBN, CT>(t + tstep, p, s_cum, g2);
+                    next_row0 = tn.m0 + BM * rank + 32 * quad;
+                    next_col = tn.h0 + 32 * c0;
+                    has_next = next_row0 < tn.row_end && next_col < p.f;
+                    have = has_next && any && ti.h0 + 32 * c0 < p.f;
+                }
+            }
             ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
@@ -819,7 +851,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     else mbar_arrive(bar_acc_empty + 8 * abuf);
                 }
             };
-            if (c0 >= c1) release();
 #pragma unroll 1
             for (int c = c0; c < c1; ++c) {
                 const int64_t col = ti.h0 + 32 * c;
@@ -833,34 +864,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_wait();
                     if (c == c1 - 1) release();
                     if (!on) continue;
-                    if (MODE == TRAIN && p.y) {
-                        // y in bf16 for the backward pass, through shared memory: four
-                        // lanes store a row's 64 bytes
+                    if (MODE == TRAIN && p.y && valid) {
+                        // y in bf16 for the backward pass, whole sectors straight from
+                        // the row's thread (through shared memory, four lanes to a row's
+                        // 64 bytes: the same time, and a stage's worth of memory)
+                        uint16_t *o = p.y + row * 2 * p.f + col;
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                        for (int h = 0; h < 4; ++h) {
+                            const float *x = (h & 2 ? u : v) + 16 * (h & 1);
+                            uint32_t w[8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float *x = (part ? u : v) + 8 * j + 2 * i;
-                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
-                                    w[i] = *reinterpret_cast<const uint32_t *>(&b2);
-                                }
-                                *reinterpret_cast<uint4 *>(buf + part * (WARP_BUF / 2) + piece64(lane, j)) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int i = 0; i < 8; ++i) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&b2);
                             }
-                        __syncwarp();
-                        uint16_t *o = p.y + (row0 + pr) * 2 * p.f + col + 8 * pi;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (row0 + pr + 8 * i < ti.row_end) {
-                                const uint8_t *b8 = buf + piece64(pr + 8 * i, pi);
-                                *reinterpret_cast<uint4 *>(o + 16 * i * p.f) = *reinterpret_cast<const uint4 *>(b8);
-                                *reinterpret_cast<uint4 *>(o + 16 * i * p.f + p.f) =
-                                    *reinterpret_cast<const uint4 *>(b8 + WARP_BUF / 2);
-                            }
-                        __syncwarp();
+                            const uint4 y2[2] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+                            store32(reinterpret_cast<uint8_t *>(o + (h & 2 ? p.f : 0) + 16 * (h & 1)), y2, p.wide_y);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
@@ -915,17 +935,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint8_t *os = p.out_sc + row * (f2 / 32) + col / 32;
                     row_block(v, q, sc);
                     store32(p.out + row * f2 + col, q, p.wide);
-                    rsc[0] = (rsc[0] >> 8) | ((uint32_t)sc << 8);
+                    os[0] = sc;
                     row_block(u, q, sc);
                     store32(p.out + row * f2 + p.f + col, q, p.wide);
-                    rsc[1] = (rsc[1] >> 8) | ((uint32_t)sc << 8);
-                    if (!p.pairs) {
-                        os[0] = (uint8_t)(rsc[0] >> 8);
-                        os[p.f / 32] = (uint8_t)(rsc[1] >> 8);
-                    } else if (c > c0) {  // (c0 and f / 32 are even)
-                        *reinterpret_cast<uint16_t *>(os - 1) = (uint16_t)rsc[0];
-                        *reinterpret_cast<uint16_t *>(os + p.f / 32 - 1) = (uint16_t)rsc[1];
-                    }
+                    os[p.f / 32] = sc;
                     __syncwarp();
                     uint8_t st[2];
                     uint8_t *qt = p.out_t + col * p.m + row0;
@@ -939,19 +952,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ot[p.f * (p.m / 32)] = st[1];
                     }
                     if (c + 1 < c1 && col + 32 < p.f) fetch_y(row0, col + 32);  // the blocks above have been read
+                    else if (has_next) fetch_y(next_row0, next_col);
                 }
             }
-            if (words && c0 < C::NCH) {
+            if (words) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_group + 8 * group);
                 ok = warp_wait(bar_group + 8 * group, collected & 1u, p.wait_ns);
                 if (!ok) break;
                 ++collected;
                 constexpr int NOUT = BWD ? 2 : 1;  // slot: chunk and (backward) gate or up
-                const int64_t col = ti.h0 + 32 * (c0 + quad / NOUT) + lane;
-                if (quad < C::CPW * NOUT && col < p.f)
-                    *reinterpret_cast<uint32_t *>(p.out_t_sc + (col + (quad % NOUT) * p.f) * (p.m / 32) + tile_row / 32) =
-                        *reinterpret_cast<const uint32_t *>(sscale + 128 * quad + 4 * lane);
+                for (int s = quad; s < C::CPW * NOUT; s += 4) {
+                    const int64_t col = ti.h0 + 32 * (c0 + s / NOUT) + lane;
+                    if (col < p.f)
+                        *reinterpret_cast<uint32_t *>(p.out_t_sc + (col + (s % NOUT) * p.f) * (p.m / 32) + tile_row / 32) =
+                            *reinterpret_cast<const uint32_t *>(sscale + 128 * s + 4 * lane);
+                }
             }
             if (++abuf == C::ACC) {
                 abuf = 0;
@@ -1144,7 +1160,7 @@ pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, c
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms / CT * CT));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1204,7 +1220,7 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
     if (!out || !out_scales || !aligned16(out) || !aligned16(out_t) || !aligned16(y_out)) return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, f, k, (int64_t)num_experts * 2 * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(y_out), aligned(out, 32),
-                    aligned(out_scales, 2), out_t && total_rows % 128 == 0 && aligned(out_t_scales, 4),
+                    aligned(y_out, 32), out_t && total_rows % 128 == 0 && aligned(out_t_scales, 4),
                     pmn_wait_limit_ns()};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (out_t || y_out) return launch<TRAIN, 192, 2>(a, a_scales, b, b_scales, args, s);
@@ -1236,6 +1252,6 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_mxfp8(const uint8_t *a, const 
         return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, f, k, (int64_t)num_experts * f,
                     out, out_scales, out_t, out_t_scales, static_cast<uint16_t *>(const_cast<void *>(y)), aligned(out, 32),
-                    aligned(out_scales, 2), total_rows % 128 == 0 && aligned(out_t_scales, 4), pmn_wait_limit_ns()};
+                    aligned(y, 32), total_rows % 128 == 0 && aligned(out_t_scales, 4), pmn_wait_limit_ns()};
     return launch<BACKWARD, 192, 2>(a, a_scales, b, b_scales, args, reinterpret_cast<cudaStream_t>(stream));
 }
