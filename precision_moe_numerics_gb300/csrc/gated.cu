@@ -1225,17 +1225,19 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (out_t || y_out) return launch<TRAIN, 192, 2>(a, a_scales, b, b_scales, args, s);
     // Serving.  A few rows: one cluster per row and 32 columns (f 1536, k 4096: one
-    // row 4.7 us against 12.7 in 128-row tiles, four of one expert 10.9 against 12.7,
-    // eight 18.7 against 12.9, eight of eight experts 25.5 against 28.0).
+    // row 4.7 us against 12.1 in tiles, four of one expert 10.9 against 12.1, eight 18.7
+    // against 12.1, eight of eight experts 25.5 against 28.0).
     if (total_rows <= 4 || (total_rows <= 8 && num_experts >= 8)) {
         gated_rows_kernel<<<dim3((unsigned)(f / 32 * FEW_CTAS), (unsigned)total_rows), 256, 0, s>>>(a, a_scales, b,
                                                                                                 b_scales, args);
         return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
     }
     // 256-row tiles on CTA pairs load less per product, 128-row tiles waste less at
-    // the segments' ends (8192 rows of 8 experts 78 us paired, 83 single; of 24 experts
-    // 101 and 98).
-    if (total_rows >= 1024 * (int64_t)num_experts) return launch<SERVE, 192, 2>(a, a_scales, b, b_scales, args, s);
+    // the segments' ends.  Paired and single, us: one expert 64 rows 12.2 and 13.0, 16384
+    // rows 119 and 141; 8 experts 8192 rows 73.5 and 83.6, 3000 rows 40.4 and 36.7; 24
+    // experts 32768 rows 267 and 308, 8192 rows 96.2 and 96.8, 512 rows 61 and 52.5.
+    if (num_experts == 1 || total_rows >= 1024 * (int64_t)num_experts)
+        return launch<SERVE, 192, 2>(a, a_scales, b, b_scales, args, s);
     return launch<SERVE, 192, 1>(a, a_scales, b, b_scales, args, s);
 }
 
