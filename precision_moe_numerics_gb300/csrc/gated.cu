@@ -21,7 +21,7 @@
 //                                                gate and up reads, code and scale stores and the
 //                                                column reduction cost 4 to 7 us each
 //   forward, serving, 512 rows of 24 experts      52 us   6.0 TB/s      HBM (46 us)
-//   forward, serving, one row                    4.7 us   2.8 TB/s      latency: a launch, two
+//   forward, serving, one row                    4.3 us   3.0 TB/s      latency: a launch, two
 //                                                dependent reads, a cluster barrier
 // What the tiles and roles are for: 192 weight rows per tile leave TMEM room for two
 // accumulators beside the scale factors, so the epilogue of one tile runs while the
@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_ctas()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 
@@ -990,12 +997,14 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
 // ---------------------------------------------------------------- few rows
 // The forward for a handful of rows (single tokens of a serving loop): its time is
 // that of reading the weights, which 128-row tiles would spread over a dozen SMs.
-// A cluster of four CTAs takes 32 columns of h for one row, each CTA a quarter of K
+// A cluster of 1 to 8 CTAs takes 32 columns of h for one row, each CTA a share of K
 // in units of 512; a warp holds 8 of the 64 weight rows, a lane 16 consecutive codes
 // of each (512 bytes per warp load), multiplied in float32 and scaled once per half
-// block.  The four partial sums meet in the leader's shared memory.  Rows of one
-// expert share its weights through L2 only.
-constexpr int FEW_CTAS = 4;
+// block.  The partial sums meet in the leader's shared memory.  Rows of one expert
+// share its weights through L2 only.  Bound by latency for one row, by the decoding
+// and multiplying for more (three CTAs per SM: 80 registers; two with more loads in
+// flight are slower).
+constexpr int FEW_CTAS = 8;  // at most
 
 // 16 E4M3 codes -> float32
 __device__ __forceinline__ void decode16(const uint4 &q, float (&v)[16])
@@ -1010,16 +1019,15 @@ __device__ __forceinline__ void decode16(const uint4 &q, float (&v)[16])
     }
 }
 
-__global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
-    gated_rows_kernel(const uint8_t *__restrict__ a, const uint8_t *__restrict__ sa, const uint8_t *__restrict__ b,
+__global__ void __launch_bounds__(256, 3) gated_rows_kernel(const uint8_t *__restrict__ a, const uint8_t *__restrict__ sa, const uint8_t *__restrict__ b,
                       const uint8_t *__restrict__ sb, const Args p)
 {
     __shared__ float part[FEW_CTAS][64];  // the leader's: gate sums 0 .. 31, up sums 32 .. 63
     __shared__ int s_expert;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
+    const int rank = (int)cluster_rank(), ctas = (int)cluster_ctas();
     const int64_t t = blockIdx.y;
-    const int64_t col = 32 * (int64_t)(blockIdx.x / FEW_CTAS);
+    const int64_t col = 32 * (int64_t)(blockIdx.x / ctas);
     if (threadIdx.x == 0) s_expert = -1;
     __syncthreads();
     bool good = true;
@@ -1045,7 +1053,7 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
     for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
     const int units = (int)(p.k / 512);
 #pragma unroll 2
-    for (int u = rank; u < units; u += FEW_CTAS) {
+    for (int u = rank; u < units; u += ctas) {
         uint4 w[8];
         uint32_t ws[8];
 #pragma unroll
@@ -1063,32 +1071,52 @@ __global__ void __launch_bounds__(256) __cluster_dims__(FEW_CTAS, 1, 1)
             decode16(w[j], wv);
             float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                d0 = fmaf(wv[i], xv[i], d0);
-                d1 = fmaf(wv[i + 1], xv[i + 1], d1);
-            }
-            acc[j] = fmaf(__fadd_rn(d0, d1) * s, e8m0_to_f32(ws[j]), acc[j]);
+            for (int i = 0; i < 16; i += 2) fma2v(wv[i], wv[i + 1], xv[i], xv[i + 1], d0, d1, d0, d1);
+            // the scales first: one of them alone may take the sum out of float32's range
+            acc[j] = fmaf(__fadd_rn(d0, d1), e8m0_to_f32(ws[j]) * s, acc[j]);
         }
     }
-    float mine = 0.0f;  // lane j keeps weight row j's sum
+    // a scale byte of 255 is NaN, where the factor above is infinite
+    bool odd = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float v = acc[j];
+    for (int j = 0; j < 8; ++j) odd |= !(fabsf(acc[j]) <= 3.402823466e38f);
+    if (odd)
+        for (int u = rank; u < units; u += ctas)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == j) mine = v;
+            for (int j = 0; j < 8; ++j)
+                if (__ldg(xsp + 16 * u) == 255 || __ldg(wsp + j * pitch + 16 * u) == 255)
+                    acc[j] = __uint_as_float(0x7FC00000u);
+    // The lanes' sums of the 8 rows: the first three steps halve the rows a lane holds.
+    float mine;
+    {
+        float a4[4], a2[2];
+        const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float give = h16 ? acc[j] : acc[j + 4];
+            a4[j] = (h16 ? acc[j + 4] : acc[j]) + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float give = h8 ? a4[j] : a4[j + 2];
+            a2[j] = (h8 ? a4[j + 2] : a4[j]) + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+        }
+        const float give = h4 ? a2[0] : a2[1];
+        mine = (h4 ? a2[1] : a2[0]) + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+        mine += __shfl_xor_sync(0xFFFFFFFFu, mine, 2);
+        mine += __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (lane < 8)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(leader_addr(smem_u32(&part[rank][8 * warp + lane]))), "f"(mine)
+    if ((lane & 3) == 0)  // lane 4 j holds row j's sum
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(leader_addr(smem_u32(&part[rank][8 * warp + lane / 4]))),
+                     "f"(mine)
                      : "memory");
     __syncwarp();
     cluster_sync();
     if (rank != 0 || warp != 0) return;
     float g = 0.0f, v = 0.0f, s0, s1;
-#pragma unroll
-    for (int c = 0; c < FEW_CTAS; ++c) {
+    for (int c = 0; c < ctas; ++c) {
         g += part[c][lane];
         v += part[c][32 + lane];
     }
@@ -1172,6 +1200,32 @@ pmn_status launch(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, c
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, msa, msb, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
+// The kernel for a few rows: as many CTAs share K as one wave of three CTAs per SM
+// allows (one, two, four rows of f 1536: 8 CTAs 4.3, 7.6, 13.4 us; 4 CTAs 5.0, 6.3, 10.9;
+// 2 CTAs 5.4, 7.3, 9.6; eight rows: one CTA 20.0, two 21.2, four 23.9).
+pmn_status launch_rows(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
+                       const Args &args, cudaStream_t s)
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PMN_ERR_CUDA;
+    unsigned ctas = FEW_CTAS;
+    while (ctas > 1 && (args.f / 32 * args.m * ctas > 3 * (int64_t)sms || ctas > args.k / 512)) ctas /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(args.f / 32) * ctas, (unsigned)args.m);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gated_rows_kernel, a, a_scales, b, b_scales, args) == cudaSuccess ? PMN_OK
+                                                                                                      : PMN_ERR_CUDA;
+}
+
 // What both directions ask of their sizes and operands.
 pmn_status check_common(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
                         const int32_t *offsets, int num_experts, int64_t total_rows, int64_t f, int64_t k)
@@ -1224,14 +1278,12 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *
                     pmn_wait_limit_ns()};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (out_t || y_out) return launch<TRAIN, 192, 2>(a, a_scales, b, b_scales, args, s);
-    // Serving.  A few rows: one cluster per row and 32 columns (f 1536, k 4096: one
-    // row 4.7 us against 12.1 in tiles, four of one expert 10.9 against 12.1, eight 18.7
-    // against 12.1, eight of eight experts 25.5 against 28.0).
-    if (total_rows <= 4 || (total_rows <= 8 && num_experts >= 8)) {
-        gated_rows_kernel<<<dim3((unsigned)(f / 32 * FEW_CTAS), (unsigned)total_rows), 256, 0, s>>>(a, a_scales, b,
-                                                                                                b_scales, args);
-        return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
-    }
+    // Serving.  A few rows, each its own cluster and its own read of the weights, against
+    // tiles (f 1536, k 4096, us): one expert, one row 4.4 and 12.2, four 9.6 and 12.0, six
+    // 12.4 and 12.2, eight 16.7 and 12.2; 8 experts, 8 rows 19.3 and 26.2, 12 rows 26.4 and
+    // 25.1; 24 experts, 8 rows 19.9 and 28.1, 24 rows 45 and 55.
+    if (total_rows <= 4 || (total_rows <= 24 && total_rows <= num_experts))
+        return launch_rows(a, a_scales, b, b_scales, args, s);
     // 256-row tiles on CTA pairs load less per product, 128-row tiles waste less at
     // the segments' ends.  Paired and single, us: one expert 64 rows 12.2 and 13.0, 16384
     // rows 119 and 141; 8 experts 8192 rows 73.5 and 83.6, 3000 rows 40.4 and 36.7; 24

@@ -192,6 +192,33 @@ def test_a_wait_that_runs_out_is_reported(pmn, which):
     assert pmn.get_device_error() == 0
 
 
+@pytest.mark.parametrize("rows", [1, 4, 48])
+@pytest.mark.parametrize("up", [114, 60, -125])
+def test_scales_far_apart(pmn, rows, up):
+    """operands whose scales are far from 1 and whose products are not: 2^up times 2^-up"""
+    a, b, _, off = problem(rows, 1, 128, 512, [0, rows], False, 71)
+    a = (a[0], np.full_like(a[1], 127 + up))
+    b = (b[0], np.full_like(b[1], 127 - up - 12))
+    h, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(off).cuda())
+    z, mass = product(a, b, off)
+    err = 512 * U * mass
+    g, u, eg, eu = z[:, :128], z[:, 128:], err[:, :128], err[:, 128:]
+    s = sigmoid(g)
+    eh = np.abs(u) * 1.1 * eg + np.abs(g * s) * eu + eg * eu + np.abs(g * s * u) * ((np.abs(g) + 8) * 2.0 ** -23 + 8 * U)
+    mx64.check_rn_abs(h[0].cpu().numpy(), h[1].cpu().numpy(), g * s * u, eh, "h")
+    assert pmn.get_device_error() == 0
+
+
+def test_a_scale_that_is_no_number(pmn):
+    """an E8M0 byte of 255 makes its row's results NaN, by every path, and no other row's"""
+    for rows in (3, 48):
+        a, b, _, off = problem(rows, 1, 128, 512, [0, rows], False, 72)
+        a[1][1, 5] = 255
+        h, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(off).cuda())
+        nan = (h[0] & 127) == 127
+        assert nan[1].all() and not nan[0].any() and not nan[2:].any()
+
+
 def test_a_few_rows_and_many_agree(pmn):
     """the kernel for a handful of rows and the tiles: their float32 sums differ, their codes by one at most"""
     a, b, _, _ = problem(8, 9, 256, 2048, [0] * 10, False, 51)
