@@ -16,7 +16,7 @@
 //                                                the bytes alone 62 us
 //   forward, serving, 16384 rows of one expert   120 us   3.4 PFLOP/s   the tensor pipe: 430 clocks a stage,
 //                                                of which 384 are MMAs, plus the ends of 14 rounds
-//   backward, 8192 rows of 24 experts             73 us   1.4 PFLOP/s   4.1 rounds take 5; as the next
+//   backward, 8192 rows of 24 experts             68 us   1.5 PFLOP/s   4.1 rounds take 5; as the next
 //   backward, 16384 rows of one expert            93 us   2.2 PFLOP/s   the epilogue beside the main loop:
 //                                                gate and up reads, code and scale stores and the
 //                                                column reduction cost 4 to 7 us each
@@ -271,7 +271,7 @@ struct Cfg {
                          RAW_OFF = WARP_OFF + EW * WARP_BYTES, BAR_OFF = RAW_OFF + RAW_SLOTS * RAW_BOX * (boxes(0) + boxes(1)),
                          SCALE_OFF = BAR_OFF + 224, CUM_OFF = SCALE_OFF + GR * GROUP_BYTES;
     static constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
-    static_assert(NCH % GR == 0 && HB % 32 == 0, "chunks per warp");
+    static_assert(NCH % GR == 0 && HB % 32 == 0 && (MODE == SERVE || CPW >= 3), "chunks per warp");
     static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 512 == 0, "TMA and descriptor alignment");
     static_assert(8 * (2 * STAGES + 8 + 2 * RAW_SLOTS) + 16 <= 224, "barrier space");
     static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
@@ -577,7 +577,13 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
     if (CT == 2) cluster_sync();  // the pair's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = __shfl_sync(0xFFFFFFFFu, *s_total, 0);
+    // A last round of few tiles: two or three pairs multiply each of them and each
+    // stores a share of its columns, so that the epilogue that nothing overlaps is short
+    // (backward of 8192 rows of 24 experts 73.5 -> 68.3 us, of 256 rows of one 18.6 -> 14.5).
+    const int all = __shfl_sync(0xFFFFFFFFu, *s_total, 0), tail = all % tstep, full = all - tail;
+    const int shares = MODE == SERVE ? 1 : 3 * tail <= tstep ? 3 : 2 * tail <= tstep ? 2 : 1;
+    const int total = full + shares * tail;
+    auto tile_at = [&](int t) { return t < full ? t : full + (t - full) / shares; };
     const int nks = (int)(p.k / 128);
     auto give_up = [&]() {  // a wait ran out: every role winds down
         if (lane == 0) {
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
             return CT == 1 || rank == 0 ? br : BWD ? br + TBN / 2 : br + p.f;
         };
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
+            const Tile ti = get_tile<MODE, TBN, CT>(tile_at(t), p, s_cum, gc);
             const int32_t arow = (int32_t)ti.m0 + BM * rank, brow = (int32_t)b_row(ti);
             for (int ks = 0; ks < nks; ++ks) {
                 ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
         int64_t asked = 0;  // groups whose scales have been asked for
         int t = tile0, q = 0, gc = 0;
         Tile ti;
-        if (t < total) ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
+        if (t < total) ti = get_tile<MODE, TBN, CT>(tile_at(t), p, s_cum, gc);
         auto fetch = [&]() {
             if (asked >= groups) return;
             const int slot = (int)(asked % C::RAW_SLOTS);
@@ -681,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
             if (++q == per_tile) {
                 q = 0;
                 t += tstep;
-                if (t < total) ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
+                if (t < total) ti = get_tile<MODE, TBN, CT>(tile_at(t), p, s_cum, gc);
             }
         };
         for (int i = 0; i < C::RAW_SLOTS; ++i) fetch();
@@ -798,9 +804,11 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
         // Warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31 of CPW chunks of
-        // 32 columns in a row.
+        // 32 columns in a row (of its share in a shared tile).
         const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0);  // warp-uniform, and known to be
-        const int quad = wu & 3, c0 = ((wu - 4) >> 2) * C::CPW, c1 = c0 + C::CPW;
+        const int quad = wu & 3, cw = ((wu - 4) >> 2) * C::CPW;
+        const int per_share = (C::CPW + shares - 1) / shares;
+        auto first_chunk = [&](int t) { return cw + (t < full ? 0 : (t - full) % shares * per_share); };
         uint8_t *buf = smem + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
         const uint32_t bufs = stages + C::WARP_OFF + (wu - 4) * C::WARP_BYTES;
         const int pr = lane >> 2, pi = lane & 3;  // four lanes cover a row's 64 bytes of y
@@ -824,7 +832,8 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
             }
         };
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<MODE, TBN, CT>(t, p, s_cum, gc);
+            const Tile ti = get_tile<MODE, TBN, CT>(tile_at(t), p, s_cum, gc);
+            const int c0 = first_chunk(t), c1 = min(t < full ? c0 + C::CPW : c0 + per_share, cw + C::CPW);
             const int64_t row0 = ti.m0 + BM * rank + 32 * quad, row = row0 + lane;
             const bool valid = row < ti.row_end, any = row0 < ti.row_end;
             const int64_t tile_row = ti.m0 + BM * rank;
@@ -839,9 +848,9 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
                 have = false;
                 if (t + tstep < total) {
                     int g2 = gc;
-                    const Tile tn = get_tile<MODE, TBN, CT>(t + tstep, p, s_cum, g2);
+                    const Tile tn = get_tile<MODE, TBN, CT>(tile_at(t + tstep), p, s_cum, g2);
                     next_row0 = tn.m0 + BM * rank + 32 * quad;
-                    next_col = tn.h0 + 32 * c0;
+                    next_col = tn.h0 + 32 * first_chunk(t + tstep);
                     has_next = next_row0 < tn.row_end && next_col < p.f;
                     have = has_next && any && ti.h0 + 32 * c0 < p.f;
                 }
@@ -969,7 +978,7 @@ __global__ void __launch_bounds__(Cfg<MODE, TBN, CT>::THREADS, 1)
                 if (!ok) break;
                 ++collected;
                 constexpr int NOUT = BWD ? 2 : 1;  // slot: chunk and (backward) gate or up
-                for (int s = quad; s < C::CPW * NOUT; s += 4) {
+                for (int s = quad; s < (c1 - c0) * NOUT; s += 4) {
                     const int64_t col = ti.h0 + 32 * (c0 + s / NOUT) + lane;
                     if (col < p.f)
                         *reinterpret_cast<uint32_t *>(p.out_t_sc + (col + (s % NOUT) * p.f) * (p.m / 32) + tile_row / 32) =

@@ -219,6 +219,26 @@ def test_a_scale_that_is_no_number(pmn):
         assert nan[1].all() and not nan[0].any() and not nan[2:].any()
 
 
+@pytest.mark.parametrize("bwd", [False, True])
+def test_a_shared_last_round_changes_no_bit(pmn, bwd):
+    """a row's results do not depend on how many tiles the call has, whose last round may be shared among CTA pairs"""
+    a, b, y, _ = problem(20480, 1, 384, 512, [0, 20480], bwd, 81)
+
+    def call(n):
+        o = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        x = cuda((a[0][:n], a[1][:n]))
+        if bwd:
+            return pmn.dh_gemm_swiglu_backward_mxfp8(x, cuda(b), y[:n].cuda(), o)
+        return pmn.w1_gemm_swiglu_mxfp8(x, cuda(b), o, want_t=True)[:2]
+
+    (q, sc), (qt, sct) = call(20480)
+    for n in (256, 2048, 4096, 6144, 8192):
+        (r, rs), (rt, rst) = call(n)
+        assert torch.equal(r, q[:n]) and torch.equal(rs, sc[:n])
+        assert torch.equal(rt, qt[:, :n]) and torch.equal(rst, sct[:, :n // 32])
+    assert pmn.get_device_error() == 0
+
+
 def test_a_few_rows_and_many_agree(pmn):
     """the kernel for a handful of rows and the tiles: their float32 sums differ, their codes by one at most"""
     a, b, _, _ = problem(8, 9, 256, 2048, [0] * 10, False, 51)
