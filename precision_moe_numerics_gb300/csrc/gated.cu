@@ -17,9 +17,9 @@
 //   forward, serving, 16384 rows of one expert   120 us   3.4 PFLOP/s   the tensor pipe: 430 clocks a stage,
 //                                                of which 384 are MMAs, plus the ends of 14 rounds
 //   backward, 8192 rows of 24 experts             68 us   1.5 PFLOP/s   4.1 rounds take 5; as the next
-//   backward, 16384 rows of one expert            93 us   2.2 PFLOP/s   the epilogue beside the main loop:
-//                                                gate and up reads, code and scale stores and the
-//                                                column reduction cost 4 to 7 us each
+//   backward, 16384 rows of one expert            93 us   2.2 PFLOP/s   the operand copies beside the
+//                                                epilogue's requests: 18 to 22 thousand clocks a
+//                                                tile, forward 15 to 16, the MMAs alone 13.8
 //   forward, serving, 512 rows of 24 experts      52 us   6.0 TB/s      HBM (46 us)
 //   forward, serving, one row                    4.3 us   3.0 TB/s      latency: a launch, two
 //                                                dependent reads, a cluster barrier
