@@ -426,6 +426,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    """memory that the call's stream may write at once: another stream's pool may hand out a block that its own
+    kernels still use, and take this one back while the call still runs"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(t, what, dtype=None):
     """2-D GPU tensor whose rows are contiguous (any row pitch); returns its pitch in elements"""
     if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
@@ -442,10 +451,9 @@ def _shaped(t, shape, dtype, what):
     return t
 
 
-def _mxfp8_out(out, rows, cols, device, what="out"):
+def _mxfp8_out(out, rows, cols, device, stream, what="out"):
     if out is None:
-        return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
-                torch.empty((rows, cols // 32), dtype=torch.uint8, device=device))
+        return (_empty((rows, cols), torch.uint8, device, stream), _empty((rows, cols // 32), torch.uint8, device, stream))
     _shaped(out[0], (rows, cols), torch.uint8, what)
     _shaped(out[1], (rows, cols // 32), torch.uint8, what + " scales")
     return out
@@ -468,20 +476,20 @@ def add_rmsnorm_mxfp8(x, residual, weight, eps=1e-6, out=None, res_out=None, y=N
         if residual.shape != x.shape:
             raise PmnError("residual must have x's shape")
         if res_out is None:
-            res_out = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
+            res_out = _empty((rows, cols), residual.dtype, dev, stream)
         else:
             _shaped(res_out, (rows, cols), residual.dtype, "res_out")
     elif res_out is not None:
         raise PmnError("res_out without a residual")
-    out = _mxfp8_out(out, rows, cols, dev)
+    out = _mxfp8_out(out, rows, cols, dev, stream)
     if y is not None:
         _shaped(y, (rows, cols), torch.bfloat16, "y")
     elif want_y:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        y = _empty((rows, cols), torch.bfloat16, dev, stream)
     if rstd is not None:
         _shaped(rstd, (rows,), torch.float32, "rstd")
     elif want_rstd:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = _empty((rows,), torch.float32, dev, stream)
     _check(lib().pmn_add_rmsnorm_mxfp8(_at(x), ldx, _at(residual), ldr, kind, _at(weight), rows, cols, eps,
                                        _at(res_out), _at(out[0]), _at(out[1]), _at(y), _at(rstd),
                                        _current_stream(stream, x)),
@@ -512,14 +520,14 @@ def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=No
     _shaped(weight, (cols,), torch.bfloat16, "weight")
     if dres is not None:
         _shaped(dres, (rows, cols), r.dtype, "dres")
-    dr = torch.empty_like(r) if dr is None else _shaped(dr, (rows, cols), r.dtype, "dr")
+    dr = _empty(r.shape, r.dtype, dev, stream) if dr is None else _shaped(dr, (rows, cols), r.dtype, "dr")
     if dx is not None:
         _shaped(dx, (rows, cols), torch.bfloat16, "dx")
     elif want_dx:
-        dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    dw = torch.empty((cols,), dtype=torch.float32, device=dev) if dw is None else _shaped(dw, (cols,), torch.float32, "dw")
+        dx = _empty((rows, cols), torch.bfloat16, dev, stream)
+    dw = _empty((cols,), torch.float32, dev, stream) if dw is None else _shaped(dw, (cols,), torch.float32, "dw")
     if workspace is None:
-        workspace = torch.empty((add_rmsnorm_backward_workspace_bytes(rows, cols),), dtype=torch.uint8, device=dev)
+        workspace = _empty((add_rmsnorm_backward_workspace_bytes(rows, cols),), torch.uint8, dev, stream)
     _dev(workspace)
     _check(lib().pmn_add_rmsnorm_backward(_at(dy), _at(r), kind, _at(rstd), _at(weight), _at(dres), rows, cols,
                                           _at(dr), _at(dx), _at(dw), _at(workspace),
@@ -551,13 +559,13 @@ def w1_gemm_swiglu_mxfp8(a, b, offsets, out=None, out_t=None, y=None, want_t=Fal
     written where they are passed in or wanted (a training step's backward pass needs them)."""
     rows, k, experts, f2 = _gated_operands(a, b, offsets, "w1_gemm_swiglu_mxfp8")
     f, dev = f2 // 2, a[0].device
-    out = _mxfp8_out(out, rows, f, dev)
+    out = _mxfp8_out(out, rows, f, dev, stream)
     if out_t is not None or want_t:
-        out_t = _mxfp8_out(out_t, f, rows, dev, "out_t")
+        out_t = _mxfp8_out(out_t, f, rows, dev, stream, "out_t")
     if y is not None:
         _shaped(y, (rows, f2), torch.bfloat16, "y")
     elif want_y:
-        y = torch.empty((rows, f2), dtype=torch.bfloat16, device=dev)
+        y = _empty((rows, f2), torch.bfloat16, dev, stream)
     t, tsc = out_t if out_t is not None else (None, None)
     _check(lib().pmn_w1_gemm_swiglu_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(offsets), experts,
                                           rows, f, k, _at(out[0]), _at(out[1]), _at(t), _at(tsc), _at(y),
@@ -576,7 +584,8 @@ def dh_gemm_swiglu_backward_mxfp8(a, b, y, offsets, out=None, out_t=None, stream
     rows, k, experts, f = _gated_operands(a, b, offsets, "dh_gemm_swiglu_backward_mxfp8")
     _shaped(y, (rows, 2 * f), torch.bfloat16, "y")
     dev = a[0].device
-    out, out_t = _mxfp8_out(out, rows, 2 * f, dev), _mxfp8_out(out_t, 2 * f, rows, dev, "out_t")
+    out = _mxfp8_out(out, rows, 2 * f, dev, stream)
+    out_t = _mxfp8_out(out_t, 2 * f, rows, dev, stream, "out_t")
     _check(lib().pmn_dh_gemm_swiglu_backward_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(y),
                                                    _at(offsets), experts, rows, f, k, _at(out[0]), _at(out[1]),
                                                    _at(out_t[0]), _at(out_t[1]), _current_stream(stream, offsets)),
