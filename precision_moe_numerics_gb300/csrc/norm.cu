@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_kernel(const uint16_t *__rest
 // one wave of CTAs has fewer loads in flight than a copy, and the partial sums are 5 MB
 // and a second kernel); 1021 x 1536 in float32 7.1 us (3.7), latency of the two
 // launches; 16384 columns 2.8 TB/s (registers spill).
-template <int T, int NP, int RK>
-__global__ void __launch_bounds__(T == 32 ? CTA : T, T == 512 ? 1 : 2) add_rmsnorm_backward_kernel(
+template <int T, int NP, int RK, int PER_SM>
+__global__ void __launch_bounds__(T == 32 ? CTA : T, PER_SM) add_rmsnorm_backward_kernel(
     const uint16_t *__restrict__ dy, const void *__restrict__ r, const float *__restrict__ rstd,
     const uint16_t *__restrict__ weight, const void *__restrict__ dres, int64_t rows, int cols, void *__restrict__ dr,
     uint16_t *__restrict__ dx, float *__restrict__ partial)
@@ -339,17 +339,27 @@ __global__ void __launch_bounds__(32 * DW_WARPS) add_rmsnorm_dw_kernel(const flo
     }
 }
 
-// CTAs of the backward kernel (rows of its partial sums): as many as the 152 SMs
-// hold at once (one of 512 threads, two of 256, four of 128), fewer where there
-// are fewer rows.  More are slower: they run in turn, and each adds a row of partial
-// sums (16384 x 4096: 304 CTAs 93 us, 456 110 us, 608 97 us; 304 of 512 threads,
-// half of them waiting, 111 us).  A constant, so that the workspace's size and the sums' order
-// depend on the sizes alone.
+// CTAs of the backward kernel per SM: as many as the SMs hold at once.  More are slower:
+// they run in turn, and each adds a row of partial sums (16384 x 4096: 304 CTAs 93 us,
+// 456 110 us, 608 97 us; 304 of 512 threads, half of them waiting, 111 us).  With one
+// piece per thread and many rows, half as many again at 80 registers keep more loads in
+// flight (16384 x 1056 47 -> 37 us, x 2048 56 -> 49); few rows are better off with fewer
+// partial sums and uneven shares (1021 x 1536 in float32 7.0 us, 8.4 with 456 CTAs).
+bool many_rows(int64_t rows) { return rows >= 4096; }
+int backward_per_sm(int64_t rows, int64_t cols)
+{
+    if (cols > 4096) return 1;                             // 512 threads
+    if (cols > 2048 || cols <= BWD_WARP_COLS) return 2;    // 256 threads
+    if (cols > 1024) return many_rows(rows) ? 3 : 2;       // 256 threads
+    return many_rows(rows) ? 6 : 4;                        // 128 threads
+}
+
+// CTAs in all: rows of partial sums.  From constants, so that the workspace's size and
+// the sums' order depend on the sizes alone.
 int64_t backward_parts(int64_t rows, int64_t cols)
 {
     const int64_t per = cols <= BWD_WARP_COLS ? CTA / 32 : 1;
-    const int64_t most = cols > 4096 ? 152 : cols > BWD_WARP_COLS && cols <= 1024 ? 608 : 304;
-    return std::min<int64_t>(most, (rows + per - 1) / per);
+    return std::min<int64_t>(152 * backward_per_sm(rows, cols), (rows + per - 1) / per);
 }
 
 struct NormArgs {
@@ -393,12 +403,12 @@ struct NormBwdArgs {
     float *partial;
 };
 
-template <int T, int NP>
+template <int T, int NP, int PER_SM>
 void launch_norm_bwd(int rk, int parts, const NormBwdArgs &a, cudaStream_t s)
 {
 #define PMN_NORM_BWD(RK)                                                                                              \
-    add_rmsnorm_backward_kernel<T, NP, RK><<<parts, T == 32 ? CTA : T, 0, s>>>(a.dy, a.r, a.rstd, a.weight, a.dres, a.rows, a.cols, \
-                                                                 a.dr, a.dx, a.partial)
+    add_rmsnorm_backward_kernel<T, NP, RK, PER_SM><<<parts, T == 32 ? CTA : T, 0, s>>>(                               \
+        a.dy, a.r, a.rstd, a.weight, a.dres, a.rows, a.cols, a.dr, a.dx, a.partial)
     if (rk == RES_BF16) PMN_NORM_BWD(RES_BF16);
     else PMN_NORM_BWD(RES_F32);
 #undef PMN_NORM_BWD
@@ -477,13 +487,16 @@ extern "C" pmn_status pmn_add_rmsnorm_backward(const void *dy, const void *r, in
     float *partial = static_cast<float *>(workspace);
     const NormBwdArgs a{static_cast<const uint16_t *>(dy), r, rstd, static_cast<const uint16_t *>(weight), dres, rows,
                         (int)cols, dr, static_cast<uint16_t *>(dx), partial};
-    if (cols <= 256) launch_norm_bwd<32, 1>(rk, parts, a, s);
-    else if (cols <= BWD_WARP_COLS) launch_norm_bwd<32, 2>(rk, parts, a, s);
-    else if (cols <= 1024) launch_norm_bwd<128, 1>(rk, parts, a, s);
-    else if (cols <= 2048) launch_norm_bwd<256, 1>(rk, parts, a, s);
-    else if (cols <= 4096) launch_norm_bwd<256, 2>(rk, parts, a, s);
-    else if (cols <= 8192) launch_norm_bwd<512, 2>(rk, parts, a, s);
-    else launch_norm_bwd<512, 4>(rk, parts, a, s);
+    const bool many = many_rows(rows);
+    if (cols <= 256) launch_norm_bwd<32, 1, 2>(rk, parts, a, s);
+    else if (cols <= BWD_WARP_COLS) launch_norm_bwd<32, 2, 2>(rk, parts, a, s);
+    else if (cols <= 1024 && many) launch_norm_bwd<128, 1, 6>(rk, parts, a, s);
+    else if (cols <= 1024) launch_norm_bwd<128, 1, 4>(rk, parts, a, s);
+    else if (cols <= 2048 && many) launch_norm_bwd<256, 1, 3>(rk, parts, a, s);
+    else if (cols <= 2048) launch_norm_bwd<256, 1, 2>(rk, parts, a, s);
+    else if (cols <= 4096) launch_norm_bwd<256, 2, 2>(rk, parts, a, s);
+    else if (cols <= 8192) launch_norm_bwd<512, 2, 1>(rk, parts, a, s);
+    else launch_norm_bwd<512, 4, 1>(rk, parts, a, s);
     if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
     // the second kernel's launch overlaps the first one's end; it waits for its writes
     cudaLaunchConfig_t cfg = {};
