@@ -17,17 +17,18 @@
 //   forward, serving, 16384 rows of one expert   120 us   3.4 PFLOP/s   the tensor pipe: 430 clocks a stage,
 //                                                of which 384 are MMAs, plus the ends of 14 rounds
 //   backward, 8192 rows of 24 experts             68 us   1.5 PFLOP/s   4.1 rounds take 5; as the next
-//   backward, 16384 rows of one expert            93 us   2.2 PFLOP/s   the operand copies beside the
+//   backward, 16384 rows of one expert            92 us   2.2 PFLOP/s   the operand copies beside the
 //                                                epilogue's requests: 18 to 22 thousand clocks a
 //                                                tile, forward 15 to 16, the MMAs alone 13.8
 //   forward, serving, 512 rows of 24 experts      52 us   6.0 TB/s      HBM (46 us)
-//   forward, serving, one row                    4.3 us   3.0 TB/s      latency: a launch, two
+//   forward, serving, one row                    4.4 us   3.0 TB/s      latency: a launch, two
 //                                                dependent reads, a cluster barrier
 // What the tiles and roles are for: 192 weight rows per tile leave TMEM room for two
 // accumulators beside the scale factors, so the epilogue of one tile runs while the
-// next is multiplied (256 rows with one accumulator: 143 / 112 / 206 us for the
-// training rows above but the second); two CTAs per 256-row tile load 28 KB per stage
-// and SM where one loads 40 KB (backward of 16384 rows 119 -> 101 us).
+// next is multiplied; two CTAs per 256-row tile load 28 KB per stage and SM where one
+// loads 40 KB.  (When both were chosen, for 8192 rows forward, 8192 and 16384 rows
+// backward: tiles of 256 with one accumulator 143, 112, 206 us, of 128 165, 112, 195,
+// of 192 132, 100, 163; backward of 16384 rows by single CTAs 119, by pairs 101.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
