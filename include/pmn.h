@@ -553,7 +553,13 @@ typedef struct pmn_adamw_tensor {
  * too: 16 random bits are added below the last place.  Random bits: Philox as
  * in pmn_requant_transpose_sr_mxfp8, with counter (j lo, j hi, 4 * index of the
  * tensor + stream, step), j = element / 16, stream 0 = param, 1 = m, 2 = v.
- * A NaN or infinite gradient makes its own element's param and m NaN or infinite.
+ * A NaN or infinite gradient makes its own element's param and m NaN or infinite,
+ * and no other element's.  An MXFP8 state holds no infinity: an infinite m, or a v
+ * that is infinite (as after a gradient above 1.8e19, whose square overflows), is
+ * stored as NaN and makes the element's param NaN in the next step; the 31
+ * neighbours under its scale keep theirs.  A finite gradient, however large,
+ * raises the scale of its block: the neighbours' nonzero sqrt(v) become at least
+ * 2^-18 of its own sqrt(v), about, and their m below 2^-18 of its own vanish.
  *  tensors  HOST array [num_tensors], copied by the call.
  *  param_kind, grad_kind  PMN_OUT_BF16 or PMN_OUT_F32;  state_kind PMN_STATE_*.
  *  beta1, beta2 in [0, 1);  eps >= 2^-126 (normal in float32);  step >= 1 (its low 32 bits are used as the

@@ -131,13 +131,23 @@ __device__ __forceinline__ void store8_b16(void *p, int64_t i, int64_t left, con
 // (A value below the smallest code 2^-9 of its block becomes that code exactly,
 // whose rounding is certain; larger ones never round to 0.  Blocks that have such
 // a value are rare, so one comparison of the thread's minimum guards the work.)
+// An infinite value takes the NaN code and has no part in the block's scale: its
+// 31 neighbours would otherwise become 0 or, kept, codes whose squares overflow.
 template <bool KEEP>
-__device__ __forceinline__ void store8_mx(uint8_t *q, uint8_t *sc, int64_t i, int64_t left, const float (&v)[8],
-                                          uint32_t r0, uint32_t r1)
+__device__ __forceinline__ void store8_mx(uint8_t *q, uint8_t *sc, int64_t i, int64_t left, float (&v)[8], uint32_t r0,
+                                          uint32_t r1)
 {
     float amax = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+    if (__float_as_uint(amax) == 0x7F800000u) {
+        amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (fabsf(v[k]) > 3.402823466e38f) v[k] = __uint_as_float(0x7FC00000u);
+            amax = fmaxf(amax, fabsf(v[k]));
+        }
+    }
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
     const int e = mx_exponent_448(amax);

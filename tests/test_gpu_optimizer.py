@@ -210,6 +210,37 @@ def test_gradients_that_are_not_finite(pmn):
             assert bad[5] and bad.sum() <= 2 and torch.isnan(p[0][5])
 
 
+@pytest.mark.parametrize("pk", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 3e19])
+def test_neighbours_of_a_gradient_that_is_not_finite(pmn, bad, pk):
+    """MXFP8 states: the 31 elements under the scale of one whose gradient is not finite (or overflows when squared)
+    keep their states and train on, as in a run where that element's gradient is 0"""
+    runs = []
+    for value in (bad, 0.0):
+        p, g, m, v = make([96], pk, torch.float32, True, 13)
+        m[0][0][37] = v[0][0][37] = 0  # no part in its block's scale without the gradient
+        g[0][37] = value
+        h = pmn.AdamWTensors(p, g, m, v)
+        pmn.adamw_step(h, **HP)
+        first = clone(p) + clone(m) + clone(v)
+        g[0][37] = 1e-2
+        pmn.adamw_step(h, **{**HP, "step": 8})
+        runs.append((first, p + m + v))
+    others = torch.arange(96, device="cuda") != 37
+    (first, second), (first0, second0) = runs
+    finite_m = abs(bad) < float("inf")  # a large finite m raises its block's scale
+    for x, y, keeps in zip(first, first0, (True, not finite_m, True)):
+        x, y = (x, y) if isinstance(x, tuple) else ((x,), (y,))
+        assert torch.equal(x[0][others], y[0][others]) or not keeps
+        assert not keeps or all(torch.equal(a, b) for a, b in zip(x[1:], y[1:]))
+    assert (first[2][0][37] & 127) == 127 and ((first[1][0][37] & 127) == 127 or finite_m)
+    assert torch.isnan(second[0][37]) and torch.isfinite(second[0][others]).all()
+    assert torch.isfinite(torch.from_numpy(values(second[2]) ** 2).float()[others.cpu()]).all()
+    if not finite_m:
+        assert torch.equal(second[0][others], second0[0][others])
+    assert (second[0][others] != first[0][others]).float().mean() > 0.5
+
+
 def test_small_changes_of_v_are_kept_on_average(pmn):
     """beta2 = 0.99 moves v by at most 1 % a step, far below half a step of E4M3: rounding to nearest would leave it
     where it starts.  Stochastic rounding settles between the two neighbouring codes; their mean square is within
