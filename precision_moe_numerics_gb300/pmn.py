@@ -416,10 +416,22 @@ def _kind(t, what):
     return k
 
 
-def _current_stream(stream, t):
-    """the raw handle of `stream`, or of the current stream of t's device"""
-    # (torch.cuda.current_stream() builds an object, 3 us of a call that takes 2 us on the GPU)
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _launch_stream(what, stream, *tensors):
+    """the raw handle of `stream`, or of the current stream.
+
+    A launch goes to the current GPU whatever its stream's handle says (the default stream's is the same on every
+    one), so the call's tensors (None left out) and `stream` have to be there."""
+    # (torch.cuda's own functions look for the library first, and current_stream() builds an object: 3 us of a call
+    # that takes 2 us on the GPU)
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise PmnError("%s: every tensor must be on the current GPU (cuda:%d), one is on %s" % (what, dev, t.device))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise PmnError("%s: the stream is of cuda:%d, the current GPU is cuda:%d" % (what, stream.device_index, dev))
+    return stream.cuda_stream
 
 
 def _at(t):
@@ -490,9 +502,9 @@ def add_rmsnorm_mxfp8(x, residual, weight, eps=1e-6, out=None, res_out=None, y=N
         _shaped(rstd, (rows,), torch.float32, "rstd")
     elif want_rstd:
         rstd = _empty((rows,), torch.float32, dev, stream)
+    raw = _launch_stream("add_rmsnorm_mxfp8", stream, x, residual, weight, res_out, out[0], out[1], y, rstd)
     _check(lib().pmn_add_rmsnorm_mxfp8(_at(x), ldx, _at(residual), ldr, kind, _at(weight), rows, cols, eps,
-                                       _at(res_out), _at(out[0]), _at(out[1]), _at(y), _at(rstd),
-                                       _current_stream(stream, x)),
+                                       _at(res_out), _at(out[0]), _at(out[1]), _at(y), _at(rstd), raw),
            "add_rmsnorm_mxfp8")
     return out, res_out, y, rstd
 
@@ -529,9 +541,10 @@ def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=No
     if workspace is None:
         workspace = _empty((add_rmsnorm_backward_workspace_bytes(rows, cols),), torch.uint8, dev, stream)
     _dev(workspace)
+    raw = _launch_stream("add_rmsnorm_backward", stream, dy, r, rstd, weight, dres, dr, dx, dw, workspace)
     _check(lib().pmn_add_rmsnorm_backward(_at(dy), _at(r), kind, _at(rstd), _at(weight), _at(dres), rows, cols,
                                           _at(dr), _at(dx), _at(dw), _at(workspace),
-                                          workspace.numel() * workspace.element_size(), _current_stream(stream, dy)),
+                                          workspace.numel() * workspace.element_size(), raw),
            "add_rmsnorm_backward")
     return dr, dx, dw
 
@@ -567,9 +580,9 @@ def w1_gemm_swiglu_mxfp8(a, b, offsets, out=None, out_t=None, y=None, want_t=Fal
     elif want_y:
         y = _empty((rows, f2), torch.bfloat16, dev, stream)
     t, tsc = out_t if out_t is not None else (None, None)
+    raw = _launch_stream("w1_gemm_swiglu_mxfp8", stream, a[0], a[1], b[0], b[1], offsets, out[0], out[1], t, tsc, y)
     _check(lib().pmn_w1_gemm_swiglu_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(offsets), experts,
-                                          rows, f, k, _at(out[0]), _at(out[1]), _at(t), _at(tsc), _at(y),
-                                          _current_stream(stream, offsets)),
+                                          rows, f, k, _at(out[0]), _at(out[1]), _at(t), _at(tsc), _at(y), raw),
            "w1_gemm_swiglu_mxfp8")
     return out, out_t, y
 
@@ -586,9 +599,11 @@ def dh_gemm_swiglu_backward_mxfp8(a, b, y, offsets, out=None, out_t=None, stream
     dev = a[0].device
     out = _mxfp8_out(out, rows, 2 * f, dev, stream)
     out_t = _mxfp8_out(out_t, 2 * f, rows, dev, stream, "out_t")
+    raw = _launch_stream("dh_gemm_swiglu_backward_mxfp8", stream, a[0], a[1], b[0], b[1], y, offsets, out[0], out[1],
+                         out_t[0], out_t[1])
     _check(lib().pmn_dh_gemm_swiglu_backward_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(y),
                                                    _at(offsets), experts, rows, f, k, _at(out[0]), _at(out[1]),
-                                                   _at(out_t[0]), _at(out_t[1]), _current_stream(stream, offsets)),
+                                                   _at(out_t[0]), _at(out_t[1]), raw),
            "dh_gemm_swiglu_backward_mxfp8")
     return out, out_t
 
@@ -614,7 +629,7 @@ class AdamWTensors:
         self.state_kind = STATE_MXFP8 if eight else STATE_F32
         self.table = (AdamWTensor * max(1, len(params)))()
         self.count = len(params)
-        self.device = params[0].get_device() if params else torch.cuda.current_device()
+        self.device = params[0].get_device() if params else None  # of every tensor
         self.tensors = (params, grads, m, v, copies)
         for t, p, g, a, b, c in zip(self.table, params, grads, m, v, copies):
             n = p.numel()
@@ -629,7 +644,7 @@ class AdamWTensors:
             _dev(p), _dev(g)
             if g.numel() != n or (c is not None and (_dev(c, torch.bfloat16).numel() != n or p.dtype != torch.float32)):
                 raise PmnError("AdamWTensors: grads and copies have their params' lengths, copies are of float32 params")
-            if len({x.device for x in [p, g] + q}) != 1:
+            if any(x is not None and x.get_device() != self.device for x in [p, g, c] + q):
                 raise PmnError("AdamWTensors: tensors of one step on one GPU")
             t.param, t.grad, t.n = p.data_ptr(), g.data_ptr(), n
             t.copy = None if c is None else c.data_ptr()
@@ -657,7 +672,7 @@ def adamw_step(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, 
     params and MXFP8 states are rounded stochastically with bits that follow from seed, step and position."""
     if grad_scale is not None and _dev(grad_scale, torch.float32).numel() != 1:
         raise PmnError("grad_scale must have one element")
-    raw = torch._C._cuda_getCurrentRawStream(tensors.device) if stream is None else stream.cuda_stream
+    raw = _launch_stream("adamw_step", stream, *tensors.tensors[0][:1], grad_scale)
     _check(lib().pmn_adamw_step(tensors.table, tensors.count, tensors.param_kind, tensors.grad_kind,
                                 tensors.state_kind, lr, beta1, beta2, eps, weight_decay, step, _at(grad_scale),
                                 seed, raw),
