@@ -33,6 +33,8 @@ struct Hyper {
     float lr1;                       // lr / (1 - beta1^step)
     float rbc2;                      // 1 / sqrt(1 - beta2^step)
     float eps;
+    int v_top;                       // v below these bits and |m| up to this: root2 and
+    float m_top;                     // quotient2 hold (0 and 0: never)
     uint32_t step;
     uint64_t seed;
     const float *grad_scale;
@@ -229,9 +231,12 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 
 // Square roots and quotients of two pairs from the hardware's approximations and one
-// Newton step on the residual (x - r^2, n - q d are exact up to one rounding of a
-// small number): within one place of the correctly rounded values.  x is 0 or a
-// normal number (the root of 0 comes out as 0), d a normal one.
+// step of Newton's method on the residual, which a fused multiply-add gives (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990):
+// x - r^2 and n - q d are exact up to one rounding of a small number, so the results
+// are within one place of the correctly rounded values (3 2^-24 for a subnormal n).
+// x is 0 or a normal number (the root of 0 comes out as 0); d is normal and below
+// 2^126, so that its reciprocal is normal too; n is finite and n / d does not overflow.
 __device__ __forceinline__ void root2(float x0, float x1, float &r0, float &r1)
 {
     const float least = 1.17549435e-38f;
@@ -320,12 +325,14 @@ __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_con
         rv[u].values(v[u], MX ? e8m0_to_f32(vs[u]) : 1.0f);
         int top = 0;                    // largest v's bits: infinity
         uint32_t odd = 0xFFFFFFFFu;     // smallest v's bits - 1, 0 not counted: subnormal
+        float m_max = 0.0f;             // largest |m|
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {  // two elements at a time
             float g0, g1, t0, t1;
             mul2(g[u][k], g[u][k + 1], gs, gs, g0, g1);
             mul2(g0, g1, h.omb1, h.omb1, t0, t1);
             fma2v(h.beta1, h.beta1, m[u][k], m[u][k + 1], t0, t1, m[u][k], m[u][k + 1]);
+            m_max = fmaxf(fmaxf(m_max, fabsf(m[u][k])), fabsf(m[u][k + 1]));
             if (MX) mul2(v[u][k], v[u][k + 1], v[u][k], v[u][k + 1], v[u][k], v[u][k + 1]);
             mul2(g0, g1, g0, g1, t0, t1);
             mul2(t0, t1, h.omb2, h.omb2, t0, t1);
@@ -333,7 +340,8 @@ __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_con
             top = max(max(top, __float_as_int(v[u][k])), __float_as_int(v[u][k + 1]));
             odd = min(min(odd, __float_as_uint(v[u][k]) - 1u), __float_as_uint(v[u][k + 1]) - 1u);
         }
-        const bool plain = top < 0x7F800000 && odd >= 0x007FFFFFu;  // every v is 0 or normal
+        // every v is 0 or normal, and no quotient leaves the range
+        const bool plain = top < h.v_top && odd >= 0x007FFFFFu && m_max <= h.m_top;
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             float r0, r1, d0, d1, t0, t1;
@@ -476,6 +484,11 @@ extern "C" pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_te
     h.lr1 = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
     h.rbc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
     h.eps = (float)eps;
+    // the denominator is at least eps, and at most eps + 2^91 (v's root is below 2^64, rbc2
+    // below 2^27: beta2 is at most 1 - 2^-53)
+    const bool usual = h.eps <= 0x1p100f;
+    h.v_top = usual ? 0x7F800000 : 0;
+    h.m_top = usual ? (float)std::fmin(3.402823466e38, (double)h.eps * 0x1p126) : 0.0f;
     h.step = (uint32_t)step;
     h.seed = seed;
     h.grad_scale = grad_scale;

@@ -241,6 +241,55 @@ def test_neighbours_of_a_gradient_that_is_not_finite(pmn, bad, pk):
     assert (second[0][others] != first[0][others]).float().mean() > 0.5
 
 
+def one_step(pmn, p, g, m, v, **hp):
+    """params after a step of float32 tensors whose factors are exact: beta1 = beta2 = 1/2, lr1 = 1, no decay"""
+    t = [torch.tensor(np.asarray(x, np.float32), device="cuda") for x in (p, g, m, v)]
+    pmn.adamw_step(pmn.AdamWTensors(*([x] for x in t)), **{**dict(lr=1.0, beta1=0.5, beta2=0.5, weight_decay=0.0, step=200), **hp})
+    return f64(t[0])
+
+
+def test_quotients_outside_float32s_range(pmn):
+    """an infinite stored m, a quotient that overflows, a denominator whose reciprocal is subnormal"""
+    # m and v are halved by the step, so that m / (sqrt(v) + eps) is as the comments say
+    m, v = np.zeros(64), np.zeros(64)
+    m[3], v[3] = np.inf, 2.0                # inf / 1
+    m[9], v[9] = -np.inf, 0.0               # -inf / eps
+    m[17], v[17] = 2e31, 0.0                # 1e31 / 1e-8: overflows
+    m[33], v[33] = 2.0, 2.0                 # 1 / 1
+    p = one_step(pmn, np.zeros(64), np.zeros(64), m, v, eps=1e-8)
+    assert p[3] == -np.inf and p[9] == np.inf and p[17] == -np.inf and abs(p[33] + 1) <= 2e-7
+    rest = np.delete(p, [3, 9, 17, 33])
+    assert (rest == 0).all()
+    m = np.full(64, 2e38)
+    for eps in (2.0 ** 126, 1.5 * 2.0 ** 126, 3e38):
+        p = one_step(pmn, np.zeros(64), np.zeros(64), m, np.zeros(64), eps=eps)
+        want = rn(1e38) / rn(eps)
+        assert (np.abs(p + want) <= 2.0 ** -22 * want).all()
+
+
+def test_roots_and_quotients_of_one_newton_step(pmn):
+    """p = -m / (sqrt(v) + eps) over the range of normal v and of m with its subnormals.
+
+    The kernel's root and quotient are within one place of the correctly rounded ones, so within 1.5 places of the
+    exact ones, a place being at most 2^-23 of the value (2^-149 below the normal range): 3 u each, u = 2^-24.  With
+    eps = 2^-126 beside a root of 2^-63 and more the denominator is the root; with v = 0 it is eps."""
+    rng = np.random.default_rng(17)
+    n = 1 << 20
+    v = np.exp2(rng.uniform(-125, 127.9, n)).astype(np.float32).astype(np.float64)
+    v[:8] = 2.0 ** -125, 2.0 ** 127, 2.0, 8.0, np.float32(3.3e38), np.nextafter(np.float32(2) ** -125, np.float32(1)), 4.5, 2.0 ** -124
+    m = np.where(np.arange(n) % 2 == 0, 2.0, np.exp2(rng.uniform(-20, 20, n)).astype(np.float32).astype(np.float64))
+    p = one_step(pmn, np.zeros(n), np.zeros(n), m, v, eps=2.0 ** -126)
+    want = m / 2 / np.sqrt(v / 2)
+    assert (np.abs(-p / want - 1) <= 6.1 * U).all()
+    for eps in (2.0 ** -126, 1e-30, 1e-8, 1.0, 3e7, 1e25, 2.0 ** 100):
+        lo, hi = max(-148.0, np.log2(eps) - 124), min(127.9, np.log2(eps) + 126)
+        m = np.exp2(rng.uniform(lo, hi, n)).astype(np.float32).astype(np.float64) * rng.choice([-1.0, 1.0], n)
+        half = rn(m / 2)
+        p = one_step(pmn, np.zeros(n), np.zeros(n), m, np.zeros(n), eps=eps)
+        want = half / rn(eps)
+        assert (np.abs(p + want) <= np.maximum(3 * U * np.abs(want), 1.5 * 2.0 ** -149)).all(), eps
+
+
 def test_small_changes_of_v_are_kept_on_average(pmn):
     """beta2 = 0.99 moves v by at most 1 % a step, far below half a step of E4M3: rounding to nearest would leave it
     where it starts.  Stochastic rounding settles between the two neighbouring codes; their mean square is within
