@@ -571,6 +571,8 @@ def w1_gemm_swiglu_mxfp8(a, b, offsets, out=None, out_t=None, y=None, want_t=Fal
     MXFP8 of h^T along the rows (u8 [F, T], u8 [F, T/32]; offsets and T multiples of 32), y = bf16 [T, 2F], both
     written where they are passed in or wanted (a training step's backward pass needs them)."""
     rows, k, experts, f2 = _gated_operands(a, b, offsets, "w1_gemm_swiglu_mxfp8")
+    if f2 % 2:
+        raise PmnError("w1_gemm_swiglu_mxfp8: b holds as many gate as up rows, got %d in all" % f2)
     f, dev = f2 // 2, a[0].device
     out = _mxfp8_out(out, rows, f, dev, stream)
     if out_t is not None or want_t:

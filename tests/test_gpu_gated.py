@@ -412,3 +412,11 @@ def test_the_same_bits_under_load(pmn):
     for _ in range(40):
         assert all(torch.equal(s, t) for s, t in zip(run(), first))
     assert pmn.get_device_error() == 0
+
+
+def test_an_odd_number_of_weight_rows_is_refused(pmn):
+    """gate and up are halves: with 2 f + 1 rows an expert's weights would be read from the wrong place"""
+    a, _, _, o = problem(64, 2, 128, 512, [0, 32, 64], False)
+    b = (torch.zeros((2, 257, 512), dtype=torch.uint8, device="cuda"), torch.zeros((2, 257, 16), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(pmn.PmnError):
+        pmn.w1_gemm_swiglu_mxfp8(cuda(a), b, torch.from_numpy(o).cuda())
