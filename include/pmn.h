@@ -566,6 +566,8 @@ typedef struct pmn_adamw_tensor {
  *           counter word).
  *  grad_scale  NULL (1), or a DEVICE float32: a clipping factor or the inverse of
  *           a loss scale, read by the kernel.
+ * Arguments are checked before anything is enqueued, fewer than 2^43 elements in
+ * each 440 tensors among them (PMN_ERR_UNSUPPORTED), so a refused step updates nothing.
  * One kernel per 440 tensors on `stream`; the arguments are fixed in a captured
  * graph (lr and step included).
  */

@@ -417,6 +417,8 @@ __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_con
     }
 }
 
+int64_t chunks_of(int64_t n) { return n / CHUNK + (n % CHUNK != 0); }
+
 template <int MAXT>
 pmn_status launch_adamw(const pmn_adamw_tensor *t, int count, uint32_t base, int kinds, const Hyper &h, cudaStream_t s)
 {
@@ -425,8 +427,7 @@ pmn_status launch_adamw(const pmn_adamw_tensor *t, int count, uint32_t base, int
     for (int i = 0; i < count; ++i) {
         tab.t[i] = t[i];
         tab.first[i] = (int)chunks;
-        chunks += (t[i].n + CHUNK - 1) / CHUNK;
-        if (chunks >= (int64_t(1) << 31)) return PMN_ERR_UNSUPPORTED;
+        chunks += chunks_of(t[i].n);
     }
     tab.first[count] = (int)chunks;
     tab.count = count;
@@ -466,14 +467,18 @@ extern "C" pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_te
           std::isfinite(weight_decay)) || !std::isfinite((float)eps) || (float)eps < 1.17549435e-38f || step < 1 ||
         ((uintptr_t)grad_scale & 3u))
         return PMN_ERR_INVALID_ARG;
+    int64_t chunks = 0;  // of a launch
     for (int i = 0; i < num_tensors; ++i) {
         const pmn_adamw_tensor &t = tensors[i];
+        if (i % LARGE_TABLE == 0) chunks = 0;
         if (t.n < 0 || (t.copy && param_kind != PMN_OUT_F32)) return PMN_ERR_INVALID_ARG;
         if (t.n == 0) continue;
         if (!t.param || !t.grad || !t.m || !t.v) return PMN_ERR_INVALID_ARG;
         if (!aligned16(t.param) || !aligned16(t.copy) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v))
             return PMN_ERR_INVALID_ARG;
         if (state_kind == PMN_STATE_MXFP8 && (!t.m_scales || !t.v_scales)) return PMN_ERR_INVALID_ARG;
+        // before the first launch: a refused step has updated nothing
+        if ((chunks += chunks_of(t.n)) >= (int64_t(1) << 31)) return PMN_ERR_UNSUPPORTED;
     }
     Hyper h;
     h.beta1 = (float)beta1;
