@@ -1086,16 +1086,33 @@ __global__ void __launch_bounds__(256, 3) gated_rows_kernel(const uint8_t *__res
             acc[j] = fmaf(__fadd_rn(d0, d1), e8m0_to_f32(ws[j]) * s, acc[j]);
         }
     }
-    // a scale byte of 255 is NaN, where the factor above is infinite
+    // A sum that is not finite is formed again: the product of the scales may have passed
+    // float32's range on its own, beside codes whose sum is 0, and a byte of 255 is NaN,
+    // where the factor above is infinite.
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) odd |= !(fabsf(acc[j]) <= 3.402823466e38f);
-    if (odd)
-        for (int u = rank; u < units; u += ctas)
+    if (odd) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (__ldg(xsp + 16 * u) == 255 || __ldg(wsp + j * pitch + 16 * u) == 255)
-                    acc[j] = __uint_as_float(0x7FC00000u);
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+        for (int u = rank; u < units; u += ctas) {
+            const uint32_t xs = __ldg(xsp + 16 * u);
+            float xv[16];
+            decode16(__ldg(reinterpret_cast<const uint4 *>(xp + 512 * u)), xv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t ws = __ldg(wsp + j * pitch + 16 * u);
+                float wv[16], d = 0.0f;
+                decode16(__ldg(reinterpret_cast<const uint4 *>(wp + j * p.k + 512 * u)), wv);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) d = fmaf(wv[i], xv[i], d);
+                const uint32_t lo = (xs + ws) >> 1, hi = xs + ws - lo;  // 2^(xs + ws - 254) in two factors
+                acc[j] = xs == 255u || ws == 255u ? __uint_as_float(0x7FC00000u)
+                                                  : fmaf(__fmul_rn(d, e8m0_to_f32(lo)), e8m0_to_f32(hi), acc[j]);
+            }
+        }
+    }
     // The lanes' sums of the 8 rows: the first three steps halve the rows a lane holds.
     float mine;
     {

@@ -420,3 +420,16 @@ def test_an_odd_number_of_weight_rows_is_refused(pmn):
     b = (torch.zeros((2, 257, 512), dtype=torch.uint8, device="cuda"), torch.zeros((2, 257, 16), dtype=torch.uint8, device="cuda"))
     with pytest.raises(pmn.PmnError):
         pmn.w1_gemm_swiglu_mxfp8(cuda(a), b, torch.from_numpy(o).cuda())
+
+
+@pytest.mark.parametrize("rows", [1, 4, 48])
+def test_zeros_under_large_scales(pmn, rows):
+    """zero codes whose scales' product leaves float32's range count as 0, by the kernel for few rows and the tiles"""
+    a, b, _, off = problem(rows, 1, 128, 512, [0, rows], False, 73)
+    a[0][:, 64:128], a[1][:, 2:4] = 0, 230
+    b[1][:, :, 2:4] = 240
+    h, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(off).cuda())
+    a[1][:, 2:4] = 0
+    want, _, _ = pmn.w1_gemm_swiglu_mxfp8(cuda(a), cuda(b), torch.from_numpy(off).cuda())
+    assert torch.equal(h[0], want[0]) and torch.equal(h[1], want[1])
+    assert ((h[0] & 127) != 127).all() and pmn.get_device_error() == 0
