@@ -164,6 +164,18 @@ def test_backward_of_many_rows(pmn, rows, cols, kind):
     test_backward(pmn, rows, cols, kind)
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(3, 64), (5003, 512), (4099, 1056), (700, 4096), (900, 8192), (400, 16384)])
+def test_backward_in_place(pmn, rows, cols, kind):
+    """dr written over dres: rows ahead are read before theirs are written"""
+    dy, r, w = make(rows, cols, kind, 31)
+    dres = make(rows, cols, kind, 32)[1]
+    rstd = torch.rand((rows,), device="cuda") + 0.5
+    want = pmn.add_rmsnorm_backward(dy, r, rstd, w, dres=dres)
+    got = pmn.add_rmsnorm_backward(dy, r, rstd, w, dres=dres, dr=dres)
+    assert got[0] is dres and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
 def test_no_rows(pmn):
     x, _, w = make(0, 64, None)
     out, _, _, _ = pmn.add_rmsnorm_mxfp8(x, None, w)
