@@ -192,6 +192,35 @@ def test_a_wait_that_runs_out_is_reported(pmn, which):
     assert pmn.get_device_error() == 0
 
 
+@pytest.mark.parametrize("which", ["serve", "train", "backward"])
+def test_a_call_that_runs_out_of_time_says_so(pmn, which):
+    """with no time to wait a call either is right or latches the timeout: an incomplete result is never silent"""
+    off = [0, 256, 640, 640, 1280]
+    a, b, y, o = problem(1280, 4, 384, 1024, off, which == "backward", 62)
+    a, b, o, y = cuda(a), cuda(b), torch.from_numpy(o).cuda(), y.cuda() if which == "backward" else None
+
+    def call():
+        if which == "backward":
+            return pmn.dh_gemm_swiglu_backward_mxfp8(a, b, y, o)
+        r = pmn.w1_gemm_swiglu_mxfp8(a, b, o, want_t=which == "train", want_y=which == "train")
+        return r[:2] if which == "train" else r[:1]
+
+    want = call()
+    assert pmn.get_device_error() == 0
+    limit = pmn.set_wait_limit_ns(0)
+    try:
+        for _ in range(5):
+            got = call()
+            error = pmn.get_device_error()
+            same = all(torch.equal(x[0], z[0]) and torch.equal(x[1], z[1]) for x, z in zip(want, got))
+            assert error == pmn.DEVERR_WAIT_TIMEOUT or (error == 0 and same)
+    finally:
+        pmn.set_wait_limit_ns(limit)
+    got = call()
+    assert all(torch.equal(x[0], z[0]) and torch.equal(x[1], z[1]) for x, z in zip(want, got))
+    assert pmn.get_device_error() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 4, 48])
 @pytest.mark.parametrize("up", [114, 60, -125])
 def test_scales_far_apart(pmn, rows, up):
