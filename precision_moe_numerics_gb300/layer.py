@@ -69,8 +69,9 @@ class ExpertLayerStep:
         self.w1q = (e(E * F2, D // 2), e(E * F2, D // 16), e(E, dtype=f32))
         self.w2q = (e(E * D, F // 2), e(E * D, F // 16), e(E, dtype=f32))
         self.xq = (e(T, D // 2), e(T, D // 16), e(T, dtype=f32))
-        self.h = e(T, F, dtype=bf16)
-        self.hq = (e(T, F // 2), e(T, F // 16), e(T, dtype=f32))
+        # (h is written on the experts' segments alone: the rows after the last one stay 0)
+        self.h = torch.zeros((T, F), dtype=bf16, device=device)
+        self.hq = tuple(torch.zeros(t, dtype=d, device=device) for t, d in (((T, F // 2), u8), ((T, F // 16), u8), ((T,), f32)))
         self.z = (e(T, D, dtype=torch.int8), e(T, D // 32))
         # backward operands
         self.xt = (e(1, D, T), e(1, D, T // 32))
