@@ -306,6 +306,28 @@ def test_many_experts(pmn):
     check_backward(pmn, problem(128, 100, 128, 512, off, True, 10))
 
 
+def test_the_most_experts(pmn):
+    """1024 experts, nearly all of them without rows: the same bytes as with the others left out"""
+    few = np.array([0, 32, 96, 224, 256], np.int32)
+    at = [3, 31, 512, 1023]
+    counts = np.zeros(1024, np.int64)
+    counts[at] = np.diff(few)
+    all_of_them = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+    for bwd in (False, True):
+        a, b, y, off = problem(256, 4, 128, 512, few, bwd, 91 + bwd)
+        a, b, y, off = cuda(a), cuda(b), y.cuda(), torch.from_numpy(off).cuda()
+        wide = tuple(torch.full((1024,) + t.shape[1:], 120, dtype=torch.uint8, device="cuda") for t in b)
+        for w, t in zip(wide, b):
+            w[at] = t
+        if bwd:
+            want, got = (pmn.dh_gemm_swiglu_backward_mxfp8(a, w, y, o) for w, o in ((b, off), (wide, all_of_them)))
+        else:
+            want, got = (pmn.w1_gemm_swiglu_mxfp8(a, w, o, want_t=True)[:2] for w, o in ((b, off), (wide, all_of_them)))
+        for x, z in zip(want, got):
+            assert torch.equal(x[0], z[0]) and torch.equal(x[1], z[1])
+    assert pmn.get_device_error() == 0
+
+
 def test_the_formula_against_differences():
     rng = np.random.default_rng(1)
     g, u, dh, h = rng.standard_normal(50) * 3, rng.standard_normal(50), rng.standard_normal(50), 1e-6
