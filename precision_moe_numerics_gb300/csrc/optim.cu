@@ -273,6 +273,13 @@ __device__ __forceinline__ void quotient2(float n0, float n1, float d0, float d1
 template <bool PF32, bool GF32, bool MX, int MAXT>
 __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_constant__ Table<MAXT> tab, const Hyper h)
 {
+    // With float32 parameters and MXFP8 states the products and sums of m and v are rounded
+    // one by one: the same states, code for code, as from the formulas in plain float32.  A
+    // fused sum differs in its last place, which turns a stochastic rounding now and then (7
+    // of 10^5 codes of m), and the next step moves the parameter by a few per cent more or
+    // less.  (Parameters in bf16 are rounded themselves, by far more than that, and their
+    // kernel is bound by issue: fused, 165 us for 75 million elements; one by one 168.)
+    constexpr bool APART = PF32 && MX;
     int lo = 0, hi = tab.count - 1;
     while (lo < hi) {  // the last tensor whose first chunk is at or before this one
         const int mid = (lo + hi + 1) >> 1;
@@ -321,22 +328,34 @@ __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_con
     for (int u = 0; u < 2; ++u) {
         rp[u].values(p[u]);
         rg[u].values(g[u]);
-        rm[u].values(m[u], MX ? e8m0_to_f32(ms[u]) : 1.0f);
+        const float m_scale = MX ? e8m0_to_f32(ms[u]) : 1.0f;
+        rm[u].values(m[u], APART ? __fmul_rn(m_scale, h.beta1) : m_scale);  // APART: beta1 m, rounded once
         rv[u].values(v[u], MX ? e8m0_to_f32(vs[u]) : 1.0f);
         int top = 0;                    // largest v's bits: infinity
         uint32_t odd = 0xFFFFFFFFu;     // smallest v's bits - 1, 0 not counted: subnormal
         float m_max = 0.0f;             // largest |m|
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {  // two elements at a time
-            float g0, g1, t0, t1;
+            float g0, g1, t0, t1, s0, s1;
             mul2(g[u][k], g[u][k + 1], gs, gs, g0, g1);
             mul2(g0, g1, h.omb1, h.omb1, t0, t1);
-            fma2v(h.beta1, h.beta1, m[u][k], m[u][k + 1], t0, t1, m[u][k], m[u][k + 1]);
+            if (APART) {
+                m[u][k] = __fadd_rn(m[u][k], t0);
+                m[u][k + 1] = __fadd_rn(m[u][k + 1], t1);
+            } else {
+                fma2v(h.beta1, h.beta1, m[u][k], m[u][k + 1], t0, t1, m[u][k], m[u][k + 1]);
+            }
             m_max = fmaxf(fmaxf(m_max, fabsf(m[u][k])), fabsf(m[u][k + 1]));
             if (MX) mul2(v[u][k], v[u][k + 1], v[u][k], v[u][k + 1], v[u][k], v[u][k + 1]);
             mul2(g0, g1, g0, g1, t0, t1);
             mul2(t0, t1, h.omb2, h.omb2, t0, t1);
-            fma2v(h.beta2, h.beta2, v[u][k], v[u][k + 1], t0, t1, v[u][k], v[u][k + 1]);
+            if (APART) {
+                mul2(v[u][k], v[u][k + 1], h.beta2, h.beta2, s0, s1);
+                v[u][k] = __fadd_rn(s0, t0);
+                v[u][k + 1] = __fadd_rn(s1, t1);
+            } else {
+                fma2v(h.beta2, h.beta2, v[u][k], v[u][k + 1], t0, t1, v[u][k], v[u][k + 1]);
+            }
             top = max(max(top, __float_as_int(v[u][k])), __float_as_int(v[u][k + 1]));
             odd = min(min(odd, __float_as_uint(v[u][k]) - 1u), __float_as_uint(v[u][k + 1]) - 1u);
         }

@@ -290,6 +290,52 @@ def test_roots_and_quotients_of_one_newton_step(pmn):
         assert (np.abs(p + want) <= np.maximum(3 * U * np.abs(want), 1.5 * 2.0 ** -149)).all(), eps
 
 
+def plain_step(p, g, m, v, seed, index, lr, beta1, beta2, eps, weight_decay, step):
+    """one step in float32 torch operations, each rounded by itself; MXFP8 states, coded from their float32 values"""
+    def value(x):
+        return torch.from_numpy(values(x)).float().cuda()  # exact: 4 bits times a power of two
+
+    m, v = value(m), value(v).square()  # (the square of 4 bits is exact too)
+    g = g.float()
+    m = beta1 * m + (1.0 - beta1) * g
+    v = beta2 * v + (1.0 - beta2) * (g * g)
+    p = p * (1.0 - lr * weight_decay) - lr / (1 - beta1 ** step) * m / (torch.sqrt(v) / (1 - beta2 ** step) ** 0.5 + eps)
+
+    def coded(x, stream, keep):
+        x = f64(x)
+        e = mx64.exponent(np.abs(mx64.blocks(x)).max(-1))
+        y = np.abs(x) / np.repeat(np.ldexp(1.0, e), 32)[:x.size]
+        place = np.ldexp(1.0, np.maximum(np.frexp(np.maximum(y, 1e-300))[1] - 1, -6) - 3)
+        low = np.floor(y / place)
+        up = np.floor((y / place - low) * 65536) + mx64.random_bits(x.size, seed, 4 * index + stream, step) >= 65536
+        q = np.minimum((low + up) * place, 448.0)
+        if keep:
+            q = np.where((q == 0) & (y > 0), 2.0 ** -9, q)
+        return torch.from_numpy(np.copysign(q, x)).float().to(torch.float8_e4m3fn).view(torch.uint8), torch.from_numpy((e + 127).astype(np.uint8))
+
+    return p, coded(m, 1, False), coded(torch.sqrt(v), 2, True)
+
+
+@pytest.mark.parametrize("gk", [torch.bfloat16, torch.float32])
+def test_float32_parameters_keep_the_states_of_plain_float32(pmn, gk):
+    """the stochastic roundings are those of the formulas evaluated one operation at a time: two steps, a million
+    elements, every code and scale equal, so that p stays within its roundings of plain float32"""
+    sizes, seed = [1 << 20, 33, 70001], 77
+    p, g, m, v = make(sizes, torch.float32, gk, True, 19)
+    hp = dict(HP)
+    for step in (7, 8):
+        hp["step"] = step
+        want = [plain_step(p[i], g[i], m[i], v[i], seed, i, **hp) for i in range(3)]
+        old = clone(p)
+        pmn.adamw_step(pmn.AdamWTensors(p, g, m, v), seed=seed, **hp)
+        for i in range(3):
+            for got, ref in ((m[i], want[i][1]), (v[i], want[i][2])):
+                assert torch.equal(got[0].cpu(), ref[0]) and torch.equal(got[1].cpu(), ref[1])
+            moved = (want[i][0] - old[i]).abs().double()
+            err = (p[i].double() - want[i][0].double()).abs()
+            assert (err <= 4 * U * (want[i][0].abs() + old[i].abs()).double() + 16 * U * moved).all()
+
+
 def test_small_changes_of_v_are_kept_on_average(pmn):
     """beta2 = 0.99 moves v by at most 1 % a step, far below half a step of E4M3: rounding to nearest would leave it
     where it starts.  Stochastic rounding settles between the two neighbouring codes; their mean square is within
