@@ -416,21 +416,15 @@ def _kind(t, what):
     return k
 
 
-def _launch_stream(what, stream, *tensors):
-    """the raw handle of `stream`, or of the current stream.
-
-    A launch goes to the current GPU whatever its stream's handle says (the default stream's is the same on every
-    one), so the call's tensors (None left out) and `stream` have to be there."""
-    # (torch.cuda's own functions look for the library first, and current_stream() builds an object: 3 us of a call
-    # that takes 2 us on the GPU)
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise PmnError("%s: every tensor must be on the current GPU (cuda:%d), one is on %s" % (what, dev, t.device))
+# A launch goes to the current GPU whatever its stream's handle says (the default stream's is the same on every one),
+# so a call's tensors and its stream have to be there: `gpu` below is the current one's number.  (torch.cuda's own
+# functions look for the library first, and current_stream() builds an object: 3 us of a call that takes 2 us on the GPU.)
+def _launch_stream(what, stream, gpu):
+    """the raw handle of `stream`, or of the current stream"""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device_index != dev:
-        raise PmnError("%s: the stream is of cuda:%d, the current GPU is cuda:%d" % (what, stream.device_index, dev))
+        return torch._C._cuda_getCurrentRawStream(gpu)
+    if stream.device_index != gpu:
+        raise PmnError("%s: the stream is of cuda:%d, the current GPU is cuda:%d" % (what, stream.device_index, gpu))
     return stream.cuda_stream
 
 
@@ -447,27 +441,27 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, what, dtype=None):
-    """2-D GPU tensor whose rows are contiguous (any row pitch); returns its pitch in elements"""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise PmnError("%s must be a 2-D GPU tensor with contiguous rows" % what)
+def _rows(t, what, gpu, dtype=None):
+    """2-D tensor on the current GPU whose rows are contiguous (any row pitch); returns its pitch in elements"""
+    if t.get_device() != gpu or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise PmnError("%s must be a 2-D tensor on the current GPU (cuda:%d) with contiguous rows" % (what, gpu))
     if dtype is not None and t.dtype != dtype:
         raise PmnError("%s: expected %s, got %s" % (what, dtype, t.dtype))
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _shaped(t, shape, dtype, what):
-    """a dense GPU tensor of this shape and type (an output or operand that the kernels index by it)"""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise PmnError("%s must be a dense %s GPU tensor of shape %s" % (what, dtype, (shape,)))
+def _shaped(t, shape, dtype, what, gpu):
+    """a dense tensor of this shape and type on the current GPU (an output or operand that the kernels index by it)"""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        raise PmnError("%s must be a dense %s tensor of shape %s on the current GPU (cuda:%d)" % (what, dtype, (shape,), gpu))
     return t
 
 
-def _mxfp8_out(out, rows, cols, device, stream, what="out"):
+def _mxfp8_out(out, rows, cols, device, stream, gpu, what="out"):
     if out is None:
         return (_empty((rows, cols), torch.uint8, device, stream), _empty((rows, cols // 32), torch.uint8, device, stream))
-    _shaped(out[0], (rows, cols), torch.uint8, what)
-    _shaped(out[1], (rows, cols // 32), torch.uint8, what + " scales")
+    _shaped(out[0], (rows, cols), torch.uint8, what, gpu)
+    _shaped(out[1], (rows, cols // 32), torch.uint8, what + " scales", gpu)
     return out
 
 
@@ -478,31 +472,32 @@ def add_rmsnorm_mxfp8(x, residual, weight, eps=1e-6, out=None, res_out=None, y=N
     x bf16 [rows, cols], residual None or bf16 / float32 [rows, cols] (both may be row-strided views), weight
     bf16 [cols].  Returns ((u8 values, u8 E8M0 scales), r or None, y or None, rstd or None); y (bf16) and rstd
     (float32) are written where they are passed in or wanted."""
-    ldx = _rows(x, "x", torch.bfloat16)
+    gpu = torch._C._cuda_getDevice()
+    ldx = _rows(x, "x", gpu, torch.bfloat16)
     rows, cols = x.shape
     dev = x.device
-    _shaped(weight, (cols,), torch.bfloat16, "weight")
+    _shaped(weight, (cols,), torch.bfloat16, "weight", gpu)
     ldr, kind = 0, OUT_BF16
     if residual is not None:
-        ldr, kind = _rows(residual, "residual"), _kind(residual, "residual")
+        ldr, kind = _rows(residual, "residual", gpu), _kind(residual, "residual")
         if residual.shape != x.shape:
             raise PmnError("residual must have x's shape")
         if res_out is None:
             res_out = _empty((rows, cols), residual.dtype, dev, stream)
         else:
-            _shaped(res_out, (rows, cols), residual.dtype, "res_out")
+            _shaped(res_out, (rows, cols), residual.dtype, "res_out", gpu)
     elif res_out is not None:
         raise PmnError("res_out without a residual")
-    out = _mxfp8_out(out, rows, cols, dev, stream)
+    out = _mxfp8_out(out, rows, cols, dev, stream, gpu)
     if y is not None:
-        _shaped(y, (rows, cols), torch.bfloat16, "y")
+        _shaped(y, (rows, cols), torch.bfloat16, "y", gpu)
     elif want_y:
         y = _empty((rows, cols), torch.bfloat16, dev, stream)
     if rstd is not None:
-        _shaped(rstd, (rows,), torch.float32, "rstd")
+        _shaped(rstd, (rows,), torch.float32, "rstd", gpu)
     elif want_rstd:
         rstd = _empty((rows,), torch.float32, dev, stream)
-    raw = _launch_stream("add_rmsnorm_mxfp8", stream, x, residual, weight, res_out, out[0], out[1], y, rstd)
+    raw = _launch_stream("add_rmsnorm_mxfp8", stream, gpu)
     _check(lib().pmn_add_rmsnorm_mxfp8(_at(x), ldx, _at(residual), ldr, kind, _at(weight), rows, cols, eps,
                                        _at(res_out), _at(out[0]), _at(out[1]), _at(y), _at(rstd), raw),
            "add_rmsnorm_mxfp8")
@@ -524,24 +519,25 @@ def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=No
     x and of the residual.  dx: dr rounded to bf16 (float32 r only).  workspace: uint8 device tensor of at least
     add_rmsnorm_backward_workspace_bytes(rows, cols) bytes, allocated here when None."""
     rows, cols = dy.shape
-    dev = dy.device
-    _shaped(dy, (rows, cols), torch.bfloat16, "dy")
+    dev, gpu = dy.device, torch._C._cuda_getDevice()
+    _shaped(dy, (rows, cols), torch.bfloat16, "dy", gpu)
     kind = _kind(r, "r")
-    _shaped(r, (rows, cols), r.dtype, "r")
-    _shaped(rstd, (rows,), torch.float32, "rstd")
-    _shaped(weight, (cols,), torch.bfloat16, "weight")
+    _shaped(r, (rows, cols), r.dtype, "r", gpu)
+    _shaped(rstd, (rows,), torch.float32, "rstd", gpu)
+    _shaped(weight, (cols,), torch.bfloat16, "weight", gpu)
     if dres is not None:
-        _shaped(dres, (rows, cols), r.dtype, "dres")
-    dr = _empty(r.shape, r.dtype, dev, stream) if dr is None else _shaped(dr, (rows, cols), r.dtype, "dr")
+        _shaped(dres, (rows, cols), r.dtype, "dres", gpu)
+    dr = _empty(r.shape, r.dtype, dev, stream) if dr is None else _shaped(dr, (rows, cols), r.dtype, "dr", gpu)
     if dx is not None:
-        _shaped(dx, (rows, cols), torch.bfloat16, "dx")
+        _shaped(dx, (rows, cols), torch.bfloat16, "dx", gpu)
     elif want_dx:
         dx = _empty((rows, cols), torch.bfloat16, dev, stream)
-    dw = _empty((cols,), torch.float32, dev, stream) if dw is None else _shaped(dw, (cols,), torch.float32, "dw")
+    dw = _empty((cols,), torch.float32, dev, stream) if dw is None else _shaped(dw, (cols,), torch.float32, "dw", gpu)
     if workspace is None:
         workspace = _empty((add_rmsnorm_backward_workspace_bytes(rows, cols),), torch.uint8, dev, stream)
-    _dev(workspace)
-    raw = _launch_stream("add_rmsnorm_backward", stream, dy, r, rstd, weight, dres, dr, dx, dw, workspace)
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise PmnError("workspace must be a dense tensor on the current GPU (cuda:%d)" % gpu)
+    raw = _launch_stream("add_rmsnorm_backward", stream, gpu)
     _check(lib().pmn_add_rmsnorm_backward(_at(dy), _at(r), kind, _at(rstd), _at(weight), _at(dres), rows, cols,
                                           _at(dr), _at(dx), _at(dw), _at(workspace),
                                           workspace.numel() * workspace.element_size(), raw),
@@ -549,7 +545,7 @@ def add_rmsnorm_backward(dy, r, rstd, weight, dres=None, dr=None, dx=None, dw=No
     return dr, dx, dw
 
 
-def _gated_operands(a, b, offsets, what):
+def _gated_operands(a, b, offsets, what, gpu):
     """checks of the operands both directions share; (rows, k, experts, rows of B per expert)"""
     aq, asc = a
     bq, bsc = b
@@ -558,8 +554,8 @@ def _gated_operands(a, b, offsets, what):
     rows, k = aq.shape
     experts, n = bq.shape[0], bq.shape[1]
     for t, shape in ((aq, (rows, k)), (asc, (rows, k // 32)), (bq, (experts, n, k)), (bsc, (experts, n, k // 32))):
-        _shaped(t, shape, torch.uint8, what + ": an operand")
-    _shaped(offsets, (experts + 1,), torch.int32, what + ": offsets")
+        _shaped(t, shape, torch.uint8, what + ": an operand", gpu)
+    _shaped(offsets, (experts + 1,), torch.int32, what + ": offsets", gpu)
     return rows, k, experts, n
 
 
@@ -570,19 +566,20 @@ def w1_gemm_swiglu_mxfp8(a, b, offsets, out=None, out_t=None, y=None, want_t=Fal
     offsets int32 [E+1] on the device.  Returns (h, h_t or None, y or None): h = (u8 [T, F], u8 [T, F/32]); h_t =
     MXFP8 of h^T along the rows (u8 [F, T], u8 [F, T/32]; offsets and T multiples of 32), y = bf16 [T, 2F], both
     written where they are passed in or wanted (a training step's backward pass needs them)."""
-    rows, k, experts, f2 = _gated_operands(a, b, offsets, "w1_gemm_swiglu_mxfp8")
+    gpu = torch._C._cuda_getDevice()
+    rows, k, experts, f2 = _gated_operands(a, b, offsets, "w1_gemm_swiglu_mxfp8", gpu)
     if f2 % 2:
         raise PmnError("w1_gemm_swiglu_mxfp8: b holds as many gate as up rows, got %d in all" % f2)
     f, dev = f2 // 2, a[0].device
-    out = _mxfp8_out(out, rows, f, dev, stream)
+    out = _mxfp8_out(out, rows, f, dev, stream, gpu)
     if out_t is not None or want_t:
-        out_t = _mxfp8_out(out_t, f, rows, dev, stream, "out_t")
+        out_t = _mxfp8_out(out_t, f, rows, dev, stream, gpu, "out_t")
     if y is not None:
-        _shaped(y, (rows, f2), torch.bfloat16, "y")
+        _shaped(y, (rows, f2), torch.bfloat16, "y", gpu)
     elif want_y:
         y = _empty((rows, f2), torch.bfloat16, dev, stream)
     t, tsc = out_t if out_t is not None else (None, None)
-    raw = _launch_stream("w1_gemm_swiglu_mxfp8", stream, a[0], a[1], b[0], b[1], offsets, out[0], out[1], t, tsc, y)
+    raw = _launch_stream("w1_gemm_swiglu_mxfp8", stream, gpu)
     _check(lib().pmn_w1_gemm_swiglu_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(offsets), experts,
                                           rows, f, k, _at(out[0]), _at(out[1]), _at(t), _at(tsc), _at(y), raw),
            "w1_gemm_swiglu_mxfp8")
@@ -596,13 +593,13 @@ def dh_gemm_swiglu_backward_mxfp8(a, b, y, offsets, out=None, out_t=None, stream
     a = MXFP8 dY (u8 [T, D], u8 [T, D/32]); b = MXFP8 W2^T (u8 [E, F, D], u8 [E, F, D/32]); y = bf16 [T, 2F] of the
     forward.  Returns ((u8 [T, 2F], u8 [T, 2F/32]), (u8 [2F, T], u8 [2F, T/32])): the operands of the dX and dW1
     GEMMs.  offsets and T are multiples of 32."""
-    rows, k, experts, f = _gated_operands(a, b, offsets, "dh_gemm_swiglu_backward_mxfp8")
-    _shaped(y, (rows, 2 * f), torch.bfloat16, "y")
+    gpu = torch._C._cuda_getDevice()
+    rows, k, experts, f = _gated_operands(a, b, offsets, "dh_gemm_swiglu_backward_mxfp8", gpu)
+    _shaped(y, (rows, 2 * f), torch.bfloat16, "y", gpu)
     dev = a[0].device
-    out = _mxfp8_out(out, rows, 2 * f, dev, stream)
-    out_t = _mxfp8_out(out_t, 2 * f, rows, dev, stream, "out_t")
-    raw = _launch_stream("dh_gemm_swiglu_backward_mxfp8", stream, a[0], a[1], b[0], b[1], y, offsets, out[0], out[1],
-                         out_t[0], out_t[1])
+    out = _mxfp8_out(out, rows, 2 * f, dev, stream, gpu)
+    out_t = _mxfp8_out(out_t, 2 * f, rows, dev, stream, gpu, "out_t")
+    raw = _launch_stream("dh_gemm_swiglu_backward_mxfp8", stream, gpu)
     _check(lib().pmn_dh_gemm_swiglu_backward_mxfp8(_at(a[0]), _at(a[1]), _at(b[0]), _at(b[1]), _at(y),
                                                    _at(offsets), experts, rows, f, k, _at(out[0]), _at(out[1]),
                                                    _at(out_t[0]), _at(out_t[1]), raw),
@@ -616,7 +613,8 @@ class AdamWTensors:
     params: GPU tensors, all bf16 or all float32; grads: all bf16 or all float32, of the same lengths; m, v: float32
     tensors, or (uint8 E4M3, uint8 E8M0 per 32) pairs of m and of sqrt(v) -- adamw_states() makes zero ones; copies:
     bf16 tensors that receive the updated float32 params, or None.  Any shapes; the kernels see flat tensors.  The
-    object keeps references to the tensors, and their storage must stay where it is."""
+    object keeps references to the tensors, and their storage must stay where it is: a loop whose gradients get new
+    storage every step makes a new object every step (4 us a tensor on the host)."""
 
     def __init__(self, params, grads, m, v, copies=None):
         params, grads, m, v = list(params), list(grads), list(m), list(v)
@@ -672,9 +670,14 @@ def adamw_step(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, 
     """One AdamW step (decoupled weight decay) over the tensors of an AdamWTensors object, in place; step counts
     from 1.  grad_scale: None, or a float32 GPU tensor of one element that the gradients are multiplied by.  bf16
     params and MXFP8 states are rounded stochastically with bits that follow from seed, step and position."""
-    if grad_scale is not None and _dev(grad_scale, torch.float32).numel() != 1:
-        raise PmnError("grad_scale must have one element")
-    raw = _launch_stream("adamw_step", stream, *tensors.tensors[0][:1], grad_scale)
+    gpu = torch._C._cuda_getDevice()
+    if tensors.device not in (None, gpu):
+        raise PmnError("adamw_step: the tensors are on cuda:%d, the current GPU is cuda:%d" % (tensors.device, gpu))
+    if grad_scale is not None:
+        if grad_scale.numel() != 1:
+            raise PmnError("grad_scale must have one element")
+        _shaped(grad_scale, grad_scale.shape, torch.float32, "grad_scale", gpu)
+    raw = _launch_stream("adamw_step", stream, gpu)
     _check(lib().pmn_adamw_step(tensors.table, tensors.count, tensors.param_kind, tensors.grad_kind,
                                 tensors.state_kind, lr, beta1, beta2, eps, weight_decay, step, _at(grad_scale),
                                 seed, raw),
