@@ -110,7 +110,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[T / 32], int slot
 // columns (16 bytes of bf16) per piece; four adjacent lanes hold one 32-column
 // block and take its maximum with two shuffles.
 // Measured on one GB300: 16384 x 4096 in bf16 with y written, 89 us, 6.85 TB/s, all
-// that HBM gives; one row 1.8 us, the latency of a launch and two dependent steps.
+// that HBM gives, in float32 127 us, 6.9 TB/s; one row 1.8 us, the latency of a launch
+// and two dependent steps.
 template <int T, int NP, int RK>
 __global__ void __launch_bounds__(CTA) add_rmsnorm_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                                                           const void *res, int64_t ldr,
@@ -207,8 +208,12 @@ __global__ void __launch_bounds__(CTA) add_rmsnorm_kernel(const uint16_t *__rest
 // written; rows of more than 8192 columns have no registers for that.
 // Measured on one GB300: 16384 x 4096 in bf16 92.6 us, 5.8 TB/s (79 us at HBM's rate:
 // one wave of CTAs has fewer loads in flight than a copy, and the partial sums are 5 MB
-// and a second kernel); 1021 x 1536 in float32 7.1 us (3.7), latency of the two
-// launches; 16384 columns 2.8 TB/s (registers spill).
+// and a second kernel); 1021 x 1536 in float32 7.0 us (3.7), latency of the two
+// launches.  16384 rows between the thread counts' steps, where threads hold nothing:
+// 1056 columns 38 us, 3.7 TB/s (132 of 256 threads at work), 2560 72 us, 4.7 TB/s, 5120
+// 140 us, 4.8 TB/s (62 %).  Spills: float32 rows of 257 to 512, 2049 to 4096 and 4097 to
+// 8192 columns 88, 36 and 36 bytes (5.0, 6.1, 6.2 TB/s), more than 8192 columns 508
+// (bf16) and 936 (2.9 and 2.6 TB/s).
 template <int T, int NP, int RK, int PER_SM>
 __global__ void __launch_bounds__(T == 32 ? CTA : T, PER_SM) add_rmsnorm_backward_kernel(
     const uint16_t *__restrict__ dy, const void *__restrict__ r, const float *__restrict__ rstd,

@@ -16,10 +16,11 @@ namespace pmn {
 // h = silu(a) * b = a * b / (1 + e^-a) in binary32, with the hardware's
 // approximate exponential and division (the __expf / __fdividef intrinsics:
 // a few dozen binary32 ulps at most for |a| <= 40; for a < -87 the quotient
-// is 0, against a true |silu(a)| < 2^-120 |a|).  Every SwiGLU of the library
-// (the w1 GEMM epilogue, the row quantisers' SwiGLU input modes) uses this
-// one function, so they give the same h bit for bit; h is rounded to bf16
-// afterwards, a step of 2^-8 relative.
+// is 0, against a true |silu(a)| < 2^-120 |a|).  The NVFP4 w1 GEMM's epilogue
+// and the row quantisers' SwiGLU input modes use this one function, so they
+// give the same h bit for bit; h is rounded to bf16 afterwards, a step of 2^-8
+// relative.  (The MXFP8 gated block codes h straight from float32, with a
+// sigmoid that its backward shares: gated.cu.)
 __device__ __forceinline__ float silu_mul(float a, float b)
 {
     return __fmul_rn(__fdividef(a, __fadd_rn(1.0f, __expf(-a))), b);

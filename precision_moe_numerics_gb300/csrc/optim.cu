@@ -265,10 +265,10 @@ __device__ __forceinline__ void quotient2(float n0, float n1, float d0, float d1
 // one block's scale has to serve.  Both are rounded stochastically: a step moves
 // v by about 1 - b2 of itself, far less than half a step of E4M3, and rounding to
 // nearest would never move it.  p is updated from the unrounded m and v.
-// Measured on one GB300, 75.5 million elements in four tensors: float32 parameters and
-// states 331 us, 6.8 TB/s, all that HBM gives; bf16 parameters and MXFP8 states 161 us,
-// 4.7 TB/s (113 us at HBM's rate): bound by issue, 62 instructions per element with the
-// issue slots 75 % busy.  With two groups a thread a pair of lanes shares two Philox
+// Measured on one GB300, 75.5 million elements in eight tensors: float32 parameters and
+// states 331 us, 6.8 TB/s, all that HBM gives; bf16 parameters and MXFP8 states 163 us,
+// 4.7 TB/s (113 us at HBM's rate): bound by issue, 63 instructions per element with the
+// issue slots 75 % busy (one of them, and 2 us, is the largest |m|).  With two groups a thread a pair of lanes shares two Philox
 // calls per state, and no random word is thrown away.
 template <bool PF32, bool GF32, bool MX, int MAXT>
 __global__ void __launch_bounds__(CTA, MX ? 4 : 3) adamw_kernel(const __grid_constant__ Table<MAXT> tab, const Hyper h)

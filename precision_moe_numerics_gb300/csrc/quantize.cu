@@ -1554,11 +1554,10 @@ pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fo
     return launch_rows_bf16(h, rows, cols, fos, codes, scales, outer, row_end, s);
 }
 
-// Reads and clears the quantisation kernels' device error bits (called by
-// pmn_get_device_error, which owns the stream synchronisation).
 pmn_status pmn_take_gated_device_error(cudaStream_t s, int *bits);  // gated.cu
 
-// The error bits of this file's kernels and of the gated block's.
+// Reads and clears the device error bits of this file's kernels and of the gated
+// block's (called by pmn_get_device_error, which adds the GEMMs').
 pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits)
 {
     int host = 0, gated = 0;

@@ -240,9 +240,17 @@ class GatedBlockTrainStep:
 
     residual [T, D] bf16 or float32 and x bf16 [T, D] are rows in expert order
     (one expert: all tokens), w1 bf16 [E, 2F, D], w2 bf16 [E, D, F], gamma bf16
-    [D]; offsets device int32 [E+1], multiples of 128, 0 .. T.  T, D and F are
-    multiples of 512.  All buffers are allocated here; forward(), backward()
-    and update() only enqueue kernels on the current stream."""
+    [D]; offsets device int32 [E+1], multiples of 128, from 0 to T (rows outside
+    the segments would enter dgamma undefined).  T, D and F are multiples of
+    512.  All buffers are allocated here; forward(), backward() and update()
+    only enqueue kernels on the current stream.  forward(x) adds to the
+    residual given here, whose contents the caller may change between steps.
+
+    Measured on one GB300 (D 4096, F 1536; forward, backward, update in us, from
+    CUDA graphs): one expert with 16384 rows 352, 874, 43, and 389, 958, 43 with
+    a float32 stream; 24 experts with 8192 rows 726, 648, 944 (called from
+    Python 2490 for the three).  The weights are quantised by two calls per
+    expert."""
 
     def __init__(self, residual, w1, w2, gamma, offsets, mxfp8_states=True, lr=1e-3, weight_decay=0.1, seed=0):
         E, F2, D = w1.shape
