@@ -77,6 +77,10 @@ typedef int pmn_status;
 #define PMN_STATE_F32 0
 #define PMN_STATE_MXFP8 1
 
+/* scores of pmn_route_topk */
+#define PMN_SCORE_SOFTMAX 0
+#define PMN_SCORE_SIGMOID 1
+
 /* device error bits (pmn_get_device_error) */
 #define PMN_DEVERR_WAIT_TIMEOUT 1
 #define PMN_DEVERR_BAD_OFFSETS 2
@@ -580,6 +584,110 @@ PMN_API pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_tenso
                                   int state_kind, double lr, double beta1, double beta2, double eps,
                                   double weight_decay, int64_t step, const float *grad_scale, uint64_t seed,
                                   void *stream);
+
+/*
+ * From a router's logits to rows in expert order and back: what the grouped
+ * calls above expect of their caller (rows by expert, offsets, the tokens' row
+ * numbers and gates), made on the device.  The pages have no counterpart.
+ */
+
+/* Rows that hold every choice whatever the experts' counts are, each expert's
+ * segment padded to a multiple of `pad`; -1 for invalid arguments.  Host only. */
+PMN_API int64_t pmn_route_rows(int64_t tokens, int experts, int k, int pad);
+
+/* Workspace bytes of pmn_route_topk (0: none needed); -1 for invalid arguments.  Host only. */
+PMN_API int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int k);
+
+/*
+ * Top-k routing.  For token t, c_e = logit_e + bias_e (one float32 sum; the bias
+ * enters the choice alone); its choices i = 0 .. k-1 are the experts of the k
+ * largest c > -inf, in that order, ties to the lowest expert (-0 ties with 0).
+ *   PMN_SCORE_SOFTMAX  p = softmax of the token's logits over all experts
+ *   PMN_SCORE_SIGMOID  p_e = 1 / (1 + e^-logit_e)
+ *   gates = scale * p_e, with `normalize` divided by the sum over the choices
+ * (formed without p itself, so that it holds where every p underflows).  A token
+ * with fewer than k experts above -inf has dropped choices: expert -1, gate 0, row
+ * -1.  A NaN ranks above every number (lowest expert first); a row with a chosen NaN
+ * or +inf (softmax without `normalize`: any) has NaN among its gates, as the formulas do.
+ * Layout: offsets[0] = 0, offsets[e+1] = offsets[e] + count_e rounded up to a
+ * multiple of `pad`; the rows of an expert are in the order of their tokens.
+ *  logits   [tokens, ldl] of logits_kind PMN_OUT_F32 or PMN_OUT_BF16 (the first
+ *           `experts` of each row);  bias NULL or float32 [experts].
+ *  experts  1 .. 1024;  k 1 .. 32, <= experts;  pad 1 .. 2^20;  normalize 0 or 1.
+ *  rows     >= pmn_route_rows(tokens, experts, k, pad), < 2^31.
+ *  chosen   int32 [tokens, k];  gates float32 [tokens, k];
+ *  row_index  int32 [tokens, k]: the routed row of each choice, -1 for a dropped one;
+ *  row_choice int32 [rows]: t * k + i of the row's choice, -1 for a padding row of a
+ *           segment, -2 for a row behind the last segment;
+ *  offsets  int32 [experts + 1].
+ *  workspace  device scratch, 16-byte aligned, of pmn_route_topk_workspace_bytes
+ *           bytes (NULL where that is 0).
+ * All other pointers are aligned to their element.  tokens <= 8384512, else
+ * PMN_ERR_UNSUPPORTED; tokens == 0 writes offsets and row_choice.  One kernel on
+ * `stream` for up to 64 tokens, two for more.
+ */
+PMN_API pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits_kind, const float *bias, int64_t tokens,
+                                  int experts, int k, int score, int normalize, float scale, int pad, int64_t rows,
+                                  int32_t *chosen, float *gates, int32_t *row_index, int32_t *row_choice,
+                                  int32_t *offsets, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of pmn_route_topk's gates with respect to the logits (the choice itself
+ * has none): dlogits [tokens, experts], dense, of logits_kind, every element
+ * written; logits, chosen, score, normalize and scale as in the forward call.
+ * With d = dgates, p as above and q = p over its sum over the choices S, per token:
+ *   softmax, normalized   scale q_e (d_e - sum_S q d)            for e in S
+ *   softmax               scale p_e (d_e [e in S] - sum_S p d)   for every e
+ *   sigmoid, normalized   scale q_e (d_e - sum_S q d) (1 - p_e)  for e in S
+ *   sigmoid               scale p_e d_e (1 - p_e)                for e in S
+ * and 0 elsewhere.  A `chosen` beyond the experts adds nothing and latches
+ * PMN_DEVERR_BAD_OFFSETS.  One kernel on `stream`.
+ */
+PMN_API pmn_status pmn_route_topk_backward(const void *logits, int64_t ldl, int logits_kind, const int32_t *chosen,
+                                           const float *dgates, int64_t tokens, int experts, int k, int score,
+                                           int normalize, float scale, void *dlogits, void *stream);
+
+/*
+ * Token rows into expert order: out[row_index[t, i]] = x[t].
+ *  x        [tokens, ldx] of kind PMN_OUT_BF16 or PMN_OUT_F32; cols and ldx in
+ *           whole 16-byte pieces (multiples of 8 or 4).
+ *  row_index  DEVICE int32 [tokens, k]; negative = a dropped choice; an index >= rows
+ *           writes nothing and latches PMN_DEVERR_BAD_OFFSETS.  No row twice.
+ *  row_choice NULL, or DEVICE int32 [rows]: rows where it is -1 are written as zeros.
+ *           No other row is written.
+ *  k        1 .. 64;  out [rows, cols] of kind.
+ * One kernel on `stream`.  (Its gradient is pmn_combine_rows without gates.)
+ */
+PMN_API pmn_status pmn_dispatch_rows(const void *x, int64_t ldx, int kind, int64_t tokens, int64_t cols,
+                                     const int32_t *row_index, int k, const int32_t *row_choice, int64_t rows, void *out,
+                                     void *stream);
+
+/*
+ * Each token's sum over its routed rows, back in token order:
+ *   out[t] = sum_i gates[t, i] * z[row_index[t, i]]
+ * by float32 fma in the order of i, rounded once (pmn_combine_receive_s2f6 for rows
+ * that were not quantised).  A token without rows gets zeros.
+ *  z        [rows, cols] of kind PMN_OUT_BF16 or PMN_OUT_F32;  out [tokens, cols] of
+ *           out_kind; cols in whole 16-byte pieces of either.
+ *  gates    NULL (1), or DEVICE float32 [tokens, k].  row_index, k as above (here a
+ *           row may be named more than once).
+ */
+PMN_API pmn_status pmn_combine_rows(const void *z, int kind, int64_t rows, int64_t cols, const int32_t *row_index,
+                                    const float *gates, int64_t tokens, int k, int out_kind, void *out, void *stream);
+
+/*
+ * Gradients of pmn_combine_rows:
+ *   dz[row_index[t, i]] = gates[t, i] * dout[t]  (rounded once)
+ *   dgates[t, i] = <dout[t], z[row_index[t, i]]>  (float32; 0 for a dropped choice)
+ *  dout     [tokens, cols], z and dz [rows, cols], all of `kind`; dz is not z.
+ *  row_index  no row twice;  row_choice as in pmn_dispatch_rows: its -1 rows of dz are
+ *           zeros, and rows that it marks otherwise and no choice names are not written.
+ *  gates    NULL (1), or float32 [tokens, k];  dgates float32 [tokens, k].
+ * The sums' order depends on cols alone.
+ */
+PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, int kind, int64_t rows, int64_t cols,
+                                             const int32_t *row_index, const int32_t *row_choice, const float *gates,
+                                             int64_t tokens, int k, void *dz, float *dgates, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,755 @@
+// route.cu -- from router logits to rows in expert order and back:
+//   pmn_route_topk             chosen experts, gates, and the routed rows' layout
+//   pmn_route_topk_backward    the logits' gradient
+//   pmn_dispatch_rows          token rows -> routed rows
+//   pmn_combine_rows           the weighted sum of each token's routed rows
+//   pmn_combine_rows_backward  its gradients
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/pmn.h"
+#include "numerics.cuh"
+
+using namespace pmn;
+
+namespace {
+
+__device__ int g_route_error = 0;
+
+constexpr int MAX_EXPERTS = 1024, MAX_K = 32, MAX_CHOICES = 64;
+constexpr unsigned FULL = 0xFFFFFFFFu;
+
+inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// ====================================================================== router
+// Tokens are counted and laid out in chunks, one CTA each: at most MAX_CHUNKS, so that
+// every CTA of the second kernel can add up the counts of all of them by itself.
+constexpr int MAX_CHUNKS = 128, MIN_CHUNK = 64, SUB = 128;
+
+inline int64_t chunk_tokens(int64_t tokens)
+{
+    const int64_t c = (tokens + MAX_CHUNKS - 1) / MAX_CHUNKS;
+    return std::max<int64_t>(MIN_CHUNK, (c + 31) / 32 * 32);
+}
+
+inline int64_t chunk_count(int64_t tokens) { return (tokens + chunk_tokens(tokens) - 1) / chunk_tokens(tokens); }
+
+struct RouteArgs {
+    const void *logits;
+    int64_t ldl;
+    const float *bias;
+    int64_t tokens, chunk, rows;
+    int experts, k, score, normalize, pad;
+    float scale;
+    int32_t *chosen;
+    float *gates;
+    int32_t *row_index, *row_choice, *offsets;
+    uint16_t *counts;  // [chunks][experts]
+};
+
+template <int KIND>
+__device__ __forceinline__ float load_logit(const void *p, int64_t i)
+{
+    if (KIND == PMN_OUT_F32) return __ldg(static_cast<const float *>(p) + i);
+    return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(p) + i) << 16);
+}
+
+// Larger value, larger key; NaN above everything; -inf 0, below every other value.
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 -> +0: equal values, equal keys
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+    const uint32_t s = (u >> 31) ? ~u : (u | 0x80000000u);
+    return s == 0x007FFFFFu ? 0u : s;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+// log(1 / (1 + e^-x)), which keeps its relative precision where the sigmoid vanishes
+__device__ __forceinline__ float log_sigmoid(float x) { return __fsub_rn(fminf(x, 0.0f), log1pf(expf(-fabsf(x)))); }
+
+// One token by one warp: lane i < k gets the i-th expert (-1: no expert is left) and its gate.
+// Lane l holds experts l, l + 32, ..; k rounds take the largest key, lowest expert first.
+template <int NV, int KIND>
+__device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int lane, int &expert, float &gate)
+{
+    const int64_t at = token * p.ldl;
+    uint32_t key[NV];
+    float top = -INFINITY, total = 0.0f;
+    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
+    {
+        float v[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = lane + 32 * j < p.experts ? load_logit<KIND>(p.logits, at + lane + 32 * j) : -INFINITY;
+        if (every) {  // the denominator runs over all experts
+#pragma unroll
+            for (int j = 0; j < NV; ++j) top = fmaxf(top, v[j]);
+            top = warp_max(top);
+            if (top == -INFINITY) top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) total += expf(v[j] - top);
+            total = warp_sum(total);
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (lane + 32 * j < p.experts) v[j] = __fadd_rn(v[j], __ldg(p.bias + lane + 32 * j));
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = lane + 32 * j < p.experts ? order_key(v[j]) : 0u;
+    }
+    expert = -1;
+    for (int i = 0; i < p.k; ++i) {
+        uint32_t best = 0;
+        int which = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                which = j;
+            }
+        const uint32_t m = __reduce_max_sync(FULL, best);
+        if (m == 0u) break;
+        const int win = __reduce_min_sync(FULL, best == m ? 32 * which + lane : 0x7FFFFFFF);
+        if (lane == i) expert = win;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (32 * j + lane == win) key[j] = 0u;
+    }
+    const float l = expert >= 0 ? load_logit<KIND>(p.logits, at + expert) : -INFINITY;
+    float g;
+    if (every) {
+        g = expf(l - top) / total;
+    } else if (!p.normalize) {
+        g = 1.0f / (1.0f + expf(-l));
+    } else {
+        const float v = p.score == PMN_SCORE_SOFTMAX ? l : expert >= 0 ? log_sigmoid(l) : -INFINITY;
+        float m = warp_max(v);
+        if (m == -INFINITY) m = 0.0f;
+        const float e = expert >= 0 ? expf(v - m) : 0.0f;
+        g = e / warp_sum(e);
+    }
+    gate = expert >= 0 ? __fmul_rn(p.scale, g) : 0.0f;
+}
+
+// What the layout of a chunk needs in shared memory.
+struct Layout {
+    uint32_t mask[MAX_EXPERTS][SUB / 32];  // which of SUB tokens chose the expert
+    int32_t base[MAX_EXPERTS];             // first row that is still free
+    int32_t total[MAX_EXPERTS], first[MAX_EXPERTS + 1];
+};
+
+// Padded running sum of the totals (first[e]: the expert's first row); one warp.
+__device__ __forceinline__ void scan_offsets(const RouteArgs &p, Layout &s, int lane)
+{
+    const int per = (p.experts + 31) / 32;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = per * lane + i;
+        if (e < p.experts) sum += (s.total[e] + p.pad - 1) / p.pad * p.pad;
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, run, o);
+        if (lane >= o) run += v;
+    }
+    run -= sum;
+    for (int i = 0; i < per; ++i) {
+        const int e = per * lane + i;
+        if (e < p.experts) {
+            s.first[e] = run;
+            run += (s.total[e] + p.pad - 1) / p.pad * p.pad;
+            if (e == p.experts - 1) s.first[p.experts] = run;
+        }
+    }
+}
+
+// Rows of the chunk's choices: an expert's rows follow its tokens' order, so a choice's
+// place is the number of earlier tokens that chose the expert -- a count of bits, the same
+// in whatever order the bits were set.  s.base holds the rows left by earlier chunks.
+__device__ void place(const RouteArgs &p, Layout &s, int64_t token0, int64_t token1)
+{
+    for (int64_t t0 = token0; t0 < token1; t0 += SUB) {
+        const int n = (int)min((int64_t)SUB, token1 - t0) * p.k;
+        for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
+#pragma unroll
+            for (int w = 0; w < SUB / 32; ++w) s.mask[e][w] = 0u;
+        __syncthreads();
+        const int32_t *chosen = p.chosen + t0 * p.k;
+        for (int c = threadIdx.x; c < n; c += blockDim.x) {
+            const int e = chosen[c], t = c / p.k;
+            if (e >= 0) atomicOr(&s.mask[e][t >> 5], 1u << (t & 31));
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < n; c += blockDim.x) {
+            const int e = chosen[c], t = c / p.k;
+            int row = -1;
+            if (e >= 0) {
+                row = s.base[e] + __popc(s.mask[e][t >> 5] & ((1u << (t & 31)) - 1u));
+                for (int w = 0; w < t >> 5; ++w) row += __popc(s.mask[e][w]);
+                p.row_choice[row] = (int32_t)(t0 * p.k + c);
+            }
+            p.row_index[t0 * p.k + c] = row;
+        }
+        if (t0 + SUB >= token1) break;
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
+#pragma unroll
+            for (int w = 0; w < SUB / 32; ++w) s.base[e] += __popc(s.mask[e][w]);
+        __syncthreads();
+    }
+}
+
+// -1 for the padding rows of the segments, -2 for the rows behind the last one.
+__device__ void mark_padding(const RouteArgs &p, const Layout &s)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int e = blockIdx.x * warps + warp; e < p.experts; e += gridDim.x * warps)
+        for (int r = s.first[e] + s.total[e] + lane; r < s.first[e + 1]; r += 32) p.row_choice[r] = -1;
+    for (int64_t r = s.first[p.experts] + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < p.rows;
+         r += (int64_t)gridDim.x * blockDim.x)
+        p.row_choice[r] = -2;
+}
+
+// One CTA per chunk, one warp per token.  ONE: a single chunk, laid out here as well.
+template <int NV, int KIND, bool ONE>
+__global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(const RouteArgs p)
+{
+    __shared__ Layout s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    int32_t *count = s.total;
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+    for (int64_t t = t0 + warp; t < t1; t += warps) {
+        int expert;
+        float gate;
+        choose<NV, KIND>(p, t, lane, expert, gate);
+        if (lane < p.k) {
+            p.chosen[t * p.k + lane] = expert;
+            p.gates[t * p.k + lane] = gate;
+            if (expert >= 0) atomicAdd(count + expert, 1);
+        }
+    }
+    __syncthreads();
+    if (!ONE) {
+        for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
+            p.counts[(int64_t)blockIdx.x * p.experts + e] = (uint16_t)count[e];
+        return;
+    }
+    if (warp == 0) scan_offsets(p, s, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
+        p.offsets[e] = s.first[e];
+        if (e < p.experts) s.base[e] = s.first[e];
+    }
+    place(p, s, t0, t1);
+    mark_padding(p, s);
+}
+
+__global__ void __launch_bounds__(512) route_place_kernel(const RouteArgs p, int chunks)
+{
+    __shared__ Layout s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the choosing kernel still runs
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
+        int before = 0, all = 0;
+        const uint16_t *c = p.counts + e;
+#pragma unroll 16
+        for (int i = 0; i < chunks; ++i) {
+            const int n = __ldcg(c + (int64_t)i * p.experts);
+            all += n;
+            if (i < (int)blockIdx.x) before += n;
+        }
+        s.total[e] = all;
+        s.base[e] = before;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) scan_offsets(p, s, threadIdx.x);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
+        if (blockIdx.x == 0) p.offsets[e] = s.first[e];
+        if (e < p.experts) s.base[e] += s.first[e];
+    }
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    place(p, s, t0, min(p.tokens, t0 + p.chunk));
+    mark_padding(p, s);
+}
+
+template <int NV, int KIND>
+pmn_status launch_route(const RouteArgs &p, cudaStream_t s)
+{
+    const int chunks = (int)chunk_count(p.tokens);
+    const int threads = std::min<int64_t>(NV > 16 ? 512 : 1024, std::max<int64_t>(128, 32 * p.tokens));
+    if (chunks == 1) {
+        route_choose_kernel<NV, KIND, true><<<1, threads, 0, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    }
+    route_choose_kernel<NV, KIND, false><<<chunks, threads, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)chunks);
+    cfg.blockDim = dim3(512);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, route_place_kernel, p, chunks) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+template <int KIND>
+pmn_status route_by_experts(const RouteArgs &p, cudaStream_t s)
+{
+    if (p.experts <= 64) return launch_route<2, KIND>(p, s);
+    if (p.experts <= 128) return launch_route<4, KIND>(p, s);
+    if (p.experts <= 256) return launch_route<8, KIND>(p, s);
+    if (p.experts <= 384) return launch_route<12, KIND>(p, s);
+    if (p.experts <= 512) return launch_route<16, KIND>(p, s);
+    return launch_route<32, KIND>(p, s);
+}
+
+__global__ void route_empty_kernel(int32_t *offsets, int experts, int32_t *row_choice, int64_t rows)
+{
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i <= experts) offsets[i] = 0;
+    for (int64_t r = i; r < rows; r += (int64_t)gridDim.x * blockDim.x) row_choice[r] = -2;
+}
+
+struct RouteGradArgs {
+    const void *logits;
+    int64_t ldl;
+    const int32_t *chosen;
+    const float *dgates;
+    int64_t tokens;
+    int experts, k, score, normalize;
+    float scale;
+    void *dlogits;
+};
+
+template <int KIND>
+__device__ __forceinline__ void store_grad(void *p, int64_t i, float v)
+{
+    if (KIND == PMN_OUT_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// One warp per token: the k chosen entries from the chosen logits (every entry, where the
+// gates' denominator runs over all experts), zeros elsewhere.
+template <int KIND>
+__global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= p.tokens) return;
+    const int64_t at = t * p.ldl, out = t * p.experts;
+    int e = -1;
+    float d = 0.0f;
+    if (lane < p.k) {
+        e = p.chosen[t * p.k + lane];
+        d = p.dgates[t * p.k + lane];
+    }
+    if (e < 0 || e >= p.experts) {  // a dropped choice, or not an expert's number
+        if (e >= p.experts) atomicOr(&g_route_error, PMN_DEVERR_BAD_OFFSETS);
+        e = -1;
+        d = 0.0f;
+    }
+    const float l = e >= 0 ? load_logit<KIND>(p.logits, at + e) : -INFINITY;
+    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
+    float g = 0.0f, top = -INFINITY, total = 0.0f, sg = 0.0f;
+    if (p.score == PMN_SCORE_SIGMOID) sg = 1.0f / (1.0f + expf(l));  // 1 - sigmoid, without its cancellation
+    if (every) {
+        for (int c = lane; c < p.experts; c += 32) top = fmaxf(top, load_logit<KIND>(p.logits, at + c));
+        top = warp_max(top);
+        if (top == -INFINITY) top = 0.0f;
+        for (int c = lane; c < p.experts; c += 32) total += expf(load_logit<KIND>(p.logits, at + c) - top);
+        total = warp_sum(total);
+        g = e >= 0 ? expf(l - top) / total : 0.0f;
+    } else if (p.normalize) {
+        const float v = e < 0 ? -INFINITY : p.score == PMN_SCORE_SOFTMAX ? l : log_sigmoid(l);
+        float m = warp_max(v);
+        if (m == -INFINITY) m = 0.0f;
+        const float x = e >= 0 ? expf(v - m) : 0.0f;
+        const float sum = warp_sum(x);
+        g = e >= 0 ? x / sum : 0.0f;
+    } else {
+        g = e >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+    }
+    const float dot = p.score == PMN_SCORE_SIGMOID && !p.normalize ? 0.0f : warp_sum(__fmul_rn(g, d));
+    float grad = __fmul_rn(__fmul_rn(p.scale, g), __fsub_rn(d, dot));
+    if (p.score == PMN_SCORE_SIGMOID) grad = __fmul_rn(grad, sg);
+    if (every) {
+        for (int c = lane; c < p.experts; c += 32) {
+            const float q = total > 0.0f || total != total ? expf(load_logit<KIND>(p.logits, at + c) - top) / total : 0.0f;
+            store_grad<KIND>(p.dlogits, out + c, -__fmul_rn(__fmul_rn(p.scale, q), dot));
+        }
+    } else {
+        for (int c = lane; c < p.experts; c += 32) store_grad<KIND>(p.dlogits, out + c, 0.0f);
+    }
+    __syncwarp();  // the chosen entries are written after the row
+    if (e >= 0) store_grad<KIND>(p.dlogits, out + e, grad);
+}
+
+// ====================================================================== rows
+// Sixteen bytes of a row: N values as float32.
+template <int KIND>
+struct Vec {
+    static constexpr int N = KIND == PMN_OUT_F32 ? 4 : 8;
+    static __device__ __forceinline__ void unpack(const uint4 &q, float (&v)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = u4_word(q, i);
+            if (KIND == PMN_OUT_F32) {
+                v[i] = __uint_as_float(w);
+            } else {
+                v[(2 * i) % N] = __uint_as_float(w << 16);
+                v[(2 * i + 1) % N] = __uint_as_float(w & 0xFFFF0000u);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[N])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (KIND == PMN_OUT_F32) {
+                w[i] = __float_as_uint(v[i]);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[(2 * i) % N], v[(2 * i + 1) % N]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// The CTAs behind the tokens' look for padding rows and write zeros there, PAD_ROWS each.
+constexpr int PAD_ROWS = 32;
+
+__device__ __forceinline__ void zero_padding(const int32_t *row_choice, int64_t rows, uint4 *out, int vecs, int64_t block)
+{
+    const int64_t r0 = block * PAD_ROWS;
+    const int n = (int)min((int64_t)PAD_ROWS, rows - r0), lane = threadIdx.x & 31;
+    uint32_t pads = __ballot_sync(FULL, lane < n && __ldg(row_choice + r0 + lane) == -1);
+    for (; pads; pads &= pads - 1) {
+        uint4 *o = out + (r0 + __ffs(pads) - 1) * vecs;
+        for (int v = threadIdx.x; v < vecs; v += blockDim.x) o[v] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// A row number of a choice: -1 where it was dropped, or is not a row (the error word then says so).
+__device__ __forceinline__ int32_t checked_row(int32_t r, int64_t rows)
+{
+    if (r >= rows) {
+        atomicOr(&g_route_error, PMN_DEVERR_BAD_OFFSETS);
+        return -1;
+    }
+    return r;
+}
+
+// Each token's row is read once and written to its k rows.
+__global__ void __launch_bounds__(256)
+    dispatch_kernel(const uint4 *__restrict__ x, int64_t ldv, int64_t tokens, int vecs, const int32_t *__restrict__ row_index,
+                    int k, const int32_t *__restrict__ row_choice, int64_t rows, uint4 *out, int64_t token_blocks, int per_block)
+{
+    if (blockIdx.x >= token_blocks) {
+        zero_padding(row_choice, rows, out, vecs, blockIdx.x - token_blocks);
+        return;
+    }
+    const int sub = per_block > 1 ? threadIdx.x / vecs : 0;
+    const int64_t t = (int64_t)blockIdx.x * per_block + sub;
+    if (sub >= per_block || t >= tokens) return;
+    const int32_t *idx = row_index + t * k;
+    for (int v = threadIdx.x - sub * vecs; v < vecs; v += blockDim.x) {
+        const uint4 q = __ldcs(x + t * ldv + v);
+        for (int i = 0; i < k; ++i) {
+            const int32_t r = checked_row(__ldg(idx + i), rows);
+            if (r >= 0) __stcs(out + (int64_t)r * vecs + v, q);
+        }
+        if (per_block > 1) break;
+    }
+}
+
+// out = sum of gate * row, in the order of the choices.
+template <int KIND, int OUT>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const uint4 *__restrict__ z, int64_t rows, int vecs, const int32_t *__restrict__ row_index,
+                   const float *__restrict__ gates, int64_t tokens, int k, void *out, int per_block)
+{
+    constexpr int N = Vec<KIND>::N;
+    const int sub = per_block > 1 ? threadIdx.x / vecs : 0;
+    const int64_t t = (int64_t)blockIdx.x * per_block + sub;
+    if (sub >= per_block || t >= tokens) return;
+    const int32_t *idx = row_index + t * k;
+    for (int v = threadIdx.x - sub * vecs; v < vecs; v += blockDim.x) {
+        float acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+        for (int i0 = 0; i0 < k; i0 += 8) {
+            uint4 q[8];
+            float g[8];
+            bool on[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t r = i0 + i < k ? checked_row(__ldg(idx + i0 + i), rows) : -1;
+                on[i] = r >= 0;
+                if (on[i]) {
+                    q[i] = __ldcs(z + (int64_t)r * vecs + v);
+                    g[i] = gates ? __ldg(gates + t * k + i0 + i) : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (on[i]) {
+                    float w[N];
+                    Vec<KIND>::unpack(q[i], w);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) acc[j] = fmaf(g[i], w[j], acc[j]);
+                }
+        }
+        if constexpr (KIND == OUT) {
+            static_cast<uint4 *>(out)[t * vecs + v] = Vec<KIND>::pack(acc);
+        } else if constexpr (OUT == PMN_OUT_F32) {
+            float4 *o = static_cast<float4 *>(out) + (t * vecs + v) * 2;
+            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            o[1] = make_float4(acc[4 % N], acc[5 % N], acc[6 % N], acc[7 % N]);
+        } else {
+            uint2 *o = static_cast<uint2 *>(out) + t * vecs + v;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(acc[0], acc[1]), b = __floats2bfloat162_rn(acc[2], acc[3]);
+            *o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        }
+        if (per_block > 1) break;
+    }
+}
+
+// One CTA per token: dz = gate * dout and the k sums <dout, z>, eight choices at a time.
+template <int KIND>
+__global__ void __launch_bounds__(256)
+    combine_backward_kernel(const uint4 *__restrict__ dout, const uint4 *__restrict__ z, int64_t tokens, int vecs,
+                            const int32_t *__restrict__ row_index, const int32_t *__restrict__ row_choice,
+                            const float *__restrict__ gates, int k, int64_t rows, uint4 *dz, float *dgates)
+{
+    constexpr int N = Vec<KIND>::N;
+    __shared__ float part[8][8];
+    if (blockIdx.x >= tokens) {
+        zero_padding(row_choice, rows, dz, vecs, blockIdx.x - tokens);
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int i0 = 0; i0 < k; i0 += 8) {
+        int32_t r[8];
+        float g[8], dot[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[i] = i0 + i < k ? checked_row(__ldg(row_index + t * k + i0 + i), rows) : -1;
+            g[i] = r[i] >= 0 && gates ? __ldg(gates + t * k + i0 + i) : 1.0f;
+            dot[i] = 0.0f;
+        }
+        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+            float d[N];
+            Vec<KIND>::unpack(__ldg(dout + t * vecs + v), d);
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r[i] >= 0) q[i] = __ldcs(z + (int64_t)r[i] * vecs + v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r[i] >= 0) {
+                    float w[N], o[N];
+                    Vec<KIND>::unpack(q[i], w);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        dot[i] = fmaf(d[j], w[j], dot[i]);
+                        o[j] = __fmul_rn(g[i], d[j]);
+                    }
+                    __stcs(dz + (int64_t)r[i] * vecs + v, Vec<KIND>::pack(o));
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[i] = warp_sum(dot[i]);
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) part[warp][i] = dot[i];
+        __syncthreads();
+        if (threadIdx.x < 8 && i0 + (int)threadIdx.x < k) {
+            float sum = 0.0f;
+            for (int w = 0; w < warps; ++w) sum = __fadd_rn(sum, part[w][threadIdx.x]);
+            dgates[t * k + i0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+int kind_bytes(int kind) { return kind == PMN_OUT_BF16 ? 2 : kind == PMN_OUT_F32 ? 4 : 0; }
+
+// What the three row calls ask of their sizes.
+bool good_rows(int64_t tokens, int64_t cols, int kind, int k, int64_t rows)
+{
+    const int b = kind_bytes(kind);
+    return b && tokens >= 0 && tokens < (int64_t(1) << 31) - 1 && cols >= 0 && cols < (int64_t(1) << 28) && cols * b % 16 == 0 &&
+           k >= 1 && k <= MAX_CHOICES && rows >= 0 && rows < (int64_t(1) << 31);
+}
+
+bool good_grid(int64_t blocks) { return blocks < (int64_t(1) << 31); }
+
+}  // namespace
+
+pmn_status pmn_take_route_device_error(cudaStream_t s, int *bits)
+{
+    int host = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&host, g_route_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return PMN_ERR_CUDA;
+    if (host != 0 &&
+        (cudaMemcpyToSymbolAsync(g_route_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+         cudaStreamSynchronize(s) != cudaSuccess))
+        return PMN_ERR_CUDA;
+    *bits = host;
+    return PMN_OK;
+}
+
+extern "C" int64_t pmn_route_rows(int64_t tokens, int experts, int k, int pad)
+{
+    if (tokens < 0 || tokens >= (int64_t(1) << 31) || experts < 1 || experts > MAX_EXPERTS || k < 1 || k > MAX_K || k > experts ||
+        pad < 1 || pad > (1 << 20))
+        return -1;
+    const int64_t n = tokens * k;
+    return (n + std::min<int64_t>(experts, n) * (pad - 1)) / pad * pad;
+}
+
+extern "C" int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int k)
+{
+    if (pmn_route_rows(tokens, experts, k, 1) < 0) return -1;
+    return tokens == 0 || chunk_count(tokens) == 1 ? 0 : (chunk_count(tokens) * experts * 2 + 15) / 16 * 16;
+}
+
+extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits_kind, const float *bias, int64_t tokens,
+                                     int experts, int k, int score, int normalize, float scale, int pad, int64_t rows,
+                                     int32_t *chosen, float *gates, int32_t *row_index, int32_t *row_choice,
+                                     int32_t *offsets, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int64_t need = pmn_route_rows(tokens, experts, k, pad);
+    if (need < 0 || rows < need || rows >= (int64_t(1) << 31) || !kind_bytes(logits_kind) || ldl < experts ||
+        (score != PMN_SCORE_SOFTMAX && score != PMN_SCORE_SIGMOID) || (normalize != 0 && normalize != 1))
+        return PMN_ERR_INVALID_ARG;
+    if (!offsets || (rows > 0 && !row_choice) || !aligned(offsets, 4) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
+    if (tokens > (int64_t)MAX_CHUNKS * 65504) return PMN_ERR_UNSUPPORTED;  // a chunk's counts are 16 bits wide
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        route_empty_kernel<<<64, 256, 0, s>>>(offsets, experts, row_choice, rows);
+        return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    }
+    const int64_t ws = pmn_route_topk_workspace_bytes(tokens, experts, k);
+    if (!logits || !chosen || !gates || !row_index || !aligned(logits, kind_bytes(logits_kind)) || !aligned(bias, 4) ||
+        !aligned(chosen, 4) || !aligned(gates, 4) || !aligned(row_index, 4) || workspace_bytes < ws ||
+        (ws > 0 && (!workspace || !aligned(workspace, 16))))
+        return PMN_ERR_INVALID_ARG;
+    const RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, score, normalize, pad, scale,
+                      chosen, gates, row_index, row_choice, offsets, static_cast<uint16_t *>(workspace)};
+    return logits_kind == PMN_OUT_F32 ? route_by_experts<PMN_OUT_F32>(a, s) : route_by_experts<PMN_OUT_BF16>(a, s);
+}
+
+extern "C" pmn_status pmn_route_topk_backward(const void *logits, int64_t ldl, int logits_kind, const int32_t *chosen,
+                                              const float *dgates, int64_t tokens, int experts, int k, int score,
+                                              int normalize, float scale, void *dlogits, void *stream)
+{
+    if (pmn_route_rows(tokens, experts, k, 1) < 0 || !kind_bytes(logits_kind) || ldl < experts ||
+        (score != PMN_SCORE_SOFTMAX && score != PMN_SCORE_SIGMOID) || (normalize != 0 && normalize != 1))
+        return PMN_ERR_INVALID_ARG;
+    if (tokens == 0) return PMN_OK;
+    if (!logits || !chosen || !dgates || !dlogits || !aligned(logits, kind_bytes(logits_kind)) ||
+        !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4))
+        return PMN_ERR_INVALID_ARG;
+    const RouteGradArgs a{logits, ldl, chosen, dgates, tokens, experts, k, score, normalize, scale, dlogits};
+    const unsigned blocks = (unsigned)((tokens + 7) / 8);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (logits_kind == PMN_OUT_F32) route_backward_kernel<PMN_OUT_F32><<<blocks, 256, 0, s>>>(a);
+    else route_backward_kernel<PMN_OUT_BF16><<<blocks, 256, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+extern "C" pmn_status pmn_dispatch_rows(const void *x, int64_t ldx, int kind, int64_t tokens, int64_t cols,
+                                        const int32_t *row_index, int k, const int32_t *row_choice, int64_t rows, void *out,
+                                        void *stream)
+{
+    if (!good_rows(tokens, cols, kind, k, rows) || ldx < cols || ldx * kind_bytes(kind) % 16 != 0) return PMN_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return PMN_OK;
+    if (!out || !aligned(out, 16) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || !row_index || !aligned(x, 16) || !aligned(row_index, 4))) return PMN_ERR_INVALID_ARG;
+    const int vecs = (int)(cols * kind_bytes(kind) / 16), per_block = vecs < 256 ? 256 / vecs : 1;
+    const int64_t token_blocks = (tokens + per_block - 1) / per_block;
+    const int64_t blocks = token_blocks + (row_choice ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0);
+    if (!good_grid(blocks)) return PMN_ERR_UNSUPPORTED;
+    if (blocks == 0) return PMN_OK;
+    dispatch_kernel<<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint4 *>(x), ldx * kind_bytes(kind) / 16, tokens, vecs, row_index, k, row_choice, rows,
+        static_cast<uint4 *>(out), token_blocks, per_block);
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+extern "C" pmn_status pmn_combine_rows(const void *z, int kind, int64_t rows, int64_t cols, const int32_t *row_index,
+                                       const float *gates, int64_t tokens, int k, int out_kind, void *out, void *stream)
+{
+    if (!good_rows(tokens, cols, kind, k, rows) || !kind_bytes(out_kind) || cols * kind_bytes(out_kind) % 16 != 0)
+        return PMN_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return PMN_OK;
+    if ((rows > 0 && !z) || !row_index || !out || !aligned(z, 16) || !aligned(out, 16) || !aligned(row_index, 4) ||
+        !aligned(gates, 4))
+        return PMN_ERR_INVALID_ARG;
+    const int vecs = (int)(cols * kind_bytes(kind) / 16), per_block = vecs < 256 ? 256 / vecs : 1;
+    const unsigned blocks = (unsigned)((tokens + per_block - 1) / per_block);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+#define PMN_COMBINE(IN, OUT)                                                                                          \
+    combine_kernel<IN, OUT><<<blocks, 256, 0, s>>>(static_cast<const uint4 *>(z), rows, vecs, row_index, gates, tokens, k, \
+                                                   out, per_block)
+    if (kind == PMN_OUT_F32 && out_kind == PMN_OUT_F32) PMN_COMBINE(PMN_OUT_F32, PMN_OUT_F32);
+    else if (kind == PMN_OUT_F32) PMN_COMBINE(PMN_OUT_F32, PMN_OUT_BF16);
+    else if (out_kind == PMN_OUT_F32) PMN_COMBINE(PMN_OUT_BF16, PMN_OUT_F32);
+    else PMN_COMBINE(PMN_OUT_BF16, PMN_OUT_BF16);
+#undef PMN_COMBINE
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+extern "C" pmn_status pmn_combine_rows_backward(const void *dout, const void *z, int kind, int64_t rows, int64_t cols,
+                                                const int32_t *row_index, const int32_t *row_choice, const float *gates,
+                                                int64_t tokens, int k, void *dz, float *dgates, void *stream)
+{
+    if (!good_rows(tokens, cols, kind, k, rows) || cols == 0) return PMN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!dout || !row_index || !dgates || !aligned(dout, 16) || !aligned(row_index, 4) || !aligned(dgates, 4)))
+        return PMN_ERR_INVALID_ARG;
+    if (rows > 0 && (!z || !dz || !aligned(z, 16) || !aligned(dz, 16))) return PMN_ERR_INVALID_ARG;
+    if (!aligned(row_choice, 4) || !aligned(gates, 4)) return PMN_ERR_INVALID_ARG;
+    const int vecs = (int)(cols * kind_bytes(kind) / 16);
+    const int64_t blocks = tokens + (row_choice ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0);
+    if (!good_grid(blocks)) return PMN_ERR_UNSUPPORTED;
+    if (blocks == 0) return PMN_OK;
+    const int threads = std::min(256, std::max(32, (vecs + 31) / 32 * 32));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+#define PMN_BACKWARD(KIND)                                                                                         \
+    combine_backward_kernel<KIND><<<(unsigned)blocks, threads, 0, s>>>(                                            \
+        static_cast<const uint4 *>(dout), static_cast<const uint4 *>(z), tokens, vecs, row_index, row_choice, gates, k, rows, \
+        static_cast<uint4 *>(dz), dgates)
+    if (kind == PMN_OUT_F32) PMN_BACKWARD(PMN_OUT_F32);
+    else PMN_BACKWARD(PMN_OUT_BF16);
+#undef PMN_BACKWARD
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}

@@ -7,6 +7,7 @@ libpmn.so, and raises on a non-zero status.  Every step of the computation
 runs in the library's CUDA kernels; there is no fallback path -- if the
 library is missing or fails to load, every call raises.
 """
+import collections
 import ctypes
 import os
 
@@ -22,6 +23,7 @@ ROUND_SR, ROUND_RN = 0, 1
 OUT_BF16, OUT_F32, OUT_RHT_S2F6, OUT_SWIGLU_BF16 = 0, 1, 2, 3
 GROUP_M, GROUP_K = 0, 1
 STATE_F32, STATE_MXFP8 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 DEVERR_WAIT_TIMEOUT = 1
 DEVERR_BAD_OFFSETS = 2
 
@@ -63,6 +65,13 @@ SIGNATURES = {
     "pmn_add_rmsnorm_backward_workspace_bytes": ([_I64, _I64], _I64),
     "pmn_w1_gemm_swiglu_mxfp8": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P], _I),
     "pmn_dh_gemm_swiglu_backward_mxfp8": ([_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P], _I),
+    "pmn_route_rows": ([_I64, _I, _I, _I], _I64),
+    "pmn_route_topk_workspace_bytes": ([_I64, _I, _I], _I64),
+    "pmn_route_topk": ([_P, _I64, _I, _P, _I64, _I, _I, _I, _I, _F, _I, _I64, _P, _P, _P, _P, _P, _P, _I64, _P], _I),
+    "pmn_route_topk_backward": ([_P, _I64, _I, _P, _P, _I64, _I, _I, _I, _I, _F, _P, _P], _I),
+    "pmn_dispatch_rows": ([_P, _I64, _I, _I64, _I64, _P, _I, _P, _I64, _P, _P], _I),
+    "pmn_combine_rows": ([_P, _I, _I64, _I64, _P, _P, _I64, _I, _I, _P, _P], _I),
+    "pmn_combine_rows_backward": ([_P, _P, _I, _I64, _I64, _P, _P, _P, _I64, _I, _P, _P, _P], _I),
     "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
@@ -682,3 +691,161 @@ def adamw_step(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, 
                                 tensors.state_kind, lr, beta1, beta2, eps, weight_decay, step, _at(grad_scale),
                                 seed, raw),
            "adamw_step")
+
+
+# ------------------------------------------------------------------ routing
+Routing = collections.namedtuple("Routing", "experts gates row_index row_choice offsets")
+Routing.__doc__ = """What route_topk makes: experts int32 [tokens, k] (-1: a dropped choice), gates float32 [tokens, k], row_index
+int32 [tokens, k] (the routed row of each choice, -1 for a dropped one), row_choice int32 [rows] (t * k + i of the row's
+choice; -1 for a segment's padding, -2 behind the last segment), offsets int32 [experts + 1]."""
+
+
+def route_rows(tokens, experts, k, pad=1):
+    """rows that hold every choice whatever the experts' counts are"""
+    n = lib().pmn_route_rows(tokens, experts, k, pad)
+    if n < 0:
+        raise PmnError("route_rows: invalid arguments")
+    return n
+
+
+def route_topk_workspace_bytes(tokens, experts, k):
+    n = lib().pmn_route_topk_workspace_bytes(tokens, experts, k)
+    if n < 0:
+        raise PmnError("route_topk_workspace_bytes: invalid arguments")
+    return n
+
+
+def route_topk(logits, k, bias=None, score=SCORE_SOFTMAX, normalize=True, scale=1.0, pad=1, rows=None, out=None,
+               workspace=None, stream=None):
+    """Top-k routing of logits [tokens, experts] (bf16 or float32, rows may be strided) -> Routing.
+
+    The k largest logit + bias choose (ties to the lowest expert; bias None or float32 [experts]); the gates are the
+    chosen softmax or sigmoid scores, divided by their sum with normalize, times scale.  Each expert's segment of rows is
+    padded to a multiple of pad; rows (default route_rows(...)): length of row_choice.  workspace: uint8 device tensor of
+    at least route_topk_workspace_bytes(...) bytes, allocated here when None."""
+    gpu = torch._C._cuda_getDevice()
+    ldl, kind = _rows(logits, "logits", gpu), _kind(logits, "logits")
+    tokens, experts = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _shaped(bias, (experts,), torch.float32, "bias", gpu)
+    if rows is None:
+        rows = out.row_choice.numel() if out is not None else route_rows(tokens, experts, k, pad)
+    shapes = ((tokens, k), torch.int32), ((tokens, k), torch.float32), ((tokens, k), torch.int32), ((rows,), torch.int32), \
+        ((experts + 1,), torch.int32)
+    if out is None:
+        out = Routing(*[_empty(shape, dtype, dev, stream) for shape, dtype in shapes])
+    else:
+        for t, (shape, dtype), name in zip(out, shapes, Routing._fields):
+            _shaped(t, shape, dtype, name, gpu)
+    if workspace is None:
+        workspace = _empty((route_topk_workspace_bytes(tokens, experts, k),), torch.uint8, dev, stream)
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise PmnError("workspace must be a dense tensor on the current GPU (cuda:%d)" % gpu)
+    raw = _launch_stream("route_topk", stream, gpu)
+    _check(lib().pmn_route_topk(_at(logits), ldl, kind, _at(bias), tokens, experts, k, score, int(normalize), scale, pad,
+                                rows, *[_at(t) for t in out], _at(workspace),
+                                workspace.numel() * workspace.element_size(), raw),
+           "route_topk")
+    return out
+
+
+def route_topk_backward(logits, experts, dgates, score=SCORE_SOFTMAX, normalize=True, scale=1.0, dlogits=None, stream=None):
+    """Gradient of route_topk's gates: dlogits [tokens, experts] of the logits' type, from dgates float32 [tokens, k] and
+    the Routing's experts."""
+    gpu = torch._C._cuda_getDevice()
+    ldl, kind = _rows(logits, "logits", gpu), _kind(logits, "logits")
+    tokens, n = logits.shape
+    if experts.dim() != 2:
+        raise PmnError("experts is [tokens, k]")
+    k = experts.shape[1]
+    _shaped(experts, (tokens, k), torch.int32, "experts", gpu)
+    _shaped(dgates, (tokens, k), torch.float32, "dgates", gpu)
+    if dlogits is None:
+        dlogits = _empty((tokens, n), logits.dtype, logits.device, stream)
+    else:
+        _shaped(dlogits, (tokens, n), logits.dtype, "dlogits", gpu)
+    raw = _launch_stream("route_topk_backward", stream, gpu)
+    _check(lib().pmn_route_topk_backward(_at(logits), ldl, kind, _at(experts), _at(dgates), tokens, n, k, score,
+                                         int(normalize), scale, _at(dlogits), raw),
+           "route_topk_backward")
+    return dlogits
+
+
+def _choices(row_index, row_choice, gates, what, gpu):
+    """checks of the tensors that tie tokens to rows; (tokens, k)"""
+    if row_index.dim() != 2:
+        raise PmnError("%s: row_index is [tokens, k]" % what)
+    tokens, k = row_index.shape
+    _shaped(row_index, (tokens, k), torch.int32, what + ": row_index", gpu)
+    if gates is not None:
+        _shaped(gates, (tokens, k), torch.float32, what + ": gates", gpu)
+    if row_choice is not None:
+        _shaped(row_choice, (row_choice.numel(),), torch.int32, what + ": row_choice", gpu)
+    return tokens, k
+
+
+def dispatch_rows(x, row_index, row_choice, out=None, stream=None):
+    """Token rows x [tokens, cols] (bf16 or float32, rows may be strided) into expert order: out [rows, cols] with
+    out[row_index[t, i]] = x[t], zeros where row_choice [rows] is -1; rows that it marks -2 are not written.  The gradient
+    of x is combine_rows of the rows' gradient."""
+    gpu = torch._C._cuda_getDevice()
+    tokens, k = _choices(row_index, row_choice, None, "dispatch_rows", gpu)
+    ldx, kind = _rows(x, "x", gpu), _kind(x, "x")
+    if x.shape[0] != tokens:
+        raise PmnError("dispatch_rows: x and row_index have one row per token")
+    rows, cols = row_choice.numel(), x.shape[1]
+    if out is None:
+        out = _empty((rows, cols), x.dtype, x.device, stream)
+    else:
+        _shaped(out, (rows, cols), x.dtype, "out", gpu)
+    raw = _launch_stream("dispatch_rows", stream, gpu)
+    _check(lib().pmn_dispatch_rows(_at(x), ldx, kind, tokens, cols, _at(row_index), k, _at(row_choice), rows, _at(out), raw),
+           "dispatch_rows")
+    return out
+
+
+def combine_rows(z, row_index, gates=None, out_dtype=None, out=None, stream=None):
+    """out[t] = sum_i gates[t, i] * z[row_index[t, i]] (gates None: 1) of rows z [rows, cols], bf16 or float32; out
+    [tokens, cols] of out_dtype (default: z's)."""
+    gpu = torch._C._cuda_getDevice()
+    tokens, k = _choices(row_index, None, gates, "combine_rows", gpu)
+    kind = _kind(z, "z")
+    if z.dim() != 2:
+        raise PmnError("combine_rows: z is [rows, cols]")
+    rows, cols = z.shape
+    _shaped(z, (rows, cols), z.dtype, "z", gpu)
+    if out is None:
+        out = _empty((tokens, cols), out_dtype or z.dtype, z.device, stream)
+    else:
+        _shaped(out, (tokens, cols), out_dtype or out.dtype, "out", gpu)
+    raw = _launch_stream("combine_rows", stream, gpu)
+    _check(lib().pmn_combine_rows(_at(z), kind, rows, cols, _at(row_index), _at(gates), tokens, k, _kind(out, "out"),
+                                  _at(out), raw),
+           "combine_rows")
+    return out
+
+
+def combine_rows_backward(dout, z, row_index, row_choice, gates=None, dz=None, dgates=None, stream=None):
+    """Gradients of combine_rows: (dz [rows, cols] of z's type, dgates float32 [tokens, k]) from dout [tokens, cols] of z's
+    type; rows of dz that row_choice marks -1 are zeros, those it marks -2 are not written."""
+    gpu = torch._C._cuda_getDevice()
+    tokens, k = _choices(row_index, row_choice, gates, "combine_rows_backward", gpu)
+    kind = _kind(z, "z")
+    if z.dim() != 2:
+        raise PmnError("combine_rows_backward: z is [rows, cols]")
+    rows, cols = z.shape
+    _shaped(z, (rows, cols), z.dtype, "z", gpu)
+    _shaped(dout, (tokens, cols), z.dtype, "dout", gpu)
+    if row_choice is not None and row_choice.numel() != rows:
+        raise PmnError("combine_rows_backward: z and row_choice have one entry per row")
+    dz = _empty((rows, cols), z.dtype, z.device, stream) if dz is None else _shaped(dz, (rows, cols), z.dtype, "dz", gpu)
+    if dgates is None:
+        dgates = _empty((tokens, k), torch.float32, z.device, stream)
+    else:
+        _shaped(dgates, (tokens, k), torch.float32, "dgates", gpu)
+    raw = _launch_stream("combine_rows_backward", stream, gpu)
+    _check(lib().pmn_combine_rows_backward(_at(dout), _at(z), kind, rows, cols, _at(row_index), _at(row_choice), _at(gates),
+                                           tokens, k, _at(dz), _at(dgates), raw),
+           "combine_rows_backward")
+    return dz, dgates
