@@ -689,6 +689,57 @@ PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, in
                                              const int32_t *row_index, const int32_t *row_choice, const float *gates,
                                              int64_t tokens, int k, void *dz, float *dgates, void *stream);
 
+/*
+ * The products of an expert layer whose experts are kept in bf16 (the precision that
+ * the low formats are held against, and a layer's choice where they are not wanted);
+ * the pages have no counterpart.  float32 accumulation on the tensor cores.  The
+ * experts' segments of rows may have any lengths; nothing has to be padded.
+ *
+ * group_mode PMN_GROUP_M: for the rows r of group g, offsets[g] <= r < offsets[g+1],
+ *     out[r, :] = a[r, :] . B_g^T  with b [num_groups, n, k]   (b_transposed 0)
+ *     out[r, :] = a[r, :] . B_g    with b [num_groups, k, n]   (b_transposed 1: weights
+ *                                  as the forward has them, dX = dY . W)
+ *   a [m, lda], out [m, n]; rows outside every segment are not written.
+ * group_mode PMN_GROUP_K: out[g] = sum over the rows r of group g of a[r, :]^T b[r, :]
+ *     (dW = dY^T . X, both as they are stored); a [k, lda] of m columns, b [k, ldb]
+ *     of n columns, out [num_groups, m, n]; zeros where a group has no rows.  b_transposed 0.
+ * A NaN or infinity reaches the rows (GROUP_K: sums) that it takes part in and no others.
+ *  offsets  DEVICE int32 [num_groups + 1], non-decreasing, within [0, m] (GROUP_K:
+ *           [0, k]); checked on the device: bad offsets run nothing and latch
+ *           PMN_DEVERR_BAD_OFFSETS.  num_groups <= 1024.
+ *  n, lda, ldb multiples of 8, and k (GROUP_M) or m (GROUP_K); ldb is read for GROUP_K alone.
+ *  out_kind PMN_OUT_BF16 (nearest even) or PMN_OUT_F32.
+ * One kernel on `stream`.
+ */
+PMN_API pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,
+                                         int num_groups, int group_mode, int b_transposed, int64_t m, int64_t n,
+                                         int64_t k, int out_kind, void *out, void *stream);
+
+/*
+ * The gated projection of a bf16 expert in one kernel:
+ *   y = a . B_e^T (gate = its first f columns, up = the last f; float32)
+ *   out = silu(gate) * up from the float32 y, rounded once to bf16
+ *  a [total_rows, lda] of k columns;  b [num_experts, 2 f, k];  out [total_rows, f];
+ *  y_out    NULL, or bf16 [total_rows, 2 f]: y rounded to nearest even.
+ *  f        multiple of 16;  k and lda of 8;  offsets and the rest as above (GROUP_M).
+ * The sigmoid has a relative error of (|gate| + 8) 2^-23 at most.
+ */
+PMN_API pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const void *b, const int32_t *offsets,
+                                           int num_experts, int64_t total_rows, int64_t f, int64_t k, void *out,
+                                           void *y_out, void *stream);
+
+/*
+ * Backward of the gated projection as far as its pre-activations, in one kernel:
+ *   dh = a . B_e (a = dY [total_rows, lda] of k columns, b = W2 [num_experts, k, f]; float32)
+ *   s = 1 / (1 + e^-gate);  dup = dh * gate * s;
+ *   dgate = dh * up * s * (1 + gate * (1 - s));   out = [dgate | dup], rounded once
+ *  y        bf16 [total_rows, 2 f]: gate | up as the forward wrote them.
+ *  out      bf16 [total_rows, 2 f].  f, k and lda multiples of 8; the rest as above.
+ */
+PMN_API pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t lda, const void *b, const void *y,
+                                                    const int32_t *offsets, int num_experts, int64_t total_rows,
+                                                    int64_t f, int64_t k, void *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1249,6 +1249,7 @@ extern "C" const char *pmn_status_string(pmn_status st)
 
 pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits);  // quantize.cu
 pmn_status pmn_take_route_device_error(cudaStream_t s, int *bits);  // route.cu
+pmn_status pmn_take_bf16_device_error(cudaStream_t s, int *bits);   // gemm_bf16.cu
 pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fos, uint8_t *codes,
                                uint8_t *scales, float *outer, const int32_t *row_end, cudaStream_t s);  // quantize.cu
 
@@ -1256,8 +1257,9 @@ extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
 {
     if (!err) return PMN_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int qbits = 0, rbits = 0;
-    if (pmn_take_quant_device_error(s, &qbits) != PMN_OK || pmn_take_route_device_error(s, &rbits) != PMN_OK)
+    int qbits = 0, rbits = 0, bbits = 0;
+    if (pmn_take_quant_device_error(s, &qbits) != PMN_OK || pmn_take_route_device_error(s, &rbits) != PMN_OK ||
+        pmn_take_bf16_device_error(s, &bbits) != PMN_OK)
         return PMN_ERR_CUDA;
     int host = 0;
     if (cudaMemcpyFromSymbolAsync(&host, g_pmn_device_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
@@ -1271,7 +1273,7 @@ extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
             cudaStreamSynchronize(s) != cudaSuccess)
             return PMN_ERR_CUDA;
     }
-    *err = host | qbits | rbits;
+    *err = host | qbits | rbits | bbits;
     return PMN_OK;
 }
 

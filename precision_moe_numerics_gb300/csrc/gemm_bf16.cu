@@ -1,0 +1,653 @@
+// gemm_bf16.cu -- the bf16 products of experts whose row counts are ragged:
+//   pmn_grouped_gemm_bf16               rows by expert, or sums over each expert's rows
+//   pmn_w1_gemm_swiglu_bf16             gate and up projections and silu(gate) * up
+//   pmn_dh_gemm_swiglu_backward_bf16    dH = dY . W2 and SwiGLU's gradient
+// One persistent kernel of CTA pairs (tcgen05 kind::f16, float32 accumulators in TMEM).
+// The tensor core's M side (256 TMEM lanes of a pair) are the columns of the output -- weight rows, or
+// the columns of X in a weight gradient -- and its N side the output's rows, the ragged
+// axis: a tile is 32 to 256 of them wide, in steps of 32, so an expert's rows are
+// divided evenly and waste less than 32 of them where a tile with rows on the M side wastes up to
+// 255.  An accumulator column is then a row of the output, 32 lanes of a warp write 32
+// neighbours of it, and the rows behind a segment are simply not stored.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "../../include/pmn.h"
+#include "numerics.cuh"
+#include "sm100.cuh"
+#include "tensormap.cuh"
+
+using namespace pmn;
+using namespace pmn::sm100;
+
+uint64_t pmn_wait_limit_ns();  // gemm.cu: the limit of every bounded device wait
+
+namespace {
+
+__device__ int g_bf16_error = 0;
+
+constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int TILE = 256;       // output columns of a pair's tile, and most rows
+constexpr int STAGES = 6, SIDE_BYTES = 128 * 128, STAGE_BYTES = 2 * SIDE_BYTES;  // a CTA's 128 x 64 of either operand
+constexpr int EW = 8, THREADS = 128 + 32 * EW;
+constexpr int BAR_OFF = STAGES * STAGE_BYTES, CUM_OFF = BAR_OFF + 256;
+constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
+constexpr int MT_BLOCK = 8;  // column tiles that share a tile's rows before the next rows are taken
+constexpr uint64_t DRAIN_NS = 100000000ull;
+
+// Rows times weights [n, k] and [k, n], the forward with SwiGLU, the gradient of h, sums over rows.
+constexpr int ROWS_NK = 0, ROWS_KN = 1, GATED = 2, GATED_BACKWARD = 3, SUMS = 4;
+
+struct Args {
+    const int32_t *offsets;
+    int groups;
+    int64_t rows;      // of the ragged axis, all groups
+    int64_t m, n, k;   // SUMS: out [groups, m, n]; else: weight rows n (of h: f), contraction k
+    void *out;
+    uint16_t *y;       // GATED: written (or NULL); GATED_BACKWARD: read
+    uint64_t wait_ns;
+};
+
+struct Maps {
+    CUtensorMap w;      // M side
+    CUtensorMap w8, w1; // SUMS: 8 rows and 1 row of it
+    CUtensorMap x;      // N side: 128 rows (SUMS: 64 columns of 64 rows)
+    CUtensorMap x8, x1; // 16 rows (SUMS: 8 rows); SUMS: 1 row
+};
+
+struct Tile {
+    int g, width;      // N side, a multiple of 32
+    int64_t lo, hi;    // the group's rows
+    int64_t r0;        // first output row
+    int64_t row_end;   // output rows end here
+    int c0;            // first output column of the pair
+};
+
+__device__ __forceinline__ int even_width(int64_t m)
+{
+    const int nt = (int)((m + TILE - 1) / TILE);
+    return (int)(((m + nt - 1) / nt + 31) / 32 * 32);
+}
+
+template <int FORM>
+struct Form {
+    static constexpr bool sums = FORM == SUMS, gated = FORM == GATED, backward = FORM == GATED_BACKWARD;
+    static constexpr bool m_major_w = FORM == ROWS_KN || backward || sums;  // the M side's contiguous axis is M
+    static constexpr int cols = gated ? TILE / 2 : TILE;                    // output columns of a pair's tile
+};
+
+template <int FORM>
+__device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int &gc)
+{
+    constexpr int COLS = Form<FORM>::cols;
+    const int mt = (int)((p.n + COLS - 1) / COLS);
+    while (gc + 1 < p.groups && s_cum[gc + 1] <= t) ++gc;  // every role walks its tiles upwards
+    Tile ti;
+    ti.g = gc;
+    ti.lo = __ldg(p.offsets + gc);
+    ti.hi = __ldg(p.offsets + gc + 1);
+    const int64_t rows = Form<FORM>::sums ? p.m : ti.hi - ti.lo;
+    const int nt = (int)((rows + TILE - 1) / TILE);
+    ti.width = even_width(rows);
+    // column tiles in blocks: the tiles in flight read few rows and few weights
+    const int local = t - s_cum[gc], block = local / (MT_BLOCK * nt), rest = local - block * MT_BLOCK * nt;
+    const int bw = min(MT_BLOCK, mt - block * MT_BLOCK), ri = rest / bw;
+    ti.c0 = (block * MT_BLOCK + rest - ri * bw) * COLS;
+    ti.r0 = (Form<FORM>::sums ? 0 : ti.lo) + (int64_t)ri * ti.width;
+    ti.row_end = Form<FORM>::sums ? p.m : ti.hi;
+    return ti;
+}
+
+// 64-deep stages of a tile.
+template <int FORM>
+__device__ __forceinline__ int stages_of(const Tile &ti, const Args &p)
+{
+    return (int)(((Form<FORM>::sums ? ti.hi - ti.lo : p.k) + 63) / 64);
+}
+
+__device__ __forceinline__ void latch_error(int bit) { atomicOr(&g_bf16_error, bit); }
+
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_5d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int a, int b, int c, int d,
+                                            int e)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(el)
+        : "memory");
+}
+
+// SUMS: `rows` (1 to 64) of a stage's 64 ragged rows of 64 columns, then zeros up to a
+// multiple of 16: another expert's rows, or the buffer's last contents, would enter the
+// sums.  Rows behind the tensor read as zeros.
+__device__ __forceinline__ uint32_t sum_rows(int rows) { return (uint32_t)(rows + 15) & ~15u; }
+
+__device__ __forceinline__ void load_sum_rows(uint32_t dst, const CUtensorMap *m64, const CUtensorMap *m8,
+                                              const CUtensorMap *m1, uint32_t bar, int x, int y, int rows, int outside)
+{
+    if (rows == 64) {
+        tma_load_2d_pair(dst, m64, bar, x, y);
+        return;
+    }
+    const int end = (int)sum_rows(rows);
+    int r = 0;
+    for (; r + 8 <= rows; r += 8) tma_load_2d_pair(dst + 128 * r, m8, bar, x, y + r);
+    if (r < rows) {
+        const int stop = r + 8;
+        for (; r < rows; ++r) tma_load_2d_pair(dst + 128 * r, m1, bar, x, y + r);
+        for (; r < stop; ++r) tma_load_2d_pair(dst + 128 * r, m1, bar, x, outside);
+    }
+    for (; r < end; r += 8) tma_load_2d_pair(dst + 128 * r, m8, bar, x, outside);
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
+
+__device__ __forceinline__ void store_one(uint16_t *p, float v)
+{
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    *p = *reinterpret_cast<const uint16_t *>(&b);
+}
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Roles: warp 0 loads by TMA, warp 1 of the leader issues the pair's MMAs, warps 4.. store.
+// Every wait is bounded: on a timeout an error bit is latched and the CTA winds down.
+template <int FORM, typename OUT>
+__global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant__ Maps maps, const Args p)
+{
+    using F = Form<FORM>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw;
+    asm volatile("" : "+l"(smem));
+    const uint32_t stages = smem_u32(smem);
+    const uint32_t bar_full = stages + BAR_OFF, bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 5));
+    int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
+    int *s_total = s_abort + 1;
+    int *s_cum = reinterpret_cast<int *>(smem + CUM_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int tile0 = blockIdx.x / 2, tstep = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_acc_full + 8 * b, 1);
+            mbar_init(bar_acc_empty + 8 * b, 2 * EW);
+        }
+        mbar_init(bar_drain, 1);
+        *s_abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&maps.w);
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.x8);
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc_ct<2>(smem_u32(tmem_slot), TMEM_COLS);
+    }
+    if (warp == 1) {
+        // tiles of each group and their running sum, 32 groups at a time; offsets that
+        // are not monotone and in range run no tile
+        const int mt = (int)((p.n + F::cols - 1) / F::cols);
+        int base = 0;
+        bool good = true;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            const int g = g0 + lane;
+            int lo = 0, hi = 0;
+            if (g < p.groups) {
+                lo = __ldg(p.offsets + g);
+                hi = __ldg(p.offsets + g + 1);
+                if (lo < 0 || hi < lo || hi > p.rows) good = false;
+            }
+            good = __all_sync(0xFFFFFFFFu, good);
+            if (!good) break;
+            const int64_t rows = F::sums ? (g < p.groups ? p.m : 0) : hi - lo;
+            int n = (int)((rows + TILE - 1) / TILE) * mt, sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (g < p.groups) s_cum[g] = base + sum - n;
+            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (lane == 0) {
+            s_cum[p.groups] = base;
+            *s_total = good ? base : 0;
+            if (!good && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the pair's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = __shfl_sync(0xFFFFFFFFu, *s_total, 0);
+    auto give_up = [&]() {  // a wait ran out: every role winds down
+        if (lane == 0) {
+            *(volatile int *)s_abort = 1;
+            latch_error(PMN_DEVERR_WAIT_TIMEOUT);
+        }
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        uint32_t stage = 0, phase = 0, issued = 0, last = 0;
+        int gc = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok; t += tstep) {
+            const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
+            const int nks = stages_of<FORM>(ti, p), half = ti.width / 2;
+            for (int ks = 0; ks < nks; ++ks) {
+                ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
+                    if (!ok) give_up();
+                    ok = false;
+                    break;
+                }
+                const uint32_t w = stages + stage * STAGE_BYTES, x = w + SIDE_BYTES, fb = bar_full + 8 * stage;
+                if (elect_one()) {
+                    const uint32_t lb = leader_addr(fb);
+                    if constexpr (F::sums) {
+                        const int64_t k0 = ti.lo + 64 * ks;
+                        const int rows = (int)min((int64_t)64, ti.hi - k0), xb = (half + 63) / 64, out = (int)p.rows;
+                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * 128 * sum_rows(rows) * (2 + xb));
+                        for (int b = 0; b < 2; ++b)
+                            load_sum_rows(w + 8192 * b, &maps.w, &maps.w8, &maps.w1, lb, ti.c0 + 128 * rank + 64 * b, (int)k0, rows, out);
+                        for (int b = 0; b < xb; ++b)
+                            load_sum_rows(x + 8192 * b, &maps.x, &maps.x8, &maps.x1, lb, (int)ti.r0 + half * rank + 64 * b, (int)k0, rows, out);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * (SIDE_BYTES + 128 * half));
+                        if constexpr (FORM == ROWS_NK) {
+                            tma_3d_pair(w, &maps.w, lb, 64 * ks, ti.c0 + 128 * rank, ti.g);
+                        } else if constexpr (FORM == GATED) {
+                            tma_5d_pair(w, &maps.w, lb, 64 * ks, 0, 0, (ti.c0 + 64 * rank) / 16, ti.g);
+                        } else {
+                            tma_3d_pair(w, &maps.w, lb, ti.c0 + 128 * rank, 64 * ks, ti.g);
+                            tma_3d_pair(w + 8192, &maps.w, lb, ti.c0 + 128 * rank + 64, 64 * ks, ti.g);
+                        }
+                        const int row = (int)ti.r0 + half * rank;
+                        if (half == 128) tma_load_2d_pair(x, &maps.x, lb, 64 * ks, row);
+                        else
+                            for (int r = 0; r < half; r += 16) tma_load_2d_pair(x + 128 * r, &maps.x8, lb, 64 * ks, row + r);
+                    }
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                last = (last & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // no copy may still be landing when the CTA ends; a pair's copies are counted by
+        // its leader, and both CTAs end together
+        for (int s = 0; s < STAGES; ++s)
+            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, (last >> s) & 1u, DRAIN_NS);
+        if (*(volatile int *)s_abort) {  // one side may have given up before the other: let copies land
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 10000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        // The whole warp walks the loop; one elected lane issues.
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), el = elect_one();
+            uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
+            int gc = 0;
+            bool ok = true, ready = false;
+            for (int t = tile0; t < total && ok; t += tstep) {
+                const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
+                const int nks = stages_of<FORM>(ti, p);
+                // D float32, A and B bf16, M = 256
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (F::m_major_w ? 1u << 15 : 0u) |
+                                       (F::sums ? 1u << 16 : 0u) | ((uint32_t)(ti.width >> 3) << 17) | (16u << 24);
+                ok = warp_wait(bar_acc_empty + 8 * abuf, aphase ^ 1, p.wait_ns);
+                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
+                    if (!ok) give_up();
+                    break;
+                }
+                const uint32_t d = tm + abuf * TILE;
+                for (int ks = 0; ks < nks; ++ks) {
+                    // asked for a stage ahead, the answer is there when it is needed
+                    if (__all_sync(0xFFFFFFFFu, ready) == 0) {
+                        ok = warp_wait(bar_full + 8 * stage, phase, p.wait_ns);
+                        if (!ok) {
+                            give_up();
+                            break;
+                        }
+                    }
+                    tc_fence_after();
+                    const uint32_t w = stages + stage * STAGE_BYTES, x = w + SIDE_BYTES, done = bar_empty + 8 * stage;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    ready = mbar_test(bar_full + 8 * stage, phase);
+                    // 16 of K per MMA: 32 bytes of the swizzled rows where K is contiguous, 16 rows
+                    // where it is not (8192 bytes between 64-wide blocks of the other axis)
+                    const int steps = F::sums ? (int)min((int64_t)4, (ti.hi - ti.lo - 64 * ks + 15) / 16) : 4;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (s < steps)
+                            mma_bf16_pair(el, d, F::m_major_w ? smem_desc(w + 2048 * s, 8192, 1024, 2) : smem_desc(w + 32 * s, 16, 1024, 2),
+                                          F::sums ? smem_desc(x + 2048 * s, 8192, 1024, 2) : smem_desc(x + 32 * s, 16, 1024, 2),
+                                          idesc, (ks > 0 || s > 0) ? 1u : 0u);
+                    }
+                    tc_commit_ct<2>(el, done);
+                }
+                if (!ok) break;
+                tc_commit_ct<2>(el, bar_acc_full + 8 * abuf);
+                if (++abuf == 2) {
+                    abuf = 0;
+                    aphase ^= 1;
+                }
+            }
+            if (elect_one()) tc_commit_own<2>(bar_drain);  // every tcgen05 operation of this warp has completed
+            __syncwarp();
+            (void)warp_wait(bar_drain, 0, DRAIN_NS);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---------------------------------------------------- epilogue
+        // A lane holds one column of the output, a register one row; a warp has every
+        // (EW / 4)th chunk of 32 rows.
+        const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0), quad = wu & 3, c_first = (wu - 4) >> 2;
+        uint32_t abuf = 0, aphase = 0;
+        int gc = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok; t += tstep) {
+            const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
+            const int chunks = ti.width / 32;
+            const bool nothing = F::sums && ti.hi == ti.lo;  // a sum over no rows
+            ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * TILE;
+            for (int c = c_first; c < chunks; c += EW / 4) {
+                float v[32];
+                tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
+                tmem_ld_wait();
+                if (nothing) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                const int64_t r0 = ti.r0 + 32 * c;
+                const int rows = (int)min((int64_t)32, ti.row_end - r0);
+                if constexpr (FORM == GATED) {
+                    // lanes 0 .. 15 gate, 16 .. 31 up of the same 16 columns: the halves trade
+                    // values, so that the lower half makes h of the even rows, the upper of the odd
+                    const int col = ti.c0 + 64 * rank + 16 * quad + (lane & 15);
+                    const bool up = lane >= 16, on = col < p.n;
+                    uint16_t *y = p.y ? p.y + r0 * 2 * p.n + col + (up ? p.n : 0) : nullptr;
+                    uint16_t *h = static_cast<uint16_t *>(p.out) + (r0 + up) * p.n + col;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        if (y && on && j < rows) store_one(y + j * 2 * p.n, v[j]);
+                        if (y && on && j + 1 < rows) store_one(y + (j + 1) * 2 * p.n, v[j + 1]);
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
+                        const float g = up ? got : v[j], u = up ? v[j + 1] : got;
+                        if (on && j + up < rows) store_one(h + j * p.n, __fmul_rn(__fmul_rn(g, sigmoid(g)), u));
+                    }
+                } else {
+                    const int col = ti.c0 + 128 * rank + 32 * quad + lane;
+                    if (col < p.n) {
+                        if constexpr (FORM == GATED_BACKWARD) {
+                            const uint16_t *y = p.y + r0 * 2 * p.n + col;
+                            uint16_t *o = static_cast<uint16_t *>(p.out) + r0 * 2 * p.n + col;
+#pragma unroll
+                            for (int j0 = 0; j0 < 32; j0 += 16) {
+                                uint16_t gate[16], up[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (j0 + j < rows) {
+                                        gate[j] = __ldg(y + (j0 + j) * 2 * p.n);
+                                        up[j] = __ldg(y + (j0 + j) * 2 * p.n + p.n);
+                                    }
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (j0 + j < rows) {
+                                        const float g = bf16_value(gate[j]), u = bf16_value(up[j]), dh = v[j0 + j];
+                                        const float s = sigmoid(g), a = __fmul_rn(dh, s);
+                                        store_one(o + (j0 + j) * 2 * p.n, __fmul_rn(__fmul_rn(a, u), fmaf(g, 1.0f - s, 1.0f)));
+                                        store_one(o + (j0 + j) * 2 * p.n + p.n, __fmul_rn(a, g));
+                                    }
+                            }
+                        } else {
+                            OUT *o = static_cast<OUT *>(p.out) + (F::sums ? (int64_t)ti.g * p.m * p.n : 0) + r0 * p.n + col;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < rows) store_one(o + j * p.n, v[j]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(bar_acc_empty + 8 * abuf);
+            if (++abuf == 2) {
+                abuf = 0;
+                aphase ^= 1;
+            }
+        }
+        if (!ok) give_up();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA's memory is still in use by the other
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc_ct<2>(tmem, TMEM_COLS);
+    cluster_sync();
+}
+
+// ====================================================================== host
+bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// rows [rows, width] of pitch ld, 64 columns (128 bytes) of box_rows rows
+bool rows_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int64_t ld, int box_rows)
+{
+    const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, st[1] = {(uint64_t)ld * 2};
+    const uint32_t box[2] = {64, (uint32_t)box_rows};
+    return make_map(m, base, 2, dims, st, box);
+}
+
+inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <int FORM, typename OUT>
+pmn_status launch(const Maps &maps, const Args &args, cudaStream_t s)
+{
+    auto kern = bf16_kernel<FORM, OUT>;
+    static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return PMN_ERR_CUDA;
+    int sms = dev < MAX_DEVICES ? sm_count[dev].load(std::memory_order_acquire) : 0;
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2 ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+            return PMN_ERR_CUDA;
+        if (dev < MAX_DEVICES) sm_count[dev].store(sms, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+constexpr int64_t LIMIT = int64_t(1) << 31;
+
+// Sizes that every form asks for: rows in 16-byte pieces, 32-bit coordinates and tile counts.
+pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k)
+{
+    if (groups <= 0 || groups > MAX_GROUPS || rows < 0 || rows >= LIMIT - TILE || m < 0 || m >= LIMIT - TILE || n <= 0 ||
+        n >= LIMIT / 2 - TILE || n % 8 != 0 || k < 0 || k >= LIMIT / 2 - TILE)
+        return PMN_ERR_INVALID_ARG;
+    const int64_t tiles = (m ? groups * (m / TILE + 1) : rows / TILE + groups) * (n / (TILE / 2) + 1);
+    return tiles >= LIMIT / 2 ? PMN_ERR_UNSUPPORTED : PMN_OK;
+}
+
+// Maps of the token rows [rows, k].
+bool token_maps(Maps &maps, const void *a, int64_t rows, int64_t k, int64_t lda)
+{
+    return rows_map(&maps.x, a, k, rows, lda, 128) && rows_map(&maps.x8, a, k, rows, lda, 16);
+}
+
+// Weights [groups, rows, cols], 64 columns of box_rows rows at a time.
+bool weight_map(CUtensorMap *m, const void *b, int groups, int64_t rows, int64_t cols, int box_rows)
+{
+    const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)groups};
+    const uint64_t st[2] = {(uint64_t)cols * 2, (uint64_t)rows * cols * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+    return make_map(m, b, 3, dims, st, box);
+}
+
+}  // namespace
+
+pmn_status pmn_take_bf16_device_error(cudaStream_t s, int *bits)
+{
+    int host = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&host, g_bf16_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return PMN_ERR_CUDA;
+    if (host != 0 &&
+        (cudaMemcpyToSymbolAsync(g_bf16_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+         cudaStreamSynchronize(s) != cudaSuccess))
+        return PMN_ERR_CUDA;
+    *bits = host;
+    return PMN_OK;
+}
+
+extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,
+                                            int num_groups, int group_mode, int b_transposed, int64_t m, int64_t n,
+                                            int64_t k, int out_kind, void *out, void *stream)
+{
+    if ((group_mode != PMN_GROUP_M && group_mode != PMN_GROUP_K) || (b_transposed != 0 && b_transposed != 1) ||
+        (out_kind != PMN_OUT_BF16 && out_kind != PMN_OUT_F32))
+        return PMN_ERR_INVALID_ARG;
+    const bool sums = group_mode == PMN_GROUP_K;
+    const pmn_status st = check_sizes(num_groups, sums ? k : m, sums ? m : 0, n, sums ? 0 : k);
+    if (st != PMN_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(offsets, 4) || lda % 8 != 0) return PMN_ERR_INVALID_ARG;
+    Maps maps = {};
+    if (sums) {
+        if (b_transposed || m <= 0 || m % 8 != 0 || lda < m || ldb < n || ldb % 8 != 0) return PMN_ERR_INVALID_ARG;
+        if (!out || !offsets) return PMN_ERR_INVALID_ARG;
+        if (k == 0)  // sums over no rows
+            return cudaMemsetAsync(out, 0, (size_t)num_groups * m * n * (out_kind == PMN_OUT_F32 ? 4 : 2), s) == cudaSuccess
+                       ? PMN_OK : PMN_ERR_CUDA;
+        if (!a || !b) return PMN_ERR_INVALID_ARG;
+        if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.w8, b, n, k, ldb, 8) || !rows_map(&maps.w1, b, n, k, ldb, 1) ||
+            !rows_map(&maps.x, a, m, k, lda, 64) || !rows_map(&maps.x8, a, m, k, lda, 8) || !rows_map(&maps.x1, a, m, k, lda, 1))
+            return PMN_ERR_CUDA;
+        const Args args{offsets, num_groups, k, m, n, 0, out, nullptr, pmn_wait_limit_ns()};
+        return out_kind == PMN_OUT_F32 ? launch<SUMS, float>(maps, args, s) : launch<SUMS, uint16_t>(maps, args, s);
+    }
+    if (k <= 0 || k % 8 != 0 || lda < k) return PMN_ERR_INVALID_ARG;
+    if (m == 0) return PMN_OK;
+    if (!a || !b || !out || !offsets) return PMN_ERR_INVALID_ARG;
+    if (!token_maps(maps, a, m, k, lda) || !(b_transposed ? weight_map(&maps.w, b, num_groups, k, n, 64)
+                                                          : weight_map(&maps.w, b, num_groups, n, k, 128)))
+        return PMN_ERR_CUDA;
+    const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
+    if (b_transposed)
+        return out_kind == PMN_OUT_F32 ? launch<ROWS_KN, float>(maps, args, s) : launch<ROWS_KN, uint16_t>(maps, args, s);
+    return out_kind == PMN_OUT_F32 ? launch<ROWS_NK, float>(maps, args, s) : launch<ROWS_NK, uint16_t>(maps, args, s);
+}
+
+extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const void *b, const int32_t *offsets,
+                                              int num_experts, int64_t total_rows, int64_t f, int64_t k, void *out,
+                                              void *y_out, void *stream)
+{
+    const pmn_status st = check_sizes(num_experts, total_rows, 0, f, k);
+    if (st != PMN_OK) return st;
+    if (f % 16 != 0 || k <= 0 || k % 8 != 0 || lda < k || lda % 8 != 0) return PMN_ERR_INVALID_ARG;
+    if (total_rows == 0) return PMN_OK;
+    if (!a || !b || !offsets || !out || !aligned(a, 16) || !aligned(b, 16) || !aligned(offsets, 4) || !aligned(out, 16) ||
+        !aligned(y_out, 16))
+        return PMN_ERR_INVALID_ARG;
+    // 16 gate rows, the 16 up rows of the same columns, the next 16 gate rows, ..
+    const uint64_t dims[5] = {(uint64_t)k, 16, 2, (uint64_t)f / 16, (uint64_t)num_experts};
+    const uint64_t str[4] = {(uint64_t)k * 2, (uint64_t)f * k * 2, (uint64_t)k * 32, (uint64_t)f * k * 4};
+    const uint32_t box[5] = {64, 16, 2, 4, 1};
+    Maps maps = {};
+    if (!token_maps(maps, a, total_rows, k, lda) || !make_map(&maps.w, b, 5, dims, str, box)) return PMN_ERR_CUDA;
+    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out), pmn_wait_limit_ns()};
+    return launch<GATED, uint16_t>(maps, args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t lda, const void *b, const void *y,
+                                                       const int32_t *offsets, int num_experts, int64_t total_rows,
+                                                       int64_t f, int64_t k, void *out, void *stream)
+{
+    const pmn_status st = check_sizes(num_experts, total_rows, 0, f, k);
+    if (st != PMN_OK) return st;
+    if (k <= 0 || k % 8 != 0 || lda < k || lda % 8 != 0) return PMN_ERR_INVALID_ARG;
+    if (total_rows == 0) return PMN_OK;
+    if (!a || !b || !y || !offsets || !out || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(offsets, 4) ||
+        !aligned(out, 16))
+        return PMN_ERR_INVALID_ARG;
+    Maps maps = {};
+    if (!token_maps(maps, a, total_rows, k, lda) || !weight_map(&maps.w, b, num_experts, k, f, 64)) return PMN_ERR_CUDA;
+    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(const_cast<void *>(y)),
+                    pmn_wait_limit_ns()};
+    return launch<GATED_BACKWARD, uint16_t>(maps, args, reinterpret_cast<cudaStream_t>(stream));
+}

@@ -233,5 +233,137 @@ __device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, uint32_t r0, u
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    const bool ok = mbar_wait(bar, parity, limit_ns);
+    return __all_sync(0xFFFFFFFFu, ok) != 0;  // warp-uniform, also on a timeout
+}
+
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// tcgen05 with cta_group::2: two CTAs of a cluster compute one 256-row tile, each
+// with its own 128 rows of A and half of B's rows; the leader (rank 0) issues.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_ctas()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The leader's copy of a shared-memory address of this CTA.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrives on the leader's copy of a barrier.  CTA scope: what the arrival stands
+// for lies in this CTA's own shared memory or TMEM, was put in order before it
+// (fence.proxy.async, tcgen05.wait) and is read there by tensor instructions.  A
+// release at cluster scope takes ~1000 clocks here (measured: a pair's stage
+// 1200-1700 clocks, bound by that).
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+
+// A tile load whose bytes are counted on a barrier of the pair's leader.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+template <int CT>
+__device__ __forceinline__ void tmem_alloc_ct(uint32_t dst_smem, uint32_t ncols)
+{
+    if (CT == 1) {
+        tmem_alloc(dst_smem, ncols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CT>
+__device__ __forceinline__ void tmem_dealloc_ct(uint32_t taddr, uint32_t ncols)
+{
+    if (CT == 1) tmem_dealloc(taddr, ncols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// The tensor instructions are executed by whole warps in step and issued by one
+// lane, by a predicate inside the instruction (`el`: this is the lane): a branch
+// around them costs a reconvergence per stage, and a branch around the loop hides
+// from the compiler that their operands are warp-uniform.  Clocks per 128-deep stage
+// that the issuing warp needs: the loop in one lane 940, a branch per stage 510 to
+// 600, this form 430 (the MMAs of a pair's stage take 384).
+
+// Arrives on `bar` (in both CTAs of a pair) once the issuing lane's tcgen05
+// operations so far have completed.
+template <int CT>
+__device__ __forceinline__ void tc_commit_ct(uint32_t el, uint32_t bar)
+{
+    if (CT == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(el), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"(el),
+            "r"(bar), "h"((uint16_t)3)
+            : "memory");
+}
+
+// The same in this CTA alone.
+template <int CT>
+__device__ __forceinline__ void tc_commit_own(uint32_t bar)
+{
+    if (CT == 1) tc_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 }  // namespace sm100
 }  // namespace pmn

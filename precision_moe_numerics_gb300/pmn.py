@@ -72,6 +72,9 @@ SIGNATURES = {
     "pmn_dispatch_rows": ([_P, _I64, _I, _I64, _I64, _P, _I, _P, _I64, _P, _P], _I),
     "pmn_combine_rows": ([_P, _I, _I64, _I64, _P, _P, _I64, _I, _I, _P, _P], _I),
     "pmn_combine_rows_backward": ([_P, _P, _I, _I64, _I64, _P, _P, _P, _I64, _I, _P, _P, _P], _I),
+    "pmn_grouped_gemm_bf16": ([_P, _I64, _P, _I64, _P, _I, _I, _I, _I64, _I64, _I64, _I, _P, _P], _I),
+    "pmn_w1_gemm_swiglu_bf16": ([_P, _I64, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P], _I),
+    "pmn_dh_gemm_swiglu_backward_bf16": ([_P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P], _I),
     "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
@@ -849,3 +852,99 @@ def combine_rows_backward(dout, z, row_index, row_choice, gates=None, dz=None, d
                                            tokens, k, _at(dz), _at(dgates), raw),
            "combine_rows_backward")
     return dz, dgates
+
+
+# ------------------------------------------------------------------ bf16 experts
+def _offsets(offsets, groups, what, gpu):
+    return _shaped(offsets, (groups + 1,), torch.int32, what + ": offsets", gpu)
+
+
+def _weights(b, what, gpu):
+    if b.dim() != 3:
+        raise PmnError("%s: b is [experts, rows, columns]" % what)
+    return _shaped(b, tuple(b.shape), torch.bfloat16, what + ": b", gpu)
+
+
+def grouped_gemm_bf16(a, b, offsets, group_mode, b_transposed=False, out_dtype=None, out=None, stream=None):
+    """bf16 products over ragged groups of rows; offsets int32 [G+1] on the device, any segment lengths.
+
+    GROUP_M: a [M, K] (rows may be strided), b [G, N, K] -> [M, N], or b [G, K, N] with b_transposed; rows outside every
+    segment are not written.  GROUP_K: a [R, M], b [R, N] (both may be strided) -> [G, M, N], each group's sum of
+    a[r]^T b[r].  out_dtype: bf16 or float32 (default: bf16 rows, float32 sums)."""
+    gpu = torch._C._cuda_getDevice()
+    lda = _rows(a, "a", gpu, torch.bfloat16)
+    if group_mode == GROUP_K:
+        ldb = _rows(b, "b", gpu, torch.bfloat16)
+        if b.shape[0] != a.shape[0] or offsets.dim() != 1 or b_transposed:
+            raise PmnError("grouped_gemm_bf16: a [rows, m], b [rows, n], offsets [groups + 1]; b_transposed is GROUP_M's")
+        groups, m, n, k = offsets.numel() - 1, a.shape[1], b.shape[1], a.shape[0]
+        shape, default = (groups, m, n), torch.float32
+    else:
+        groups, n, k = _weights(b, "grouped_gemm_bf16", gpu).shape
+        if b_transposed:
+            n, k = k, n
+        if a.shape[1] != k:
+            raise PmnError("grouped_gemm_bf16: a has %d columns, the weights contract %d" % (a.shape[1], k))
+        ldb, m = 0, a.shape[0]
+        shape, default = (m, n), torch.bfloat16
+    _offsets(offsets, groups, "grouped_gemm_bf16", gpu)
+    if out is None:
+        out = _empty(shape, out_dtype or default, a.device, stream)
+    else:
+        _shaped(out, shape, out_dtype or out.dtype, "out", gpu)
+    raw = _launch_stream("grouped_gemm_bf16", stream, gpu)
+    _check(lib().pmn_grouped_gemm_bf16(_at(a), lda, _at(b), ldb, _at(offsets), groups, group_mode, int(b_transposed), m, n,
+                                       k, _kind(out, "out"), _at(out), raw),
+           "grouped_gemm_bf16")
+    return out
+
+
+def w1_gemm_swiglu_bf16(a, b, offsets, out=None, y=None, want_y=False, stream=None):
+    """The gated projection of bf16 experts in one kernel: h = silu(X . Wg^T) * (X . Wu^T).
+
+    a bf16 [T, K] (rows may be strided); b bf16 [E, 2F, K], gate rows first; offsets int32 [E+1] on the device, any
+    segment lengths.  Returns (h [T, F], y or None): y = bf16 [T, 2F], the pre-activations that a training step's
+    backward pass needs, written where it is passed in or wanted.  Rows outside every segment are not written."""
+    gpu = torch._C._cuda_getDevice()
+    lda = _rows(a, "a", gpu, torch.bfloat16)
+    experts, f2, k = _weights(b, "w1_gemm_swiglu_bf16", gpu).shape
+    rows, f = a.shape[0], f2 // 2
+    if f2 % 2 or a.shape[1] != k:
+        raise PmnError("w1_gemm_swiglu_bf16: a is [rows, k], b [experts, 2 f, k]")
+    _offsets(offsets, experts, "w1_gemm_swiglu_bf16", gpu)
+    if out is None:
+        out = _empty((rows, f), torch.bfloat16, a.device, stream)
+    else:
+        _shaped(out, (rows, f), torch.bfloat16, "out", gpu)
+    if y is not None:
+        _shaped(y, (rows, f2), torch.bfloat16, "y", gpu)
+    elif want_y:
+        y = _empty((rows, f2), torch.bfloat16, a.device, stream)
+    raw = _launch_stream("w1_gemm_swiglu_bf16", stream, gpu)
+    _check(lib().pmn_w1_gemm_swiglu_bf16(_at(a), lda, _at(b), _at(offsets), experts, rows, f, k, _at(out), _at(y), raw),
+           "w1_gemm_swiglu_bf16")
+    return out, y
+
+
+def dh_gemm_swiglu_backward_bf16(a, b, y, offsets, out=None, stream=None):
+    """Backward of the gated projection as far as its pre-activations: dH = dY . W2, then dY1 = [dgate | dup].
+
+    a = dY bf16 [T, D] (rows may be strided); b = W2 bf16 [E, D, F]; y = bf16 [T, 2F] of the forward.  Returns bf16
+    [T, 2F]: an operand of the dX and dW1 products.  Rows outside every segment are not written."""
+    gpu = torch._C._cuda_getDevice()
+    lda = _rows(a, "a", gpu, torch.bfloat16)
+    experts, k, f = _weights(b, "dh_gemm_swiglu_backward_bf16", gpu).shape
+    rows = a.shape[0]
+    if a.shape[1] != k:
+        raise PmnError("dh_gemm_swiglu_backward_bf16: a is [rows, d], b [experts, d, f]")
+    _offsets(offsets, experts, "dh_gemm_swiglu_backward_bf16", gpu)
+    _shaped(y, (rows, 2 * f), torch.bfloat16, "y", gpu)
+    if out is None:
+        out = _empty((rows, 2 * f), torch.bfloat16, a.device, stream)
+    else:
+        _shaped(out, (rows, 2 * f), torch.bfloat16, "out", gpu)
+    raw = _launch_stream("dh_gemm_swiglu_backward_bf16", stream, gpu)
+    _check(lib().pmn_dh_gemm_swiglu_backward_bf16(_at(a), lda, _at(b), _at(y), _at(offsets), experts, rows, f, k, _at(out),
+                                                  raw),
+           "dh_gemm_swiglu_backward_bf16")
+    return out
