@@ -740,6 +740,34 @@ PMN_API pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t lda, 
                                                     const int32_t *offsets, int num_experts, int64_t total_rows,
                                                     int64_t f, int64_t k, void *out, void *stream);
 
+/*
+ * The rows of a decode batch times NVFP4 weights, activations in bf16 (4-bit weights,
+ * 16-bit activations: what a serving step reads are the weights, and its few rows
+ * need not be quantised).  The pages have no counterpart.
+ *   y[r, j] = sum_i (code * scale)[e, j, i] * outer[e] * x[r', i]  for r in expert e's segment
+ *   out = y, or with swiglu silu(y[:, :n/2]) * y[:, n/2:]; rounded once
+ *  x        bf16 [tokens, ldx], the first k of each row.
+ *  codes, scales, outer  NVFP4 [num_experts, n, k] with a scale per expert.
+ *  offsets  DEVICE int32 [num_experts + 1], non-decreasing, within [0, total_rows];
+ *           checked on the device: bad offsets run nothing and latch
+ *           PMN_DEVERR_BAD_OFFSETS.  num_experts <= 1024.
+ *  row_choice NULL: r' = r (tokens == total_rows).  Or DEVICE int32 [total_rows]:
+ *           r' = row_choice[r] / choices (what pmn_route_topk writes: its tokens' rows
+ *           need not be copied); where it is negative the row counts as zeros, where r' >=
+ *           tokens too, and PMN_DEVERR_BAD_OFFSETS is latched.
+ *  n        multiple of 16 (with swiglu the n/2 gate rows come first);  k multiple of 256;
+ *           ldx of 8;  choices >= 1.
+ *  out      [total_rows, n or n/2] of out_kind PMN_OUT_BF16 or PMN_OUT_F32; rows outside
+ *           every segment are not written.
+ * Right for any number of rows, and fast for few: an expert's weights are read once
+ * per 16 of its rows (per 8 where total_rows <= 8).
+ * One kernel on `stream`; float32 sums whose order depends on k alone.
+ */
+PMN_API pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t tokens, const uint8_t *codes,
+                                    const uint8_t *scales, const float *outer, const int32_t *offsets, int num_experts,
+                                    int64_t total_rows, int64_t n, int64_t k, const int32_t *row_choice, int choices,
+                                    int swiglu, int out_kind, void *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

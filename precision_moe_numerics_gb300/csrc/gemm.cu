@@ -1250,6 +1250,7 @@ extern "C" const char *pmn_status_string(pmn_status st)
 pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits);  // quantize.cu
 pmn_status pmn_take_route_device_error(cudaStream_t s, int *bits);  // route.cu
 pmn_status pmn_take_bf16_device_error(cudaStream_t s, int *bits);   // gemm_bf16.cu
+pmn_status pmn_take_matvec_device_error(cudaStream_t s, int *bits);  // matvec.cu
 pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fos, uint8_t *codes,
                                uint8_t *scales, float *outer, const int32_t *row_end, cudaStream_t s);  // quantize.cu
 
@@ -1257,9 +1258,9 @@ extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
 {
     if (!err) return PMN_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int qbits = 0, rbits = 0, bbits = 0;
+    int qbits = 0, rbits = 0, bbits = 0, mbits = 0;
     if (pmn_take_quant_device_error(s, &qbits) != PMN_OK || pmn_take_route_device_error(s, &rbits) != PMN_OK ||
-        pmn_take_bf16_device_error(s, &bbits) != PMN_OK)
+        pmn_take_bf16_device_error(s, &bbits) != PMN_OK || pmn_take_matvec_device_error(s, &mbits) != PMN_OK)
         return PMN_ERR_CUDA;
     int host = 0;
     if (cudaMemcpyFromSymbolAsync(&host, g_pmn_device_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
@@ -1273,7 +1274,7 @@ extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
             cudaStreamSynchronize(s) != cudaSuccess)
             return PMN_ERR_CUDA;
     }
-    *err = host | qbits | rbits | bbits;
+    *err = host | qbits | rbits | bbits | mbits;
     return PMN_OK;
 }
 

@@ -75,6 +75,7 @@ SIGNATURES = {
     "pmn_grouped_gemm_bf16": ([_P, _I64, _P, _I64, _P, _I, _I, _I, _I64, _I64, _I64, _I, _P, _P], _I),
     "pmn_w1_gemm_swiglu_bf16": ([_P, _I64, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P], _I),
     "pmn_dh_gemm_swiglu_backward_bf16": ([_P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P], _I),
+    "pmn_matvec_nvfp4": ([_P, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _I, _P, _P], _I),
     "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
@@ -947,4 +948,39 @@ def dh_gemm_swiglu_backward_bf16(a, b, y, offsets, out=None, stream=None):
     _check(lib().pmn_dh_gemm_swiglu_backward_bf16(_at(a), lda, _at(b), _at(y), _at(offsets), experts, rows, f, k, _at(out),
                                                   raw),
            "dh_gemm_swiglu_backward_bf16")
+    return out
+
+
+# ------------------------------------------------------------------ few rows, 4-bit weights
+def matvec_nvfp4(x, w, offsets, row_choice=None, k=1, swiglu=False, out_dtype=None, out=None, stream=None):
+    """The rows of a decode batch times NVFP4 weights, activations in bf16.
+
+    x bf16 [T, K] (rows may be strided); w = (codes u8 [E, N, K/2], scales u8 [E, N, K/16], outer f32 [E]); offsets int32
+    [E+1] on the device.  Routed row r reads x[r], or with row_choice (int32 [rows], a Routing's) x[row_choice[r] // k].
+    Returns [rows, N], or with swiglu [rows, N/2] = silu(gate) * up of the N/2 gate rows and N/2 up rows, in bf16 or
+    float32 (default bf16); rows outside every segment are not written."""
+    gpu = torch._C._cuda_getDevice()
+    ldx = _rows(x, "x", gpu, torch.bfloat16)
+    codes, scales, outer = w
+    if codes.dim() != 3 or codes.shape[2] * 2 != x.shape[1]:
+        raise PmnError("matvec_nvfp4: x is [tokens, k], codes [experts, n, k / 2]")
+    tokens, kdim = x.shape
+    experts, n = codes.shape[0], codes.shape[1]
+    _shaped(codes, (experts, n, kdim // 2), torch.uint8, "codes", gpu)
+    _shaped(scales, (experts, n, kdim // 16), torch.uint8, "scales", gpu)
+    _shaped(outer, (experts,), torch.float32, "outer", gpu)
+    _offsets(offsets, experts, "matvec_nvfp4", gpu)
+    rows = tokens
+    if row_choice is not None:
+        rows = row_choice.numel()
+        _shaped(row_choice, (rows,), torch.int32, "row_choice", gpu)
+    shape = (rows, n // 2 if swiglu else n)
+    if out is None:
+        out = _empty(shape, out_dtype or torch.bfloat16, x.device, stream)
+    else:
+        _shaped(out, shape, out_dtype or out.dtype, "out", gpu)
+    raw = _launch_stream("matvec_nvfp4", stream, gpu)
+    _check(lib().pmn_matvec_nvfp4(_at(x), ldx, tokens, _at(codes), _at(scales), _at(outer), _at(offsets), experts, rows, n,
+                                  kdim, _at(row_choice), k, int(swiglu), _kind(out, "out"), _at(out), raw),
+           "matvec_nvfp4")
     return out
