@@ -740,6 +740,9 @@ PMN_API pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t lda, 
                                                     const int32_t *offsets, int num_experts, int64_t total_rows,
                                                     int64_t f, int64_t k, void *out, void *stream);
 
+/* Workspace bytes of pmn_matvec_nvfp4; -1 for invalid sizes.  Host only. */
+PMN_API int64_t pmn_matvec_nvfp4_workspace_bytes(int64_t total_rows, int64_t k);
+
 /*
  * The rows of a decode batch times NVFP4 weights, activations in bf16 (4-bit weights,
  * 16-bit activations: what a serving step reads are the weights, and its few rows
@@ -756,17 +759,25 @@ PMN_API pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t lda, 
  *           need not be copied); where it is negative the row counts as zeros, where r' >=
  *           tokens too, and PMN_DEVERR_BAD_OFFSETS is latched.
  *  n        multiple of 16 (with swiglu the n/2 gate rows come first);  k multiple of 256;
- *           ldx of 8;  choices >= 1.
+ *           ldx of 8;  choices >= 1;  total_rows < 2^28 - 256;  num_experts * n < 2^31 - 256.
  *  out      [total_rows, n or n/2] of out_kind PMN_OUT_BF16 or PMN_OUT_F32; rows outside
  *           every segment are not written.
+ *  workspace  device scratch, 16-byte aligned, of at least
+ *           pmn_matvec_nvfp4_workspace_bytes(total_rows, k) bytes; its contents do not
+ *           matter; calls that share one must not overlap.
+ * x enters the products as eight 4-bit digits under a scale per 16 values: a value is
+ * exact unless it is below 2^-15 of the largest of its 16 (or those below 2^-17 of the
+ * row's), and then off by 2^-23 of that (2^-40 of the row's) at most.  Sums in float32.  A
+ * row with a NaN or an infinity is multiplied value by value, slowly.
  * Right for any number of rows, and fast for few: an expert's weights are read once
- * per 16 of its rows (per 8 where total_rows <= 8).
- * One kernel on `stream`; float32 sums whose order depends on k alone.
+ * per 16 of its rows.  Two kernels on `stream`; the sums' order depends on the sizes and
+ * the segments alone.
  */
 PMN_API pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t tokens, const uint8_t *codes,
                                     const uint8_t *scales, const float *outer, const int32_t *offsets, int num_experts,
                                     int64_t total_rows, int64_t n, int64_t k, const int32_t *row_choice, int choices,
-                                    int swiglu, int out_kind, void *out, void *stream);
+                                    int swiglu, int out_kind, void *out, void *workspace, int64_t workspace_bytes,
+                                    void *stream);
 
 #ifdef __cplusplus
 }

@@ -59,21 +59,6 @@ namespace {
 __device__ int g_gated_error = 0;
 
 template <int CT>
-__device__ __forceinline__ void tc_cp_ct(uint32_t el, uint32_t taddr, uint64_t sdesc)
-{
-    if (CT == 1)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
-            : "memory");
-}
-
-template <int CT>
 __device__ __forceinline__ void mma_mxfp8_ct(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
 {

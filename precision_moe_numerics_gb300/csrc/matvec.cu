@@ -1,10 +1,16 @@
 // matvec.cu -- the few rows of a decode batch times NVFP4 weights, activations in bf16:
 //   pmn_matvec_nvfp4   y = W_e x for the rows of each expert, SwiGLU where wanted
-// A weight is code * scale (E2M1 times E4M3: at most 6 significant bits, exact in f16) times
-// the expert's float32 scale.  x is brought into f16's range by a power of two per 256
-// of K and row, chosen from the largest magnitude there: what that loses lies 2^-40
-// below the largest element.  f16 products of the tensor cores (mma.sync) add up in
-// float32; a share of K per warp, joined in float32 in a fixed order.
+// The weights go to the tensor cores as they are stored (tcgen05 kind::mxf4nvf4, their own
+// scales), so no instruction is spent on decoding them: on the CUDA cores that alone took
+// four times as long as reading them.  What has to be in 4 bits for that is x,
+// and it is brought there without loss: a value is a sum of eight E2M1 digits,
+//   x = 2^e * scale_block * sum_c 8^-c d_c,   d_c in {0, +-1/2, +-1, +-3/2, +-2}
+// (balanced octal digits, halved), each digit a row of the small operand of its own, under a
+// scale per 16 values (a power of two, E4M3) and an exponent per row.  A value is exact
+// down to 2^-15 of the largest of its 16, and below that within 2^-23 of it; the digits'
+// sums are joined in float32.
+// Two kernels: the digits of x, then the product.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,6 +21,7 @@
 #include "../../include/pmn.h"
 #include "numerics.cuh"
 #include "sm100.cuh"
+#include "tensormap.cuh"
 
 using namespace pmn;
 using namespace pmn::sm100;
@@ -25,25 +32,25 @@ namespace {
 
 __device__ int g_matvec_error = 0;
 
-constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64;
-constexpr int WARPS = 16, THREADS = 32 * WARPS;
-constexpr int SLICE = 256;                       // of K, for one warp
-constexpr int CODE_BYTES = WARPS * 16 * SLICE / 2, SCALE_BYTES = WARPS * 16 * SLICE / 16;
-constexpr int STAGES = 5, STAGE_BYTES = CODE_BYTES + SCALE_BYTES;
-constexpr int PITCH = 20, PART = 8 * PITCH;      // floats of a warp's 8 x 16 sums: both accesses free of conflicts
+constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64, MAX_GRID = 256;
+constexpr int DIGITS = 8;
+constexpr int CHUNK = 16, NB = CHUNK * DIGITS;   // rows of x, and of the small operand, per pass over the weights
+constexpr int BM = 128;                          // weight rows of a tile (gated: 64 gate and the 64 up rows of the same columns)
+constexpr int KSTEP = 256;                       // of K per stage: 128 bytes of codes, 16 scales
+constexpr int A_BYTES = BM * 128, B_BYTES = NB * 128, SF_BYTES = 2 * 4 * 512;
+constexpr int STAGES = 5, STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+constexpr int RAW_STEPS = 4, RAW_W = 16 * RAW_STEPS;  // scale rows come 64 bytes (four stages) at a time
+constexpr int RAW_A = BM * RAW_W, RAW_BYTES = RAW_A + CHUNK * RAW_W, RAW_SLOTS = 3;
+constexpr int RAW_OFF = STAGES * STAGE_BYTES, XCH_OFF = RAW_OFF + RAW_SLOTS * RAW_BYTES;
+constexpr int BAR_OFF = XCH_OFF + 64 * 20 * 4, CUM_OFF = BAR_OFF + 256;
+constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t TMEM_COLS = 512, SF_COL0 = 2 * NB, SF_COLS = 32;
+static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
+// warps: 0 weights, 1 MMA, 2 scale rows, 3 digits; 4 .. 7 scale factors; 8 .. 11 epilogue
+constexpr int THREADS = 384;
 constexpr uint64_t DRAIN_NS = 100000000ull;
 
-template <int NT>
-struct Smem {
-    static constexpr int PART_OFF = STAGES * STAGE_BYTES, PART_BYTES = WARPS * NT * PART * 4;
-    static constexpr int BAR_OFF = PART_OFF + 2 * PART_BYTES, CUM_OFF = BAR_OFF + 8 * STAGES + 24;
-    static constexpr int BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
-    static_assert(BYTES <= 232448, "shared memory budget");
-};
-
-// An item is 16 rows of the weights (gated: 8 gate and the 8 up rows of the same
-// columns) times `groups`, as many as keep the warps busy when K is short; K is taken in
-// `passes` of up to `slices` warps' shares.
 struct Args {
     const uint16_t *x;
     int64_t ldx, tokens;
@@ -55,58 +62,148 @@ struct Args {
     const int32_t *row_choice;
     int choices;
     void *out;
-    int all_slices, slices, passes, groups, items;  // items per expert
+    int tiles, nks;      // tiles per expert, stages per tile
+    // workspace: digits [rows * 8, k / 2], their scales [rows, k / 16], per row the exponent and
+    // whether it holds a value that is not finite, the sums of tiles that CTAs share, and of
+    // each such tile's first CTA how many have left theirs
+    uint8_t *digits, *digit_scales;
+    int2 *meta;
+    float *part;
+    unsigned *count;
     uint64_t wait_ns;
 };
 
 __device__ __forceinline__ void latch_error(int bit) { atomicOr(&g_matvec_error, bit); }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+__device__ __forceinline__ float pow2(int e)  // e in [-126, 127]
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a)
+__device__ __forceinline__ int64_t token_of(const Args &p, int64_t row)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
+    if (!p.row_choice) return row;
+    const int c = __ldg(p.row_choice + row);
+    const int64_t t = c < 0 ? -1 : c / p.choices;
+    if (t < p.tokens) return t;
+    latch_error(PMN_DEVERR_BAD_OFFSETS);
+    return -1;
 }
 
-// D (16 x 8, float32) += A (16 x 16) B (16 x 8), f16
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
+// ---------------------------------------------------------------- digits
+// One CTA per routed row: the row's largest finite magnitude, then eight values per thread at
+// a time.
+__global__ void __launch_bounds__(256) digits_kernel(const Args p, int grid)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float s_top[8];
+    __shared__ int s_odd;
+    const int64_t row = blockIdx.x, token = token_of(p, row);
+    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + token * p.ldx);
+    const int vecs = (int)(p.k / 8);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < grid; i += 256) p.count[i] = 0u;
+    if (threadIdx.x == 0) s_odd = 0;
+    __syncthreads();
+    float top = 0.0f;
+    bool odd = false;
+    for (int v = threadIdx.x; v < vecs && token >= 0; v += 256) {
+        const uint4 q = __ldg(x + v);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float a = __uint_as_float((u4_word(q, w) & 0x7FFFu) << 16), b = __uint_as_float(u4_word(q, w) & 0x7FFF0000u);
+            odd = odd || !(a < INFINITY) || !(b < INFINITY);
+            top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    if (odd) s_odd = 1;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_top[w]);
+    // top in [2^e, 2^(e+1)); below float32's normal range any larger e will do
+    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -126);
+    if (threadIdx.x == 0) p.meta[row] = make_int2(e - 8, s_odd);
+    const float down = e == 127 ? __uint_as_float(0x00400000u) : pow2(-e);  // 2^-127 is below the normal range
+    for (int v0 = 0; v0 < vecs; v0 += 256) {  // whole warps: k is a multiple of 256
+        const int v = v0 + threadIdx.x;
+        if (v >= vecs) break;
+        uint4 q = token >= 0 ? __ldg(x + v) : make_uint4(0u, 0u, 0u, 0u);
+        float f[8], big = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = u4_word(q, i >> 1);
+            float y = __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+            y = fabsf(y) < INFINITY ? y : 0.0f;
+            f[i] = __fmul_rn(y, down);
+            big = fmaxf(big, fabsf(f[i]));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));  // of the 16
+        // the scale 2^s: s = 8 + the exponent of the largest, within E4M3's powers of two
+        const int s = max(-9, min(8, (int)(__float_as_uint(big) >> 23) - 119));
+        if ((v & 1) == 0) p.digit_scales[row * (p.k / 16) + (v >> 1)] = (uint8_t)(s >= -6 ? (s + 7) << 3 : 1 << (s + 9));
+        // 2^22 * 2^8 / 2^s: the value in units of the last digit
+        const float up = pow2(30 - s);
+        uint32_t d[DIGITS] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // octal digits of the value plus 4 in every place, less 4 each: -4 .. 3, the first -4 .. 4
+            const uint32_t u = (uint32_t)(__float2int_rn(__fmul_rn(f[i], up)) + 9586980);
+#pragma unroll
+            for (int c = 0; c < DIGITS; ++c) {
+                const uint32_t o = c == 0 ? u >> 21 : (u >> (3 * (7 - c))) & 7u;
+                // E2M1 code of (o - 4) / 2: the magnitude |o - 4| itself, sign in bit 3
+                const uint32_t code = c == 0 && o == 8 ? 4u : (0x32109ABCu >> (4 * o)) & 15u;
+                d[c] |= code << (4 * i);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < DIGITS; ++c)
+            *reinterpret_cast<uint32_t *>(p.digits + (row * DIGITS + c) * (p.k / 2) + 4 * v) = d[c];
+    }
 }
 
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-struct Item {
-    int e, tile;       // expert; 16 * groups weight rows
-    int r0, m;         // first routed row of the chunk, rows left in the segment
+// ---------------------------------------------------------------- product
+// Steps (256 of K of a tile of a chunk of up to 16 rows) in one line, an even share of it
+// for each CTA: a piece is what a CTA has of one tile.
+struct Piece {
+    int e, unit, tile, k0, k1;  // expert, chunk of all experts, tile, stages of K
+    int r0, m;                  // first routed row of the chunk, rows left in the segment
 };
 
-template <int NT>
-__device__ __forceinline__ Item get_item(int64_t i, const Args &p, const int *s_cum, int &gc)
+struct Walk {
+    int64_t at, end;
+    int e;
+    __device__ __forceinline__ bool next(const Args &p, const int *s_cum, Piece &q)
+    {
+        if (at >= end) return false;
+        const int64_t line = at / p.nks;  // tile of all chunks
+        q.k0 = (int)(at - line * p.nks);
+        q.k1 = (int)min((int64_t)p.nks, q.k0 + (end - at));
+        at += q.k1 - q.k0;
+        q.unit = (int)(line / p.tiles);
+        q.tile = (int)(line - (int64_t)q.unit * p.tiles);
+        while (e + 1 < p.experts && s_cum[e + 1] <= q.unit) ++e;
+        q.e = e;
+        q.r0 = __ldg(p.offsets + e) + (q.unit - s_cum[e]) * CHUNK;
+        q.m = __ldg(p.offsets + e + 1) - q.r0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ int digit_rows(const Piece &q) { return (min(q.m, CHUNK) + 1) / 2 * 2 * DIGITS; }  // a multiple of 16
+
+__device__ __forceinline__ void mma_nvfp4_by(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
 {
-    const int unit = (int)(i / p.items);  // a chunk of 8 NT rows of an expert
-    while (gc + 1 < p.experts && s_cum[gc + 1] <= unit) ++gc;
-    Item it;
-    it.e = gc;
-    it.tile = (int)(i - (int64_t)unit * p.items);
-    it.r0 = __ldg(p.offsets + gc) + (unit - s_cum[gc]) * 8 * NT;
-    it.m = __ldg(p.offsets + gc + 1) - it.r0;
-    return it;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(el)
+        : "memory");
 }
 
 __device__ __forceinline__ void store_one(uint16_t *p, float v)
@@ -116,28 +213,65 @@ __device__ __forceinline__ void store_one(uint16_t *p, float v)
 }
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 
-template <int NT, bool GATED, typename OUT>
-__global__ void __launch_bounds__(THREADS, 1) matvec_kernel(const Args p)
+// The row's product by plain float32 sums: for rows with values that no digit stands for.
+__device__ __noinline__ float plain_dot(const Args &p, int64_t wrow, int64_t token)
 {
-    using S = Smem<NT>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t base = smem_u32(smem), bar_full = base + S::BAR_OFF;
-    int *s_abort = reinterpret_cast<int *>(smem + S::BAR_OFF + 8 * STAGES), *s_total = s_abort + 1, *s_bad = s_abort + 2;
-    int *s_cum = reinterpret_cast<int *>(smem + S::CUM_OFF);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint8_t *c = p.codes + wrow * (p.k / 2), *s = p.scales + wrow * (p.k / 16);
+    const uint16_t *x = p.x + token * p.ldx;
+    float acc = 0.0f;
+    for (int64_t i = 0; i < p.k; ++i) {
+        const uint32_t b = __ldg(s + (i >> 4)), code = __ldg(c + (i >> 1)) >> (4 * (i & 1));
+        const float w = __fmul_rn(e2m1_to_f32(code & 15u), (b & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_to_f32(b));
+        acc = fmaf(w, __uint_as_float((uint32_t)__ldg(x + i) << 16), acc);
+    }
+    return acc;
+}
+
+template <bool GATED, typename OUT>
+__global__ void __launch_bounds__(THREADS, 1)
+    matvec_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
+                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDS, const Args p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw;
+    asm volatile("" : "+l"(smem));
+    const uint32_t stages = smem_u32(smem);
+    const uint32_t bar_full = stages + BAR_OFF, bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_raw = bar_empty + 8 * STAGES, bar_raw_empty = bar_raw + 8 * RAW_SLOTS;
+    const uint32_t bar_acc_full = bar_raw_empty + 8 * RAW_SLOTS, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 2 * RAW_SLOTS + 5));
+    int *s_abort = reinterpret_cast<int *>(tmem_slot + 1), *s_units = s_abort + 1, *s_bad = s_abort + 2, *s_last = s_abort + 3;
+    int *s_cum = reinterpret_cast<int *>(smem + CUM_OFF);
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) mbar_init(bar_full + 8 * s, 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 6);  // weights, digits, four scale-factor warps
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < RAW_SLOTS; ++s) {
+            mbar_init(bar_raw + 8 * s, 1);
+            mbar_init(bar_raw_empty + 8 * s, 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_acc_full + 8 * b, 1);
+            mbar_init(bar_acc_empty + 8 * b, 4);
+        }
+        mbar_init(bar_drain, 1);
         *s_abort = 0;
         *s_bad = 0;
         fence_barrier_init();
     }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc_ct<1>(smem_u32(tmem_slot), TMEM_COLS);
+    }
     __syncthreads();
-    // chunks of 8 NT rows of each expert, then their running sum
+    // chunks of each expert, then their running sum
     for (int e = threadIdx.x; e < p.experts; e += THREADS) {
         const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
         if (lo < 0 || hi < lo || hi > p.rows) *s_bad = 1;
-        s_cum[e] = (hi - lo + 8 * NT - 1) / (8 * NT);
+        s_cum[e] = (hi - lo + CHUNK - 1) / CHUNK;
     }
     __syncthreads();
     if (warp == 0) {
@@ -155,235 +289,376 @@ __global__ void __launch_bounds__(THREADS, 1) matvec_kernel(const Args p)
         }
         if (lane == 0) {
             s_cum[p.experts] = sum;
-            *s_total = *s_bad ? 0 : sum;
+            *s_units = *s_bad ? 0 : sum;
             if (*s_bad && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         }
     }
+    tc_fence_before();
     __syncthreads();
-    const int64_t total = (int64_t)*s_total * p.items;
-    const int64_t first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
-    const int tile_rows = 16 * p.groups, half_rows = GATED ? tile_rows / 2 : tile_rows;  // gated: gate rows, up rows
-    const int64_t half_n = GATED ? p.n / 2 : p.n;
-
-    // Weights come by bulk copies, STAGES passes ahead.  One warp asks for the next pass
-    // whenever the barrier that ends one has freed its stage.
-    const int64_t all_passes = (last - first) * p.passes;
-    int64_t asked = 0;
-    int ask_gc = 0;
-    auto ask = [&]() {
-        if (asked >= all_passes || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) return;
-        const int64_t ahead = asked / p.passes;
-        const int pass = (int)(asked - ahead * p.passes), stage = (int)(asked % STAGES);
-        const Item it = get_item<NT>(first + ahead, p, s_cum, ask_gc);
-        const int row0 = it.tile * half_rows, rows = (int)min((int64_t)half_rows, half_n - row0);
-        const int64_t cp = p.k / 2, sp = p.k / 16;  // row pitches
-        const uint32_t st = base + stage * STAGE_BYTES, fb = bar_full + 8 * stage;
-        const int s0 = pass * p.slices, ns = min(p.slices, p.all_slices - s0);
-        const int halves = GATED ? 2 : 1;
-        if (lane == 0) mbar_arrive_expect_tx(fb, halves * rows * ns * (SLICE / 2 + SLICE / 16));
-        __syncwarp();
-        for (int h = 0; h < halves; ++h) {
-            const int64_t row = (int64_t)it.e * p.n + h * half_n + row0;
-            const uint32_t cd = st + h * half_rows * ns * (SLICE / 2), sd = st + CODE_BYTES + h * half_rows * ns * (SLICE / 16);
-            const uint8_t *c = p.codes + row * cp + s0 * (SLICE / 2), *sc = p.scales + row * sp + s0 * (SLICE / 16);
-            if (p.passes == 1) {  // the rows lie end to end
-                if (lane == 0) bulk_load(cd, c, rows * cp, fb);
-                if (lane == 1) bulk_load(sd, sc, rows * sp, fb);
-            } else {
-                for (int r = lane; r < rows; r += 32) {
-                    bulk_load(cd + r * ns * (SLICE / 2), c + r * cp, ns * (SLICE / 2), fb);
-                    bulk_load(sd + r * ns * (SLICE / 16), sc + r * sp, ns * (SLICE / 16), fb);
-                }
-            }
-        }
-        __syncwarp();
-        ++asked;
-    };
-    if (warp == WARPS - 1)
-        for (int s = 0; s < STAGES; ++s) ask();
-
-    // Lane 4 r + q holds, of weight rows r and r + 8 and of row r of x, 32 of every 128 of
-    // the warp's slice of K: what mma.sync sees as its K is this order, the same on both sides.
-    const int r = lane >> 2, q = lane & 3;
-    const int group = warp / p.slices, slice = warp - group * p.slices;
-    uint32_t xf[NT][32];
-    float unscale[NT][2];  // of columns 2 q and 2 q + 1 of the sums
-    int have_unit = -1, have_pass = -1;
-    uint32_t stage = 0, phase = 0;
-    int gc = 0, buf = 0;
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t total = (int64_t)*s_units * p.tiles * p.nks;
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total));  // with a share
+    auto share = [&](int64_t b) { return total * b / ctas; };             // first step of CTA b
+    Walk walk{0, 0, 0};
+    if (blockIdx.x < ctas) walk = Walk{share(blockIdx.x), share(blockIdx.x + 1), 0};
+    const int half = GATED ? BM / 2 : BM;
     bool dead = false;
-    for (int64_t i = first; i < last; ++i, buf ^= 1) {
-        const Item it = get_item<NT>(i, p, s_cum, gc);
-        const int unit = (int)(i / p.items);
-        const float outer = __ldg(p.outer + it.e);
-        float sum[NT][4] = {};
-        for (int pass = 0; pass < p.passes; ++pass) {
-            const int s0 = pass * p.slices, ns = min(p.slices, p.all_slices - s0);
-            const bool active = group < p.groups && slice < ns;
-            if (active && (unit != have_unit || pass != have_pass)) {
-                have_unit = unit;
-                have_pass = pass;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int row = 8 * t + r;
-                    int64_t token = -1;
-                    if (row < it.m) {
-                        token = it.r0 + row;
-                        if (p.row_choice) {
-                            const int c = __ldg(p.row_choice + token);
-                            token = c < 0 ? -1 : c / p.choices;
-                            if (token >= p.tokens) {
-                                latch_error(PMN_DEVERR_BAD_OFFSETS);
-                                token = -1;
-                            }
-                        }
-                    }
-                    uint4 raw[8];
-                    const uint16_t *xp = p.x + token * p.ldx + (s0 + slice) * SLICE + 32 * q;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        raw[j] = token >= 0 ? __ldg(reinterpret_cast<const uint4 *>(xp + 128 * (j >> 2) + 8 * (j & 3)))
-                                            : make_uint4(0u, 0u, 0u, 0u);
-                    float top = 0.0f;  // the largest finite magnitude
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t v = u4_word(raw[j], w);
-                            const float a = __uint_as_float((v & 0x7FFFu) << 16), b = __uint_as_float(v & 0x7FFF0000u);
-                            top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    // top * 2^e in [2^14, 2^15)
-                    const int e = max(-126, min(126, 141 - (int)(__float_as_uint(top) >> 23)));
-                    const float f = __uint_as_float((uint32_t)(127 + e) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
-                    unscale[t][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * q);      // lane 4 (2 q)
-                    unscale[t][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * q + 4);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t v = u4_word(raw[j], w);
-                            xf[t][4 * j + w] = f16x2(__fmul_rn(__uint_as_float(v << 16), f),
-                                                     __fmul_rn(__uint_as_float(v & 0xFFFF0000u), f));
-                        }
-                }
-            }
-            dead = dead || *(volatile int *)s_abort != 0;
-            if (!dead && !warp_wait(bar_full + 8 * stage, phase, p.wait_ns)) {
-                dead = true;
-                if (lane == 0) {
-                    *(volatile int *)s_abort = 1;
-                    latch_error(PMN_DEVERR_WAIT_TIMEOUT);
-                }
-            }
-            dead = __any_sync(0xFFFFFFFFu, dead);
-            if (active && !dead) {
-                const int ra = GATED ? 8 * group + r : 16 * group + r, rb = GATED ? half_rows + ra : ra + 8;
-                const uint32_t st = base + stage * STAGE_BYTES, code = st + slice * (SLICE / 2) + 16 * q;
-                const uint32_t scale = st + CODE_BYTES + slice * (SLICE / 16);
-                // even rows take the first 64 bytes first, odd rows the last: 8 lanes meet all banks
-                const uint32_t ca = code + ra * ns * (SLICE / 2), cb = code + rb * ns * (SLICE / 2), odd = (r & 1) * 64;
-                uint4 wa[2], wb[2];
-                const uint4 a0 = lds128(ca + odd), a1 = lds128(ca + (odd ^ 64)), b0 = lds128(cb + odd), b1 = lds128(cb + (odd ^ 64));
-                const uint4 sa = lds128(scale + ra * ns * (SLICE / 16)), sb = lds128(scale + rb * ns * (SLICE / 16));
-                wa[0] = odd ? a1 : a0, wa[1] = odd ? a0 : a1, wb[0] = odd ? b1 : b0, wb[1] = odd ? b0 : b1;
-                float acc[NT][4] = {};
-                const bool second = NT > 1 && it.m > 8;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    // the two scales of these 32 weights: bytes 8 c + 2 q, + 1
-                    const uint32_t a2 = (q & 2 ? (c ? sa.w : sa.y) : (c ? sa.z : sa.x)) >> (16 * (q & 1));
-                    const uint32_t b2 = (q & 2 ? (c ? sb.w : sb.y) : (c ? sb.z : sb.x)) >> (16 * (q & 1));
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t va[4], vb[4];
-                        e2m1x8_mul_h2(u4_word(wa[c], w), e4m3_to_h2(a2 >> (8 * (w >> 1))), va);
-                        e2m1x8_mul_h2(u4_word(wb[c], w), e4m3_to_h2(b2 >> (8 * (w >> 1))), vb);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int x = 16 * c + 4 * w + 2 * h;
-                            mma_f16(acc[0], va[2 * h], vb[2 * h], va[2 * h + 1], vb[2 * h + 1], xf[0][x], xf[0][x + 1]);
-                            if (NT > 1 && second)
-                                mma_f16(acc[NT - 1], va[2 * h], vb[2 * h], va[2 * h + 1], vb[2 * h + 1], xf[NT - 1][x], xf[NT - 1][x + 1]);
-                        }
-                    }
-                }
-                // the expert's scale first: the sums are within f16's range times 2^20 here
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        sum[t][j] = fmaf(__fmul_rn(acc[t][j], outer), unscale[t][j & 1], sum[t][j]);
-            }
-            if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
-            if (pass + 1 < p.passes) {
-                __syncthreads();  // the pass has been read
-                if (warp == WARPS - 1) ask();
+    auto wait = [&](uint32_t bar, uint32_t parity) {  // false: a wait ran out, here or in another warp
+        dead = dead || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0);
+        if (!dead && !warp_wait(bar, parity, p.wait_ns)) {
+            dead = true;
+            if (lane == 0) {
+                *(volatile int *)s_abort = 1;
+                latch_error(PMN_DEVERR_WAIT_TIMEOUT);
             }
         }
-        // join the warps' shares of K
-        float *part = reinterpret_cast<float *>(smem + S::PART_OFF + buf * S::PART_BYTES);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float *o = part + (warp * NT + t) * PART + r;
-            o[(2 * q) * PITCH] = sum[t][0];
-            o[(2 * q + 1) * PITCH] = sum[t][1];
-            o[(2 * q) * PITCH + 8] = sum[t][2];
-            o[(2 * q + 1) * PITCH + 8] = sum[t][3];
+        return !dead;
+    };
+    uint32_t stage = 0, phase = 0;
+    auto next_stage = [&]() {
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
         }
-        __syncthreads();
-        if (warp == WARPS - 1) ask();
-        if (*(volatile int *)s_abort) continue;
-        const int m = min(8 * NT, it.m), row0 = it.tile * half_rows, cols = (int)min((int64_t)half_rows, half_n - row0);
-        for (int o = threadIdx.x; o < m * half_rows; o += THREADS) {
-            const int n = o / half_rows, c = o - n * half_rows;
-            if (c >= cols) continue;
-            const int g = GATED ? c >> 3 : c >> 4, rr = GATED ? c & 7 : c & 15;
-            const float *v = part + (g * p.slices * NT + (n >> 3)) * PART + (n & 7) * PITCH + rr;
-            float a = 0.0f, b = 0.0f;
-            for (int w = 0; w < p.slices; ++w) {
-                a = __fadd_rn(a, v[w * NT * PART]);
-                if (GATED) b = __fadd_rn(b, v[w * NT * PART + 8]);
+    };
+    Piece q;
+
+    if (warp == 0) {
+        // ---------------------------------------------------- weights, 64 rows a box
+        while (!dead && walk.next(p, s_cum, q)) {
+            const int64_t row = (int64_t)q.e * p.n + q.tile * half;
+            const int32_t ra = (int32_t)row, rb = (int32_t)(row + (GATED ? p.n / 2 : 64));
+            for (int k = q.k0; k < q.k1; ++k) {
+                if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
+                if (elect_one()) {
+                    const uint32_t st = stages + stage * STAGE_BYTES, fb = bar_full + 8 * stage;
+                    mbar_arrive_expect_tx(fb, A_BYTES);
+                    tma_load_2d(st, &tmW, fb, 128 * k, ra);
+                    tma_load_2d(st + A_BYTES / 2, &tmW, fb, 128 * k, rb);
+                }
+                __syncwarp();
+                next_stage();
             }
-            if (GATED) a = __fmul_rn(__fmul_rn(a, __fdividef(1.0f, __fadd_rn(1.0f, __expf(-a)))), b);
-            store_one(static_cast<OUT *>(p.out) + (it.r0 + n) * half_n + row0 + c, a);
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------- digits, 16 rows a box
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        while (!dead && walk.next(p, s_cum, q)) {
+            const int nb = digit_rows(q);
+            for (int k = q.k0; k < q.k1; ++k) {
+                if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
+                if (elect_one()) {
+                    const uint32_t st = stages + stage * STAGE_BYTES + A_BYTES, fb = bar_full + 8 * stage;
+                    mbar_arrive_expect_tx(fb, nb * 128);
+                    for (int r = 0; r < nb; r += 16) tma_load_2d(st + 128 * r, &tmD, fb, 128 * k, q.r0 * DIGITS + r);
+                }
+                __syncwarp();
+                next_stage();
+            }
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------- scale rows, four stages at a time
+        uint32_t slot = 0, sphase = 0;
+        bool waited = false;
+        int pending = 0;  // slots whose digits' scales are still to be asked for
+        int32_t px[RAW_SLOTS], pr[RAW_SLOTS];
+        auto ask_digits = [&](int s, int32_t x, int32_t r) {
+            if (elect_one()) tma_load_2d(stages + RAW_OFF + s * RAW_BYTES + RAW_A, &tmDS, bar_raw + 8 * s, x, r);
+            __syncwarp();
+        };
+        auto flush = [&]() {  // the digits have been written
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+#pragma unroll
+            for (int s = 0; s < RAW_SLOTS; ++s)
+                if (s < pending) ask_digits(s, px[s], pr[s]);
+        };
+        while (!dead && walk.next(p, s_cum, q)) {
+            const int64_t row = (int64_t)q.e * p.n + q.tile * half;
+            const int32_t ra = (int32_t)row, rb = (int32_t)(row + (GATED ? p.n / 2 : 64));
+            for (int k = q.k0; k < q.k1; k += RAW_STEPS) {
+                if (!waited && pending == RAW_SLOTS) flush();
+                if (!wait(bar_raw_empty + 8 * slot, sphase ^ 1)) break;
+                if (elect_one()) {
+                    const uint32_t st = stages + RAW_OFF + slot * RAW_BYTES, fb = bar_raw + 8 * slot;
+                    mbar_arrive_expect_tx(fb, RAW_BYTES);
+                    tma_load_2d(st, &tmS, fb, 16 * k, ra);
+                    tma_load_2d(st + RAW_A / 2, &tmS, fb, 16 * k, rb);
+                }
+                __syncwarp();
+                if (waited) ask_digits(slot, 16 * k, q.r0);
+                else {
+#pragma unroll
+                    for (int s = 0; s < RAW_SLOTS; ++s)
+                        if (s == pending) px[s] = 16 * k, pr[s] = q.r0;
+                    ++pending;
+                }
+                if (++slot == RAW_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1;
+                }
+            }
+        }
+        if (!waited) flush();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), el = elect_one();
+        uint32_t abuf = 0, aphase = 0;
+        while (!dead && walk.next(p, s_cum, q)) {
+            const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(digit_rows(q) >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+            if (!wait(bar_acc_empty + 8 * abuf, aphase ^ 1)) break;
+            const uint32_t d = tm + abuf * NB;
+            for (int k = q.k0; k < q.k1; ++k) {
+                if (!wait(bar_full + 8 * stage, phase)) break;
+                tc_fence_after();
+                const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES, sf = b + B_BYTES;
+                const uint32_t sfa = tm + SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    tc_cp_ct<1>(el, sfa + 4 * s, smem_desc(sf + 512 * s, 0, 128, 0));
+                    tc_cp_ct<1>(el, sfb + 4 * s, smem_desc(sf + 2048 + 512 * s, 0, 128, 0));
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)  // 64 of K: 32 bytes of the swizzled rows
+                    mma_nvfp4_by(el, d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2), idesc, sfa + 4 * s,
+                                 sfb + 4 * s, k > q.k0 || s > 0);
+                tc_commit_ct<1>(el, bar_empty + 8 * stage);
+                next_stage();
+            }
+            if (dead) break;
+            tc_commit_ct<1>(el, bar_acc_full + 8 * abuf);
+            if (++abuf == 2) {
+                abuf = 0;
+                aphase ^= 1;
+            }
+        }
+        if (elect_one()) tc_commit(bar_drain);  // every tcgen05 operation of this warp has completed
+        __syncwarp();
+        (void)warp_wait(bar_drain, 0, DRAIN_NS);
+    } else if (warp < 8) {
+        // ---------------------------------------------------- scale factors
+        // Step s of a stage, lane r, word j: the four scale bytes of row 32 j + r.  A thread has
+        // weight row i and row i of the digits, whose eight rows per value share a scale.
+        const int i = threadIdx.x - 128, word = 16 * (i & 31) + 4 * (i >> 5);
+        uint32_t slot = 0, sphase = 0;
+        while (!dead && walk.next(p, s_cum, q)) {
+            for (int k = q.k0; k < q.k1 && !dead; k += RAW_STEPS) {
+                if (!wait(bar_raw + 8 * slot, sphase)) break;
+                const uint8_t *raw = smem + RAW_OFF + slot * RAW_BYTES;
+                uint4 va[RAW_STEPS], vb[RAW_STEPS];
+#pragma unroll
+                for (int c = 0; c < RAW_STEPS; ++c) {
+                    va[c] = *reinterpret_cast<const uint4 *>(raw + RAW_W * i + 16 * c);
+                    vb[c] = *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * (i >> 3) + 16 * c);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
+                if (++slot == RAW_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1;
+                }
+#pragma unroll
+                for (int c = 0; c < RAW_STEPS; ++c) {
+                    if (k + c >= q.k1 || dead) break;
+                    if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
+                    uint8_t *sf = smem + stage * STAGE_BYTES + A_BYTES + B_BYTES + word;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        *reinterpret_cast<uint32_t *>(sf + 512 * s) = u4_word(va[c], s);
+                        *reinterpret_cast<uint32_t *>(sf + 2048 + 512 * s) = u4_word(vb[c], s);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_full + 8 * stage);
+                    next_stage();
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue: a weight row per thread
+        const int quad = warp & 3, i = threadIdx.x - 256;
+        uint32_t abuf = 0, aphase = 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        while (walk.next(p, s_cum, q)) {  // to the end, also after a timeout: the four warps meet at barriers
+            const int m = min(q.m, CHUNK);
+            float y[CHUNK];
+            if (wait(bar_acc_full + 8 * abuf, aphase)) {
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * NB;
+#pragma unroll
+                for (int t = 0; t < CHUNK; t += 2) {
+                    if (t >= m) break;
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(acc + DIGITS * t, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float sum = __uint_as_float(v[8 * u + 7]);
+#pragma unroll
+                        for (int c = 6; c >= 0; --c) sum = fmaf(sum, 0.125f, __uint_as_float(v[8 * u + c]));
+                        y[t + u] = sum;
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
+            if (++abuf == 2) {
+                abuf = 0;
+                aphase ^= 1;
+            }
+            if (q.k1 - q.k0 < p.nks) {
+                // A tile that CTAs first .. last share: each leaves its sums, and the one that
+                // comes last adds them up in the order of K.  A CTA's slot 0 is for a tile that began
+                // before its share, slot 1 for one that begins in it.
+                const int64_t line = (int64_t)q.unit * p.tiles + q.tile, s0 = line * p.nks, s1 = s0 + p.nks;
+                int first = blockIdx.x, last = blockIdx.x;
+                while (share(first) > s0) --first;
+                while (share(last + 1) < s1) ++last;
+                float *mine = p.part + ((int64_t)blockIdx.x * 2 + (q.k0 == 0)) * CHUNK * BM;
+#pragma unroll
+                for (int t = 0; t < CHUNK; ++t)
+                    if (t < m) __stcg(mine + t * BM + i, y[t]);
+                __threadfence();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (i == 0) *s_last = atomicAdd(p.count + first, 1u) == (unsigned)(last - first);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const bool finish = *(volatile int *)s_last;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (!finish) continue;
+                __threadfence();
+#pragma unroll
+                for (int t = 0; t < CHUNK; ++t) y[t] = 0.0f;
+                for (int b = first; b <= last; ++b) {
+                    const float *from = p.part + ((int64_t)b * 2 + (b == first)) * CHUNK * BM + i;
+#pragma unroll
+                    for (int t = 0; t < CHUNK; ++t)
+                        if (t < m) y[t] = __fadd_rn(y[t], __ldcg(from + t * BM));
+                }
+            }
+            const int half_n = (int)(GATED ? p.n / 2 : p.n), c = GATED ? i & 63 : i, col = q.tile * half + c;
+            const int64_t wrow = (int64_t)q.e * p.n + col + (GATED && i >= 64 ? half_n : 0);
+            const bool on = col < half_n && !dead;
+            const float outer = __ldg(p.outer + q.e);
+#pragma unroll
+            for (int t = 0; t < CHUNK; ++t) {
+                if (t >= m) break;
+                const int2 meta = __ldcg(p.meta + q.r0 + t);
+                const int e1 = max(meta.x, -126);
+                y[t] = __fmul_rn(__fmul_rn(__fmul_rn(y[t], outer), pow2(e1)), pow2(meta.x - e1));
+                if (meta.y && on) {
+                    const int64_t token = token_of(p, q.r0 + t);
+                    y[t] = __fmul_rn(plain_dot(p, wrow, token), outer);
+                }
+            }
+            OUT *o = static_cast<OUT *>(p.out) + (int64_t)q.r0 * half_n + col;
+            if (!GATED) {
+#pragma unroll
+                for (int t = 0; t < CHUNK; ++t)
+                    if (t < m && on) store_one(o + (int64_t)t * half_n, y[t]);
+            } else {
+                // the up rows' threads hand theirs to the gate rows'
+                float *xch = reinterpret_cast<float *>(smem + XCH_OFF) + c * 20;
+                if (i >= 64) {
+#pragma unroll
+                    for (int t = 0; t < CHUNK; t += 4)
+                        *reinterpret_cast<float4 *>(xch + t) = make_float4(y[t], y[t + 1], y[t + 2], y[t + 3]);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (i < 64) {
+#pragma unroll
+                    for (int t = 0; t < CHUNK; ++t) {
+                        if (t >= m) break;
+                        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-y[t])));
+                        if (on) store_one(o + (int64_t)t * half_n, __fmul_rn(__fmul_rn(y[t], s), xch[t]));
+                    }
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
         }
     }
-    // after a timeout copies that nobody waited for may still be landing
-    if (warp == WARPS - 1 && dead)
-        for (int64_t a = max((int64_t)0, asked - STAGES); a < asked; ++a)
-            (void)warp_wait(bar_full + 8 * (uint32_t)(a % STAGES), (uint32_t)(a / STAGES) & 1u, DRAIN_NS);
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*(volatile int *)s_abort) {  // copies that nobody waited for may still be landing
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 10000000ull) {
+        }
+    }
+    __syncthreads();
+    if (warp == 1) tmem_dealloc_ct<1>(tmem, TMEM_COLS);
+}
+
+// ====================================================================== host
+// Bytes [rows, width] in boxes of box_w (128: with the 128-byte swizzle) x box_rows.
+bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, uint32_t box_w, uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width};
+    const cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              box_w == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <int NT, bool GATED, typename OUT>
-pmn_status launch(const Args &args, cudaStream_t s)
+inline int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
+
+// The workspace's parts, each on a 128-byte boundary.
+struct Parts {
+    int64_t digits, scales, meta, part, count, end;
+    Parts(int64_t rows, int64_t k)
+    {
+        digits = 0;
+        scales = digits + up128(rows * DIGITS * (k / 2));
+        meta = scales + up128(rows * (k / 16));
+        part = meta + up128(rows * 8);
+        count = part + (int64_t)MAX_GRID * 2 * CHUNK * BM * 4;
+        end = count + MAX_GRID * 4;
+    }
+};
+
+constexpr int64_t LIMIT = int64_t(1) << 31;
+
+bool good_sizes(int64_t rows, int64_t k)
 {
-    auto kern = matvec_kernel<NT, GATED, OUT>;
+    return rows >= 0 && rows < LIMIT / DIGITS - 256 && k > 0 && k % KSTEP == 0 && k < LIMIT / 4;
+}
+
+template <bool GATED, typename OUT>
+pmn_status launch(const CUtensorMap (&maps)[4], const Args &args, cudaStream_t s)
+{
+    auto kern = matvec_kernel<GATED, OUT>;
     static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return PMN_ERR_CUDA;
     int sms = dev < MAX_DEVICES ? sm_count[dev].load(std::memory_order_acquire) : 0;
     if (sms == 0) {
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::BYTES) != cudaSuccess)
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
             return PMN_ERR_CUDA;
+        sms = std::min(sms, MAX_GRID);
         if (dev < MAX_DEVICES) sm_count[dev].store(sms, std::memory_order_release);
     }
-    kern<<<sms, THREADS, Smem<NT>::BYTES, s>>>(args);
-    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
-}
-
-template <bool GATED, typename OUT>
-pmn_status launch_by_rows(const Args &args, cudaStream_t s)
-{
-    return args.rows <= 8 ? launch<1, GATED, OUT>(args, s) : launch<2, GATED, OUT>(args, s);
+    digits_kernel<<<(unsigned)args.rows, 256, 0, s>>>(args, sms);
+    if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
+    // launched while the digits are made: the weights need not wait for them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 }  // namespace
@@ -403,28 +678,39 @@ pmn_status pmn_take_matvec_device_error(cudaStream_t s, int *bits)
     return PMN_OK;
 }
 
+extern "C" int64_t pmn_matvec_nvfp4_workspace_bytes(int64_t total_rows, int64_t k)
+{
+    return !good_sizes(total_rows, k) ? -1 : total_rows == 0 ? 0 : Parts(total_rows, k).end;
+}
+
 extern "C" pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t tokens, const uint8_t *codes,
                                        const uint8_t *scales, const float *outer, const int32_t *offsets,
                                        int num_experts, int64_t total_rows, int64_t n, int64_t k,
                                        const int32_t *row_choice, int choices, int swiglu, int out_kind, void *out,
-                                       void *stream)
+                                       void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (num_experts <= 0 || num_experts > MAX_GROUPS || total_rows < 0 || total_rows >= (int64_t(1) << 31) - 64 || tokens < 0 ||
-        tokens >= (int64_t(1) << 31) || n <= 0 || n % 16 != 0 || n >= (int64_t(1) << 28) || k <= 0 || k % 256 != 0 ||
-        k >= (int64_t(1) << 28) || ldx < k || ldx % 8 != 0 || (swiglu != 0 && swiglu != 1) || choices < 1 ||
-        (out_kind != PMN_OUT_BF16 && out_kind != PMN_OUT_F32) || (!row_choice && tokens != total_rows))
+    if (num_experts <= 0 || num_experts > MAX_GROUPS || !good_sizes(total_rows, k) || tokens < 0 || tokens >= LIMIT || n <= 0 ||
+        n % 16 != 0 || n >= LIMIT / 2 || num_experts * n >= LIMIT - 256 || ldx < k || ldx % 8 != 0 || (swiglu != 0 && swiglu != 1) ||
+        choices < 1 || (out_kind != PMN_OUT_BF16 && out_kind != PMN_OUT_F32) || (!row_choice && tokens != total_rows))
         return PMN_ERR_INVALID_ARG;
     if (total_rows == 0) return PMN_OK;
-    if ((!x && tokens > 0) || !codes || !scales || !outer || !offsets || !out || !aligned(x, 16) || !aligned(codes, 16) ||
-        !aligned(scales, 16) || !aligned(outer, 4) || !aligned(offsets, 4) || !aligned(row_choice, 4) || !aligned(out, 16))
+    const Parts w(total_rows, k);
+    if ((!x && tokens > 0) || !codes || !scales || !outer || !offsets || !out || !workspace || workspace_bytes < w.end ||
+        !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(outer, 4) || !aligned(offsets, 4) ||
+        !aligned(row_choice, 4) || !aligned(out, 16) || !aligned(workspace, 16))
         return PMN_ERR_INVALID_ARG;
-    const int all = (int)(k / SLICE), passes = (all + WARPS - 1) / WARPS, slices = (all + passes - 1) / passes;
-    const int groups = WARPS / slices, per_half = (swiglu ? 8 : 16) * groups;
-    const int64_t half_n = swiglu ? n / 2 : n;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int64_t half_n = swiglu ? n / 2 : n, half = swiglu ? BM / 2 : BM;
     const Args a{static_cast<const uint16_t *>(x), ldx, tokens, codes, scales, outer, offsets, num_experts, total_rows, n, k,
-                 row_choice, choices, out, all, slices, passes, groups, (int)((half_n + per_half - 1) / per_half),
-                 pmn_wait_limit_ns()};
+                 row_choice, choices, out, (int)((half_n + half - 1) / half), (int)(k / KSTEP), ws + w.digits, ws + w.scales,
+                 reinterpret_cast<int2 *>(ws + w.meta), reinterpret_cast<float *>(ws + w.part),
+                 reinterpret_cast<unsigned *>(ws + w.count), pmn_wait_limit_ns()};
+    CUtensorMap maps[4];
+    if (!make_map(&maps[0], codes, k / 2, num_experts * n, 128, 64) || !make_map(&maps[1], scales, k / 16, num_experts * n, RAW_W, 64) ||
+        !make_map(&maps[2], a.digits, k / 2, total_rows * DIGITS, 128, 16) ||
+        !make_map(&maps[3], a.digit_scales, k / 16, total_rows, RAW_W, CHUNK))
+        return PMN_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (swiglu) return out_kind == PMN_OUT_F32 ? launch_by_rows<true, float>(a, s) : launch_by_rows<true, uint16_t>(a, s);
-    return out_kind == PMN_OUT_F32 ? launch_by_rows<false, float>(a, s) : launch_by_rows<false, uint16_t>(a, s);
+    if (swiglu) return out_kind == PMN_OUT_F32 ? launch<true, float>(maps, a, s) : launch<true, uint16_t>(maps, a, s);
+    return out_kind == PMN_OUT_F32 ? launch<false, float>(maps, a, s) : launch<false, uint16_t>(maps, a, s);
 }

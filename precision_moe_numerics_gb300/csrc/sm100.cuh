@@ -365,5 +365,20 @@ __device__ __forceinline__ void tc_commit_own(uint32_t bar)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+template <int CT>
+__device__ __forceinline__ void tc_cp_ct(uint32_t el, uint32_t taddr, uint64_t sdesc)
+{
+    if (CT == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(el), "r"(taddr), "l"(sdesc)
+            : "memory");
+}
+
 }  // namespace sm100
 }  // namespace pmn

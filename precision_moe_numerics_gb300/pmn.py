@@ -75,7 +75,8 @@ SIGNATURES = {
     "pmn_grouped_gemm_bf16": ([_P, _I64, _P, _I64, _P, _I, _I, _I, _I64, _I64, _I64, _I, _P, _P], _I),
     "pmn_w1_gemm_swiglu_bf16": ([_P, _I64, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P], _I),
     "pmn_dh_gemm_swiglu_backward_bf16": ([_P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P], _I),
-    "pmn_matvec_nvfp4": ([_P, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _I, _P, _P], _I),
+    "pmn_matvec_nvfp4_workspace_bytes": ([_I64, _I64], _I64),
+    "pmn_matvec_nvfp4": ([_P, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _I, _P, _P, _I64, _P], _I),
     "pmn_adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _I64, _P, _U64, _P], _I),
 }
 
@@ -952,13 +953,21 @@ def dh_gemm_swiglu_backward_bf16(a, b, y, offsets, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ few rows, 4-bit weights
-def matvec_nvfp4(x, w, offsets, row_choice=None, k=1, swiglu=False, out_dtype=None, out=None, stream=None):
+def matvec_nvfp4_workspace_bytes(rows, k):
+    n = lib().pmn_matvec_nvfp4_workspace_bytes(rows, k)
+    if n < 0:
+        raise PmnError("matvec_nvfp4_workspace_bytes: invalid arguments")
+    return n
+
+
+def matvec_nvfp4(x, w, offsets, row_choice=None, k=1, swiglu=False, out_dtype=None, out=None, workspace=None, stream=None):
     """The rows of a decode batch times NVFP4 weights, activations in bf16.
 
     x bf16 [T, K] (rows may be strided); w = (codes u8 [E, N, K/2], scales u8 [E, N, K/16], outer f32 [E]); offsets int32
     [E+1] on the device.  Routed row r reads x[r], or with row_choice (int32 [rows], a Routing's) x[row_choice[r] // k].
     Returns [rows, N], or with swiglu [rows, N/2] = silu(gate) * up of the N/2 gate rows and N/2 up rows, in bf16 or
-    float32 (default bf16); rows outside every segment are not written."""
+    float32 (default bf16); rows outside every segment are not written.  workspace: uint8 device tensor of at least
+    matvec_nvfp4_workspace_bytes(rows, K) bytes, allocated here when None."""
     gpu = torch._C._cuda_getDevice()
     ldx = _rows(x, "x", gpu, torch.bfloat16)
     codes, scales, outer = w
@@ -979,8 +988,13 @@ def matvec_nvfp4(x, w, offsets, row_choice=None, k=1, swiglu=False, out_dtype=No
         out = _empty(shape, out_dtype or torch.bfloat16, x.device, stream)
     else:
         _shaped(out, shape, out_dtype or out.dtype, "out", gpu)
+    if workspace is None:
+        workspace = _empty((matvec_nvfp4_workspace_bytes(rows, kdim),), torch.uint8, x.device, stream)
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise PmnError("workspace must be a dense tensor on the current GPU (cuda:%d)" % gpu)
     raw = _launch_stream("matvec_nvfp4", stream, gpu)
     _check(lib().pmn_matvec_nvfp4(_at(x), ldx, tokens, _at(codes), _at(scales), _at(outer), _at(offsets), experts, rows, n,
-                                  kdim, _at(row_choice), k, int(swiglu), _kind(out, "out"), _at(out), raw),
+                                  kdim, _at(row_choice), k, int(swiglu), _kind(out, "out"), _at(out), _at(workspace),
+                                  workspace.numel() * workspace.element_size(), raw),
            "matvec_nvfp4")
     return out

@@ -1,9 +1,13 @@
 """Rows times NVFP4 weights against a plain 64-bit implementation.
 
-Tolerances.  u = 2^-24.  Codes times scales and the f16 activations multiply exactly; the float32 sums of K terms are
-within 2 K u S of the exact one (S: the sum of the terms' magnitudes), the expert's scale and the joining of the shares
-add 24 u S.  An activation's f16 is off by at most 2^-39 of the largest finite one of its 256.  The sigmoid has a relative
-error of (|g| + 8) 2^-23.  Rounding to bf16: half a step, 2^-8 of the value; to float32 2^-24."""
+Tolerances.  u = 2^-24.  An activation is a sum of eight octal digits in units of 2^-22 of 2^b, b the exponent of the
+largest of its 16: bf16's 8 bits are all there unless it lies below 2^-15 of 2^b, and then rounding leaves half a unit,
+2^-23 of 2^b; 16 values below 2^-17 of the row's largest, 2^e, have units of 2^-39 of it and leave 2^-40.  Each digit's sum
+of K terms is formed in float32 with truncation, at least 16 terms at a time: K / 16 * 2 u of its magnitude, and the
+magnitudes of all digits together are at most 5 times the value's (a digit rounds a remainder r to at most 2 r; what it
+leaves is at most r, and from the second on an eighth of that each), so 2 K u S holds with room, S the sum of the terms' magnitudes; the joining of
+digits and shares and the expert's scale add 24 u S.  The sigmoid has a relative error of (|g| + 8) 2^-23.  Rounding to bf16:
+half a step, 2^-8 of the value; to float32 2^-24."""
 import numpy as np
 import pytest
 import torch
@@ -64,7 +68,9 @@ def check(pmn, x, w, offsets, out, swiglu=False, choice=None, k=1, got=None):
         inside[r] = True
         xr = X[r] if choice is None else np.where((np.array(choice)[r] >= 0)[:, None], X[np.maximum(np.array(choice)[r], 0) // k], 0)
         y, mag = xr @ W[e].T, np.abs(xr) @ np.abs(W[e].T)
-        err = (2 * K + 24) * U * mag + 2.0 ** -39 * np.abs(xr).max(1, initial=0)[:, None] * np.abs(W[e]).sum(1)[None]
+        block = np.repeat(np.abs(xr).reshape(len(r), K // 16, 16).max(-1), 16, -1)
+        left = np.where(np.abs(xr) < 2.0 ** -14 * block, 2.0 ** -23 * block, 0) + 2.0 ** -40 * np.abs(xr).max(1, initial=0)[:, None]
+        err = (2 * K + 24) * U * mag + left @ np.abs(W[e].T)
         if swiglu:
             g, u, eg, eu = y[:, :n // 2], y[:, n // 2:], err[:, :n // 2], err[:, n // 2:]
             s = 1 / (1 + np.exp(-np.clip(g, -700, None)))
