@@ -34,9 +34,11 @@ __device__ int g_bf16_error = 0;
 constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int TILE = 256;       // output columns of a pair's tile, and most rows
-constexpr int STAGES = 6, SIDE_BYTES = 128 * 128, STAGE_BYTES = 2 * SIDE_BYTES;  // a CTA's 128 x 64 of either operand
+constexpr int STAGES = 5, SIDE_BYTES = 128 * 128, STAGE_BYTES = 2 * SIDE_BYTES;  // a CTA's 128 x 64 of either operand
 constexpr int EW = 8, THREADS = 128 + 32 * EW;
-constexpr int BAR_OFF = STAGES * STAGE_BYTES, CUM_OFF = BAR_OFF + 256;
+constexpr int CH = 16;           // output rows that an epilogue warp handles at a time, 32 columns of them
+constexpr int WARP_BUF = 4096;   // .. on their way to or from memory, two buffers
+constexpr int BUF_OFF = STAGES * STAGE_BYTES, BAR_OFF = BUF_OFF + EW * WARP_BUF, CUM_OFF = BAR_OFF + 384;
 constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
 constexpr int MT_BLOCK = 8;  // column tiles that share a tile's rows before the next rows are taken
 constexpr uint64_t DRAIN_NS = 100000000ull;
@@ -58,7 +60,9 @@ struct Maps {
     CUtensorMap w;      // M side
     CUtensorMap w8, w1; // SUMS: 8 rows and 1 row of it
     CUtensorMap x;      // N side: 128 rows (SUMS: 64 columns of 64 rows)
+    CUtensorMap x64, x32;
     CUtensorMap x8, x1; // 16 rows (SUMS: 8 rows); SUMS: 1 row
+    CUtensorMap out, y; // 16 rows of 32 columns (GATED: of 16)
 };
 
 struct Tile {
@@ -82,21 +86,27 @@ struct Form {
     static constexpr int cols = gated ? TILE / 2 : TILE;                    // output columns of a pair's tile
 };
 
+// The group that row tile u of all groups belongs to (a whole warp asks).
+__device__ __forceinline__ int find_group(int u, const int *s_cum, int groups, int lane)
+{
+    const int hi = __popc(__ballot_sync(0xFFFFFFFFu, 32 * lane < groups && s_cum[32 * lane] <= u)) - 1;
+    return 32 * hi + __popc(__ballot_sync(0xFFFFFFFFu, 32 * hi + lane < groups && s_cum[32 * hi + lane] <= u)) - 1;
+}
+
 template <int FORM>
-__device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int &gc)
+__device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int lane)
 {
     constexpr int COLS = Form<FORM>::cols;
     const int mt = (int)((p.n + COLS - 1) / COLS);
-    while (gc + 1 < p.groups && s_cum[gc + 1] <= t) ++gc;  // every role walks its tiles upwards
     Tile ti;
-    ti.g = gc;
-    ti.lo = __ldg(p.offsets + gc);
-    ti.hi = __ldg(p.offsets + gc + 1);
+    ti.g = find_group(t / mt, s_cum, p.groups, lane);
+    ti.lo = __ldg(p.offsets + ti.g);
+    ti.hi = __ldg(p.offsets + ti.g + 1);
     const int64_t rows = Form<FORM>::sums ? p.m : ti.hi - ti.lo;
-    const int nt = (int)((rows + TILE - 1) / TILE);
     ti.width = even_width(rows);
     // column tiles in blocks: the tiles in flight read few rows and few weights
-    const int local = t - s_cum[gc], block = local / (MT_BLOCK * nt), rest = local - block * MT_BLOCK * nt;
+    const int nt = (int)((rows + TILE - 1) / TILE);
+    const int local = t - s_cum[ti.g] * mt, block = local / (MT_BLOCK * nt), rest = local - block * MT_BLOCK * nt;
     const int bw = min(MT_BLOCK, mt - block * MT_BLOCK), ri = rest / bw;
     ti.c0 = (block * MT_BLOCK + rest - ri * bw) * COLS;
     ti.r0 = (Form<FORM>::sums ? 0 : ti.lo) + (int64_t)ri * ti.width;
@@ -130,6 +140,14 @@ __device__ __forceinline__ void tma_5d_pair(uint32_t dst, const CUtensorMap *m, 
         "%4, %5, %6, %7}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e)
         : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16_pair(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -188,7 +206,8 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
     const uint32_t stages = smem_u32(smem);
     const uint32_t bar_full = stages + BAR_OFF, bar_empty = bar_full + 8 * STAGES;
     const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 5));
+    const uint32_t bar_y = bar_drain + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 5 + 2 * EW));
     int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
     int *s_total = s_abort + 1;
     int *s_cum = reinterpret_cast<int *>(smem + CUM_OFF);
@@ -206,6 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
             mbar_init(bar_acc_empty + 8 * b, 2 * EW);
         }
         mbar_init(bar_drain, 1);
+        for (int b = 0; b < 2 * EW; ++b) mbar_init(bar_y + 8 * b, 1);
         *s_abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&maps.w);
@@ -217,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         tmem_alloc_ct<2>(smem_u32(tmem_slot), TMEM_COLS);
     }
     if (warp == 1) {
-        // tiles of each group and their running sum, 32 groups at a time; offsets that
+        // row tiles of each group and their running sum, 32 groups at a time; offsets that
         // are not monotone and in range run no tile
         const int mt = (int)((p.n + F::cols - 1) / F::cols);
         int base = 0;
@@ -233,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
             good = __all_sync(0xFFFFFFFFu, good);
             if (!good) break;
             const int64_t rows = F::sums ? (g < p.groups ? p.m : 0) : hi - lo;
-            int n = (int)((rows + TILE - 1) / TILE) * mt, sum = n;
+            int n = (int)((rows + TILE - 1) / TILE), sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         }
         if (lane == 0) {
             s_cum[p.groups] = base;
-            *s_total = good ? base : 0;
+            *s_total = good ? base * mt : 0;
             if (!good && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         }
     }
@@ -264,10 +284,9 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         uint32_t stage = 0, phase = 0, issued = 0, last = 0;
-        int gc = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
+            const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
             const int nks = stages_of<FORM>(ti, p), half = ti.width / 2;
             for (int ks = 0; ks < nks; ++ks) {
                 ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
@@ -298,9 +317,11 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                             tma_3d_pair(w + 8192, &maps.w, lb, ti.c0 + 128 * rank + 64, 64 * ks, ti.g);
                         }
                         const int row = (int)ti.r0 + half * rank;
-                        if (half == 128) tma_load_2d_pair(x, &maps.x, lb, 64 * ks, row);
-                        else
-                            for (int r = 0; r < half; r += 16) tma_load_2d_pair(x + 128 * r, &maps.x8, lb, 64 * ks, row + r);
+                        // few boxes: with 16 rows each the forward of 8192 rows takes 12 % longer
+                        if (half & 128) tma_load_2d_pair(x, &maps.x, lb, 64 * ks, row);
+                        if (half & 64) tma_load_2d_pair(x, &maps.x64, lb, 64 * ks, row);
+                        if (half & 32) tma_load_2d_pair(x + 128 * (half & 64), &maps.x32, lb, 64 * ks, row + (half & 64));
+                        if (half & 16) tma_load_2d_pair(x + 128 * (half & 96), &maps.x8, lb, 64 * ks, row + (half & 96));
                     }
                 }
                 __syncwarp();
@@ -328,10 +349,9 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), el = elect_one();
             uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
-            int gc = 0;
             bool ok = true, ready = false;
             for (int t = tile0; t < total && ok; t += tstep) {
-                const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
+                const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
                 const int nks = stages_of<FORM>(ti, p);
                 // D float32, A and B bf16, M = 256
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (F::m_major_w ? 1u << 15 : 0u) |
@@ -384,78 +404,153 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
-        // A lane holds one column of the output, a register one row; a warp has every
-        // (EW / 4)th chunk of 32 rows.
+        // A lane holds one column of the output, a register one row.  A warp takes every
+        // (EW / 4)th 16 rows of its 32 columns, puts them into shared memory and has TMA write
+        // them: the stores then cost the warp nothing and arrive as whole lines.  Rows
+        // behind the segment's end may not be written, so the last few of a segment are stored singly.
         const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0), quad = wu & 3, c_first = (wu - 4) >> 2;
-        uint32_t abuf = 0, aphase = 0;
-        int gc = 0;
+        uint8_t *const buf0 = smem + BUF_OFF + (wu - 4) * WARP_BUF;
+        const uint32_t bufs0 = stages + BUF_OFF + (wu - 4) * WARP_BUF, ybar = bar_y + 16 * (wu - 4);
+        uint32_t abuf = 0, aphase = 0, n = 0;  // n: chunks so far
         bool ok = true;
+        // first column of the warp in a tile, the tile's rows
+        auto col_of = [&](const Tile &ti) { return F::gated ? ti.c0 + 64 * rank + 16 * quad : ti.c0 + 128 * rank + 32 * quad; };
+        auto chunks_of = [&](const Tile &ti) {
+            return col_of(ti) < p.n ? (int)((min((int64_t)ti.width, ti.row_end - ti.r0) + CH - 1) / CH) : 0;
+        };
+        // GATED_BACKWARD: gate and up come by TMA too, a chunk ahead, into the buffer that takes their gradients
+        int at = tile0, ac = c_first;
+        Tile ahead;
+        auto fetch = [&]() {
+            while (at < total && ac >= chunks_of(ahead)) {
+                at += tstep;
+                ac = c_first;
+                if (at < total) ahead = get_tile<FORM>(at, p, s_cum, lane);
+            }
+            if (at >= total) return;
+            if (lane == 0) {
+                const uint32_t b = n & 1u, d = bufs0 + 2048 * b, bar = ybar + 8 * b;
+                const int x = col_of(ahead), r = (int)ahead.r0 + CH * ac;
+                bulk_wait_group_read<1>();
+                mbar_arrive_expect_tx(bar, 2048);
+                tma_load_2d(d, &maps.y, bar, x, r);
+                tma_load_2d(d + 1024, &maps.y, bar, (int)p.n + x, r);
+            }
+            __syncwarp();
+            ac += EW / 4;
+        };
+        if (F::backward) {
+            if (at < total) ahead = get_tile<FORM>(at, p, s_cum, lane);
+            fetch();
+        }
         for (int t = tile0; t < total && ok; t += tstep) {
-            const Tile ti = get_tile<FORM>(t, p, s_cum, gc);
-            const int chunks = ti.width / 32;
+            const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
+            const int chunks = chunks_of(ti), col0 = col_of(ti);
             const bool nothing = F::sums && ti.hi == ti.lo;  // a sum over no rows
             ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * TILE;
-            for (int c = c_first; c < chunks; c += EW / 4) {
-                float v[32];
-                tmem_ld_32x32b_x32(acc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v));
+            for (int c = c_first; c < chunks; c += EW / 4, ++n) {
+                float v[CH];
+                tmem_ld_32x32b_x16(acc + CH * c, reinterpret_cast<uint32_t(&)[CH]>(v));
                 tmem_ld_wait();
                 if (nothing) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int j = 0; j < CH; ++j) v[j] = 0.0f;
                 }
-                const int64_t r0 = ti.r0 + 32 * c;
-                const int rows = (int)min((int64_t)32, ti.row_end - r0);
-                if constexpr (FORM == GATED) {
+                const int64_t r0 = ti.r0 + CH * c;
+                const int rows = (int)min((int64_t)CH, ti.row_end - r0);
+                if constexpr (F::gated) {
                     // lanes 0 .. 15 gate, 16 .. 31 up of the same 16 columns: the halves trade
                     // values, so that the lower half makes h of the even rows, the upper of the odd
-                    const int col = ti.c0 + 64 * rank + 16 * quad + (lane & 15);
-                    const bool up = lane >= 16, on = col < p.n;
-                    uint16_t *y = p.y ? p.y + r0 * 2 * p.n + col + (up ? p.n : 0) : nullptr;
-                    uint16_t *h = static_cast<uint16_t *>(p.out) + (r0 + up) * p.n + col;
+                    const bool up = lane >= 16;
+                    const int cl = lane & 15;
+                    uint16_t *b = reinterpret_cast<uint16_t *>(buf0 + 2048 * (n & 1u));  // gate, up, h: 16 x 16 each
+                    if (lane == 0) bulk_wait_group_read<1>();
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        if (y && on && j < rows) store_one(y + j * 2 * p.n, v[j]);
-                        if (y && on && j + 1 < rows) store_one(y + (j + 1) * 2 * p.n, v[j + 1]);
+                    for (int j = 0; j < CH; j += 2) {
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
                         const float g = up ? got : v[j], u = up ? v[j + 1] : got;
-                        if (on && j + up < rows) store_one(h + j * p.n, __fmul_rn(__fmul_rn(g, sigmoid(g)), u));
+                        store_one(b + 256 * up + 16 * j + cl, v[j]);
+                        store_one(b + 256 * up + 16 * j + 16 + cl, v[j + 1]);
+                        store_one(b + 512 + 16 * (j + up) + cl, __fmul_rn(__fmul_rn(g, sigmoid(g)), u));
                     }
-                } else {
-                    const int col = ti.c0 + 128 * rank + 32 * quad + lane;
-                    if (col < p.n) {
-                        if constexpr (FORM == GATED_BACKWARD) {
-                            const uint16_t *y = p.y + r0 * 2 * p.n + col;
-                            uint16_t *o = static_cast<uint16_t *>(p.out) + r0 * 2 * p.n + col;
-#pragma unroll
-                            for (int j0 = 0; j0 < 32; j0 += 16) {
-                                uint16_t gate[16], up[16];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (j0 + j < rows) {
-                                        gate[j] = __ldg(y + (j0 + j) * 2 * p.n);
-                                        up[j] = __ldg(y + (j0 + j) * 2 * p.n + p.n);
-                                    }
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (j0 + j < rows) {
-                                        const float g = bf16_value(gate[j]), u = bf16_value(up[j]), dh = v[j0 + j];
-                                        const float s = sigmoid(g), a = __fmul_rn(dh, s);
-                                        store_one(o + (j0 + j) * 2 * p.n, __fmul_rn(__fmul_rn(a, u), fmaf(g, 1.0f - s, 1.0f)));
-                                        store_one(o + (j0 + j) * 2 * p.n + p.n, __fmul_rn(a, g));
-                                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (rows == CH) {
+                        if (lane == 0) {
+                            const uint32_t d = bufs0 + 2048 * (n & 1u);
+                            if (p.y) {
+                                tma_store_2d(&maps.y, d, col0, (int)r0);
+                                tma_store_2d(&maps.y, d + 512, (int)p.n + col0, (int)r0);
                             }
-                        } else {
-                            OUT *o = static_cast<OUT *>(p.out) + (F::sums ? (int64_t)ti.g * p.m * p.n : 0) + r0 * p.n + col;
+                            tma_store_2d(&maps.out, d + 1024, col0, (int)r0);
+                        }
+                    } else {
+                        for (int j = 0; j < rows; ++j) {
+                            if (p.y) p.y[(r0 + j) * 2 * p.n + col0 + cl + (up ? p.n : 0)] = b[256 * up + 16 * j + cl];
+                            if (!up) static_cast<uint16_t *>(p.out)[(r0 + j) * p.n + col0 + cl] = b[512 + 16 * j + cl];
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) bulk_commit_group();
+                } else if constexpr (F::backward) {
+                    const uint32_t which = n & 1u;
+                    uint16_t *b = reinterpret_cast<uint16_t *>(buf0 + 2048 * which);  // gate, up: 16 x 32 each
+                    ok = warp_wait(ybar + 8 * which, (n >> 1) & 1u, p.wait_ns);
+                    if (!ok) break;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < rows) store_one(o + j * p.n, v[j]);
+                    for (int j = 0; j < CH; ++j) {
+                        const float g = bf16_value(b[32 * j + lane]), u = bf16_value(b[512 + 32 * j + lane]), dh = v[j];
+                        const float s = sigmoid(g), a = __fmul_rn(dh, s);
+                        store_one(b + 32 * j + lane, __fmul_rn(__fmul_rn(a, u), fmaf(g, 1.0f - s, 1.0f)));
+                        store_one(b + 512 + 32 * j + lane, __fmul_rn(a, g));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (rows == CH && col0 + 32 <= p.n) {  // (a box may not reach from gate's columns into up's)
+                        if (lane == 0) {
+                            const uint32_t d = bufs0 + 2048 * which;
+                            tma_store_2d(&maps.out, d, col0, (int)r0);
+                            tma_store_2d(&maps.out, d + 1024, (int)p.n + col0, (int)r0);
+                        }
+                    } else if (col0 + lane < p.n) {
+                        uint16_t *o = static_cast<uint16_t *>(p.out) + r0 * 2 * p.n + col0 + lane;
+                        for (int j = 0; j < rows; ++j) {
+                            o[j * 2 * p.n] = b[32 * j + lane];
+                            o[j * 2 * p.n + p.n] = b[512 + 32 * j + lane];
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) bulk_commit_group();
+                    ++n;
+                    fetch();  // into the other buffer, whose store has been under way for a chunk
+                    --n;
+                } else {
+                    constexpr int BUFS = WARP_BUF / (CH * 32 * (int)sizeof(OUT));
+                    const uint32_t off = CH * 32 * sizeof(OUT) * (n % BUFS);
+                    OUT *b = reinterpret_cast<OUT *>(buf0 + off);
+                    if (lane == 0) bulk_wait_group_read<BUFS - 1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) store_one(b + 32 * j + lane, v[j]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (F::sums) {
+                        if (lane == 0) tma_store_3d(&maps.out, bufs0 + off, col0, (int)r0, ti.g);
+                    } else if (rows == CH) {
+                        if (lane == 0) tma_store_2d(&maps.out, bufs0 + off, col0, (int)r0);
+                    } else if (col0 + lane < p.n) {
+                        OUT *o = static_cast<OUT *>(p.out) + r0 * p.n + col0 + lane;
+                        for (int j = 0; j < rows; ++j) o[j * p.n] = b[32 * j + lane];
+                    }
+                    __syncwarp();
+                    if (lane == 0) bulk_commit_group();
                 }
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_leader(bar_acc_empty + 8 * abuf);
@@ -465,6 +560,13 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
             }
         }
         if (!ok) give_up();
+        if (F::backward && !ok) {  // a load that nobody waited for may still be landing
+            (void)warp_wait(ybar, 0, DRAIN_NS);
+            (void)warp_wait(ybar, 1, DRAIN_NS);
+            (void)warp_wait(ybar + 8, 0, DRAIN_NS);
+            (void)warp_wait(ybar + 8, 1, DRAIN_NS);
+        }
+        if (lane == 0) bulk_wait_group_all();  // shared memory is read until then
         __syncwarp();
     }
 
@@ -477,7 +579,8 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
 }
 
 // ====================================================================== host
-bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box)
+bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, bool swizzle = true)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -489,8 +592,19 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, 
         b[i] = box[i];
         if (i + 1 < rank) st[i] = strides[i];
     }
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, type, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The epilogue's pieces: CH rows of `cols` columns of [groups, rows, n] (groups 0: of [rows, n]).
+bool piece_map(CUtensorMap *m, const void *base, int groups, int64_t rows, int64_t n, int kind, int cols)
+{
+    const uint64_t b = kind == PMN_OUT_F32 ? 4 : 2;
+    const uint64_t dims[3] = {(uint64_t)n, (uint64_t)rows, (uint64_t)groups}, st[2] = {n * b, (uint64_t)rows * n * b};
+    const uint32_t box[3] = {(uint32_t)cols, CH, 1};
+    return make_map(m, base, groups ? 3 : 2, dims, st, box,
+                    kind == PMN_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false);
 }
 
 // rows [rows, width] of pitch ld, 64 columns (128 bytes) of box_rows rows
@@ -546,7 +660,8 @@ pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k
 // Maps of the token rows [rows, k].
 bool token_maps(Maps &maps, const void *a, int64_t rows, int64_t k, int64_t lda)
 {
-    return rows_map(&maps.x, a, k, rows, lda, 128) && rows_map(&maps.x8, a, k, rows, lda, 16);
+    return rows_map(&maps.x, a, k, rows, lda, 128) && rows_map(&maps.x64, a, k, rows, lda, 64) &&
+           rows_map(&maps.x32, a, k, rows, lda, 32) && rows_map(&maps.x8, a, k, rows, lda, 16);
 }
 
 // Weights [groups, rows, cols], 64 columns of box_rows rows at a time.
@@ -596,7 +711,8 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
                        ? PMN_OK : PMN_ERR_CUDA;
         if (!a || !b) return PMN_ERR_INVALID_ARG;
         if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.w8, b, n, k, ldb, 8) || !rows_map(&maps.w1, b, n, k, ldb, 1) ||
-            !rows_map(&maps.x, a, m, k, lda, 64) || !rows_map(&maps.x8, a, m, k, lda, 8) || !rows_map(&maps.x1, a, m, k, lda, 1))
+            !rows_map(&maps.x, a, m, k, lda, 64) || !rows_map(&maps.x8, a, m, k, lda, 8) || !rows_map(&maps.x1, a, m, k, lda, 1) ||
+            !piece_map(&maps.out, out, num_groups, m, n, out_kind, 32))
             return PMN_ERR_CUDA;
         const Args args{offsets, num_groups, k, m, n, 0, out, nullptr, pmn_wait_limit_ns()};
         return out_kind == PMN_OUT_F32 ? launch<SUMS, float>(maps, args, s) : launch<SUMS, uint16_t>(maps, args, s);
@@ -605,7 +721,8 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
     if (m == 0) return PMN_OK;
     if (!a || !b || !out || !offsets) return PMN_ERR_INVALID_ARG;
     if (!token_maps(maps, a, m, k, lda) || !(b_transposed ? weight_map(&maps.w, b, num_groups, k, n, 64)
-                                                          : weight_map(&maps.w, b, num_groups, n, k, 128)))
+                                                          : weight_map(&maps.w, b, num_groups, n, k, 128)) ||
+        !piece_map(&maps.out, out, 0, m, n, out_kind, 32))
         return PMN_ERR_CUDA;
     const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
     if (b_transposed)
@@ -629,8 +746,12 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
     const uint64_t str[4] = {(uint64_t)k * 2, (uint64_t)f * k * 2, (uint64_t)k * 32, (uint64_t)f * k * 4};
     const uint32_t box[5] = {64, 16, 2, 4, 1};
     Maps maps = {};
-    if (!token_maps(maps, a, total_rows, k, lda) || !make_map(&maps.w, b, 5, dims, str, box)) return PMN_ERR_CUDA;
-    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out), pmn_wait_limit_ns()};
+    if (!token_maps(maps, a, total_rows, k, lda) || !make_map(&maps.w, b, 5, dims, str, box) ||
+        !piece_map(&maps.out, out, 0, total_rows, f, PMN_OUT_BF16, 16) ||
+        (y_out && !piece_map(&maps.y, y_out, 0, total_rows, 2 * f, PMN_OUT_BF16, 16)))
+        return PMN_ERR_CUDA;
+    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
+                    pmn_wait_limit_ns()};
     return launch<GATED, uint16_t>(maps, args, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -646,7 +767,10 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t ld
         !aligned(out, 16))
         return PMN_ERR_INVALID_ARG;
     Maps maps = {};
-    if (!token_maps(maps, a, total_rows, k, lda) || !weight_map(&maps.w, b, num_experts, k, f, 64)) return PMN_ERR_CUDA;
+    if (!token_maps(maps, a, total_rows, k, lda) || !weight_map(&maps.w, b, num_experts, k, f, 64) ||
+        !piece_map(&maps.out, out, 0, total_rows, 2 * f, PMN_OUT_BF16, 32) ||
+        !piece_map(&maps.y, y, 0, total_rows, 2 * f, PMN_OUT_BF16, 32))
+        return PMN_ERR_CUDA;
     const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(const_cast<void *>(y)),
                     pmn_wait_limit_ns()};
     return launch<GATED_BACKWARD, uint16_t>(maps, args, reinterpret_cast<cudaStream_t>(stream));
