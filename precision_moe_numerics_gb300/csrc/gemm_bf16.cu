@@ -33,14 +33,18 @@ __device__ int g_bf16_error = 0;
 
 constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int TILE = 256;       // output columns of a pair's tile, and most rows
-constexpr int STAGES = 5, SIDE_BYTES = 128 * 128, STAGE_BYTES = 2 * SIDE_BYTES;  // a CTA's 128 x 64 of either operand
+constexpr int TILE = 256;        // output columns of a pair's tile, and most rows
+constexpr int SIDE_BYTES = 128 * 128;  // a CTA's 128 x 64 of either operand
+constexpr int RING_BYTES = 12 * SIDE_BYTES, MAX_SLOTS = 9;
 constexpr int EW = 8, THREADS = 128 + 32 * EW;
 constexpr int CH = 16;           // output rows that an epilogue warp handles at a time, 32 columns of them
 constexpr int WARP_BUF = 4096;   // .. on their way to or from memory, two buffers
-constexpr int BUF_OFF = STAGES * STAGE_BYTES, BAR_OFF = BUF_OFF + EW * WARP_BUF, CUM_OFF = BAR_OFF + 384;
-constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
-constexpr int MT_BLOCK = 8;  // column tiles that share a tile's rows before the next rows are taken
+constexpr int BUF_OFF = RING_BYTES, BAR_OFF = BUF_OFF + EW * WARP_BUF;
+constexpr int BARRIERS = 3 * MAX_SLOTS + 5 + 2 * EW;
+constexpr int CUM_OFF = BAR_OFF + 8 * BARRIERS + 16;
+constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS / 32 + 1) * 4;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int MT_BLOCK = 8;      // column tiles that share a tile's rows before the next rows are taken
 constexpr uint64_t DRAIN_NS = 100000000ull;
 
 // Rows times weights [n, k] and [k, n], the forward with SwiGLU, the gradient of h, sums over rows.
@@ -57,27 +61,18 @@ struct Args {
 };
 
 struct Maps {
-    CUtensorMap w;      // M side
-    CUtensorMap w8, w1; // SUMS: 8 rows and 1 row of it
-    CUtensorMap x;      // N side: 128 rows (SUMS: 64 columns of 64 rows)
-    CUtensorMap x64, x32;
-    CUtensorMap x8, x1; // 16 rows (SUMS: 8 rows); SUMS: 1 row
-    CUtensorMap out, y; // 16 rows of 32 columns (GATED: of 16)
+    CUtensorMap w;                   // M side
+    CUtensorMap x, x64, x32, x16;    // N side: 128, 64, 32, 16 rows (SUMS: x alone, 64 columns of 64 rows)
+    CUtensorMap out, y;              // CH rows of 32 columns (GATED: of 16)
 };
 
 struct Tile {
-    int g, width;      // N side, a multiple of 32
+    int g, width;      // rows, a multiple of 32
     int64_t lo, hi;    // the group's rows
     int64_t r0;        // first output row
     int64_t row_end;   // output rows end here
     int c0;            // first output column of the pair
 };
-
-__device__ __forceinline__ int even_width(int64_t m)
-{
-    const int nt = (int)((m + TILE - 1) / TILE);
-    return (int)(((m + nt - 1) / nt + 31) / 32 * 32);
-}
 
 template <int FORM>
 struct Form {
@@ -86,31 +81,43 @@ struct Form {
     static constexpr int cols = gated ? TILE / 2 : TILE;                    // output columns of a pair's tile
 };
 
-// The group that row tile u of all groups belongs to (a whole warp asks).
-__device__ __forceinline__ int find_group(int u, const int *s_cum, int groups, int lane)
-{
-    const int hi = __popc(__ballot_sync(0xFFFFFFFFu, 32 * lane < groups && s_cum[32 * lane] <= u)) - 1;
-    return 32 * hi + __popc(__ballot_sync(0xFFFFFFFFu, 32 * hi + lane < groups && s_cum[32 * hi + lane] <= u)) - 1;
-}
+__device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + TILE - 1) / TILE); }
 
+// Tile t of all (a whole warp asks).  s_cum: row tiles before every 32nd group.
 template <int FORM>
 __device__ __forceinline__ Tile get_tile(int t, const Args &p, const int *s_cum, int lane)
 {
-    constexpr int COLS = Form<FORM>::cols;
-    const int mt = (int)((p.n + COLS - 1) / COLS);
+    using F = Form<FORM>;
+    const int mt = (int)((p.n + F::cols - 1) / F::cols), u = t / mt;
+    const int b = __popc(__ballot_sync(0xFFFFFFFFu, 32 * lane < p.groups && s_cum[lane] <= u)) - 1, g = 32 * b + lane;
+    int lo = 0, hi = 0;
+    if (g < p.groups) {
+        lo = __ldg(p.offsets + g);
+        hi = __ldg(p.offsets + g + 1);
+    }
+    const int n = g < p.groups ? tiles_of(F::sums ? p.m : hi - lo) : 0;
+    int first = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, first, o);
+        if (lane >= o) first += v;
+    }
+    first += s_cum[b] - n;
+    // the last group that begins at or before u: those before it without tiles begin there too
+    const int at = __popc(__ballot_sync(0xFFFFFFFFu, g < p.groups && first <= u)) - 1;
     Tile ti;
-    ti.g = find_group(t / mt, s_cum, p.groups, lane);
-    ti.lo = __ldg(p.offsets + ti.g);
-    ti.hi = __ldg(p.offsets + ti.g + 1);
-    const int64_t rows = Form<FORM>::sums ? p.m : ti.hi - ti.lo;
-    ti.width = even_width(rows);
+    ti.g = 32 * b + at;
+    ti.lo = __shfl_sync(0xFFFFFFFFu, lo, at);
+    ti.hi = __shfl_sync(0xFFFFFFFFu, hi, at);
+    const int64_t rows = F::sums ? p.m : ti.hi - ti.lo;
+    const int nt = tiles_of(rows);
+    ti.width = (int)(((rows + nt - 1) / nt + 31) / 32 * 32);
     // column tiles in blocks: the tiles in flight read few rows and few weights
-    const int nt = (int)((rows + TILE - 1) / TILE);
-    const int local = t - s_cum[ti.g] * mt, block = local / (MT_BLOCK * nt), rest = local - block * MT_BLOCK * nt;
+    const int local = t - __shfl_sync(0xFFFFFFFFu, first, at) * mt, block = local / (MT_BLOCK * nt), rest = local - block * MT_BLOCK * nt;
     const int bw = min(MT_BLOCK, mt - block * MT_BLOCK), ri = rest / bw;
-    ti.c0 = (block * MT_BLOCK + rest - ri * bw) * COLS;
-    ti.r0 = (Form<FORM>::sums ? 0 : ti.lo) + (int64_t)ri * ti.width;
-    ti.row_end = Form<FORM>::sums ? p.m : ti.hi;
+    ti.c0 = (block * MT_BLOCK + rest - ri * bw) * F::cols;
+    ti.r0 = (F::sums ? 0 : ti.lo) + (int64_t)ri * ti.width;
+    ti.row_end = F::sums ? p.m : ti.hi;
     return ti;
 }
 
@@ -120,6 +127,34 @@ __device__ __forceinline__ int stages_of(const Tile &ti, const Args &p)
 {
     return (int)(((Form<FORM>::sums ? ti.hi - ti.lo : p.k) + 63) / 64);
 }
+
+// The ring of stages.  A slot holds the weights' 16 KB and the rows: 4 KB of a tile of up to 64,
+// 16 KB of up to 256; what is in flight counts (loads and products of the forward of 8192 rows: 3 slots
+// of 32 KB 211 us, 4 182, 5 162, 6 158).  A tile of the other kind than the one before starts
+// at slot 0, once the stages before it have been read.
+template <int FORM>
+struct Ring {
+    uint32_t kind = 2, slot = 0, phases = 0;  // bit s: parity of slot s's next use
+    __device__ __forceinline__ static uint32_t kind_of(const Tile &ti)
+    {
+        return Form<FORM>::sums || ti.width > 64 ? 1u : 0u;
+    }
+    __device__ __forceinline__ uint32_t slots() const { return kind == 0 ? 9u : 6u; }
+    __device__ __forceinline__ uint32_t bytes() const { return kind == 0 ? 20480u : 32768u; }
+    __device__ __forceinline__ uint32_t parity() const { return (phases >> slot) & 1u; }
+    __device__ __forceinline__ void enter(const Tile &ti)
+    {
+        const uint32_t k = kind_of(ti);
+        if (k != kind) slot = 0;
+        kind = k;
+    }
+    __device__ __forceinline__ void step()
+    {
+        phases ^= 1u << slot;
+        if (++slot == slots()) slot = 0;
+    }
+};
+static_assert(9 * 20480 <= RING_BYTES && 6 * 32768 <= RING_BYTES, "slots");
 
 __device__ __forceinline__ void latch_error(int bit) { atomicOr(&g_bf16_error, bit); }
 
@@ -150,37 +185,19 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src,
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16_pair(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// The descriptors' high words are constants (smem_desc: 1024 bytes between groups of 8 rows,
+// version, 128-byte swizzle); the low ones hold the address and the other stride.
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t el, uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                               uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(el)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(el), "n"(DESC_HIGH)
         : "memory");
-}
-
-// SUMS: `rows` (1 to 64) of a stage's 64 ragged rows of 64 columns, then zeros up to a
-// multiple of 16: another expert's rows, or the buffer's last contents, would enter the
-// sums.  Rows behind the tensor read as zeros.
-__device__ __forceinline__ uint32_t sum_rows(int rows) { return (uint32_t)(rows + 15) & ~15u; }
-
-__device__ __forceinline__ void load_sum_rows(uint32_t dst, const CUtensorMap *m64, const CUtensorMap *m8,
-                                              const CUtensorMap *m1, uint32_t bar, int x, int y, int rows, int outside)
-{
-    if (rows == 64) {
-        tma_load_2d_pair(dst, m64, bar, x, y);
-        return;
-    }
-    const int end = (int)sum_rows(rows);
-    int r = 0;
-    for (; r + 8 <= rows; r += 8) tma_load_2d_pair(dst + 128 * r, m8, bar, x, y + r);
-    if (r < rows) {
-        const int stop = r + 8;
-        for (; r < rows; ++r) tma_load_2d_pair(dst + 128 * r, m1, bar, x, y + r);
-        for (; r < stop; ++r) tma_load_2d_pair(dst + 128 * r, m1, bar, x, outside);
-    }
-    for (; r < end; r += 8) tma_load_2d_pair(dst + 128 * r, m8, bar, x, outside);
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
@@ -194,8 +211,9 @@ __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
-// Roles: warp 0 loads by TMA, warp 1 of the leader issues the pair's MMAs, warps 4.. store.
-// Every wait is bounded: on a timeout an error bit is latched and the CTA winds down.
+// Roles: warp 0 loads by TMA, warp 1 of the leader issues the pair's MMAs, warp 2 (SUMS) clears
+// rows that are not the group's, warps 4.. store.  Every wait is bounded: on a timeout an
+// error bit is latched and the CTA winds down.
 template <int FORM, typename OUT>
 __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant__ Maps maps, const Args p)
 {
@@ -203,11 +221,11 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw;
     asm volatile("" : "+l"(smem));
-    const uint32_t stages = smem_u32(smem);
-    const uint32_t bar_full = stages + BAR_OFF, bar_empty = bar_full + 8 * STAGES;
-    const uint32_t bar_acc_full = bar_empty + 8 * STAGES, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t bar_full = ring + BAR_OFF, bar_empty = bar_full + 8 * MAX_SLOTS, bar_land = bar_empty + 8 * MAX_SLOTS;
+    const uint32_t bar_acc_full = bar_land + 8 * MAX_SLOTS, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
     const uint32_t bar_y = bar_drain + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 5 + 2 * EW));
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * BARRIERS);
     int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
     int *s_total = s_abort + 1;
     int *s_cum = reinterpret_cast<int *>(smem + CUM_OFF);
@@ -216,9 +234,10 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
     const int tile0 = blockIdx.x / 2, tstep = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
+        for (int s = 0; s < MAX_SLOTS; ++s) {
+            mbar_init(bar_full + 8 * s, F::sums ? 2 : 1);  // SUMS: each CTA's word that its rows are there, and clean
             mbar_init(bar_empty + 8 * s, 1);
+            mbar_init(bar_land + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
@@ -230,15 +249,13 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         fence_barrier_init();
         tma_prefetch_desc(&maps.w);
         tma_prefetch_desc(&maps.x);
-        tma_prefetch_desc(&maps.x8);
     }
     if (warp == 0) {
         __syncwarp();
         tmem_alloc_ct<2>(smem_u32(tmem_slot), TMEM_COLS);
     }
     if (warp == 1) {
-        // row tiles of each group and their running sum, 32 groups at a time; offsets that
-        // are not monotone and in range run no tile
+        // row tiles before every 32nd group; offsets that are not monotone and in range run no tile
         const int mt = (int)((p.n + F::cols - 1) / F::cols);
         int base = 0;
         bool good = true;
@@ -250,20 +267,11 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                 hi = __ldg(p.offsets + g + 1);
                 if (lo < 0 || hi < lo || hi > p.rows) good = false;
             }
-            good = __all_sync(0xFFFFFFFFu, good);
-            if (!good) break;
-            const int64_t rows = F::sums ? (g < p.groups ? p.m : 0) : hi - lo;
-            int n = (int)((rows + TILE - 1) / TILE), sum = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            if (g < p.groups) s_cum[g] = base + sum - n;
-            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            if (lane == 0) s_cum[g0 / 32] = base;
+            base += __reduce_add_sync(0xFFFFFFFFu, g < p.groups ? tiles_of(F::sums ? p.m : hi - lo) : 0);
         }
+        good = __all_sync(0xFFFFFFFFu, good);
         if (lane == 0) {
-            s_cum[p.groups] = base;
             *s_total = good ? base * mt : 0;
             if (!good && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         }
@@ -283,60 +291,71 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
-        uint32_t stage = 0, phase = 0, issued = 0, last = 0;
+        Ring<FORM> at;
+        uint32_t issued = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t += tstep) {
             const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
             const int nks = stages_of<FORM>(ti, p), half = ti.width / 2;
-            for (int ks = 0; ks < nks; ++ks) {
-                ok = warp_wait(bar_empty + 8 * stage, phase ^ 1, p.wait_ns);
+            const int row = (int)ti.r0 + half * rank;  // of the N side, first accumulator
+            if (at.kind != 2 && at.kind != Ring<FORM>::kind_of(ti))
+                for (uint32_t s = 0; s < at.slots() && ok; ++s) {
+                    ok = warp_wait(bar_empty + 8 * s, ((at.phases >> s) & 1u) ^ 1, p.wait_ns);
+                    if (!ok) give_up();
+                }
+            at.enter(ti);
+            for (int ks = 0; ks < nks && ok; ++ks) {
+                ok = warp_wait(bar_empty + 8 * at.slot, at.parity() ^ 1, p.wait_ns);
                 if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
                     if (!ok) give_up();
                     ok = false;
                     break;
                 }
-                const uint32_t w = stages + stage * STAGE_BYTES, x = w + SIDE_BYTES, fb = bar_full + 8 * stage;
                 if (elect_one()) {
-                    const uint32_t lb = leader_addr(fb);
+                    const uint32_t w = ring + at.slot * at.bytes(), x = w + SIDE_BYTES, fb = bar_full + 8 * at.slot, lb = leader_addr(fb);
+                    const int k = 64 * ks;
                     if constexpr (F::sums) {
-                        const int64_t k0 = ti.lo + 64 * ks;
-                        const int rows = (int)min((int64_t)64, ti.hi - k0), xb = (half + 63) / 64, out = (int)p.rows;
-                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * 128 * sum_rows(rows) * (2 + xb));
-                        for (int b = 0; b < 2; ++b)
-                            load_sum_rows(w + 8192 * b, &maps.w, &maps.w8, &maps.w1, lb, ti.c0 + 128 * rank + 64 * b, (int)k0, rows, out);
-                        for (int b = 0; b < xb; ++b)
-                            load_sum_rows(x + 8192 * b, &maps.x, &maps.x8, &maps.x1, lb, (int)ti.r0 + half * rank + 64 * b, (int)k0, rows, out);
+                        // Where the group ends inside 16 rows, this CTA's warp 2 clears the rest of them and
+                        // reports the stage; else both CTAs report here.
+                        const int64_t k0 = ti.lo + k;
+                        const int boxes = (half + 63) / 64;
+                        if (ti.hi - k0 < 64 && (ti.hi - k0) % 16 != 0) {
+                            const uint32_t own = bar_land + 8 * at.slot;
+                            mbar_arrive_expect_tx(own, 8192 * (2 + boxes));
+                            for (int b = 0; b < 2; ++b) tma_load_2d(w + 8192 * b, &maps.w, own, ti.c0 + 128 * rank + 64 * b, (int)k0);
+                            for (int b = 0; b < boxes; ++b) tma_load_2d(x + 8192 * b, &maps.x, own, row + 64 * b, (int)k0);
+                        } else {
+                            if (rank == 0) mbar_arrive_expect_tx(fb, 2 * 8192 * (2 + boxes));
+                            else mbar_arrive_leader(fb);
+                            for (int b = 0; b < 2; ++b) tma_load_2d_pair(w + 8192 * b, &maps.w, lb, ti.c0 + 128 * rank + 64 * b, (int)k0);
+                            for (int b = 0; b < boxes; ++b) tma_load_2d_pair(x + 8192 * b, &maps.x, lb, row + 64 * b, (int)k0);
+                        }
                     } else {
                         if (rank == 0) mbar_arrive_expect_tx(fb, 2 * (SIDE_BYTES + 128 * half));
                         if constexpr (FORM == ROWS_NK) {
-                            tma_3d_pair(w, &maps.w, lb, 64 * ks, ti.c0 + 128 * rank, ti.g);
+                            tma_3d_pair(w, &maps.w, lb, k, ti.c0 + 128 * rank, ti.g);
                         } else if constexpr (FORM == GATED) {
-                            tma_5d_pair(w, &maps.w, lb, 64 * ks, 0, 0, (ti.c0 + 64 * rank) / 16, ti.g);
+                            tma_5d_pair(w, &maps.w, lb, k, 0, 0, (ti.c0 + 64 * rank) / 16, ti.g);
                         } else {
-                            tma_3d_pair(w, &maps.w, lb, ti.c0 + 128 * rank, 64 * ks, ti.g);
-                            tma_3d_pair(w + 8192, &maps.w, lb, ti.c0 + 128 * rank + 64, 64 * ks, ti.g);
+                            tma_3d_pair(w, &maps.w, lb, ti.c0 + 128 * rank, k, ti.g);
+                            tma_3d_pair(w + 8192, &maps.w, lb, ti.c0 + 128 * rank + 64, k, ti.g);
                         }
-                        const int row = (int)ti.r0 + half * rank;
-                        // few boxes: with 16 rows each the forward of 8192 rows takes 12 % longer
-                        if (half & 128) tma_load_2d_pair(x, &maps.x, lb, 64 * ks, row);
-                        if (half & 64) tma_load_2d_pair(x, &maps.x64, lb, 64 * ks, row);
-                        if (half & 32) tma_load_2d_pair(x + 128 * (half & 64), &maps.x32, lb, 64 * ks, row + (half & 64));
-                        if (half & 16) tma_load_2d_pair(x + 128 * (half & 96), &maps.x8, lb, 64 * ks, row + (half & 96));
+                        // few boxes: with 16 rows in each the forward of 8192 rows takes 12 % longer
+                        if (half & 128) tma_load_2d_pair(x, &maps.x, lb, k, row);
+                        if (half & 64) tma_load_2d_pair(x, &maps.x64, lb, k, row);
+                        if (half & 32) tma_load_2d_pair(x + 128 * (half & 64), &maps.x32, lb, k, row + (half & 64));
+                        if (half & 16) tma_load_2d_pair(x + 128 * (half & 96), &maps.x16, lb, k, row + (half & 96));
                     }
                 }
                 __syncwarp();
-                issued |= 1u << stage;
-                last = (last & ~(1u << stage)) | (phase << stage);
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+                issued |= 1u << at.slot;
+                at.step();
             }
         }
         // no copy may still be landing when the CTA ends; a pair's copies are counted by
         // its leader, and both CTAs end together
-        for (int s = 0; s < STAGES; ++s)
-            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, (last >> s) & 1u, DRAIN_NS);
+        for (int s = 0; s < MAX_SLOTS; ++s)
+            if (rank == 0 && (issued & (1u << s))) (void)warp_wait(bar_full + 8 * s, ((at.phases >> s) & 1u) ^ 1, DRAIN_NS);
         if (*(volatile int *)s_abort) {  // one side may have given up before the other: let copies land
             const uint64_t t0 = globaltimer();
             while (globaltimer() - t0 < 10000000ull) {
@@ -348,47 +367,42 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         // The whole warp walks the loop; one elected lane issues.
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), el = elect_one();
-            uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
+            Ring<FORM> at;
+            uint32_t abuf = 0, aphase = 0;
             bool ok = true, ready = false;
-            for (int t = tile0; t < total && ok; t += tstep) {
-                const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
+            // strides between 64-wide blocks of M (N) where that axis is contiguous: 8192 bytes
+            constexpr uint32_t W_LOW = (F::m_major_w ? 8192u >> 4 : 1u) << 16, X_LOW = (F::sums ? 8192u >> 4 : 1u) << 16;
+            // 16 of K per MMA: 32 bytes of the swizzled rows where K is contiguous, 16 rows where it is not
+            constexpr uint32_t W_STEP = (F::m_major_w ? 2048u : 32u) >> 4, X_STEP = (F::sums ? 2048u : 32u) >> 4;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = warp_wait(bar, parity, p.wait_ns);
+                if (!ok) give_up();
+                return ok;
+            };
+            Tile ti, next;
+            if (tile0 < total) ti = get_tile<FORM>(tile0, p, s_cum, lane);
+            for (int t = tile0; t < total && ok; t += tstep, ti = next) {
                 const int nks = stages_of<FORM>(ti, p);
+                at.enter(ti);
+                const uint32_t bytes = at.bytes() >> 4, base = ring >> 4;
                 // D float32, A and B bf16, M = 256
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (F::m_major_w ? 1u << 15 : 0u) |
                                        (F::sums ? 1u << 16 : 0u) | ((uint32_t)(ti.width >> 3) << 17) | (16u << 24);
-                ok = warp_wait(bar_acc_empty + 8 * abuf, aphase ^ 1, p.wait_ns);
-                if (!ok || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) {
-                    if (!ok) give_up();
-                    break;
-                }
+                if (!wait(bar_acc_empty + 8 * abuf, aphase ^ 1) || __any_sync(0xFFFFFFFFu, *(volatile int *)s_abort != 0)) break;
                 const uint32_t d = tm + abuf * TILE;
                 for (int ks = 0; ks < nks; ++ks) {
                     // asked for a stage ahead, the answer is there when it is needed
-                    if (__all_sync(0xFFFFFFFFu, ready) == 0) {
-                        ok = warp_wait(bar_full + 8 * stage, phase, p.wait_ns);
-                        if (!ok) {
-                            give_up();
-                            break;
-                        }
-                    }
+                    if (__all_sync(0xFFFFFFFFu, ready) == 0 && !wait(bar_full + 8 * at.slot, at.parity())) break;
                     tc_fence_after();
-                    const uint32_t w = stages + stage * STAGE_BYTES, x = w + SIDE_BYTES, done = bar_empty + 8 * stage;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    ready = mbar_test(bar_full + 8 * stage, phase);
-                    // 16 of K per MMA: 32 bytes of the swizzled rows where K is contiguous, 16 rows
-                    // where it is not (8192 bytes between 64-wide blocks of the other axis)
+                    const uint32_t slot = at.slot;
+                    at.step();
+                    ready = ks + 1 < nks && mbar_test(bar_full + 8 * at.slot, at.parity());
+                    const uint32_t w = (base + slot * bytes) | W_LOW, x = (base + slot * bytes + (SIDE_BYTES >> 4)) | X_LOW;
                     const int steps = F::sums ? (int)min((int64_t)4, (ti.hi - ti.lo - 64 * ks + 15) / 16) : 4;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        if (s < steps)
-                            mma_bf16_pair(el, d, F::m_major_w ? smem_desc(w + 2048 * s, 8192, 1024, 2) : smem_desc(w + 32 * s, 16, 1024, 2),
-                                          F::sums ? smem_desc(x + 2048 * s, 8192, 1024, 2) : smem_desc(x + 32 * s, 16, 1024, 2),
-                                          idesc, (ks > 0 || s > 0) ? 1u : 0u);
-                    }
-                    tc_commit_ct<2>(el, done);
+                    for (int s = 0; s < 4; ++s)
+                        if (!F::sums || s < steps) mma_bf16_pair(el, d, w + W_STEP * s, x + X_STEP * s, idesc, ks > 0 || s > 0);
+                    tc_commit_ct<2>(el, bar_empty + 8 * slot);
                 }
                 if (!ok) break;
                 tc_commit_ct<2>(el, bar_acc_full + 8 * abuf);
@@ -396,10 +410,42 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                     abuf = 0;
                     aphase ^= 1;
                 }
+                // the next tile is looked up while MMAs run
+                if (t + tstep < total) next = get_tile<FORM>(t + tstep, p, s_cum, lane);
             }
             if (elect_one()) tc_commit_own<2>(bar_drain);  // every tcgen05 operation of this warp has completed
             __syncwarp();
             (void)warp_wait(bar_drain, 0, DRAIN_NS);
+        }
+        __syncwarp();
+    } else if (F::sums && warp == 2) {
+        // ---------------------------------------------------- rows that are not the group's
+        // A last stage of a group that ends inside 16 rows: those up to the next 16 become zeros (another
+        // group's rows would enter the sums, and a NaN among them even times zero).
+        Ring<FORM> at;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok; t += tstep) {
+            const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
+            const int nks = stages_of<FORM>(ti, p), rest = (int)((ti.hi - ti.lo) & 63);
+            at.enter(ti);
+            for (int ks = 0; ks < nks; ++ks, at.step()) {
+                if (ks + 1 < nks || rest % 16 == 0) continue;
+                ok = warp_wait(bar_land + 8 * at.slot, (parity >> at.slot) & 1u, p.wait_ns);
+                if (!ok) {
+                    give_up();
+                    break;
+                }
+                parity ^= 1u << at.slot;
+                const int blocks = 2 + (ti.width / 2 + 63) / 64;
+                for (int b = 0; b < blocks; ++b) {
+                    uint4 *d = reinterpret_cast<uint4 *>(smem + at.slot * at.bytes() + 8192 * b);
+                    for (int i = 8 * rest + lane; i < 8 * ((rest + 15) & ~15); i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(bar_full + 8 * at.slot);
+            }
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -410,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         // behind the segment's end may not be written, so the last few of a segment are stored singly.
         const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0), quad = wu & 3, c_first = (wu - 4) >> 2;
         uint8_t *const buf0 = smem + BUF_OFF + (wu - 4) * WARP_BUF;
-        const uint32_t bufs0 = stages + BUF_OFF + (wu - 4) * WARP_BUF, ybar = bar_y + 16 * (wu - 4);
+        const uint32_t bufs0 = ring + BUF_OFF + (wu - 4) * WARP_BUF, ybar = bar_y + 16 * (wu - 4);
         uint32_t abuf = 0, aphase = 0, n = 0;  // n: chunks so far
         bool ok = true;
         // first column of the warp in a tile, the tile's rows
@@ -419,12 +465,12 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
             return col_of(ti) < p.n ? (int)((min((int64_t)ti.width, ti.row_end - ti.r0) + CH - 1) / CH) : 0;
         };
         // GATED_BACKWARD: gate and up come by TMA too, a chunk ahead, into the buffer that takes their gradients
-        int at = tile0, ac = c_first;
+        int at = tile0, ac = c_first;  // tile, chunk
         Tile ahead;
         auto fetch = [&]() {
             while (at < total && ac >= chunks_of(ahead)) {
-                at += tstep;
                 ac = c_first;
+                at += tstep;
                 if (at < total) ahead = get_tile<FORM>(at, p, s_cum, lane);
             }
             if (at >= total) return;
@@ -661,7 +707,7 @@ pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k
 bool token_maps(Maps &maps, const void *a, int64_t rows, int64_t k, int64_t lda)
 {
     return rows_map(&maps.x, a, k, rows, lda, 128) && rows_map(&maps.x64, a, k, rows, lda, 64) &&
-           rows_map(&maps.x32, a, k, rows, lda, 32) && rows_map(&maps.x8, a, k, rows, lda, 16);
+           rows_map(&maps.x32, a, k, rows, lda, 32) && rows_map(&maps.x16, a, k, rows, lda, 16);
 }
 
 // Weights [groups, rows, cols], 64 columns of box_rows rows at a time.
@@ -710,8 +756,7 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
             return cudaMemsetAsync(out, 0, (size_t)num_groups * m * n * (out_kind == PMN_OUT_F32 ? 4 : 2), s) == cudaSuccess
                        ? PMN_OK : PMN_ERR_CUDA;
         if (!a || !b) return PMN_ERR_INVALID_ARG;
-        if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.w8, b, n, k, ldb, 8) || !rows_map(&maps.w1, b, n, k, ldb, 1) ||
-            !rows_map(&maps.x, a, m, k, lda, 64) || !rows_map(&maps.x8, a, m, k, lda, 8) || !rows_map(&maps.x1, a, m, k, lda, 1) ||
+        if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.x, a, m, k, lda, 64) ||
             !piece_map(&maps.out, out, num_groups, m, n, out_kind, 32))
             return PMN_ERR_CUDA;
         const Args args{offsets, num_groups, k, m, n, 0, out, nullptr, pmn_wait_limit_ns()};
