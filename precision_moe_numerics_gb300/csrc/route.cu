@@ -47,7 +47,7 @@ struct RouteArgs {
     int32_t *chosen;
     float *gates;
     int32_t *row_index, *row_choice, *offsets;
-    uint16_t *counts;  // [chunks][experts]
+    uint16_t *counts;  // [chunks][experts, rounded up to an even number]
 };
 
 template <int KIND>
@@ -57,20 +57,21 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i)
     return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(p) + i) << 16);
 }
 
-// Larger value, larger key; NaN above everything; -inf 0, below every other value.
+// Larger value, larger key; NaN above everything; NONE (-inf) below every other value.  The sum
+// makes +0 of -0 (equal values, equal keys) and a positive NaN of any.
+constexpr uint32_t NONE = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float v)
 {
-    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 -> +0: equal values, equal keys
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
-    const uint32_t s = (u >> 31) ? ~u : (u | 0x80000000u);
-    return s == 0x007FFFFFu ? 0u : s;
+    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
+// The largest of the lanes' values, NaN left out.
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-    return v;
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -83,39 +84,16 @@ __device__ __forceinline__ float warp_sum(float v)
 // log(1 / (1 + e^-x)), which keeps its relative precision where the sigmoid vanishes
 __device__ __forceinline__ float log_sigmoid(float x) { return __fsub_rn(fminf(x, 0.0f), log1pf(expf(-fabsf(x)))); }
 
-// One token by one warp: lane i < k gets the i-th expert (-1: no expert is left) and its gate.
-// Lane l holds experts l, l + 32, ..; k rounds take the largest key, lowest expert first.
-template <int NV, int KIND>
-__device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int lane, int &expert, float &gate)
+// k experts by k rounds over all keys: many equals, or a large k.
+template <int NV>
+__device__ __noinline__ int choose_slowly(const uint32_t (&given)[NV], int k, int lane)
 {
-    const int64_t at = token * p.ldl;
     uint32_t key[NV];
-    float top = -INFINITY, total = 0.0f;
-    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
-    {
-        float v[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) v[j] = lane + 32 * j < p.experts ? load_logit<KIND>(p.logits, at + lane + 32 * j) : -INFINITY;
-        if (every) {  // the denominator runs over all experts
-#pragma unroll
-            for (int j = 0; j < NV; ++j) top = fmaxf(top, v[j]);
-            top = warp_max(top);
-            if (top == -INFINITY) top = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) total += expf(v[j] - top);
-            total = warp_sum(total);
-        }
-        if (p.bias) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (lane + 32 * j < p.experts) v[j] = __fadd_rn(v[j], __ldg(p.bias + lane + 32 * j));
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = lane + 32 * j < p.experts ? order_key(v[j]) : 0u;
-    }
-    expert = -1;
-    for (int i = 0; i < p.k; ++i) {
-        uint32_t best = 0;
+    for (int j = 0; j < NV; ++j) key[j] = given[j];
+    int expert = -1;
+    for (int i = 0; i < k; ++i) {
+        uint32_t best = NONE;
         int which = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -124,27 +102,134 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int la
                 which = j;
             }
         const uint32_t m = __reduce_max_sync(FULL, best);
-        if (m == 0u) break;
+        if (m == NONE) break;
         const int win = __reduce_min_sync(FULL, best == m ? 32 * which + lane : 0x7FFFFFFF);
         if (lane == i) expert = win;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (32 * j + lane == win) key[j] = 0u;
+            if (32 * j + lane == win) key[j] = NONE;
     }
-    const float l = expert >= 0 ? load_logit<KIND>(p.logits, at + expert) : -INFINITY;
-    float g;
-    if (every) {
-        g = expf(l - top) / total;
-    } else if (!p.normalize) {
-        g = 1.0f / (1.0f + expf(-l));
-    } else {
-        const float v = p.score == PMN_SCORE_SOFTMAX ? l : expert >= 0 ? log_sigmoid(l) : -INFINITY;
-        float m = warp_max(v);
-        if (m == -INFINITY) m = 0.0f;
-        const float e = expert >= 0 ? expf(v - m) : 0.0f;
-        g = e / warp_sum(e);
+    return expert;
+}
+
+// T tokens (token, token + step, ..) by one warp, side by side: lane i < k gets each one's i-th expert (-1:
+// none is left) and its gate.  Lane l holds experts l, l + 32, ..  The k-th largest of the lanes' own largest
+// keys bounds the token's k-th largest from below, so what is not less than it -- little more
+// than k keys -- holds the choice; those few are packed, one to a lane, in the experts' order,
+// and taken one by one.  Bound by the latency of these steps, each of which the whole warp takes part in:
+// hence two tokens at a time (16384 tokens of 384 experts: k rounds over all keys 27 us, this 21, two at a time 15).
+template <int T, int NV, int KIND, bool EXACT>
+__device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_t step, int lane, uint2 (*few)[32],
+                                       int (&expert)[T], float (&gate)[T])
+{
+    uint32_t key[T][NV], best[T], bound[T];
+    float top[T], total[T];
+    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
+    {
+        float v[T][NV];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                v[t][j] = (EXACT || lane + 32 * j < p.experts) && token + t * step < p.tokens
+                              ? load_logit<KIND>(p.logits, (token + t * step) * p.ldl + lane + 32 * j) : -INFINITY;
+        if (every) {  // the denominator runs over all experts
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                top[t] = -INFINITY;
+                total[t] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) top[t] = fmaxf(top[t], v[t][j]);
+                top[t] = warp_max(top[t]);
+                if (top[t] == -INFINITY) top[t] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) total[t] += expf(v[t][j] - top[t]);
+                total[t] = warp_sum(total[t]);
+            }
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const float b = EXACT || lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
+#pragma unroll
+                for (int t = 0; t < T; ++t) v[t][j] = __fadd_rn(v[t][j], b);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            best[t] = NONE;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                key[t][j] = order_key(v[t][j]);
+                best[t] = max(best[t], key[t][j]);
+            }
+            bound[t] = NONE + 1;  // every expert above -inf, where fewer than k lanes have one
+        }
     }
-    gate = expert >= 0 ? __fmul_rn(p.scale, g) : 0.0f;
+    for (int i = 0; i < p.k; ++i) {
+        uint32_t m[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) m[t] = __reduce_max_sync(FULL, best[t]);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            bound[t] = max(m[t], NONE + 1);
+            if (best[t] == m[t]) best[t] = NONE;
+        }
+    }
+    int count[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        expert[t] = -1;
+        count[t] = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t in = __ballot_sync(FULL, key[t][j] >= bound[t]);
+            if (in == 0u) continue;
+            const int to = count[t] + __popc(in & ((1u << lane) - 1u));
+            if (key[t][j] >= bound[t] && to < 32) few[t][to] = make_uint2(key[t][j], 32 * j + lane);
+            count[t] += __popc(in);
+        }
+    }
+    __syncwarp();
+    uint2 mine[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) mine[t] = lane < count[t] ? few[t][lane] : make_uint2(NONE, 0u);
+    __syncwarp();
+    for (int i = 0; i < p.k; ++i) {
+        uint32_t m[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) m[t] = __reduce_max_sync(FULL, mine[t].x);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int win = __ffs(__ballot_sync(FULL, mine[t].x == m[t])) - 1;
+            const int e = __shfl_sync(FULL, (int)mine[t].y, win);
+            if (lane == i && m[t] != NONE) expert[t] = e;
+            if (lane == win) mine[t].x = NONE;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (count[t] > 32) expert[t] = choose_slowly<NV>(key[t], p.k, lane);
+    float l[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        l[t] = expert[t] >= 0 ? load_logit<KIND>(p.logits, (token + t * step) * p.ldl + expert[t]) : -INFINITY;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        float g;
+        if (every) {
+            g = expf(l[t] - top[t]) / total[t];
+        } else if (!p.normalize) {
+            g = 1.0f / (1.0f + expf(-l[t]));
+        } else {
+            const float v = p.score == PMN_SCORE_SOFTMAX ? l[t] : expert[t] >= 0 ? log_sigmoid(l[t]) : -INFINITY;
+            float m = warp_max(v);
+            if (m == -INFINITY) m = 0.0f;
+            const float e = expert[t] >= 0 ? expf(v - m) : 0.0f;
+            g = e / warp_sum(e);
+        }
+        gate[t] = expert[t] >= 0 ? __fmul_rn(p.scale, g) : 0.0f;
+    }
 }
 
 // What the layout of a chunk needs in shared memory.
@@ -152,38 +237,40 @@ struct Layout {
     uint32_t mask[MAX_EXPERTS][SUB / 32];  // which of SUB tokens chose the expert
     int32_t base[MAX_EXPERTS];             // first row that is still free
     int32_t total[MAX_EXPERTS], first[MAX_EXPERTS + 1];
+    int32_t sums[32];
 };
 
-// Padded running sum of the totals (first[e]: the expert's first row); one warp.
-__device__ __forceinline__ void scan_offsets(const RouteArgs &p, Layout &s, int lane)
+// Padded running sum of the totals (first[e]: the expert's first row), by the whole CTA.
+__device__ void scan_offsets(const RouteArgs &p, Layout &s)
 {
-    const int per = (p.experts + 31) / 32;
-    int sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = per * lane + i;
-        if (e < p.experts) sum += (s.total[e] + p.pad - 1) / p.pad * p.pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto padded = [&](int e) { return e < p.experts ? (int)((uint32_t)(s.total[e] + p.pad - 1) / (uint32_t)p.pad) * p.pad : 0; };
+    __syncthreads();
+    for (int e0 = 0; e0 < p.experts; e0 += blockDim.x) {  // sums of 32 experts each
+        const int e = e0 + threadIdx.x, n = __reduce_add_sync(FULL, padded(e));
+        if (lane == 0 && e < p.experts) s.sums[e >> 5] = n;
     }
-    int run = sum;
+    __syncthreads();
+    for (int e0 = 0; e0 < p.experts; e0 += blockDim.x) {
+        const int e = e0 + 32 * warp + lane, n = padded(e);
+        int run = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, run, o);
-        if (lane >= o) run += v;
-    }
-    run -= sum;
-    for (int i = 0; i < per; ++i) {
-        const int e = per * lane + i;
-        if (e < p.experts) {
-            s.first[e] = run;
-            run += (s.total[e] + p.pad - 1) / p.pad * p.pad;
-            if (e == p.experts - 1) s.first[p.experts] = run;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, run, o);
+            if (lane >= o) run += v;
         }
+        run += __reduce_add_sync(FULL, lane < (e >> 5) ? s.sums[lane] : 0) - n;
+        if (e < p.experts) s.first[e] = run;
+        if (e == p.experts - 1) s.first[p.experts] = run + n;
     }
+    __syncthreads();
 }
 
 // Rows of the chunk's choices: an expert's rows follow its tokens' order, so a choice's
 // place is the number of earlier tokens that chose the expert -- a count of bits, the same
-// in whatever order the bits were set.  s.base holds the rows left by earlier chunks.
-__device__ void place(const RouteArgs &p, Layout &s, int64_t token0, int64_t token1)
+// in whatever order the bits were set.  s.base holds the rows left by earlier chunks, mine the
+// thread's first choice.
+__device__ void place(const RouteArgs &p, Layout &s, int64_t token0, int64_t token1, int mine)
 {
     for (int64_t t0 = token0; t0 < token1; t0 += SUB) {
         const int n = (int)min((int64_t)SUB, token1 - t0) * p.k;
@@ -193,12 +280,12 @@ __device__ void place(const RouteArgs &p, Layout &s, int64_t token0, int64_t tok
         __syncthreads();
         const int32_t *chosen = p.chosen + t0 * p.k;
         for (int c = threadIdx.x; c < n; c += blockDim.x) {
-            const int e = chosen[c], t = c / p.k;
+            const int e = t0 == token0 && c == (int)threadIdx.x ? mine : chosen[c], t = c / p.k;
             if (e >= 0) atomicOr(&s.mask[e][t >> 5], 1u << (t & 31));
         }
         __syncthreads();
         for (int c = threadIdx.x; c < n; c += blockDim.x) {
-            const int e = chosen[c], t = c / p.k;
+            const int e = t0 == token0 && c == (int)threadIdx.x ? mine : chosen[c], t = c / p.k;
             int row = -1;
             if (e >= 0) {
                 row = s.base[e] + __popc(s.mask[e][t >> 5] & ((1u << (t & 31)) - 1u));
@@ -228,83 +315,100 @@ __device__ void mark_padding(const RouteArgs &p, const Layout &s)
 }
 
 // One CTA per chunk, one warp per token.  ONE: a single chunk, laid out here as well.
-template <int NV, int KIND, bool ONE>
+template <int NV, int KIND, bool EXACT, bool ONE>
 __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(const RouteArgs p)
 {
     __shared__ Layout s;
+    constexpr int T = NV > 12 ? 1 : 2;
+    __shared__ uint2 few[NV > 16 ? 16 : 32][T][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     int32_t *count = s.total;
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
-    for (int64_t t = t0 + warp; t < t1; t += warps) {
-        int expert;
-        float gate;
-        choose<NV, KIND>(p, t, lane, expert, gate);
-        if (lane < p.k) {
-            p.chosen[t * p.k + lane] = expert;
-            p.gates[t * p.k + lane] = gate;
-            if (expert >= 0) atomicAdd(count + expert, 1);
-        }
+    for (int64_t t = t0 + warp; t < t1; t += T * warps) {
+        int expert[T];
+        float gate[T];
+        choose<T, NV, KIND, EXACT>(p, t, warps, lane, few[warp], expert, gate);
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+            if (lane < p.k && t + i * warps < t1) {
+                p.chosen[(t + i * warps) * p.k + lane] = expert[i];
+                p.gates[(t + i * warps) * p.k + lane] = gate[i];
+                if (expert[i] >= 0) atomicAdd(count + expert[i], 1);
+            }
     }
     __syncthreads();
     if (!ONE) {
-        for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
-            p.counts[(int64_t)blockIdx.x * p.experts + e] = (uint16_t)count[e];
+        const int pitch = (p.experts + 1) / 2 * 2;
+        for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+            p.counts[(int64_t)blockIdx.x * pitch + e] = e < p.experts ? (uint16_t)count[e] : (uint16_t)0;
         return;
     }
-    if (warp == 0) scan_offsets(p, s, lane);
-    __syncthreads();
+    scan_offsets(p, s);
     for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
         p.offsets[e] = s.first[e];
         if (e < p.experts) s.base[e] = s.first[e];
     }
-    place(p, s, t0, t1);
+    place(p, s, t0, t1, (int)threadIdx.x < (t1 - t0) * p.k ? p.chosen[threadIdx.x] : -1);
     mark_padding(p, s);
 }
 
-__global__ void __launch_bounds__(512) route_place_kernel(const RouteArgs p, int chunks)
+__global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs p, int chunks)
 {
     __shared__ Layout s;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the choosing kernel still runs
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
-        int before = 0, all = 0;
-        const uint16_t *c = p.counts + e;
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+    const int mine = threadIdx.x < (t1 - t0) * p.k ? __ldcg(p.chosen + t0 * p.k + threadIdx.x) : -1;
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s.total[e] = s.base[e] = 0;
+    __syncthreads();
+    // a thread adds up two experts over every `parts`th chunk
+    const int pitch = (p.experts + 1) / 2, parts = max(1, (int)blockDim.x / pitch);
+    for (int i = threadIdx.x; i < pitch * parts; i += blockDim.x) {
+        const int pair = i % pitch;
+        int before0 = 0, before1 = 0, all0 = 0, all1 = 0;
+        const uint32_t *c = reinterpret_cast<const uint32_t *>(p.counts) + pair;
 #pragma unroll 16
-        for (int i = 0; i < chunks; ++i) {
-            const int n = __ldcg(c + (int64_t)i * p.experts);
-            all += n;
-            if (i < (int)blockIdx.x) before += n;
+        for (int ch = i / pitch; ch < chunks; ch += parts) {
+            const uint32_t n = __ldcg(c + (int64_t)ch * pitch);
+            all0 += n & 0xFFFFu;
+            all1 += n >> 16;
+            if (ch < (int)blockIdx.x) {
+                before0 += n & 0xFFFFu;
+                before1 += n >> 16;
+            }
         }
-        s.total[e] = all;
-        s.base[e] = before;
+        atomicAdd(&s.total[2 * pair], all0);
+        atomicAdd(&s.base[2 * pair], before0);
+        if (2 * pair + 1 < p.experts) {
+            atomicAdd(&s.total[2 * pair + 1], all1);
+            atomicAdd(&s.base[2 * pair + 1], before1);
+        }
     }
-    __syncthreads();
-    if (threadIdx.x < 32) scan_offsets(p, s, threadIdx.x);
-    __syncthreads();
+    scan_offsets(p, s);
     for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
         if (blockIdx.x == 0) p.offsets[e] = s.first[e];
         if (e < p.experts) s.base[e] += s.first[e];
     }
-    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
-    place(p, s, t0, min(p.tokens, t0 + p.chunk));
+    place(p, s, t0, t1, mine);
     mark_padding(p, s);
 }
 
-template <int NV, int KIND>
+template <int NV, int KIND, bool EXACT>
 pmn_status launch_route(const RouteArgs &p, cudaStream_t s)
 {
     const int chunks = (int)chunk_count(p.tokens);
     const int threads = std::min<int64_t>(NV > 16 ? 512 : 1024, std::max<int64_t>(128, 32 * p.tokens));
     if (chunks == 1) {
-        route_choose_kernel<NV, KIND, true><<<1, threads, 0, s>>>(p);
+        route_choose_kernel<NV, KIND, EXACT, true><<<1, threads, 0, s>>>(p);
         return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
     }
-    route_choose_kernel<NV, KIND, false><<<chunks, threads, 0, s>>>(p);
+    route_choose_kernel<NV, KIND, EXACT, false><<<chunks, threads, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)chunks);
-    cfg.blockDim = dim3(512);
+    cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -317,12 +421,16 @@ pmn_status launch_route(const RouteArgs &p, cudaStream_t s)
 template <int KIND>
 pmn_status route_by_experts(const RouteArgs &p, cudaStream_t s)
 {
-    if (p.experts <= 64) return launch_route<2, KIND>(p, s);
-    if (p.experts <= 128) return launch_route<4, KIND>(p, s);
-    if (p.experts <= 256) return launch_route<8, KIND>(p, s);
-    if (p.experts <= 384) return launch_route<12, KIND>(p, s);
-    if (p.experts <= 512) return launch_route<16, KIND>(p, s);
-    return launch_route<32, KIND>(p, s);
+    // a count of experts that fills the lanes needs no checks
+    if (p.experts == 128) return launch_route<4, KIND, true>(p, s);
+    if (p.experts == 256) return launch_route<8, KIND, true>(p, s);
+    if (p.experts == 384) return launch_route<12, KIND, true>(p, s);
+    if (p.experts <= 64) return launch_route<2, KIND, false>(p, s);
+    if (p.experts <= 128) return launch_route<4, KIND, false>(p, s);
+    if (p.experts <= 256) return launch_route<8, KIND, false>(p, s);
+    if (p.experts <= 384) return launch_route<12, KIND, false>(p, s);
+    if (p.experts <= 512) return launch_route<16, KIND, false>(p, s);
+    return launch_route<32, KIND, false>(p, s);
 }
 
 __global__ void route_empty_kernel(int32_t *offsets, int experts, int32_t *row_choice, int64_t rows)
@@ -341,6 +449,7 @@ struct RouteGradArgs {
     int experts, k, score, normalize;
     float scale;
     void *dlogits;
+    bool wide;  // dlogits is 16-byte aligned
 };
 
 template <int KIND>
@@ -359,6 +468,16 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs
     const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= p.tokens) return;
     const int64_t at = t * p.ldl, out = t * p.experts;
+    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
+    if (!every) {  // the rest of the row, while the chosen logits are on their way
+        constexpr int N = KIND == PMN_OUT_F32 ? 4 : 8;
+        uint8_t *row = static_cast<uint8_t *>(p.dlogits) + out * (16 / N);
+        if (p.experts % N == 0 && p.wide) {
+            for (int c = lane; c < p.experts / N; c += 32) reinterpret_cast<uint4 *>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            for (int c = lane; c < p.experts; c += 32) store_grad<KIND>(p.dlogits, out + c, 0.0f);
+        }
+    }
     int e = -1;
     float d = 0.0f;
     if (lane < p.k) {
@@ -371,7 +490,6 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs
         d = 0.0f;
     }
     const float l = e >= 0 ? load_logit<KIND>(p.logits, at + e) : -INFINITY;
-    const bool every = p.score == PMN_SCORE_SOFTMAX && !p.normalize;
     float g = 0.0f, top = -INFINITY, total = 0.0f, sg = 0.0f;
     if (p.score == PMN_SCORE_SIGMOID) sg = 1.0f / (1.0f + expf(l));  // 1 - sigmoid, without its cancellation
     if (every) {
@@ -399,8 +517,6 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs
             const float q = total > 0.0f || total != total ? expf(load_logit<KIND>(p.logits, at + c) - top) / total : 0.0f;
             store_grad<KIND>(p.dlogits, out + c, -__fmul_rn(__fmul_rn(p.scale, q), dot));
         }
-    } else {
-        for (int c = lane; c < p.experts; c += 32) store_grad<KIND>(p.dlogits, out + c, 0.0f);
     }
     __syncwarp();  // the chosen entries are written after the row
     if (e >= 0) store_grad<KIND>(p.dlogits, out + e, grad);
@@ -639,7 +755,7 @@ extern "C" int64_t pmn_route_rows(int64_t tokens, int experts, int k, int pad)
 extern "C" int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int k)
 {
     if (pmn_route_rows(tokens, experts, k, 1) < 0) return -1;
-    return tokens == 0 || chunk_count(tokens) == 1 ? 0 : (chunk_count(tokens) * experts * 2 + 15) / 16 * 16;
+    return tokens == 0 || chunk_count(tokens) == 1 ? 0 : (chunk_count(tokens) * ((experts + 1) / 2 * 4) + 15) / 16 * 16;
 }
 
 extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits_kind, const float *bias, int64_t tokens,
@@ -679,7 +795,7 @@ extern "C" pmn_status pmn_route_topk_backward(const void *logits, int64_t ldl, i
     if (!logits || !chosen || !dgates || !dlogits || !aligned(logits, kind_bytes(logits_kind)) ||
         !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4))
         return PMN_ERR_INVALID_ARG;
-    const RouteGradArgs a{logits, ldl, chosen, dgates, tokens, experts, k, score, normalize, scale, dlogits};
+    const RouteGradArgs a{logits, ldl, chosen, dgates, tokens, experts, k, score, normalize, scale, dlogits, aligned(dlogits, 16)};
     const unsigned blocks = (unsigned)((tokens + 7) / 8);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (logits_kind == PMN_OUT_F32) route_backward_kernel<PMN_OUT_F32><<<blocks, 256, 0, s>>>(a);
