@@ -34,19 +34,28 @@ __device__ int g_matvec_error = 0;
 
 constexpr int MAX_GROUPS = 1024, MAX_DEVICES = 64, MAX_GRID = 256;
 constexpr int DIGITS = 8;
-constexpr int CHUNK = 16, NB = CHUNK * DIGITS;   // rows of x, and of the small operand, per pass over the weights
+constexpr int MAX_CHUNK = 16;                    // most rows of x per pass over the weights
 constexpr int BM = 128;                          // weight rows of a tile (gated: 64 gate and the 64 up rows of the same columns)
 constexpr int KSTEP = 256;                       // of K per stage: 128 bytes of codes, 16 scales
-constexpr int A_BYTES = BM * 128, B_BYTES = NB * 128, SF_BYTES = 2 * 4 * 512;
-constexpr int STAGES = 5, STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+constexpr int A_BYTES = BM * 128, SF_BYTES = 2 * 4 * 512;
 constexpr int RAW_STEPS = 4, RAW_W = 16 * RAW_STEPS;  // scale rows come 64 bytes (four stages) at a time
-constexpr int RAW_A = BM * RAW_W, RAW_BYTES = RAW_A + CHUNK * RAW_W, RAW_SLOTS = 3;
-constexpr int RAW_OFF = STAGES * STAGE_BYTES, XCH_OFF = RAW_OFF + RAW_SLOTS * RAW_BYTES;
-constexpr int BAR_OFF = XCH_OFF + 64 * 20 * 4, CUM_OFF = BAR_OFF + 256;
-constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-constexpr uint32_t TMEM_COLS = 512, SF_COL0 = 2 * NB, SF_COLS = 32;
-static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
+constexpr int RAW_A = BM * RAW_W, RAW_BYTES = RAW_A + MAX_CHUNK * RAW_W, RAW_SLOTS = 3;
+constexpr uint32_t TMEM_COLS = 512, SF_COLS = 32;
+
+// CHUNK rows of x at a time: the fewer, the more of the weights fits in flight.
+template <int CHUNK>
+struct Cfg {
+    static constexpr int NB = CHUNK * DIGITS;  // rows of the small operand
+    static constexpr int B_BYTES = NB * 128, STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+    static constexpr int STAGES = CHUNK == 8 ? 6 : 5;
+    static constexpr int RAW_OFF = STAGES * STAGE_BYTES, XCH_OFF = RAW_OFF + RAW_SLOTS * RAW_BYTES;
+    static constexpr int BAR_OFF = XCH_OFF + 64 * 20 * 4, CUM_OFF = BAR_OFF + 256;
+    static constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
+    static constexpr uint32_t SF_COL0 = 2 * NB;
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "TMEM budget");
+    static_assert(8 * (2 * STAGES + 2 * RAW_SLOTS + 5) + 24 <= 256, "barrier space");
+};
 // warps: 0 weights, 1 MMA, 2 scale rows, 3 digits; 4 .. 7 scale factors; 8 .. 11 epilogue
 constexpr int THREADS = 384;
 constexpr uint64_t DRAIN_NS = 100000000ull;
@@ -91,24 +100,24 @@ __device__ __forceinline__ int64_t token_of(const Args &p, int64_t row)
 }
 
 // ---------------------------------------------------------------- digits
-// One CTA per routed row: the row's largest finite magnitude, then eight values per thread at
-// a time.
-__global__ void __launch_bounds__(256) digits_kernel(const Args p, int grid)
+// One CTA per routed row, eight values per thread at a time: first the row's largest finite
+// magnitude (up to 4096 of K stay in registers), then the digits.
+constexpr int DIGIT_THREADS = 512;
+__global__ void __launch_bounds__(DIGIT_THREADS) digits_kernel(const Args p, int grid)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float s_top[8];
-    __shared__ int s_odd;
+    __shared__ float s_top[DIGIT_THREADS / 32];
     const int64_t row = blockIdx.x, token = token_of(p, row);
     const uint4 *x = reinterpret_cast<const uint4 *>(p.x + token * p.ldx);
     const int vecs = (int)(p.k / 8);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 mine = token >= 0 && (int)threadIdx.x < vecs ? __ldg(x + threadIdx.x) : zero;
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < grid; i += 256) p.count[i] = 0u;
-    if (threadIdx.x == 0) s_odd = 0;
-    __syncthreads();
+        for (int i = threadIdx.x; i < grid; i += DIGIT_THREADS) p.count[i] = 0u;
     float top = 0.0f;
     bool odd = false;
-    for (int v = threadIdx.x; v < vecs && token >= 0; v += 256) {
-        const uint4 q = __ldg(x + v);
+    for (int v = threadIdx.x; v < vecs && token >= 0; v += DIGIT_THREADS) {
+        const uint4 q = v < DIGIT_THREADS ? mine : __ldg(x + v);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const float a = __uint_as_float((u4_word(q, w) & 0x7FFFu) << 16), b = __uint_as_float(u4_word(q, w) & 0x7FFF0000u);
@@ -116,21 +125,16 @@ __global__ void __launch_bounds__(256) digits_kernel(const Args p, int grid)
             top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-    if (odd) s_odd = 1;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_top[w]);
+    const uint32_t warp_top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = __uint_as_float(warp_top);
+    odd = __syncthreads_or(odd) != 0;
+    top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(s_top[threadIdx.x & (DIGIT_THREADS / 32 - 1)])));
     // top in [2^e, 2^(e+1)); below float32's normal range any larger e will do
     const int e = max((int)(__float_as_uint(top) >> 23) - 127, -126);
-    if (threadIdx.x == 0) p.meta[row] = make_int2(e - 8, s_odd);
+    if (threadIdx.x == 0) p.meta[row] = make_int2(e - 8, odd);
     const float down = e == 127 ? __uint_as_float(0x00400000u) : pow2(-e);  // 2^-127 is below the normal range
-    for (int v0 = 0; v0 < vecs; v0 += 256) {  // whole warps: k is a multiple of 256
-        const int v = v0 + threadIdx.x;
-        if (v >= vecs) break;
-        uint4 q = token >= 0 ? __ldg(x + v) : make_uint4(0u, 0u, 0u, 0u);
+    for (int v = threadIdx.x; v < vecs; v += DIGIT_THREADS) {  // whole warps: k is a multiple of 256
+        const uint4 q = v < DIGIT_THREADS ? mine : token >= 0 ? __ldg(x + v) : zero;
         float f[8], big = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -166,34 +170,35 @@ __global__ void __launch_bounds__(256) digits_kernel(const Args p, int grid)
 }
 
 // ---------------------------------------------------------------- product
-// Steps (256 of K of a tile of a chunk of up to 16 rows) in one line, an even share of it
-// for each CTA: a piece is what a CTA has of one tile.
+// Steps (256 of K of a tile of a chunk of rows) in one line, an even share of it for each
+// CTA: a piece is what a CTA has of one tile.
 struct Piece {
-    int e, unit, tile, k0, k1;  // expert, chunk of all experts, tile, stages of K
-    int r0, m;                  // first routed row of the chunk, rows left in the segment
+    int e, line, tile, k0, k1;  // expert, tile of all chunks, tile, stages of K
+    int r0, m;                  // first routed row of the chunk, rows of it
 };
 
+template <int CHUNK>
 struct Walk {
-    int64_t at, end;
+    uint32_t at, end;
     int e;
     __device__ __forceinline__ bool next(const Args &p, const int *s_cum, Piece &q)
     {
         if (at >= end) return false;
-        const int64_t line = at / p.nks;  // tile of all chunks
-        q.k0 = (int)(at - line * p.nks);
-        q.k1 = (int)min((int64_t)p.nks, q.k0 + (end - at));
+        q.line = (int)(at / (uint32_t)p.nks);
+        q.k0 = (int)(at - (uint32_t)q.line * p.nks);
+        q.k1 = (int)min((uint32_t)p.nks, q.k0 + (end - at));
         at += q.k1 - q.k0;
-        q.unit = (int)(line / p.tiles);
-        q.tile = (int)(line - (int64_t)q.unit * p.tiles);
-        while (e + 1 < p.experts && s_cum[e + 1] <= q.unit) ++e;
+        const int unit = q.line / p.tiles;
+        q.tile = q.line - unit * p.tiles;
+        while (e + 1 < p.experts && s_cum[e + 1] <= unit) ++e;
         q.e = e;
-        q.r0 = __ldg(p.offsets + e) + (q.unit - s_cum[e]) * CHUNK;
-        q.m = __ldg(p.offsets + e + 1) - q.r0;
+        q.r0 = __ldg(p.offsets + e) + (unit - s_cum[e]) * CHUNK;
+        q.m = min(CHUNK, __ldg(p.offsets + e + 1) - q.r0);
         return true;
     }
 };
 
-__device__ __forceinline__ int digit_rows(const Piece &q) { return (min(q.m, CHUNK) + 1) / 2 * 2 * DIGITS; }  // a multiple of 16
+__device__ __forceinline__ int digit_rows(const Piece &q) { return (q.m + 1) / 2 * 2 * DIGITS; }  // a multiple of 16
 
 __device__ __forceinline__ void mma_nvfp4_by(uint32_t el, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
@@ -227,21 +232,23 @@ __device__ __noinline__ float plain_dot(const Args &p, int64_t wrow, int64_t tok
     return acc;
 }
 
-template <bool GATED, typename OUT>
+template <int CHUNK, bool GATED, typename OUT>
 __global__ void __launch_bounds__(THREADS, 1)
     matvec_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDS, const Args p)
 {
+    using C = Cfg<CHUNK>;
+    constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES, B_BYTES = C::B_BYTES, NB = C::NB, RAW_OFF = C::RAW_OFF;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw;
     asm volatile("" : "+l"(smem));
     const uint32_t stages = smem_u32(smem);
-    const uint32_t bar_full = stages + BAR_OFF, bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_full = stages + C::BAR_OFF, bar_empty = bar_full + 8 * STAGES;
     const uint32_t bar_raw = bar_empty + 8 * STAGES, bar_raw_empty = bar_raw + 8 * RAW_SLOTS;
     const uint32_t bar_acc_full = bar_raw_empty + 8 * RAW_SLOTS, bar_acc_empty = bar_acc_full + 16, bar_drain = bar_acc_empty + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + BAR_OFF + 8 * (2 * STAGES + 2 * RAW_SLOTS + 5));
-    int *s_abort = reinterpret_cast<int *>(tmem_slot + 1), *s_units = s_abort + 1, *s_bad = s_abort + 2, *s_last = s_abort + 3;
-    int *s_cum = reinterpret_cast<int *>(smem + CUM_OFF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * (2 * STAGES + 2 * RAW_SLOTS + 5));
+    int *s_abort = reinterpret_cast<int *>(tmem_slot + 1), *s_units = s_abort + 1, *s_last = s_abort + 2;
+    int *s_cum = reinterpret_cast<int *>(smem + C::CUM_OFF);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -259,21 +266,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mbar_init(bar_drain, 1);
         *s_abort = 0;
-        *s_bad = 0;
         fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmS);
+        tma_prefetch_desc(&tmD);
+        tma_prefetch_desc(&tmDS);
     }
     if (warp == 1) {
         __syncwarp();
         tmem_alloc_ct<1>(smem_u32(tmem_slot), TMEM_COLS);
     }
-    __syncthreads();
     // chunks of each expert, then their running sum
+    bool bad = false;
     for (int e = threadIdx.x; e < p.experts; e += THREADS) {
         const int lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
-        if (lo < 0 || hi < lo || hi > p.rows) *s_bad = 1;
+        if (lo < 0 || hi < lo || hi > p.rows) bad = true;
         s_cum[e] = (hi - lo + CHUNK - 1) / CHUNK;
     }
-    __syncthreads();
+    bad = __syncthreads_or(bad) != 0;
     if (warp == 0) {
         int sum = 0;
         for (int g0 = 0; g0 < p.experts; g0 += 32) {
@@ -289,19 +299,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (lane == 0) {
             s_cum[p.experts] = sum;
-            *s_units = *s_bad ? 0 : sum;
-            if (*s_bad && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
+            *s_units = bad ? 0 : sum;
+            if (bad && blockIdx.x == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int64_t total = (int64_t)*s_units * p.tiles * p.nks;
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total));  // with a share
-    auto share = [&](int64_t b) { return total * b / ctas; };             // first step of CTA b
-    Walk walk{0, 0, 0};
-    if (blockIdx.x < ctas) walk = Walk{share(blockIdx.x), share(blockIdx.x + 1), 0};
+    // (fewer than 2^31 steps: the host's checks)
+    const uint32_t total = (uint32_t)*s_units * p.tiles * p.nks, ctas = max(1u, min(gridDim.x, total));  // with a share
+    const uint32_t each = total / ctas, more = total - each * ctas;
+    auto share = [&](uint32_t b) { return each * b + min(b, more); };  // first step of CTA b
+    Walk<CHUNK> walk{0, 0, 0};
+    if (blockIdx.x < ctas) walk = Walk<CHUNK>{share(blockIdx.x), share(blockIdx.x + 1), 0};
     const int half = GATED ? BM / 2 : BM;
     bool dead = false;
     auto wait = [&](uint32_t bar, uint32_t parity) {  // false: a wait ran out, here or in another warp
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait(bar_raw_empty + 8 * slot, sphase ^ 1)) break;
                 if (elect_one()) {
                     const uint32_t st = stages + RAW_OFF + slot * RAW_BYTES, fb = bar_raw + 8 * slot;
-                    mbar_arrive_expect_tx(fb, RAW_BYTES);
+                    mbar_arrive_expect_tx(fb, RAW_A + CHUNK * RAW_W);
                     tma_load_2d(st, &tmS, fb, 16 * k, ra);
                     tma_load_2d(st + RAW_A / 2, &tmS, fb, 16 * k, rb);
                 }
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait(bar_full + 8 * stage, phase)) break;
                 tc_fence_after();
                 const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES, sf = b + B_BYTES;
-                const uint32_t sfa = tm + SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
+                const uint32_t sfa = tm + C::SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     tc_cp_ct<1>(el, sfa + 4 * s, smem_desc(sf + 512 * s, 0, 128, 0));
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < RAW_STEPS; ++c) {
                     va[c] = *reinterpret_cast<const uint4 *>(raw + RAW_W * i + 16 * c);
-                    vb[c] = *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * (i >> 3) + 16 * c);
+                    vb[c] = *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * min(i >> 3, CHUNK - 1) + 16 * c);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t abuf = 0, aphase = 0;
         asm volatile("griddepcontrol.wait;" ::: "memory");
         while (walk.next(p, s_cum, q)) {  // to the end, also after a timeout: the four warps meet at barriers
-            const int m = min(q.m, CHUNK);
+            const int m = q.m;
             float y[CHUNK];
             if (wait(bar_acc_full + 8 * abuf, aphase)) {
                 tc_fence_after();
@@ -512,11 +523,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // A tile that CTAs first .. last share: each leaves its sums, and the one that
                 // comes last adds them up in the order of K.  A CTA's slot 0 is for a tile that began
                 // before its share, slot 1 for one that begins in it.
-                const int64_t line = (int64_t)q.unit * p.tiles + q.tile, s0 = line * p.nks, s1 = s0 + p.nks;
+                const uint32_t s0 = (uint32_t)q.line * p.nks, s1 = s0 + p.nks;
                 int first = blockIdx.x, last = blockIdx.x;
                 while (share(first) > s0) --first;
                 while (share(last + 1) < s1) ++last;
-                float *mine = p.part + ((int64_t)blockIdx.x * 2 + (q.k0 == 0)) * CHUNK * BM;
+                float *mine = p.part + ((int64_t)blockIdx.x * 2 + (q.k0 == 0)) * MAX_CHUNK * BM;
 #pragma unroll
                 for (int t = 0; t < CHUNK; ++t)
                     if (t < m) __stcg(mine + t * BM + i, y[t]);
@@ -531,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int t = 0; t < CHUNK; ++t) y[t] = 0.0f;
                 for (int b = first; b <= last; ++b) {
-                    const float *from = p.part + ((int64_t)b * 2 + (b == first)) * CHUNK * BM + i;
+                    const float *from = p.part + ((int64_t)b * 2 + (b == first)) * MAX_CHUNK * BM + i;
 #pragma unroll
                     for (int t = 0; t < CHUNK; ++t)
                         if (t < m) y[t] = __fadd_rn(y[t], __ldcg(from + t * BM));
@@ -559,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (t < m && on) store_one(o + (int64_t)t * half_n, y[t]);
             } else {
                 // the up rows' threads hand theirs to the gate rows'
-                float *xch = reinterpret_cast<float *>(smem + XCH_OFF) + c * 20;
+                float *xch = reinterpret_cast<float *>(smem + C::XCH_OFF) + c * 20;
                 if (i >= 64) {
 #pragma unroll
                     for (int t = 0; t < CHUNK; t += 4)
@@ -618,7 +629,7 @@ struct Parts {
         scales = digits + up128(rows * DIGITS * (k / 2));
         meta = scales + up128(rows * (k / 16));
         part = meta + up128(rows * 8);
-        count = part + (int64_t)MAX_GRID * 2 * CHUNK * BM * 4;
+        count = part + (int64_t)MAX_GRID * 2 * MAX_CHUNK * BM * 4;
         end = count + MAX_GRID * 4;
     }
 };
@@ -630,28 +641,33 @@ bool good_sizes(int64_t rows, int64_t k)
     return rows >= 0 && rows < LIMIT / DIGITS - 256 && k > 0 && k % KSTEP == 0 && k < LIMIT / 4;
 }
 
-template <bool GATED, typename OUT>
-pmn_status launch(const CUtensorMap (&maps)[4], const Args &args, cudaStream_t s)
+template <int CHUNK, bool GATED, typename OUT>
+pmn_status launch_chunk(const Args &args, int64_t n, cudaStream_t s)
 {
-    auto kern = matvec_kernel<GATED, OUT>;
+    CUtensorMap maps[4];
+    if (!make_map(&maps[0], args.codes, args.k / 2, n, 128, 64) || !make_map(&maps[1], args.scales, args.k / 16, n, RAW_W, 64) ||
+        !make_map(&maps[2], args.digits, args.k / 2, args.rows * DIGITS, 128, 16) ||
+        !make_map(&maps[3], args.digit_scales, args.k / 16, args.rows, RAW_W, CHUNK))
+        return PMN_ERR_CUDA;
+    auto kern = matvec_kernel<CHUNK, GATED, OUT>;
     static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return PMN_ERR_CUDA;
     int sms = dev < MAX_DEVICES ? sm_count[dev].load(std::memory_order_acquire) : 0;
     if (sms == 0) {
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CHUNK>::SMEM_BYTES) != cudaSuccess)
             return PMN_ERR_CUDA;
         sms = std::min(sms, MAX_GRID);
         if (dev < MAX_DEVICES) sm_count[dev].store(sms, std::memory_order_release);
     }
-    digits_kernel<<<(unsigned)args.rows, 256, 0, s>>>(args, sms);
+    digits_kernel<<<(unsigned)args.rows, DIGIT_THREADS, 0, s>>>(args, sms);
     if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
     // launched while the digits are made: the weights need not wait for them
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.dynamicSmemBytes = Cfg<CHUNK>::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -659,6 +675,13 @@ pmn_status launch(const CUtensorMap (&maps)[4], const Args &args, cudaStream_t s
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+template <bool GATED, typename OUT>
+pmn_status launch(const Args &args, int64_t n, cudaStream_t s)
+{
+    if (args.rows <= 8 * (int64_t)args.experts) return launch_chunk<8, GATED, OUT>(args, n, s);
+    return launch_chunk<16, GATED, OUT>(args, n, s);
 }
 
 }  // namespace
@@ -699,18 +722,15 @@ extern "C" pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t token
         !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(outer, 4) || !aligned(offsets, 4) ||
         !aligned(row_choice, 4) || !aligned(out, 16) || !aligned(workspace, 16))
         return PMN_ERR_INVALID_ARG;
+    // steps are counted in 32 bits
+    if ((total_rows / 8 + num_experts) * (n / 64 + 1) * (k / KSTEP) >= LIMIT) return PMN_ERR_UNSUPPORTED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int64_t half_n = swiglu ? n / 2 : n, half = swiglu ? BM / 2 : BM;
     const Args a{static_cast<const uint16_t *>(x), ldx, tokens, codes, scales, outer, offsets, num_experts, total_rows, n, k,
                  row_choice, choices, out, (int)((half_n + half - 1) / half), (int)(k / KSTEP), ws + w.digits, ws + w.scales,
                  reinterpret_cast<int2 *>(ws + w.meta), reinterpret_cast<float *>(ws + w.part),
                  reinterpret_cast<unsigned *>(ws + w.count), pmn_wait_limit_ns()};
-    CUtensorMap maps[4];
-    if (!make_map(&maps[0], codes, k / 2, num_experts * n, 128, 64) || !make_map(&maps[1], scales, k / 16, num_experts * n, RAW_W, 64) ||
-        !make_map(&maps[2], a.digits, k / 2, total_rows * DIGITS, 128, 16) ||
-        !make_map(&maps[3], a.digit_scales, k / 16, total_rows, RAW_W, CHUNK))
-        return PMN_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (swiglu) return out_kind == PMN_OUT_F32 ? launch<true, float>(maps, a, s) : launch<true, uint16_t>(maps, a, s);
-    return out_kind == PMN_OUT_F32 ? launch<false, float>(maps, a, s) : launch<false, uint16_t>(maps, a, s);
+    if (swiglu) return out_kind == PMN_OUT_F32 ? launch<true, float>(a, num_experts * n, s) : launch<true, uint16_t>(a, num_experts * n, s);
+    return out_kind == PMN_OUT_F32 ? launch<false, float>(a, num_experts * n, s) : launch<false, uint16_t>(a, num_experts * n, s);
 }
