@@ -37,7 +37,7 @@ constexpr int DIGITS = 8;
 constexpr int MAX_CHUNK = 16;                    // most rows of x per pass over the weights
 constexpr int BM = 128;                          // weight rows of a tile (gated: 64 gate and the 64 up rows of the same columns)
 constexpr int KSTEP = 256;                       // of K per stage: 128 bytes of codes, 16 scales
-constexpr int A_BYTES = BM * 128, SF_BYTES = 2 * 4 * 512;
+constexpr int A_BYTES = BM * 128;
 constexpr int RAW_STEPS = 4, RAW_W = 16 * RAW_STEPS;  // scale rows come 64 bytes (four stages) at a time
 constexpr int RAW_A = BM * RAW_W, RAW_BYTES = RAW_A + MAX_CHUNK * RAW_W, RAW_SLOTS = 3;
 constexpr uint32_t TMEM_COLS = 512, SF_COLS = 32;
@@ -46,8 +46,10 @@ constexpr uint32_t TMEM_COLS = 512, SF_COLS = 32;
 template <int CHUNK>
 struct Cfg {
     static constexpr int NB = CHUNK * DIGITS;  // rows of the small operand
-    static constexpr int B_BYTES = NB * 128, STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
-    static constexpr int STAGES = CHUNK == 8 ? 6 : 5;
+    static constexpr int B_BYTES = NB * 128, STAGE_BYTES = A_BYTES + B_BYTES;
+    // More in flight is not better (512 rows of 384 experts, k 1536 and 4096: 7 stages 191 and 272 us, 6 172 and
+    // 274, 5 164 and 278, 4 156 and 285; one token 20.5, 21.5, 20.5, 22.5).
+    static constexpr int STAGES = 5;
     static constexpr int RAW_OFF = STAGES * STAGE_BYTES, XCH_OFF = RAW_OFF + RAW_SLOTS * RAW_BYTES;
     static constexpr int BAR_OFF = XCH_OFF + 64 * 20 * 4, CUM_OFF = BAR_OFF + 256;
     static constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS + 1) * 4;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDS, const Args p)
 {
     using C = Cfg<CHUNK>;
-    constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES, B_BYTES = C::B_BYTES, NB = C::NB, RAW_OFF = C::RAW_OFF;
+    constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES, NB = C::NB, RAW_OFF = C::RAW_OFF;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw;
     asm volatile("" : "+l"(smem));
@@ -423,13 +425,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = q.k0; k < q.k1; ++k) {
                 if (!wait(bar_full + 8 * stage, phase)) break;
                 tc_fence_after();
-                const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES, sf = b + B_BYTES;
+                const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES;
                 const uint32_t sfa = tm + C::SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    tc_cp_ct<1>(el, sfa + 4 * s, smem_desc(sf + 512 * s, 0, 128, 0));
-                    tc_cp_ct<1>(el, sfb + 4 * s, smem_desc(sf + 2048 + 512 * s, 0, 128, 0));
-                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s)  // 64 of K: 32 bytes of the swizzled rows
                     mma_nvfp4_by(el, d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2), idesc, sfa + 4 * s,
@@ -449,40 +446,51 @@ __global__ void __launch_bounds__(THREADS, 1)
         (void)warp_wait(bar_drain, 0, DRAIN_NS);
     } else if (warp < 8) {
         // ---------------------------------------------------- scale factors
-        // Step s of a stage, lane r, word j: the four scale bytes of row 32 j + r.  A thread has
-        // weight row i and row i of the digits, whose eight rows per value share a scale.
-        const int i = threadIdx.x - 128, word = 16 * (i & 31) + 4 * (i >> 5);
+        // For 64 of K (s) the tensor core finds the four scale bytes of row 32 j + r in column
+        // 4 s + j of lane r, in each of TMEM's four groups of 32 lanes: one group per warp, which
+        // writes all rows' there.  The eight digits of a value share a scale.  (By way of shared memory,
+        // eight tcgen05.cp a stage, one token takes 22.5 us for 20.5.)
+        const int quad = warp & 3;
         uint32_t slot = 0, sphase = 0;
         while (!dead && walk.next(p, s_cum, q)) {
             for (int k = q.k0; k < q.k1 && !dead; k += RAW_STEPS) {
                 if (!wait(bar_raw + 8 * slot, sphase)) break;
                 const uint8_t *raw = smem + RAW_OFF + slot * RAW_BYTES;
-                uint4 va[RAW_STEPS], vb[RAW_STEPS];
-#pragma unroll
-                for (int c = 0; c < RAW_STEPS; ++c) {
-                    va[c] = *reinterpret_cast<const uint4 *>(raw + RAW_W * i + 16 * c);
-                    vb[c] = *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * min(i >> 3, CHUNK - 1) + 16 * c);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
-                if (++slot == RAW_SLOTS) {
-                    slot = 0;
-                    sphase ^= 1;
-                }
 #pragma unroll
                 for (int c = 0; c < RAW_STEPS; ++c) {
                     if (k + c >= q.k1 || dead) break;
-                    if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
-                    uint8_t *sf = smem + stage * STAGE_BYTES + A_BYTES + B_BYTES + word;
+                    uint32_t sa[16], sb[16];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        *reinterpret_cast<uint32_t *>(sf + 512 * s) = u4_word(va[c], s);
-                        *reinterpret_cast<uint32_t *>(sf + 2048 + 512 * s) = u4_word(vb[c], s);
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = 32 * j + lane;
+                        // (64-byte swizzle: eight lanes meet all banks)
+                        const uint4 va = *reinterpret_cast<const uint4 *>(raw + RAW_W * row + 16 * (c ^ ((row >> 1) & 3)));
+                        const uint4 vb = 32 * j < NB ? *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * (row >> 3) + 16 * c)
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            sa[4 * s + j] = u4_word(va, s);
+                            sb[4 * s + j] = u4_word(vb, s);
+                        }
                     }
-                    fence_proxy_async_smem();
+                    if (c == RAW_STEPS - 1 || k + c == q.k1 - 1) {  // the slot has been read
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
+                    }
+                    if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
+                    tc_fence_after();
+                    const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + C::SF_COL0 + stage * SF_COLS;
+                    tmem_st_32x32b_x16(to, sa);
+                    tmem_st_32x32b_x16(to + 16, sb);
+                    tmem_st_wait();
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_full + 8 * stage);
                     next_stage();
+                }
+                if (++slot == RAW_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1;
                 }
             }
         }
@@ -603,15 +611,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ====================================================================== host
-// Bytes [rows, width] in boxes of box_w (128: with the 128-byte swizzle) x box_rows.
-bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, uint32_t box_w, uint32_t box_rows)
+// Bytes [rows, width] in boxes of box_w x box_rows.
+bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, uint32_t box_w, uint32_t box_rows,
+              CUtensorMapSwizzle swizzle)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width};
     const cuuint32_t box[2] = {box_w, box_rows}, es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, box_w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
               box_w == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -645,9 +654,10 @@ template <int CHUNK, bool GATED, typename OUT>
 pmn_status launch_chunk(const Args &args, int64_t n, cudaStream_t s)
 {
     CUtensorMap maps[4];
-    if (!make_map(&maps[0], args.codes, args.k / 2, n, 128, 64) || !make_map(&maps[1], args.scales, args.k / 16, n, RAW_W, 64) ||
-        !make_map(&maps[2], args.digits, args.k / 2, args.rows * DIGITS, 128, 16) ||
-        !make_map(&maps[3], args.digit_scales, args.k / 16, args.rows, RAW_W, CHUNK))
+    if (!make_map(&maps[0], args.codes, args.k / 2, n, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&maps[1], args.scales, args.k / 16, n, RAW_W, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&maps[2], args.digits, args.k / 2, args.rows * DIGITS, 128, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&maps[3], args.digit_scales, args.k / 16, args.rows, RAW_W, CHUNK, CU_TENSOR_MAP_SWIZZLE_NONE))
         return PMN_ERR_CUDA;
     auto kern = matvec_kernel<CHUNK, GATED, OUT>;
     static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
