@@ -314,6 +314,101 @@ class GatedBlockTrainStep:
                        grad_scale=grad_scale)
 
 
+class RoutedExpertsStep:
+    """Forward and backward of a routed layer whose experts are kept in bf16, from
+    the tokens and their router logits back to the tokens:
+      gates, offsets = top-k of the logits                 on the device
+      xr = the tokens' rows in expert order
+      h = silu(xr . Wg^T) * (xr . Wu^T);  z = h . W2^T      ragged segments
+      out = sum over a token's choices of gate * z
+      dz, dgates from dout; dY1 from dz, W2 and y
+      dW2 = dz^T . h, dW1 = dY1^T . xr                      float32, sums over ragged rows
+      dx = sum over a token's choices of (dY1 . W1);  dlogits from dgates
+    x bf16 [tokens, D], logits [tokens, E] bf16 or float32, w1 bf16 [E, 2F, D],
+    w2 bf16 [E, D, F]; F a multiple of 16, D of 8.  All buffers are allocated
+    here, rows that no expert uses as zeros; forward() and backward() only
+    enqueue kernels on the current stream, and backward() belongs to the
+    forward() before it, whose inputs it reads again."""
+
+    def __init__(self, tokens, w1, w2, k, logits_dtype=torch.float32, bias=None, score=pmn.SCORE_SOFTMAX, normalize=True,
+                 scale=1.0, pad=1):
+        E, F2, D = w1.shape
+        F, dev = F2 // 2, w1.device
+        if w2.shape != (E, D, F) or F % 16 or D % 8:
+            raise ValueError("RoutedExpertsStep: w1 [E, 2F, D], w2 [E, D, F]; F a multiple of 16, D of 8")
+        self.w1, self.w2, self.k, self.bias, self.pad = w1, w2, k, bias, pad
+        self.how = dict(score=score, normalize=normalize, scale=scale)
+        bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        R = pmn.route_rows(tokens, E, k, pad)
+
+        def z(*shape, dtype=bf16):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        self.routing = pmn.Routing(z(tokens, k, dtype=i32), z(tokens, k, dtype=f32), z(tokens, k, dtype=i32),
+                                   z(R, dtype=i32), z(E + 1, dtype=i32))
+        self.ws = z(pmn.route_topk_workspace_bytes(tokens, E, k), dtype=torch.uint8)
+        self.xr, self.y, self.h, self.z, self.out = z(R, D), z(R, F2), z(R, F), z(R, D), z(tokens, D)
+        self.dz, self.dy1, self.dxr, self.dx = z(R, D), z(R, F2), z(R, D), z(tokens, D)
+        self.dgates, self.dlogits = z(tokens, k, dtype=f32), z(tokens, E, dtype=logits_dtype)
+        self.dw1, self.dw2 = z(E, F2, D, dtype=f32), z(E, D, F, dtype=f32)
+        self.logits = None
+
+    def forward(self, x, logits):
+        """The tokens' sums over their experts (bf16 [tokens, D])."""
+        P, r = pmn, self.routing
+        self.logits = logits
+        P.route_topk(logits, self.k, bias=self.bias, pad=self.pad, out=r, workspace=self.ws, **self.how)
+        P.dispatch_rows(x, r.row_index, r.row_choice, out=self.xr)
+        P.w1_gemm_swiglu_bf16(self.xr, self.w1, r.offsets, out=self.h, y=self.y)
+        P.grouped_gemm_bf16(self.h, self.w2, r.offsets, P.GROUP_M, out=self.z)
+        return P.combine_rows(self.z, r.row_index, r.gates, out=self.out)
+
+    def backward(self, dout):
+        """Gradients from dout (bf16 [tokens, D]): (dx, dlogits, dW1, dW2)."""
+        P, r = pmn, self.routing
+        P.combine_rows_backward(dout, self.z, r.row_index, r.row_choice, r.gates, dz=self.dz, dgates=self.dgates)
+        P.grouped_gemm_bf16(self.dz, self.h, r.offsets, P.GROUP_K, out=self.dw2)
+        P.dh_gemm_swiglu_backward_bf16(self.dz, self.w2, self.y, r.offsets, out=self.dy1)
+        P.grouped_gemm_bf16(self.dy1, self.xr, r.offsets, P.GROUP_K, out=self.dw1)
+        P.grouped_gemm_bf16(self.dy1, self.w1, r.offsets, P.GROUP_M, b_transposed=True, out=self.dxr)
+        P.combine_rows(self.dxr, r.row_index, out=self.dx)
+        P.route_topk_backward(self.logits, r.experts, self.dgates, dlogits=self.dlogits, **self.how)
+        return self.dx, self.dlogits, self.dw1, self.dw2
+
+
+class RoutedDecode:
+    """The forward of a decode batch from its tokens and router logits, with
+    NVFP4 weights (as an ExpertLayerStep's w1q3() and w2q3()) and bf16
+    activations throughout: the tokens are routed on the device, their rows are
+    read where they are, and each token gets the gated sum of its experts.
+    DecodeForward takes rows that were routed before and quantises them; its
+    time is set by the same weights' bytes."""
+
+    def __init__(self, tokens, w1q3, w2q3, k, bias=None, score=pmn.SCORE_SOFTMAX, normalize=True, scale=1.0):
+        E, F2, D = w1q3[0].shape[0], w1q3[0].shape[1], 2 * w1q3[0].shape[2]
+        F, dev, R = F2 // 2, w1q3[0].device, tokens * k
+        self.w1q3, self.w2q3, self.k, self.bias = w1q3, w2q3, k, bias
+        self.how = dict(score=score, normalize=normalize, scale=scale)
+
+        def z(*shape, dtype=torch.bfloat16):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        i32 = torch.int32
+        self.routing = pmn.Routing(z(tokens, k, dtype=i32), z(tokens, k, dtype=torch.float32), z(tokens, k, dtype=i32),
+                                   z(R, dtype=i32), z(E + 1, dtype=i32))
+        self.route_ws = z(pmn.route_topk_workspace_bytes(tokens, E, k), dtype=torch.uint8)
+        self.ws = z(max(pmn.matvec_nvfp4_workspace_bytes(R, D), pmn.matvec_nvfp4_workspace_bytes(R, F)), dtype=torch.uint8)
+        self.h, self.z, self.out = z(R, F), z(R, D), z(tokens, D)
+
+    def forward(self, x, logits):
+        """x bf16 [tokens, D], logits [tokens, E] -> bf16 [tokens, D]."""
+        P, r = pmn, self.routing
+        P.route_topk(logits, self.k, bias=self.bias, out=r, workspace=self.route_ws, **self.how)
+        P.matvec_nvfp4(x, self.w1q3, r.offsets, row_choice=r.row_choice, k=self.k, swiglu=True, out=self.h, workspace=self.ws)
+        P.matvec_nvfp4(self.h, self.w2q3, r.offsets, out=self.z, workspace=self.ws)
+        return P.combine_rows(self.z, r.row_index, r.gates, out=self.out)
+
+
 def mxfp8_forward_algorithmic(real_rows, experts, d_model, d_ff):
     """(flops, algorithmic HBM bytes) of MXFP8Forward on the real routed rows:
     bf16 weights and X read once, their MXFP8 copies written and read once,
