@@ -37,10 +37,10 @@ constexpr int TILE = 256;        // output columns of a pair's tile, and most ro
 constexpr int SIDE_BYTES = 128 * 128;  // a CTA's 128 x 64 of either operand
 constexpr int RING_BYTES = 12 * SIDE_BYTES, MAX_SLOTS = 9;
 constexpr int EW = 8, THREADS = 128 + 32 * EW;
-constexpr int CH = 16;           // output rows that an epilogue warp handles at a time, 32 columns of them
-constexpr int WARP_BUF = 4096;   // .. on their way to or from memory, two buffers
-constexpr int BUF_OFF = RING_BYTES, BAR_OFF = BUF_OFF + EW * WARP_BUF;
-constexpr int BARRIERS = 3 * MAX_SLOTS + 5 + 2 * EW;
+constexpr int GROUPS = EW / 4;      // of four epilogue warps, which hold a CTA's 128 columns
+constexpr int GROUP_BUF = 16384;   // rows on their way to or from memory
+constexpr int BUF_OFF = RING_BYTES, BAR_OFF = BUF_OFF + GROUPS * GROUP_BUF;
+constexpr int BARRIERS = 3 * MAX_SLOTS + 5 + 4 * GROUPS;
 constexpr int CUM_OFF = BAR_OFF + 8 * BARRIERS + 16;
 constexpr int SMEM_BYTES = CUM_OFF + (MAX_GROUPS / 32 + 1) * 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -63,7 +63,7 @@ struct Args {
 struct Maps {
     CUtensorMap w;                   // M side
     CUtensorMap x, x64, x32, x16;    // N side: 128, 64, 32, 16 rows (SUMS: x alone, 64 columns of 64 rows)
-    CUtensorMap out, y;              // CH rows of 32 columns (GATED: of 16)
+    CUtensorMap out, y;              // the epilogue's pieces
 };
 
 struct Tile {
@@ -79,6 +79,7 @@ struct Form {
     static constexpr bool sums = FORM == SUMS, gated = FORM == GATED, backward = FORM == GATED_BACKWARD;
     static constexpr bool m_major_w = FORM == ROWS_KN || backward || sums;  // the M side's contiguous axis is M
     static constexpr int cols = gated ? TILE / 2 : TILE;                    // output columns of a pair's tile
+    static constexpr int ch = backward ? 8 : 16;                            // output rows of an epilogue piece
 };
 
 __device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + TILE - 1) / TILE); }
@@ -177,6 +178,14 @@ __device__ __forceinline__ void tma_5d_pair(uint32_t dst, const CUtensorMap *m, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
             mbar_init(bar_acc_empty + 8 * b, 2 * EW);
         }
         mbar_init(bar_drain, 1);
-        for (int b = 0; b < 2 * EW; ++b) mbar_init(bar_y + 8 * b, 1);
+        for (int b = 0; b < 4 * GROUPS; ++b) mbar_init(bar_y + 8 * b, 1);
         *s_abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&maps.w);
@@ -450,56 +459,63 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
-        // A lane holds one column of the output, a register one row.  A warp takes every
-        // (EW / 4)th 16 rows of its 32 columns, puts them into shared memory and has TMA write
-        // them: the stores then cost the warp nothing and arrive as whole lines.  Rows
-        // behind the segment's end may not be written, so the last few of a segment are stored singly.
-        const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0), quad = wu & 3, c_first = (wu - 4) >> 2;
-        uint8_t *const buf0 = smem + BUF_OFF + (wu - 4) * WARP_BUF;
-        const uint32_t bufs0 = ring + BUF_OFF + (wu - 4) * WARP_BUF, ybar = bar_y + 16 * (wu - 4);
-        uint32_t abuf = 0, aphase = 0, n = 0;  // n: chunks so far
+        // A lane holds one column of the output, a register one row.  Four warps take every other
+        // CH rows of the CTA's 128 columns, put them into shared memory and have TMA write them:
+        // the stores then cost the warps nothing and arrive as whole lines (boxes of 32 columns: dw1
+        // of 8192 rows 262 us for 252).  Rows behind the segment's end may not be
+        // written, so the last few of a segment are stored singly.
+        constexpr int CH = F::ch, COLS = F::cols / 2;
+        constexpr int PIECE = F::gated ? 8192 : F::backward ? CH * 2 * COLS * 2 : CH * COLS * (int)sizeof(OUT);  // bytes
+        constexpr int BUFS = GROUP_BUF / PIECE;
+        const int wu = __shfl_sync(0xFFFFFFFFu, warp, 0), quad = wu & 3, group = (wu - 4) >> 2;
+        uint8_t *const buf0 = smem + BUF_OFF + group * GROUP_BUF;
+        const uint32_t bufs0 = ring + BUF_OFF + group * GROUP_BUF, ybar = bar_y + 32 * group;
+        const bool issuer = quad == 0 && lane == 0;
+        uint32_t abuf = 0, aphase = 0, n = 0;  // n: pieces so far
         bool ok = true;
-        // first column of the warp in a tile, the tile's rows
-        auto col_of = [&](const Tile &ti) { return F::gated ? ti.c0 + 64 * rank + 16 * quad : ti.c0 + 128 * rank + 32 * quad; };
-        auto chunks_of = [&](const Tile &ti) {
-            return col_of(ti) < p.n ? (int)((min((int64_t)ti.width, ti.row_end - ti.r0) + CH - 1) / CH) : 0;
+        auto pieces_of = [&](const Tile &ti) {
+            return ti.c0 + COLS * rank < p.n ? (int)((min((int64_t)ti.width, ti.row_end - ti.r0) + CH - 1) / CH) : 0;
         };
-        // GATED_BACKWARD: gate and up come by TMA too, a chunk ahead, into the buffer that takes their gradients
-        int at = tile0, ac = c_first;  // tile, chunk
+        auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
+        // GATED_BACKWARD: gate and up come by TMA too, BUFS - 1 pieces ahead, into the buffer that takes their gradients
+        int at = tile0, ac = group;  // tile, piece
+        uint32_t asked = 0;
         Tile ahead;
         auto fetch = [&]() {
-            while (at < total && ac >= chunks_of(ahead)) {
-                ac = c_first;
+            while (at < total && ac >= pieces_of(ahead)) {
+                ac = group;
                 at += tstep;
                 if (at < total) ahead = get_tile<FORM>(at, p, s_cum, lane);
             }
             if (at >= total) return;
             if (lane == 0) {
-                const uint32_t b = n & 1u, d = bufs0 + 2048 * b, bar = ybar + 8 * b;
-                const int x = col_of(ahead), r = (int)ahead.r0 + CH * ac;
-                bulk_wait_group_read<1>();
-                mbar_arrive_expect_tx(bar, 2048);
-                tma_load_2d(d, &maps.y, bar, x, r);
-                tma_load_2d(d + 1024, &maps.y, bar, (int)p.n + x, r);
+                const uint32_t b = asked % BUFS, bar = ybar + 8 * b;
+                mbar_arrive_expect_tx(bar, PIECE);
+                tma_load_3d(bufs0 + PIECE * b, &maps.y, bar, ahead.c0 + COLS * rank, 0, (int)ahead.r0 + CH * ac);
             }
             __syncwarp();
-            ac += EW / 4;
+            ++asked;
+            ac += GROUPS;
         };
-        if (F::backward) {
+        if (F::backward && quad == 0) {
             if (at < total) ahead = get_tile<FORM>(at, p, s_cum, lane);
-            fetch();
+            for (int i = 0; i < BUFS - 1; ++i) fetch();
         }
-        for (int t = tile0; t < total && ok; t += tstep) {
+        for (int t = tile0; t < total; t += tstep) {
             const Tile ti = get_tile<FORM>(t, p, s_cum, lane);
-            const int chunks = chunks_of(ti), col0 = col_of(ti);
+            const int pieces = pieces_of(ti), col0 = ti.c0 + COLS * rank;
             const bool nothing = F::sums && ti.hi == ti.lo;  // a sum over no rows
-            ok = warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
-            if (!ok) break;
+            // after a timeout the four warps go on to the end together, without waiting or storing
+            ok = ok && warp_wait(bar_acc_full + 8 * abuf, aphase, p.wait_ns);
+            if (!ok) give_up();
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * TILE;
-            for (int c = c_first; c < chunks; c += EW / 4, ++n) {
+            for (int c = group; c < pieces; c += GROUPS, ++n) {
+                const uint32_t which = n % BUFS;
+                uint8_t *const buf = buf0 + PIECE * which;
                 float v[CH];
-                tmem_ld_32x32b_x16(acc + CH * c, reinterpret_cast<uint32_t(&)[CH]>(v));
+                if constexpr (CH == 16) tmem_ld_32x32b_x16(acc + CH * c, reinterpret_cast<uint32_t(&)[CH]>(v));
+                else tmem_ld_32x32b_x8(acc + CH * c, reinterpret_cast<uint32_t(&)[CH]>(v));
                 tmem_ld_wait();
                 if (nothing) {
 #pragma unroll
@@ -507,96 +523,83 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                 }
                 const int64_t r0 = ti.r0 + CH * c;
                 const int rows = (int)min((int64_t)CH, ti.row_end - r0);
+                const bool whole = F::sums || rows == CH;
                 if constexpr (F::gated) {
                     // lanes 0 .. 15 gate, 16 .. 31 up of the same 16 columns: the halves trade
                     // values, so that the lower half makes h of the even rows, the upper of the odd
                     const bool up = lane >= 16;
-                    const int cl = lane & 15;
-                    uint16_t *b = reinterpret_cast<uint16_t *>(buf0 + 2048 * (n & 1u));  // gate, up, h: 16 x 16 each
-                    if (lane == 0) bulk_wait_group_read<1>();
-                    __syncwarp();
+                    const int cl = 16 * quad + (lane & 15), col = col0 + cl;
+                    uint16_t *y = reinterpret_cast<uint16_t *>(buf), *h = y + CH * 2 * COLS;  // [CH][2][COLS], [CH][COLS]
 #pragma unroll
                     for (int j = 0; j < CH; j += 2) {
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
                         const float g = up ? got : v[j], u = up ? v[j + 1] : got;
-                        store_one(b + 256 * up + 16 * j + cl, v[j]);
-                        store_one(b + 256 * up + 16 * j + 16 + cl, v[j + 1]);
-                        store_one(b + 512 + 16 * (j + up) + cl, __fmul_rn(__fmul_rn(g, sigmoid(g)), u));
+                        store_one(y + (2 * j + up) * COLS + cl, v[j]);
+                        store_one(y + (2 * j + 2 + up) * COLS + cl, v[j + 1]);
+                        store_one(h + (j + up) * COLS + cl, __fmul_rn(__fmul_rn(g, sigmoid(g)), u));
                     }
-                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (rows == CH) {
-                        if (lane == 0) {
-                            const uint32_t d = bufs0 + 2048 * (n & 1u);
-                            if (p.y) {
-                                tma_store_2d(&maps.y, d, col0, (int)r0);
-                                tma_store_2d(&maps.y, d + 512, (int)p.n + col0, (int)r0);
-                            }
-                            tma_store_2d(&maps.out, d + 1024, col0, (int)r0);
-                        }
-                    } else {
+                    if (!whole && ok && col < p.n)
                         for (int j = 0; j < rows; ++j) {
-                            if (p.y) p.y[(r0 + j) * 2 * p.n + col0 + cl + (up ? p.n : 0)] = b[256 * up + 16 * j + cl];
-                            if (!up) static_cast<uint16_t *>(p.out)[(r0 + j) * p.n + col0 + cl] = b[512 + 16 * j + cl];
+                            if (p.y) p.y[(r0 + j) * 2 * p.n + col + (up ? p.n : 0)] = y[(2 * j + up) * COLS + cl];
+                            if (!up) static_cast<uint16_t *>(p.out)[(r0 + j) * p.n + col] = h[j * COLS + cl];
                         }
-                        __syncwarp();
-                    }
-                    if (lane == 0) bulk_commit_group();
                 } else if constexpr (F::backward) {
-                    const uint32_t which = n & 1u;
-                    uint16_t *b = reinterpret_cast<uint16_t *>(buf0 + 2048 * which);  // gate, up: 16 x 32 each
-                    ok = warp_wait(ybar + 8 * which, (n >> 1) & 1u, p.wait_ns);
-                    if (!ok) break;
+                    const int cl = 32 * quad + lane, col = col0 + cl;
+                    uint16_t *b = reinterpret_cast<uint16_t *>(buf);  // [CH][2][COLS]: gate, up
+                    ok = ok && warp_wait(ybar + 8 * which, (n / BUFS) & 1u, p.wait_ns);
+                    if (!ok) give_up();
 #pragma unroll
                     for (int j = 0; j < CH; ++j) {
-                        const float g = bf16_value(b[32 * j + lane]), u = bf16_value(b[512 + 32 * j + lane]), dh = v[j];
+                        const float g = bf16_value(b[2 * j * COLS + cl]), u = bf16_value(b[(2 * j + 1) * COLS + cl]), dh = v[j];
                         const float s = sigmoid(g), a = __fmul_rn(dh, s);
-                        store_one(b + 32 * j + lane, __fmul_rn(__fmul_rn(a, u), fmaf(g, 1.0f - s, 1.0f)));
-                        store_one(b + 512 + 32 * j + lane, __fmul_rn(a, g));
+                        store_one(b + 2 * j * COLS + cl, __fmul_rn(__fmul_rn(a, u), fmaf(g, 1.0f - s, 1.0f)));
+                        store_one(b + (2 * j + 1) * COLS + cl, __fmul_rn(a, g));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (rows == CH && col0 + 32 <= p.n) {  // (a box may not reach from gate's columns into up's)
-                        if (lane == 0) {
-                            const uint32_t d = bufs0 + 2048 * which;
-                            tma_store_2d(&maps.out, d, col0, (int)r0);
-                            tma_store_2d(&maps.out, d + 1024, (int)p.n + col0, (int)r0);
-                        }
-                    } else if (col0 + lane < p.n) {
-                        uint16_t *o = static_cast<uint16_t *>(p.out) + r0 * 2 * p.n + col0 + lane;
+                    if (!whole && ok && col < p.n) {
+                        uint16_t *o = static_cast<uint16_t *>(p.out) + r0 * 2 * p.n + col;
                         for (int j = 0; j < rows; ++j) {
-                            o[j * 2 * p.n] = b[32 * j + lane];
-                            o[j * 2 * p.n + p.n] = b[512 + 32 * j + lane];
+                            o[j * 2 * p.n] = b[2 * j * COLS + cl];
+                            o[j * 2 * p.n + p.n] = b[(2 * j + 1) * COLS + cl];
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) bulk_commit_group();
-                    ++n;
-                    fetch();  // into the other buffer, whose store has been under way for a chunk
-                    --n;
                 } else {
-                    constexpr int BUFS = WARP_BUF / (CH * 32 * (int)sizeof(OUT));
-                    const uint32_t off = CH * 32 * sizeof(OUT) * (n % BUFS);
-                    OUT *b = reinterpret_cast<OUT *>(buf0 + off);
-                    if (lane == 0) bulk_wait_group_read<BUFS - 1>();
-                    __syncwarp();
+                    const int cl = 32 * quad + lane, col = col0 + cl;
+                    OUT *b = reinterpret_cast<OUT *>(buf);  // [CH][COLS]
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) store_one(b + 32 * j + lane, v[j]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (F::sums) {
-                        if (lane == 0) tma_store_3d(&maps.out, bufs0 + off, col0, (int)r0, ti.g);
-                    } else if (rows == CH) {
-                        if (lane == 0) tma_store_2d(&maps.out, bufs0 + off, col0, (int)r0);
-                    } else if (col0 + lane < p.n) {
-                        OUT *o = static_cast<OUT *>(p.out) + r0 * p.n + col0 + lane;
-                        for (int j = 0; j < rows; ++j) o[j * p.n] = b[32 * j + lane];
+                    for (int j = 0; j < CH; ++j) store_one(b + j * COLS + cl, v[j]);
+                    if (!whole && ok && col < p.n) {
+                        OUT *o = static_cast<OUT *>(p.out) + r0 * p.n + col;
+                        for (int j = 0; j < rows; ++j) o[j * p.n] = b[j * COLS + cl];
+                    }
+                }
+                fence_proxy_async_smem();
+                if (issuer) bulk_wait_group_read<BUFS - 2>();  // the next piece's buffer has been read
+                meet();
+                if (quad == 0) {
+                    if (lane == 0) {
+                        const uint32_t d = bufs0 + PIECE * which;
+                        if (whole && ok) {
+                            if constexpr (F::gated) {
+                                if (p.y) tma_store_3d(&maps.y, d, col0, 0, (int)r0);
+                                tma_store_2d(&maps.out, d + CH * 2 * COLS * 2, col0, (int)r0);
+                            } else if constexpr (F::backward) {
+                                tma_store_3d(&maps.out, d, col0, 0, (int)r0);
+                            } else if constexpr (F::sums) {
+                                tma_store_3d(&maps.out, d, col0, (int)r0, ti.g);
+                            } else {
+                                tma_store_2d(&maps.out, d, col0, (int)r0);
+                            }
+                        }
+                        bulk_commit_group();
                     }
                     __syncwarp();
-                    if (lane == 0) bulk_commit_group();
+                    if (F::backward && ok) {  // the buffer of the piece before this one
+                        if (lane == 0) bulk_wait_group_read<1>();
+                        fetch();
+                    }
                 }
             }
-            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_leader(bar_acc_empty + 8 * abuf);
@@ -605,13 +608,11 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                 aphase ^= 1;
             }
         }
-        if (!ok) give_up();
-        if (F::backward && !ok) {  // a load that nobody waited for may still be landing
-            (void)warp_wait(ybar, 0, DRAIN_NS);
-            (void)warp_wait(ybar, 1, DRAIN_NS);
-            (void)warp_wait(ybar + 8, 0, DRAIN_NS);
-            (void)warp_wait(ybar + 8, 1, DRAIN_NS);
-        }
+        if (F::backward && quad == 0 && !ok)  // loads that nobody waited for may still be landing
+            for (int b = 0; b < BUFS; ++b) {
+                (void)warp_wait(ybar + 8 * b, 0, DRAIN_NS);
+                (void)warp_wait(ybar + 8 * b, 1, DRAIN_NS);
+            }
         if (lane == 0) bulk_wait_group_all();  // shared memory is read until then
         __syncwarp();
     }
@@ -643,13 +644,13 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The epilogue's pieces: CH rows of `cols` columns of [groups, rows, n] (groups 0: of [rows, n]).
-bool piece_map(CUtensorMap *m, const void *base, int groups, int64_t rows, int64_t n, int kind, int cols)
+// The epilogue's pieces, `box` of [outer, middle, n].
+bool piece_map(CUtensorMap *m, const void *base, int64_t outer, int64_t middle, int64_t n, int kind, int b2, int b1, int b0)
 {
     const uint64_t b = kind == PMN_OUT_F32 ? 4 : 2;
-    const uint64_t dims[3] = {(uint64_t)n, (uint64_t)rows, (uint64_t)groups}, st[2] = {n * b, (uint64_t)rows * n * b};
-    const uint32_t box[3] = {(uint32_t)cols, CH, 1};
-    return make_map(m, base, groups ? 3 : 2, dims, st, box,
+    const uint64_t dims[3] = {(uint64_t)n, (uint64_t)middle, (uint64_t)outer}, st[2] = {n * b, (uint64_t)middle * n * b};
+    const uint32_t box[3] = {(uint32_t)b0, (uint32_t)b1, (uint32_t)b2};
+    return make_map(m, base, b2 ? 3 : 2, dims, st, box,
                     kind == PMN_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false);
 }
 
@@ -757,7 +758,7 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
                        ? PMN_OK : PMN_ERR_CUDA;
         if (!a || !b) return PMN_ERR_INVALID_ARG;
         if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.x, a, m, k, lda, 64) ||
-            !piece_map(&maps.out, out, num_groups, m, n, out_kind, 32))
+            !piece_map(&maps.out, out, num_groups, m, n, out_kind, 1, 16, 128))
             return PMN_ERR_CUDA;
         const Args args{offsets, num_groups, k, m, n, 0, out, nullptr, pmn_wait_limit_ns()};
         return out_kind == PMN_OUT_F32 ? launch<SUMS, float>(maps, args, s) : launch<SUMS, uint16_t>(maps, args, s);
@@ -767,7 +768,7 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
     if (!a || !b || !out || !offsets) return PMN_ERR_INVALID_ARG;
     if (!token_maps(maps, a, m, k, lda) || !(b_transposed ? weight_map(&maps.w, b, num_groups, k, n, 64)
                                                           : weight_map(&maps.w, b, num_groups, n, k, 128)) ||
-        !piece_map(&maps.out, out, 0, m, n, out_kind, 32))
+        !piece_map(&maps.out, out, 1, m, n, out_kind, 0, 16, 128))
         return PMN_ERR_CUDA;
     const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
     if (b_transposed)
@@ -792,8 +793,8 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
     const uint32_t box[5] = {64, 16, 2, 4, 1};
     Maps maps = {};
     if (!token_maps(maps, a, total_rows, k, lda) || !make_map(&maps.w, b, 5, dims, str, box) ||
-        !piece_map(&maps.out, out, 0, total_rows, f, PMN_OUT_BF16, 16) ||
-        (y_out && !piece_map(&maps.y, y_out, 0, total_rows, 2 * f, PMN_OUT_BF16, 16)))
+        !piece_map(&maps.out, out, 1, total_rows, f, PMN_OUT_BF16, 0, 16, 64) ||
+        (y_out && !piece_map(&maps.y, y_out, total_rows, 2, f, PMN_OUT_BF16, 16, 2, 64)))
         return PMN_ERR_CUDA;
     const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
                     pmn_wait_limit_ns()};
@@ -813,8 +814,8 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t ld
         return PMN_ERR_INVALID_ARG;
     Maps maps = {};
     if (!token_maps(maps, a, total_rows, k, lda) || !weight_map(&maps.w, b, num_experts, k, f, 64) ||
-        !piece_map(&maps.out, out, 0, total_rows, 2 * f, PMN_OUT_BF16, 32) ||
-        !piece_map(&maps.y, y, 0, total_rows, 2 * f, PMN_OUT_BF16, 32))
+        !piece_map(&maps.out, out, total_rows, 2, f, PMN_OUT_BF16, 8, 2, 128) ||
+        !piece_map(&maps.y, y, total_rows, 2, f, PMN_OUT_BF16, 8, 2, 128))
         return PMN_ERR_CUDA;
     const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(const_cast<void *>(y)),
                     pmn_wait_limit_ns()};
