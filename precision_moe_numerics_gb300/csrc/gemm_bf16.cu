@@ -644,6 +644,134 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
     cluster_sync();
 }
 
+// ---------------------------------------------------------------- few rows
+// The forward calls for a handful of rows (single tokens of a serving loop): their time is that of
+// reading the weights, which 256-column tiles would spread over few SMs.  A CTA takes
+// 16 weight rows (gated: 8 gate rows and the 8 up rows of the same columns) for up to eight
+// rows of one expert; its warps share K, each lane loads 16 bytes of a weight row at a time, which are
+// the tensor core's operands as they are (mma.sync; what it sees as its K is the lanes'
+// order, the same for weights and rows).  The warps' sums meet in shared memory.
+constexpr int FEW_THREADS = 256, FEW_UNROLL = 4;
+
+__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// grid: blocks of 16 weight rows x chunks of eight rows of an expert (as many as there can be)
+template <bool GATED, typename OUT>
+__global__ void __launch_bounds__(FEW_THREADS, 3)
+    few_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, const Args p)
+{
+    constexpr int WARPS = FEW_THREADS / 32;
+    __shared__ int s_sum[WARPS], s_found[3];
+    __shared__ float s_part[WARPS][16][9];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, unit = blockIdx.y;
+    // the expert whose chunk this is
+    if (threadIdx.x == 0) s_found[0] = -1;
+    int base = 0;
+    bool bad = false;
+    for (int g0 = 0; g0 < p.groups; g0 += FEW_THREADS) {
+        const int g = g0 + threadIdx.x;
+        int lo = 0, hi = 0;
+        if (g < p.groups) {
+            lo = __ldg(p.offsets + g);
+            hi = __ldg(p.offsets + g + 1);
+            bad = bad || lo < 0 || hi < lo || hi > p.rows;
+        }
+        const int n = (hi - lo + 7) / 8;
+        int run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) s_sum[warp] = run;
+        __syncthreads();
+        int before = base, all = base;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+            if (i < warp) before += s_sum[i];
+            all += s_sum[i];
+        }
+        if (unit >= before + run - n && unit < before + run) {
+            s_found[0] = g;
+            s_found[1] = lo + 8 * (unit - (before + run - n));
+            s_found[2] = hi;
+        }
+        base = all;
+        __syncthreads();
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && unit == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
+        return;
+    }
+    const int g = s_found[0], r0 = s_found[1], m = min(8, s_found[2] - r0);
+    if (g < 0) return;
+
+    const int r = lane >> 2, q = lane & 3;
+    const int64_t col = (GATED ? 8 : 16) * (int64_t)blockIdx.x + r, cols = p.n;  // p.n: of the output
+    const uint16_t *w0 = w + ((int64_t)g * (GATED ? 2 * cols : cols) + min(col, cols - 1)) * p.k;
+    const uint16_t *w1 = w + ((int64_t)g * (GATED ? 2 * cols : cols) + (GATED ? cols + min(col, cols - 1) : min(col + 8, cols - 1))) * p.k;
+    const uint16_t *xr = x + (r0 + min(r, m - 1)) * ldx;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float acc[4] = {};
+    // (the same passes for all lanes of a warp, which multiply together)
+    for (int64_t kw = 32 * FEW_UNROLL * warp; kw < p.k; kw += 32 * FEW_UNROLL * WARPS) {
+        uint4 a[FEW_UNROLL], b[FEW_UNROLL], c[FEW_UNROLL];
+#pragma unroll
+        for (int i = 0; i < FEW_UNROLL; ++i) {
+            const int64_t k = kw + 32 * i + 8 * q;
+            const bool on = k < p.k;
+            a[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
+            b[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
+            c[i] = on && r < m ? __ldg(reinterpret_cast<const uint4 *>(xr + k)) : zero;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < FEW_UNROLL; ++i) {
+            mma_m16n8k16(acc, a[i].x, b[i].x, a[i].y, b[i].y, c[i].x, c[i].y);
+            mma_m16n8k16(acc, a[i].z, b[i].z, a[i].w, b[i].w, c[i].z, c[i].w);
+        }
+    }
+    s_part[warp][r][2 * q] = acc[0];
+    s_part[warp][r][2 * q + 1] = acc[1];
+    s_part[warp][r + 8][2 * q] = acc[2];
+    s_part[warp][r + 8][2 * q + 1] = acc[3];
+    __syncthreads();
+    if (threadIdx.x >= (GATED ? 64 : 128)) return;
+    const int c = threadIdx.x & (GATED ? 7 : 15), n = threadIdx.x / (GATED ? 8 : 16);
+    const int64_t oc = (GATED ? 8 : 16) * (int64_t)blockIdx.x + c;
+    if (n >= m || oc >= cols) return;
+    float s = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        s = __fadd_rn(s, s_part[i][c][n]);
+        if (GATED) u = __fadd_rn(u, s_part[i][c + 8][n]);
+    }
+    if (GATED) {
+        if (p.y) {
+            store_one(p.y + (r0 + n) * 2 * cols + oc, s);
+            store_one(p.y + (r0 + n) * 2 * cols + cols + oc, u);
+        }
+        s = __fmul_rn(__fmul_rn(s, sigmoid(s)), u);
+    }
+    store_one(static_cast<OUT *>(p.out) + (r0 + n) * cols + oc, s);
+}
+
+template <bool GATED, typename OUT>
+pmn_status launch_few(const void *a, int64_t lda, const void *b, const Args &p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)((p.n + (GATED ? 7 : 15)) / (GATED ? 8 : 16)),
+                    (unsigned)std::min<int64_t>(p.rows, p.rows / 8 + p.groups));
+    few_rows_kernel<GATED, OUT><<<grid, FEW_THREADS, 0, s>>>(static_cast<const uint16_t *>(a), lda,
+                                                              static_cast<const uint16_t *>(b), p);
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
 // ====================================================================== host
 bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
               CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, bool swizzle = true)
@@ -723,6 +851,10 @@ pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k
     return tiles >= LIMIT / 2 ? PMN_ERR_UNSUPPORTED : PMN_OK;
 }
 
+// Whether the kernel for a few rows serves a call.  f 1536, k 4096, it and the tiles, us: one expert, one and
+// eight rows 12 and 25, 16 rows 16 and 25, 32 rows 27 and 25; 24 experts, 8 rows 37 and 47, 32 rows 68 and 69.
+bool few(int64_t rows) { return rows <= 16; }
+
 // Maps of the token rows [rows, k].
 bool token_maps(Maps &maps, const void *a, int64_t rows, int64_t k, int64_t lda)
 {
@@ -785,11 +917,13 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
     if (k <= 0 || k % 8 != 0 || lda < k) return PMN_ERR_INVALID_ARG;
     if (m == 0) return PMN_OK;
     if (!a || !b || !out || !offsets) return PMN_ERR_INVALID_ARG;
+    const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
+    if (!b_transposed && few(m))
+        return out_kind == PMN_OUT_F32 ? launch_few<false, float>(a, lda, b, args, s) : launch_few<false, uint16_t>(a, lda, b, args, s);
     if (!token_maps(maps, a, m, k, lda) || !(b_transposed ? weight_map(&maps.w, b, num_groups, k, n, 64)
                                                           : weight_map(&maps.w, b, num_groups, n, k, 128)) ||
         !piece_map(&maps.out, out, 1, m, n, out_kind, 0, 16, 128))
         return PMN_ERR_CUDA;
-    const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
     if (b_transposed)
         return out_kind == PMN_OUT_F32 ? launch<ROWS_KN, float>(maps, args, s) : launch<ROWS_KN, uint16_t>(maps, args, s);
     return out_kind == PMN_OUT_F32 ? launch<ROWS_NK, float>(maps, args, s) : launch<ROWS_NK, uint16_t>(maps, args, s);
@@ -806,6 +940,9 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
     if (!a || !b || !offsets || !out || !aligned(a, 16) || !aligned(b, 16) || !aligned(offsets, 4) || !aligned(out, 16) ||
         !aligned(y_out, 16))
         return PMN_ERR_INVALID_ARG;
+    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
+                    pmn_wait_limit_ns()};
+    if (few(total_rows)) return launch_few<true, uint16_t>(a, lda, b, args, reinterpret_cast<cudaStream_t>(stream));
     // 16 gate rows, the 16 up rows of the same columns, the next 16 gate rows, ..
     const uint64_t dims[5] = {(uint64_t)k, 16, 2, (uint64_t)f / 16, (uint64_t)num_experts};
     const uint64_t str[4] = {(uint64_t)k * 2, (uint64_t)f * k * 2, (uint64_t)k * 32, (uint64_t)f * k * 4};
@@ -815,8 +952,6 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
         !piece_map(&maps.out, out, 1, total_rows, f, PMN_OUT_BF16, 0, 16, 64) ||
         (y_out && !piece_map(&maps.y, y_out, total_rows, 2, f, PMN_OUT_BF16, 16, 2, 64)))
         return PMN_ERR_CUDA;
-    const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
-                    pmn_wait_limit_ns()};
     return launch<GATED, uint16_t>(maps, args, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -43,7 +43,7 @@ def strided(t):
 
 
 SEGMENTS = [  # rows, offsets
-    (1, [0, 1]), (7, [0, 0, 7, 7]), (33, [0, 32, 33]), (300, [3, 3, 40, 296]), (513, [0, 513]), (777, [0, 256, 257, 770]),
+    (1, [0, 1]), (7, [0, 0, 7, 7]), (16, [0, 1, 1, 10, 13, 15]), (17, [0, 17]), (33, [0, 32, 33]), (300, [3, 3, 40, 296]), (513, [0, 513]), (777, [0, 256, 257, 770]),
     (640, [0, 31, 62, 95, 129, 130, 130, 131, 400, 640]), (1100, [5, 1029, 1100]),
 ]
 
@@ -211,6 +211,31 @@ def test_many_experts_and_wide_rows(pmn):
     got = f64(pmn.grouped_gemm_bf16(a, b, gpu_offsets([0, 2, 4099]), pmn.GROUP_K))
     A, B = f64(a[2:4099]), f64(b[2:4099])
     assert (np.abs(got[1] - A.T @ B) <= 2 * 4097 * U * (np.abs(A).T @ np.abs(B))).all()
+
+
+@pytest.mark.parametrize("experts,k", [(1024, 264), (257, 1032), (3, 4104)])
+def test_few_rows_of_many_experts(pmn, experts, k):
+    """the kernel for a few rows: experts found among many, K that ends inside a warp's share, both outputs"""
+    gen = torch.Generator(device="cuda").manual_seed(experts)
+    counts = [0] * experts
+    for e, c in ((0, 2), (experts // 2, 9), (experts - 1, 3)):
+        counts[e] = c
+    offsets = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    a, w = bf16(gen, 14, k), bf16(gen, experts, 32, k, std=k ** -0.5)
+    off = gpu_offsets(offsets)
+    rows = f64(pmn.grouped_gemm_bf16(a, w, off, pmn.GROUP_M, out_dtype=torch.float32))
+    h, y = pmn.w1_gemm_swiglu_bf16(a, w, off, want_y=True)
+    for e in (0, experts // 2, experts - 1):
+        r = slice(offsets[e], offsets[e + 1])
+        A, W = f64(a[r]), f64(w[e])
+        want, err = A @ W.T, 2 * k * U * (np.abs(A) @ np.abs(W.T))
+        assert (np.abs(rows[r] - want) <= err).all()
+        assert (np.abs(f64(y)[r] - want) <= err + HALF["bf16"] * np.abs(want)).all()
+        g, u, eg, eu = want[:, :16], want[:, 16:], err[:, :16], err[:, 16:]
+        s = 1 / (1 + np.exp(-g))
+        tol = eu * np.abs(g * s) + eg * np.abs(u) * 1.1 + np.abs(g * s * u) * ((np.abs(g) + 8) * 2 ** -23 + 16 * U)  # |silu'| < 1.1
+        assert (np.abs(f64(h)[r] - g * s * u) <= tol * 1.01 + HALF["bf16"] * np.abs(g * s * u) + 1e-38).all()
+    assert pmn.get_device_error() == 0
 
 
 def test_captured_and_replayed_with_other_rows(pmn):
