@@ -449,44 +449,59 @@ __global__ void __launch_bounds__(THREADS, 1)
         // For 64 of K (s) the tensor core finds the four scale bytes of row 32 j + r in column
         // 4 s + j of lane r, in each of TMEM's four groups of 32 lanes: one group per warp, which
         // writes all rows' there.  The eight digits of a value share a scale.  (By way of shared memory,
-        // eight tcgen05.cp a stage, one token takes 22.5 us for 20.5.)
+        // eight tcgen05.cp a stage, one token takes 22.5 us for 20.5;
+        // a wait for every stage's store: 512 rows of 384 experts, k 1536, 164 to 182 us for 148.)
         const int quad = warp & 3;
         uint32_t slot = 0, sphase = 0;
         while (!dead && walk.next(p, s_cum, q)) {
             for (int k = q.k0; k < q.k1 && !dead; k += RAW_STEPS) {
                 if (!wait(bar_raw + 8 * slot, sphase)) break;
                 const uint8_t *raw = smem + RAW_OFF + slot * RAW_BYTES;
+                // two stages at a time: the store's completion is waited for once
 #pragma unroll
-                for (int c = 0; c < RAW_STEPS; ++c) {
+                for (int c = 0; c < RAW_STEPS; c += 2) {
                     if (k + c >= q.k1 || dead) break;
-                    uint32_t sa[16], sb[16];
+                    const bool two = k + c + 1 < q.k1;
+                    uint32_t sa[2][16], sb[2][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int row = 32 * j + lane;
-                        // (64-byte swizzle: eight lanes meet all banks)
-                        const uint4 va = *reinterpret_cast<const uint4 *>(raw + RAW_W * row + 16 * (c ^ ((row >> 1) & 3)));
-                        const uint4 vb = 32 * j < NB ? *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * (row >> 3) + 16 * c)
-                                                     : make_uint4(0u, 0u, 0u, 0u);
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            sa[4 * s + j] = u4_word(va, s);
-                            sb[4 * s + j] = u4_word(vb, s);
+                        for (int j = 0; j < 4; ++j) {
+                            const int row = 32 * j + lane, piece = c + h;
+                            // (64-byte swizzle: eight lanes meet all banks)
+                            const uint4 va = *reinterpret_cast<const uint4 *>(raw + RAW_W * row + 16 * (piece ^ ((row >> 1) & 3)));
+                            const uint4 vb = 32 * j < NB ? *reinterpret_cast<const uint4 *>(raw + RAW_A + RAW_W * (row >> 3) + 16 * piece)
+                                                         : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                sa[h][4 * s + j] = u4_word(va, s);
+                                sb[h][4 * s + j] = u4_word(vb, s);
+                            }
                         }
-                    }
-                    if (c == RAW_STEPS - 1 || k + c == q.k1 - 1) {  // the slot has been read
+                    if (c == RAW_STEPS - 2 || k + c + 2 >= q.k1) {  // the slot has been read
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
                     }
+                    const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + C::SF_COL0, first = stage;
                     if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
                     tc_fence_after();
-                    const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + C::SF_COL0 + stage * SF_COLS;
-                    tmem_st_32x32b_x16(to, sa);
-                    tmem_st_32x32b_x16(to + 16, sb);
+                    tmem_st_32x32b_x16(to + stage * SF_COLS, sa[0]);
+                    tmem_st_32x32b_x16(to + stage * SF_COLS + 16, sb[0]);
+                    next_stage();
+                    if (two) {
+                        if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
+                        tc_fence_after();
+                        tmem_st_32x32b_x16(to + stage * SF_COLS, sa[1]);
+                        tmem_st_32x32b_x16(to + stage * SF_COLS + 16, sb[1]);
+                    }
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_full + 8 * stage);
-                    next_stage();
+                    if (lane == 0) {
+                        mbar_arrive(bar_full + 8 * first);
+                        if (two) mbar_arrive(bar_full + 8 * stage);
+                    }
+                    if (two) next_stage();
                 }
                 if (++slot == RAW_SLOTS) {
                     slot = 0;
@@ -502,6 +517,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         while (walk.next(p, s_cum, q)) {  // to the end, also after a timeout: the four warps meet at barriers
             const int m = q.m;
             float y[CHUNK];
+            const float outer = __ldg(p.outer + q.e);
+            int exponent[CHUNK], odd = 0;  // bit t: row t holds a value that is not finite
+#pragma unroll
+            for (int t = 0; t < CHUNK; ++t) {
+                const int2 meta = t < m ? __ldcg(p.meta + q.r0 + t) : make_int2(0, 0);
+                exponent[t] = meta.x;
+                odd |= meta.y << t;
+            }
             if (wait(bar_acc_full + 8 * abuf, aphase)) {
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * NB;
@@ -559,14 +582,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int half_n = (int)(GATED ? p.n / 2 : p.n), c = GATED ? i & 63 : i, col = q.tile * half + c;
             const int64_t wrow = (int64_t)q.e * p.n + col + (GATED && i >= 64 ? half_n : 0);
             const bool on = col < half_n && !dead;
-            const float outer = __ldg(p.outer + q.e);
 #pragma unroll
             for (int t = 0; t < CHUNK; ++t) {
                 if (t >= m) break;
-                const int2 meta = __ldcg(p.meta + q.r0 + t);
-                const int e1 = max(meta.x, -126);
-                y[t] = __fmul_rn(__fmul_rn(__fmul_rn(y[t], outer), pow2(e1)), pow2(meta.x - e1));
-                if (meta.y && on) {
+                const int e1 = max(exponent[t], -126);
+                y[t] = __fmul_rn(__fmul_rn(__fmul_rn(y[t], outer), pow2(e1)), pow2(exponent[t] - e1));
+                if (((odd >> t) & 1) && on) {
                     const int64_t token = token_of(p, q.r0 + t);
                     y[t] = __fmul_rn(plain_dot(p, wrow, token), outer);
                 }
