@@ -224,3 +224,32 @@ def test_captured_and_replayed(pmn):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(captured, call())
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_a_call_that_runs_out_of_time_says_so(pmn, rows):
+    """with no time to wait a call either is right or latches the timeout, and the next one is right"""
+    rng = np.random.default_rng(10)
+    x, w = activations(rng, rows, 1024), cuda(*weights(rng, 2, 512, 1024))
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+    want = pmn.matvec_nvfp4(x, w, off)
+    assert pmn.get_device_error() == 0
+    limit = pmn.set_wait_limit_ns(0)
+    try:
+        for _ in range(3):
+            got = pmn.matvec_nvfp4(x, w, off)
+            error = pmn.get_device_error()
+            assert error == pmn.DEVERR_WAIT_TIMEOUT or (error == 0 and torch.equal(got, want))
+    finally:
+        pmn.set_wait_limit_ns(limit)
+    assert torch.equal(pmn.matvec_nvfp4(x, w, off), want) and pmn.get_device_error() == 0
+
+
+def test_the_same_bits_every_time(pmn):
+    """tiles that CTAs share are joined in the order of K, whoever comes last"""
+    rng = np.random.default_rng(11)
+    x, w = activations(rng, 9, 4096), cuda(*weights(rng, 3, 528, 4096))
+    off = torch.tensor([0, 1, 3, 9], dtype=torch.int32, device="cuda")
+    want = pmn.matvec_nvfp4(x, w, off, out_dtype=torch.float32)
+    for _ in range(20):
+        assert torch.equal(pmn.matvec_nvfp4(x, w, off, out_dtype=torch.float32), want)
