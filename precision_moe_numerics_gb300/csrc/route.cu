@@ -42,7 +42,7 @@ struct RouteArgs {
     int64_t ldl;
     const float *bias;
     int64_t tokens, chunk, rows;
-    int experts, k, score, normalize, pad;
+    int experts, k, half, score, normalize, pad;  // half: half the power of two that holds k
     float scale;
     int32_t *chosen;
     float *gates;
@@ -116,8 +116,8 @@ __device__ __noinline__ int choose_slowly(const uint32_t (&given)[NV], int k, in
 // none is left) and its gate.  Lane l holds experts l, l + 32, ..  The k-th largest of the lanes' own largest
 // keys bounds the token's k-th largest from below, so what is not less than it -- little more
 // than k keys -- holds the choice; those few are packed, one to a lane, in the experts' order,
-// and taken one by one.  Bound by the latency of these steps, each of which the whole warp takes part in:
-// hence two tokens at a time (16384 tokens of 384 experts: k rounds over all keys 27 us, this 21, two at a time 15).
+// and ordered by comparing them all.  (16384 tokens of 384 experts: k rounds over all keys 27 us, k rounds over the
+// few 18, this 17; bound by instructions, 530 of them a token.)
 template <int T, int NV, int KIND, bool EXACT>
 __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_t step, int lane, uint2 (*few)[32],
                                        int (&expert)[T], float (&gate)[T])
@@ -195,18 +195,27 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
 #pragma unroll
     for (int t = 0; t < T; ++t) mine[t] = lane < count[t] ? few[t][lane] : make_uint2(NONE, 0u);
     __syncwarp();
-    for (int i = 0; i < p.k; ++i) {
-        uint32_t m[T];
+    // a key's place among them: how many are larger, or equal and of a lower expert
+    int most = 0, place[T];
 #pragma unroll
-        for (int t = 0; t < T; ++t) m[t] = __reduce_max_sync(FULL, mine[t].x);
+    for (int t = 0; t < T; ++t) {
+        most = max(most, min(count[t], 32));
+        place[t] = 0;
+    }
+    for (int c = 0; c < most; ++c)
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int win = __ffs(__ballot_sync(FULL, mine[t].x == m[t])) - 1;
-            const int e = __shfl_sync(FULL, (int)mine[t].y, win);
-            if (lane == i && m[t] != NONE) expert[t] = e;
-            if (lane == win) mine[t].x = NONE;
+            const uint32_t other = __shfl_sync(FULL, mine[t].x, c);
+            place[t] += other > mine[t].x || (other == mine[t].x && c < lane);
         }
-    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (mine[t].x != NONE && place[t] < p.k) few[t][place[t]].y = mine[t].y;
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (lane < min(p.k, count[t])) expert[t] = (int)few[t][lane].y;
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < T; ++t)
         if (count[t] > 32) expert[t] = choose_slowly<NV>(key[t], p.k, lane);
@@ -226,7 +235,9 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
             float m = warp_max(v);
             if (m == -INFINITY) m = 0.0f;
             const float e = expert[t] >= 0 ? expf(v - m) : 0.0f;
-            g = e / warp_sum(e);
+            float sum = e;
+            for (int o = p.half; o; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(FULL, sum, o));  // of the first k lanes
+            g = e / sum;
         }
         gate[t] = expert[t] >= 0 ? __fmul_rn(p.scale, g) : 0.0f;
     }
@@ -808,7 +819,9 @@ extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits
         !aligned(chosen, 4) || !aligned(gates, 4) || !aligned(row_index, 4) || workspace_bytes < ws ||
         (ws > 0 && (!workspace || !aligned(workspace, 16))))
         return PMN_ERR_INVALID_ARG;
-    const RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, score, normalize, pad, scale,
+    int half = 0;
+    while ((half ? 2 * half : 1) < k) half = half ? 2 * half : 1;
+    const RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, half, score, normalize, pad, scale,
                       chosen, gates, row_index, row_choice, offsets, static_cast<uint16_t *>(workspace)};
     return logits_kind == PMN_OUT_F32 ? route_by_experts<PMN_OUT_F32>(a, s) : route_by_experts<PMN_OUT_BF16>(a, s);
 }
