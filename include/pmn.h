@@ -621,7 +621,8 @@ PMN_API int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int 
  *           segment, -2 for a row behind the last segment;
  *  offsets  int32 [experts + 1].
  *  workspace  device scratch, 16-byte aligned, of pmn_route_topk_workspace_bytes
- *           bytes (NULL where that is 0).
+ *           bytes (NULL where that is 0); its contents do not matter; calls that share one
+ *           must not overlap.
  * All other pointers are aligned to their element.  tokens <= 8384512, else
  * PMN_ERR_UNSUPPORTED; tokens == 0 writes offsets and row_choice.  One kernel on
  * `stream` for up to 64 tokens, two for more.
@@ -709,7 +710,10 @@ PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, in
  *           PMN_DEVERR_BAD_OFFSETS.  num_groups <= 1024.
  *  n, lda, ldb multiples of 8, and k (GROUP_M) or m (GROUP_K); ldb is read for GROUP_K alone.
  *  out_kind PMN_OUT_BF16 (nearest even) or PMN_OUT_F32.
- * One kernel on `stream`.
+ * One kernel on `stream`: tiles, or with b [num_groups, n, k] and m <= 16 one that reads the
+ * weights straight from memory.  The sums' order depends on that choice, the sizes, the
+ * segments and the GPU's SM count alone; the tiles' sums are truncated as the tensor
+ * cores do (GROUP_K: a relative error of about 1e-6 for hundreds of rows).
  */
 PMN_API pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,
                                          int num_groups, int group_mode, int b_transposed, int64_t m, int64_t n,
@@ -770,8 +774,10 @@ PMN_API int64_t pmn_matvec_nvfp4_workspace_bytes(int64_t total_rows, int64_t k);
  * row's), and then off by 2^-23 of that (2^-40 of the row's) at most.  Sums in float32.  A
  * row with a NaN or an infinity is multiplied value by value, slowly.
  * Right for any number of rows, and fast for few: an expert's weights are read once
- * per 16 of its rows.  Two kernels on `stream`; the sums' order depends on the sizes and
- * the segments alone.
+ * per 16 of its rows (per 8 where total_rows <= 8 num_experts).  Two kernels on
+ * `stream`; the sums' order depends on the sizes, the segments and the GPU's SM count
+ * alone.  Where the passes over the weights come to 2^31 pieces of 128 x 256 or more:
+ * PMN_ERR_UNSUPPORTED.
  */
 PMN_API pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t tokens, const uint8_t *codes,
                                     const uint8_t *scales, const float *outer, const int32_t *offsets, int num_experts,
