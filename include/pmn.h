@@ -625,7 +625,7 @@ PMN_API int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int 
  *           must not overlap.
  * All other pointers are aligned to their element.  tokens <= 8384512, else
  * PMN_ERR_UNSUPPORTED; tokens == 0 writes offsets and row_choice.  One kernel on
- * `stream` for up to 64 tokens, two for more.
+ * `stream` for up to 256 tokens, two for more.
  */
 PMN_API pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits_kind, const float *bias, int64_t tokens,
                                   int experts, int k, int score, int normalize, float scale, int pad, int64_t rows,

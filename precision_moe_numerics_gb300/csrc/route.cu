@@ -27,13 +27,10 @@ inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintpt
 // ====================================================================== router
 // Tokens are counted and laid out in chunks, one CTA each: at most MAX_CHUNKS, so that
 // every CTA of the second kernel can add up the counts of all of them by itself.
-constexpr int MAX_CHUNKS = 128, MIN_CHUNK = 64, SUB = 128;
+constexpr int MAX_CHUNKS = 152, MIN_CHUNK = 64, SUB = 128;
+constexpr int CLUSTER = 8, FEW_TOKENS = 32 * CLUSTER;  // so few are routed by one cluster, a token per warp
 
-inline int64_t chunk_tokens(int64_t tokens)
-{
-    const int64_t c = (tokens + MAX_CHUNKS - 1) / MAX_CHUNKS;
-    return std::max<int64_t>(MIN_CHUNK, (c + 31) / 32 * 32);
-}
+inline int64_t chunk_tokens(int64_t tokens) { return std::max<int64_t>(MIN_CHUNK, (tokens + MAX_CHUNKS - 1) / MAX_CHUNKS); }
 
 inline int64_t chunk_count(int64_t tokens) { return (tokens + chunk_tokens(tokens) - 1) / chunk_tokens(tokens); }
 
@@ -325,23 +322,17 @@ __device__ void mark_padding(const RouteArgs &p, const Layout &s)
         p.row_choice[r] = -2;
 }
 
-// One CTA per chunk, one warp per token.  ONE: a single chunk, laid out here as well.
-template <int NV, int KIND, bool EXACT, bool ONE>
-__global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(const RouteArgs p)
+// The tokens of a chunk chosen, T by a warp at a time, and counted.
+template <int T, int NV, int KIND, bool EXACT>
+__device__ __forceinline__ void choose_chunk(const RouteArgs &p, int64_t t0, int64_t t1, uint2 (*few)[32], int32_t *count)
 {
-    __shared__ Layout s;
-    constexpr int T = NV > 12 ? 1 : 2;
-    __shared__ uint2 few[NV > 16 ? 16 : 32][T][32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    int32_t *count = s.total;
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
     for (int64_t t = t0 + warp; t < t1; t += T * warps) {
         int expert[T];
         float gate[T];
-        choose<T, NV, KIND, EXACT>(p, t, warps, lane, few[warp], expert, gate);
+        choose<T, NV, KIND, EXACT>(p, t, warps, lane, few, expert, gate);
 #pragma unroll
         for (int i = 0; i < T; ++i)
             if (lane < p.k && t + i * warps < t1) {
@@ -350,20 +341,68 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(cons
                 if (expert[i] >= 0) atomicAdd(count + expert[i], 1);
             }
     }
+}
+
+// One CTA per chunk.
+template <int NV, int KIND, bool EXACT>
+__global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(const RouteArgs p)
+{
+    __shared__ int32_t count[MAX_EXPERTS];
+    constexpr int T = NV > 12 ? 1 : 2;
+    __shared__ uint2 few[NV > 16 ? 16 : 32][T][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+    choose_chunk<T, NV, KIND, EXACT>(p, t0, t1, few[threadIdx.x >> 5], count);
     __syncthreads();
-    if (!ONE) {
-        const int pitch = (p.experts + 1) / 2 * 2;
-        for (int e = threadIdx.x; e < pitch; e += blockDim.x)
-            p.counts[(int64_t)blockIdx.x * pitch + e] = e < p.experts ? (uint16_t)count[e] : (uint16_t)0;
-        return;
+    const int pitch = (p.experts + 1) / 2 * 2;
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+        p.counts[(int64_t)blockIdx.x * pitch + e] = e < p.experts ? (uint16_t)count[e] : (uint16_t)0;
+}
+
+// Few tokens: one cluster, whose CTAs read one another's counts.  (384 experts, 64 and 256 tokens, us back to
+// back: 6.0 and 7.9; one CTA 9.7 and the two kernels 11.1.  512 tokens: 11.4 either way.  256 threads a CTA
+// instead of 512: 6.5 and 7.9.)
+template <int NV, int KIND, bool EXACT>
+__global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_few_kernel(const RouteArgs p)
+{
+    __shared__ Layout s;
+    __shared__ int32_t count[MAX_EXPERTS];
+    __shared__ uint2 few[NV > 16 ? 16 : 32][1][32];
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+    choose_chunk<1, NV, KIND, EXACT>(p, t0, t1, few[threadIdx.x >> 5], count);
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t counts = (uint32_t)__cvta_generic_to_shared(count);
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
+        int n[CLUSTER], before = 0, all = 0;
+#pragma unroll
+        for (int c = 0; c < CLUSTER; ++c) {
+            n[c] = 0;
+            if (c < (int)gridDim.x)
+                asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
+                             : "=r"(n[c])
+                             : "r"(counts + 4 * e), "r"(c));
+        }
+#pragma unroll
+        for (int c = 0; c < CLUSTER; ++c) {
+            all += n[c];
+            if (c < (int)blockIdx.x) before += n[c];
+        }
+        s.total[e] = all;
+        s.base[e] = before;
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others
+    const int mine = (int)threadIdx.x < (int)(t1 - t0) * p.k ? p.chosen[t0 * p.k + threadIdx.x] : -1;
     scan_offsets(p, s);
     for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
-        p.offsets[e] = s.first[e];
-        if (e < p.experts) s.base[e] = s.first[e];
+        if (blockIdx.x == 0) p.offsets[e] = s.first[e];
+        if (e < p.experts) s.base[e] += s.first[e];
     }
-    place(p, s, t0, t1, (int)threadIdx.x < (t1 - t0) * p.k ? p.chosen[threadIdx.x] : -1);
+    place(p, s, t0, t1, mine);
     mark_padding(p, s);
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // and the others this one
 }
 
 __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs p, int chunks)
@@ -407,15 +446,30 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs p, in
 }
 
 template <int NV, int KIND, bool EXACT>
-pmn_status launch_route(const RouteArgs &p, cudaStream_t s)
+pmn_status launch_route(RouteArgs &p, cudaStream_t s)
 {
-    const int chunks = (int)chunk_count(p.tokens);
-    const int threads = std::min<int64_t>(NV > 16 ? 512 : 1024, std::max<int64_t>(128, 32 * p.tokens));
-    if (chunks == 1) {
-        route_choose_kernel<NV, KIND, EXACT, true><<<1, threads, 0, s>>>(p);
-        return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    const int most = NV > 16 ? 512 : 1024;
+    if (p.tokens <= FEW_TOKENS) {
+        unsigned ctas = 1;
+        while (ctas < CLUSTER && 2 * (int64_t)ctas < p.tokens) ctas *= 2;
+        p.chunk = (p.tokens + ctas - 1) / ctas;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3((unsigned)std::min<int64_t>(most, std::max<int64_t>(512, 32 * p.chunk)));
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = ctas;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, route_few_kernel<NV, KIND, EXACT>, p) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
     }
-    route_choose_kernel<NV, KIND, EXACT, false><<<chunks, threads, 0, s>>>(p);
+    const int chunks = (int)chunk_count(p.tokens);
+    // as many warps as share the chunk's tokens evenly (65536 tokens of 384 experts 67 -> 61 us by this and one CTA per SM)
+    const int64_t side = NV > 12 ? 1 : 2, most_warps = most / 32, passes = (p.chunk + side * most_warps - 1) / (side * most_warps);
+    const int threads = 32 * (int)((p.chunk + side * passes - 1) / (side * passes));
+    route_choose_kernel<NV, KIND, EXACT><<<chunks, threads, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)chunks);
@@ -430,7 +484,7 @@ pmn_status launch_route(const RouteArgs &p, cudaStream_t s)
 }
 
 template <int KIND>
-pmn_status route_by_experts(const RouteArgs &p, cudaStream_t s)
+pmn_status route_by_experts(RouteArgs &p, cudaStream_t s)
 {
     // a count of experts that fills the lanes needs no checks
     if (p.experts == 128) return launch_route<4, KIND, true>(p, s);
@@ -795,7 +849,7 @@ extern "C" int64_t pmn_route_rows(int64_t tokens, int experts, int k, int pad)
 extern "C" int64_t pmn_route_topk_workspace_bytes(int64_t tokens, int experts, int k)
 {
     if (pmn_route_rows(tokens, experts, k, 1) < 0) return -1;
-    return tokens == 0 || chunk_count(tokens) == 1 ? 0 : (chunk_count(tokens) * ((experts + 1) / 2 * 4) + 15) / 16 * 16;
+    return tokens <= FEW_TOKENS ? 0 : (chunk_count(tokens) * ((experts + 1) / 2 * 4) + 15) / 16 * 16;
 }
 
 extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits_kind, const float *bias, int64_t tokens,
@@ -808,7 +862,7 @@ extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits
         (score != PMN_SCORE_SOFTMAX && score != PMN_SCORE_SIGMOID) || (normalize != 0 && normalize != 1))
         return PMN_ERR_INVALID_ARG;
     if (!offsets || (rows > 0 && !row_choice) || !aligned(offsets, 4) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
-    if (tokens > (int64_t)MAX_CHUNKS * 65504) return PMN_ERR_UNSUPPORTED;  // a chunk's counts are 16 bits wide
+    if (tokens > 8384512) return PMN_ERR_UNSUPPORTED;  // a chunk's counts are 16 bits wide
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (tokens == 0) {
         route_empty_kernel<<<64, 256, 0, s>>>(offsets, experts, row_choice, rows);
@@ -821,7 +875,7 @@ extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits
         return PMN_ERR_INVALID_ARG;
     int half = 0;
     while ((half ? 2 * half : 1) < k) half = half ? 2 * half : 1;
-    const RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, half, score, normalize, pad, scale,
+    RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, half, score, normalize, pad, scale,
                       chosen, gates, row_index, row_choice, offsets, static_cast<uint16_t *>(workspace)};
     return logits_kind == PMN_OUT_F32 ? route_by_experts<PMN_OUT_F32>(a, s) : route_by_experts<PMN_OUT_BF16>(a, s);
 }

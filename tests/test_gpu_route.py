@@ -56,6 +56,9 @@ ROUTES = [  # tokens, experts, k, pad, kind
     (1, 1, 1, 1, "f32"), (1, 384, 8, 1, "f32"), (3, 2, 2, 128, "bf16"), (64, 384, 8, 1, "f32"), (65, 60, 4, 32, "bf16"),
     (129, 33, 32, 7, "f32"), (200, 100, 5, 1, "f32"), (777, 200, 6, 8, "bf16"), (300, 500, 3, 16, "f32"), (131, 1024, 32, 3, "f32"),
     (4097, 1000, 8, 128, "bf16"), (8193, 384, 8, 128, "f32"), (20011, 24, 2, 512, "f32"),
+    (2, 128, 8, 1, "bf16"), (5, 700, 32, 4, "f32"), (9, 256, 8, 1, "bf16"), (17, 60, 4, 8, "f32"), (31, 384, 6, 1, "bf16"),
+    (255, 1024, 32, 2, "bf16"), (256, 384, 8, 128, "f32"), (257, 384, 8, 1, "bf16"), (512, 16, 16, 1, "f32"),
+    (19457, 128, 8, 1, "bf16"),
 ]
 
 

@@ -111,7 +111,7 @@ def test_route_checks_its_arguments(L):
         return L.pmn_route_rows(tokens, experts, k, pad)
 
     assert rows() == 128 and rows(pad=32) == 128 + 8 * 31 // 32 * 32 and rows(tokens=1, pad=32) == 64 and rows(tokens=0) == 0
-    assert L.pmn_route_topk_workspace_bytes(64, 384, 8) == 0 and L.pmn_route_topk_workspace_bytes(65, 384, 8) > 0
+    assert L.pmn_route_topk_workspace_bytes(256, 384, 8) == 0 and L.pmn_route_topk_workspace_bytes(257, 384, 8) > 0
     for bad in (dict(tokens=-1), dict(experts=0), dict(experts=1025), dict(k=0), dict(k=9), dict(experts=64, k=33), dict(pad=0)):
         assert rows(**bad) == -1
 
