@@ -116,12 +116,12 @@ def test_route_checks_its_arguments(L):
         assert rows(**bad) == -1
 
     def call(**k):
-        a = dict(logits=P, ldl=8, kind=1, bias=P, tokens=65, experts=8, k=2, score=0, normalize=1, scale=1.0, pad=1, rows=130, chosen=P,
+        a = dict(logits=P, ldl=8, kind=1, bias=P, tokens=257, experts=8, k=2, score=0, normalize=1, scale=1.0, pad=1, rows=514, chosen=P,
                  gates=P, row_index=P, row_choice=P, offsets=P, ws=P, bytes=1 << 20)
         a.update(k)
         return L.pmn_route_topk(*a.values(), None)
 
-    for bad in (dict(ldl=7), dict(kind=2), dict(score=2), dict(normalize=2), dict(rows=129), dict(rows=1 << 31), dict(k=9), dict(pad=0),
+    for bad in (dict(ldl=7), dict(kind=2), dict(score=2), dict(normalize=2), dict(rows=513), dict(rows=1 << 31), dict(k=9), dict(pad=0),
                 dict(logits=0), dict(logits=P + 2), dict(bias=P + 1), dict(chosen=0), dict(gates=0), dict(row_index=0), dict(row_choice=0),
                 dict(offsets=0), dict(offsets=P + 2), dict(ws=0), dict(ws=P + 8), dict(bytes=15)):
         assert call(**bad) == pmn.ERR_INVALID_ARG, bad
