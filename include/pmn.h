@@ -589,6 +589,8 @@ PMN_API pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_tenso
  * From a router's logits to rows in expert order and back: what the grouped
  * calls above expect of their caller (rows by expert, offsets, the tokens' row
  * numbers and gates), made on the device.  The pages have no counterpart.
+ * In these calls and the products below no output may overlap an input or another
+ * output; the address of an input is refused.
  */
 
 /* Rows that hold every choice whatever the experts' counts are, each expert's

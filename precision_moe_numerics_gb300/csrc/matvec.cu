@@ -755,6 +755,7 @@ extern "C" pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t token
         return PMN_ERR_INVALID_ARG;
     // steps are counted in 32 bits
     if ((total_rows / 8 + num_experts) * (n / 64 + 1) * (k / KSTEP) >= LIMIT) return PMN_ERR_UNSUPPORTED;
+    if (out == x || out == workspace) return PMN_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int64_t half_n = swiglu ? n / 2 : n, half = swiglu ? BM / 2 : BM;
     const Args a{static_cast<const uint16_t *>(x), ldx, tokens, codes, scales, outer, offsets, num_experts, total_rows, n, k,

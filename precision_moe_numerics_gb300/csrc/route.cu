@@ -889,7 +889,7 @@ extern "C" pmn_status pmn_route_topk_backward(const void *logits, int64_t ldl, i
         return PMN_ERR_INVALID_ARG;
     if (tokens == 0) return PMN_OK;
     if (!logits || !chosen || !dgates || !dlogits || !aligned(logits, kind_bytes(logits_kind)) ||
-        !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4))
+        !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4) || dlogits == logits)
         return PMN_ERR_INVALID_ARG;
     const RouteGradArgs a{logits, ldl, chosen, dgates, tokens, experts, k, score, normalize, scale, dlogits, aligned(dlogits, 16)};
     const unsigned blocks = (unsigned)((tokens + 7) / 8);
@@ -906,7 +906,7 @@ extern "C" pmn_status pmn_dispatch_rows(const void *x, int64_t ldx, int kind, in
     if (!good_rows(tokens, cols, kind, k, rows) || ldx < cols || ldx * kind_bytes(kind) % 16 != 0) return PMN_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return PMN_OK;
     if (!out || !aligned(out, 16) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
-    if (tokens > 0 && (!x || !row_index || !aligned(x, 16) || !aligned(row_index, 4))) return PMN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || !row_index || !aligned(x, 16) || !aligned(row_index, 4) || out == x)) return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const Split by = Split::of(tokens, vecs);
     const int64_t token_blocks = by.blocks(tokens);
@@ -926,7 +926,7 @@ extern "C" pmn_status pmn_combine_rows(const void *z, int kind, int64_t rows, in
         return PMN_ERR_INVALID_ARG;
     if (tokens == 0 || cols == 0) return PMN_OK;
     if ((rows > 0 && !z) || !row_index || !out || !aligned(z, 16) || !aligned(out, 16) || !aligned(row_index, 4) ||
-        !aligned(gates, 4))
+        !aligned(gates, 4) || out == z)
         return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const Split by = Split::of(tokens, vecs);
@@ -952,7 +952,8 @@ extern "C" pmn_status pmn_combine_rows_backward(const void *dout, const void *z,
     if (tokens > 0 && (!dout || !row_index || !dgates || !aligned(dout, 16) || !aligned(row_index, 4) || !aligned(dgates, 4)))
         return PMN_ERR_INVALID_ARG;
     if (rows > 0 && (!z || !dz || !aligned(z, 16) || !aligned(dz, 16))) return PMN_ERR_INVALID_ARG;
-    if (!aligned(row_choice, 4) || !aligned(gates, 4)) return PMN_ERR_INVALID_ARG;
+    if (!aligned(row_choice, 4) || !aligned(gates, 4) || (dz && (dz == z || dz == dout)) || (dgates && dgates == gates))
+        return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const int64_t blocks = tokens + (row_choice ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0);
     if (!good_grid(blocks)) return PMN_ERR_UNSUPPORTED;

@@ -103,7 +103,7 @@ def L():
     return pmn.lib()
 
 
-P = 1 << 20  # an aligned address that nothing reads: every call below is refused
+P, Q, W = 1 << 20, 2 << 20, 3 << 20  # aligned addresses that nothing reads: every call below is refused
 
 
 def test_route_checks_its_arguments(L):
@@ -128,29 +128,29 @@ def test_route_checks_its_arguments(L):
     assert call(tokens=128 * 65504 + 1, rows=(1 << 31) - 1) == pmn.ERR_UNSUPPORTED
 
     def backward(**k):
-        a = dict(logits=P, ldl=8, kind=1, chosen=P, dgates=P, tokens=65, experts=8, k=2, score=0, normalize=1, scale=1.0, dlogits=P)
+        a = dict(logits=P, ldl=8, kind=1, chosen=P, dgates=P, tokens=65, experts=8, k=2, score=0, normalize=1, scale=1.0, dlogits=Q)
         a.update(k)
         return L.pmn_route_topk_backward(*a.values(), None)
 
     for bad in (dict(ldl=7), dict(kind=3), dict(score=-1), dict(normalize=-1), dict(k=9), dict(logits=0), dict(chosen=P + 1), dict(dgates=0),
-                dict(dlogits=0)):
+                dict(dlogits=0), dict(dlogits=P)):
         assert backward(**bad) == pmn.ERR_INVALID_ARG, bad
     assert backward(tokens=0, logits=0) == pmn.OK
 
 
 def test_row_calls_check_their_arguments(L):
     def dispatch(**k):
-        a = dict(x=P, ldx=64, kind=0, tokens=4, cols=64, index=P, k=2, choice=P, rows=8, out=P)
+        a = dict(x=P, ldx=64, kind=0, tokens=4, cols=64, index=P, k=2, choice=P, rows=8, out=Q)
         a.update(k)
         return L.pmn_dispatch_rows(*a.values(), None)
 
     def combine(**k):
-        a = dict(z=P, kind=0, rows=8, cols=64, index=P, gates=P, tokens=4, k=2, out_kind=0, out=P)
+        a = dict(z=P, kind=0, rows=8, cols=64, index=P, gates=P, tokens=4, k=2, out_kind=0, out=Q)
         a.update(k)
         return L.pmn_combine_rows(*a.values(), None)
 
     def backward(**k):
-        a = dict(dout=P, z=P, kind=0, rows=8, cols=64, index=P, choice=P, gates=P, tokens=4, k=2, dz=P, dgates=P)
+        a = dict(dout=P, z=P, kind=0, rows=8, cols=64, index=P, choice=P, gates=P, tokens=4, k=2, dz=Q, dgates=Q)
         a.update(k)
         return L.pmn_combine_rows_backward(*a.values(), None)
 
@@ -159,19 +159,20 @@ def test_row_calls_check_their_arguments(L):
                 [{n: 0} for n in names] + [{n: P + 2} for n in names]:
             assert call(**bad) == pmn.ERR_INVALID_ARG, (call, bad)
     assert dispatch(ldx=63) == dispatch(ldx=60) == dispatch(ldx=68) == pmn.ERR_INVALID_ARG
+    assert dispatch(out=P) == combine(out=P) == backward(dz=P) == backward(dgates=P) == backward(dout=W, z=W, dz=W) == pmn.ERR_INVALID_ARG
     assert combine(out_kind=3) == combine(kind=1, cols=4, out_kind=0) == combine(gates=P + 2) == pmn.ERR_INVALID_ARG
     assert dispatch(rows=0) == combine(tokens=0) == backward(tokens=0, choice=0) == pmn.OK
 
 
 def test_products_check_their_arguments(L):
     def gemm(**k):
-        a = dict(a=P, lda=64, b=P, ldb=0, offsets=P, groups=2, mode=0, bt=0, m=8, n=32, k=64, kind=0, out=P)
+        a = dict(a=P, lda=64, b=P, ldb=0, offsets=P, groups=2, mode=0, bt=0, m=8, n=32, k=64, kind=0, out=Q)
         a.update(k)
         return L.pmn_grouped_gemm_bf16(*a.values(), None)
 
     for bad in (dict(lda=56), dict(lda=68), dict(groups=0), dict(groups=1025), dict(mode=2), dict(bt=2), dict(m=-1), dict(m=1 << 31),
                 dict(n=0), dict(n=36), dict(k=0), dict(k=60), dict(kind=2), dict(a=0), dict(b=0), dict(out=0), dict(offsets=0),
-                dict(a=P + 8), dict(b=P + 2), dict(out=P + 4), dict(offsets=P + 2),
+                dict(a=P + 8), dict(b=P + 2), dict(out=P + 4), dict(offsets=P + 2), dict(out=P), dict(a=W, out=W),
                 dict(mode=1, ldb=24), dict(mode=1, ldb=36), dict(mode=1, ldb=32, m=12), dict(mode=1, ldb=32, bt=1), dict(mode=1, ldb=32, m=0),
                 dict(mode=1, ldb=32, lda=0, m=8)):
         assert gemm(**bad) == pmn.ERR_INVALID_ARG, bad
@@ -179,25 +180,25 @@ def test_products_check_their_arguments(L):
     assert gemm(n=(1 << 30) - 512, m=1 << 20) == pmn.ERR_UNSUPPORTED
 
     def gated(**k):
-        a = dict(a=P, lda=64, b=P, offsets=P, experts=2, rows=8, f=32, k=64, out=P, y=P)
+        a = dict(a=P, lda=64, b=P, offsets=P, experts=2, rows=8, f=32, k=64, out=Q, y=W)
         a.update(k)
         return L.pmn_w1_gemm_swiglu_bf16(*a.values(), None)
 
     def gated_backward(**k):
-        a = dict(a=P, lda=64, b=P, y=P, offsets=P, experts=2, rows=8, f=32, k=64, out=P)
+        a = dict(a=P, lda=64, b=P, y=P, offsets=P, experts=2, rows=8, f=32, k=64, out=Q)
         a.update(k)
         return L.pmn_dh_gemm_swiglu_backward_bf16(*a.values(), None)
 
     for call in (gated, gated_backward):
         for bad in (dict(lda=56), dict(experts=0), dict(rows=-1), dict(f=0), dict(f=20), dict(k=60), dict(k=0), dict(a=0), dict(b=P + 4),
-                    dict(offsets=0), dict(out=0), dict(out=P + 8), dict(y=P + 8)):
+                    dict(offsets=0), dict(out=0), dict(out=P + 8), dict(y=P + 8), dict(out=P), dict(y=Q), dict(a=W + 16, out=W + 16)):
             assert call(**bad) == pmn.ERR_INVALID_ARG, (call, bad)
         assert call(rows=0, a=0) == pmn.OK
     assert gated(f=24) == pmn.ERR_INVALID_ARG and gated_backward(y=0) == pmn.ERR_INVALID_ARG
 
     def matvec(**k):
         a = dict(x=P, ldx=256, tokens=2, codes=P, scales=P, outer=P, offsets=P, experts=2, rows=4, n=32, k=256, choice=P, choices=2,
-                 swiglu=0, kind=0, out=P, ws=P, bytes=1 << 30)
+                 swiglu=0, kind=0, out=Q, ws=W, bytes=1 << 30)
         a.update(k)
         return L.pmn_matvec_nvfp4(*a.values(), None)
 
@@ -206,7 +207,7 @@ def test_products_check_their_arguments(L):
     for bad in (dict(ldx=248), dict(ldx=260), dict(tokens=-1), dict(experts=0), dict(experts=1025), dict(rows=-1), dict(rows=1 << 28),
                 dict(n=24), dict(n=0), dict(k=128), dict(k=0), dict(choices=0), dict(swiglu=2), dict(kind=2), dict(choice=0), dict(x=0),
                 dict(codes=0), dict(scales=P + 8), dict(outer=P + 2), dict(offsets=P + 1), dict(choice=P + 2), dict(out=0), dict(ws=0),
-                dict(ws=P + 4), dict(bytes=need - 1), dict(n=1 << 30, experts=2)):
+                dict(ws=P + 4), dict(bytes=need - 1), dict(n=1 << 30, experts=2), dict(out=P), dict(out=W)):
         assert matvec(**bad) == pmn.ERR_INVALID_ARG, bad
     assert matvec(rows=0) == pmn.OK
     assert matvec(rows=1 << 20, n=1 << 20, k=1 << 16, ldx=1 << 16, bytes=1 << 60) == pmn.ERR_UNSUPPORTED
