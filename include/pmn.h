@@ -728,7 +728,8 @@ PMN_API pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void 
  *  a [total_rows, lda] of k columns;  b [num_experts, 2 f, k];  out [total_rows, f];
  *  y_out    NULL, or bf16 [total_rows, 2 f]: y rounded to nearest even.
  *  f        multiple of 16;  k and lda of 8;  offsets and the rest as above (GROUP_M).
- * The sigmoid has a relative error of (|gate| + 8) 2^-23 at most.
+ * The sigmoid has a relative error of (|gate| + 8) 2^-23 at most, where it is below
+ * float32's normal range one of 2^-148.
  */
 PMN_API pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const void *b, const int32_t *offsets,
                                            int num_experts, int64_t total_rows, int64_t f, int64_t k, void *out,

@@ -226,8 +226,6 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t el, uint32_t d_tmem, uint
         : "memory");
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
-
 __device__ __forceinline__ void store_one(uint16_t *p, float v)
 {
     const __nv_bfloat16 b = __float2bfloat16_rn(v);

@@ -610,8 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int t = 0; t < CHUNK; ++t) {
                         if (t >= m) break;
-                        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-y[t])));
-                        if (on) store_one(o + (int64_t)t * half_n, __fmul_rn(__fmul_rn(y[t], s), xch[t]));
+                        if (on) store_one(o + (int64_t)t * half_n, __fmul_rn(__fmul_rn(y[t], sigmoid(y[t])), xch[t]));
                     }
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");

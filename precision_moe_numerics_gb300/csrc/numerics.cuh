@@ -26,6 +26,14 @@ __device__ __forceinline__ float silu_mul(float a, float b)
     return __fmul_rn(__fdividef(a, __fadd_rn(1.0f, __expf(-a))), b);
 }
 
+// 1 / (1 + e^-g) for every g: the quotient's divisor is in [1, 2], so that a far
+// negative g, where e^-g leaves float32's range, keeps e^g (to 2^-149 below the normal range).
+__device__ __forceinline__ float sigmoid(float g)
+{
+    const float t = __expf(-fabsf(g)), r = __fdividef(1.0f, __fadd_rn(1.0f, t));
+    return g < 0.0f ? __fmul_rn(t, r) : r;
+}
+
 // ---------------------------------------------------------------- decoders
 // E2M1 magnitude code m (0..7): e = m >> 1, mantissa bit m & 1; e == 0 is the
 // subnormal 0 / 0.5, otherwise (1 + mant/2) * 2^(e-1).  Built as float bits.

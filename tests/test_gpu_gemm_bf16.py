@@ -138,6 +138,39 @@ def test_gated_projection_and_its_backward(pmn, rows, offsets, f, k):
     assert pmn.get_device_error() == 0
 
 
+@pytest.mark.parametrize("rows", [13, 50])
+def test_gates_far_from_zero(pmn, rows):
+    """gate, up and dH given as they are by one-hot products.  The sigmoid's 2^-148 below the normal range reaches h times
+    gate and up, which may be large; a product of two that is itself subnormal adds 2^-149 times the third."""
+    f, k = 16, 8
+    g = torch.linspace(-103, 103, rows).bfloat16()
+    x = torch.zeros((rows, k))
+    x[:, 0], x[:, 1] = g.float(), torch.tensor([3e30, -1.5, 2e20, 1e-3, 0.0]).repeat(rows)[:rows]
+    w = torch.zeros((1, 2 * f, k))
+    w[0, :f, 0], w[0, f:, 1] = 1.0, 1.0
+    x, w, off = x.bfloat16().cuda(), w.bfloat16().cuda(), gpu_offsets([0, rows])
+    h, y = pmn.w1_gemm_swiglu_bf16(x, w, off, want_y=True)
+    assert torch.equal(y[:, :f], x[:, :1].expand(-1, f)) and torch.equal(y[:, f:], x[:, 1:2].expand(-1, f))
+    X = f64(x)
+    G, V = X[:, :1], X[:, 1:2]
+    s = 1 / (1 + np.exp(-G))
+    tiny, rel = 2.0 ** -148, (np.abs(G) + 8) * 2 ** -23 + 16 * U + HALF["bf16"]
+    want = G * s * V
+    assert (np.abs(f64(h) - want) <= np.abs(want) * rel + tiny * (np.abs(G) + 1) * np.abs(V) + 2.0 ** -133).all()
+    d = torch.zeros((rows, k))
+    d[:, 0] = torch.tensor([1e25, -2.0, 1e-2]).repeat(rows)[:rows]
+    w2 = torch.zeros((1, k, f))
+    w2[0, 0] = 1.0
+    d, v = d.bfloat16().cuda(), y.clone()
+    v[:, f:] = torch.tensor([-4.0, 1e10, 0.5, 1.0]).repeat(rows)[:rows].bfloat16().cuda()[:, None]
+    got, D, V = f64(pmn.dh_gemm_swiglu_backward_bf16(d, w2.bfloat16().cuda(), v, off)), f64(d)[:, :1], f64(v)[:, f:f + 1]
+    up, gate = D * G * s, D * V * s * (1 + G * (1 - s))
+    mag = np.abs(D * V * s) * (1 + np.abs(G))  # 1 + g (1 - s) cancels near its zero
+    assert (np.abs(got[:, f:] - up) <= np.abs(up) * rel + tiny * (np.abs(D) + 1) * (np.abs(G) + 1) + 2.0 ** -133).all()
+    assert (np.abs(got[:, :f] - gate) <= np.abs(gate) * rel + mag * (np.abs(G) + 16) * 2 ** -22
+            + tiny * (np.abs(D) + 1) * (np.abs(V) + 1) * (1 + np.abs(G)) + 2.0 ** -133).all()
+
+
 def test_gated_gradient_against_differences(pmn):
     """dY1 against central differences of sum(dz . (h W2^T)) in 64 bits"""
     gen = torch.Generator(device="cuda").manual_seed(5)
