@@ -715,7 +715,7 @@ PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, in
  * One kernel on `stream`: tiles, or with b [num_groups, n, k] and m <= 16 one that reads the
  * weights straight from memory.  The sums' order depends on that choice, the sizes, the
  * segments and the GPU's SM count alone; the tiles' sums are truncated as the tensor
- * cores do (GROUP_K: a relative error of about 1e-6 for hundreds of rows).
+ * cores do, with PMN_OUT_F32 over 512 of K at most, whose sums are added in float32.
  */
 PMN_API pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,
                                          int num_groups, int group_mode, int b_transposed, int64_t m, int64_t n,
