@@ -9,6 +9,11 @@
 // divided evenly and waste less than 32 of them where a tile with rows on the M side wastes up to
 // 255.  An accumulator column is then a row of the output, 32 lanes of a warp write 32
 // neighbours of it, and the rows behind a segment are simply not stored.
+// What bounds it, f 1536, k 4096: shared memory.  A 64-deep stage of 256 rows takes 605 clocks where
+// its MMAs take 512; forward of 8192 rows of 24 experts 170 us (tensor pipe active 58 %, DRAM 57 %), loads and products
+// alone 158, products alone 121; one expert's 16384 rows with k = n = 4096 at 1.74 PFLOP/s, the backward
+// of 16384 rows 138 us.  Weight gradients write: 1.2 GB of float32 in 254 us where no expert has more
+// than 512 rows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

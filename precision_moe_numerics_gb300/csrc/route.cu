@@ -4,6 +4,9 @@
 //   pmn_dispatch_rows          token rows -> routed rows
 //   pmn_combine_rows           the weighted sum of each token's routed rows
 //   pmn_combine_rows_backward  its gradients
+// The router is bound by instruction issue (choosing, 16384 tokens of 384 experts 16 us) and latency (placing
+// 15, half of it behind the choosing; up to 256 tokens 6 to 8 in all), the rows by HBM (16384 x 4096 bf16,
+// top-8: 215 us out, 6.2 TB/s, and 190 us back).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
