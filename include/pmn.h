@@ -712,7 +712,7 @@ PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, in
  *           PMN_DEVERR_BAD_OFFSETS.  num_groups <= 1024.
  *  n, lda, ldb multiples of 8, and k (GROUP_M) or m (GROUP_K); ldb is read for GROUP_K alone.
  *  out_kind PMN_OUT_BF16 (nearest even) or PMN_OUT_F32.
- * One kernel on `stream`: tiles, or with b [num_groups, n, k] and m <= 16 one that reads the
+ * One kernel on `stream`: tiles, or with b [num_groups, n, k] and m <= 32 one that reads the
  * weights straight from memory.  The sums' order depends on that choice, the sizes, the
  * segments and the GPU's SM count alone; the tiles' sums are truncated as the tensor
  * cores do, with PMN_OUT_F32 over 512 of K at most, whose sums are added in float32.

@@ -717,11 +717,11 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
 // ---------------------------------------------------------------- few rows
 // The forward calls for a handful of rows (single tokens of a serving loop): their time is that of
 // reading the weights, which 256-column tiles would spread over few SMs.  A CTA takes
-// 16 weight rows (gated: 8 gate rows and the 8 up rows of the same columns) for up to eight
+// 16 weight rows (gated: 8 gate rows and the 8 up rows of the same columns) for up to 8 NC
 // rows of one expert; its warps share K, each lane loads 16 bytes of a weight row at a time, which are
 // the tensor core's operands as they are (mma.sync; what it sees as its K is the lanes'
 // order, the same for weights and rows).  The warps' sums meet in shared memory.
-constexpr int FEW_THREADS = 256, FEW_UNROLL = 4;
+constexpr int FEW_THREADS = 256;
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1)
@@ -731,14 +731,14 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// grid: blocks of 16 weight rows x chunks of eight rows of an expert (as many as there can be)
-template <bool GATED, typename OUT>
+// grid: blocks of 16 weight rows x chunks of 8 NC rows of an expert (as many as there can be)
+template <bool GATED, typename OUT, int NC>
 __global__ void __launch_bounds__(FEW_THREADS, 3)
     few_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, const Args p)
 {
-    constexpr int WARPS = FEW_THREADS / 32;
+    constexpr int WARPS = FEW_THREADS / 32, CHUNK = 8 * NC, FEW_UNROLL = NC > 1 ? 2 : 4;
     __shared__ int s_sum[WARPS], s_found[3];
-    __shared__ float s_part[WARPS][16][9];
+    __shared__ float s_part[WARPS][16][CHUNK + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, unit = blockIdx.y;
     // the expert whose chunk this is
     if (threadIdx.x == 0) s_found[0] = -1;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
             hi = __ldg(p.offsets + g + 1);
             bad = bad || lo < 0 || hi < lo || hi > p.rows;
         }
-        const int n = (hi - lo + 7) / 8;
+        const int n = (hi - lo + CHUNK - 1) / CHUNK;
         int run = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
         }
         if (unit >= before + run - n && unit < before + run) {
             s_found[0] = g;
-            s_found[1] = lo + 8 * (unit - (before + run - n));
+            s_found[1] = lo + CHUNK * (unit - (before + run - n));
             s_found[2] = hi;
         }
         base = all;
@@ -779,67 +779,84 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
         if (threadIdx.x == 0 && blockIdx.x == 0 && unit == 0) latch_error(PMN_DEVERR_BAD_OFFSETS);
         return;
     }
-    const int g = s_found[0], r0 = s_found[1], m = min(8, s_found[2] - r0);
+    const int g = s_found[0], r0 = s_found[1], m = min(CHUNK, s_found[2] - r0);
     if (g < 0) return;
 
     const int r = lane >> 2, q = lane & 3;
     const int64_t col = (GATED ? 8 : 16) * (int64_t)blockIdx.x + r, cols = p.n;  // p.n: of the output
     const uint16_t *w0 = w + ((int64_t)g * (GATED ? 2 * cols : cols) + min(col, cols - 1)) * p.k;
     const uint16_t *w1 = w + ((int64_t)g * (GATED ? 2 * cols : cols) + (GATED ? cols + min(col, cols - 1) : min(col + 8, cols - 1))) * p.k;
-    const uint16_t *xr = x + (r0 + min(r, m - 1)) * ldx;
+    const uint16_t *xr[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) xr[j] = x + (r0 + min(8 * j + r, m - 1)) * ldx;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float acc[4] = {};
+    float acc[NC][4] = {};
     // (the same passes for all lanes of a warp, which multiply together)
     for (int64_t kw = 32 * FEW_UNROLL * warp; kw < p.k; kw += 32 * FEW_UNROLL * WARPS) {
-        uint4 a[FEW_UNROLL], b[FEW_UNROLL], c[FEW_UNROLL];
+        uint4 a[FEW_UNROLL], b[FEW_UNROLL], c[FEW_UNROLL][NC];
 #pragma unroll
         for (int i = 0; i < FEW_UNROLL; ++i) {
             const int64_t k = kw + 32 * i + 8 * q;
             const bool on = k < p.k;
             a[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
             b[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
-            c[i] = on && r < m ? __ldg(reinterpret_cast<const uint4 *>(xr + k)) : zero;
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                c[i][j] = on && 8 * j + r < m ? __ldg(reinterpret_cast<const uint4 *>(xr[j] + k)) : zero;
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < FEW_UNROLL; ++i) {
-            mma_m16n8k16(acc, a[i].x, b[i].x, a[i].y, b[i].y, c[i].x, c[i].y);
-            mma_m16n8k16(acc, a[i].z, b[i].z, a[i].w, b[i].w, c[i].z, c[i].w);
-        }
-    }
-    s_part[warp][r][2 * q] = acc[0];
-    s_part[warp][r][2 * q + 1] = acc[1];
-    s_part[warp][r + 8][2 * q] = acc[2];
-    s_part[warp][r + 8][2 * q + 1] = acc[3];
-    __syncthreads();
-    if (threadIdx.x >= (GATED ? 64 : 128)) return;
-    const int c = threadIdx.x & (GATED ? 7 : 15), n = threadIdx.x / (GATED ? 8 : 16);
-    const int64_t oc = (GATED ? 8 : 16) * (int64_t)blockIdx.x + c;
-    if (n >= m || oc >= cols) return;
-    float s = 0.0f, u = 0.0f;
+        for (int i = 0; i < FEW_UNROLL; ++i)
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        s = __fadd_rn(s, s_part[i][c][n]);
-        if (GATED) u = __fadd_rn(u, s_part[i][c + 8][n]);
+            for (int j = 0; j < NC; ++j) {
+                mma_m16n8k16(acc[j], a[i].x, b[i].x, a[i].y, b[i].y, c[i][j].x, c[i][j].y);
+                mma_m16n8k16(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, c[i][j].z, c[i][j].w);
+            }
     }
-    if (GATED) {
-        if (p.y) {
-            store_one(p.y + (r0 + n) * 2 * cols + oc, s);
-            store_one(p.y + (r0 + n) * 2 * cols + cols + oc, u);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        s_part[warp][r][8 * j + 2 * q] = acc[j][0];
+        s_part[warp][r][8 * j + 2 * q + 1] = acc[j][1];
+        s_part[warp][r + 8][8 * j + 2 * q] = acc[j][2];
+        s_part[warp][r + 8][8 * j + 2 * q + 1] = acc[j][3];
+    }
+    __syncthreads();
+    constexpr int OUTS = GATED ? 8 : 16;
+    for (int i = threadIdx.x; i < OUTS * CHUNK; i += FEW_THREADS) {
+        const int c = i % OUTS, n = i / OUTS;
+        const int64_t oc = OUTS * (int64_t)blockIdx.x + c;
+        if (n >= m || oc >= cols) continue;
+        float s = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WARPS; ++v) {
+            s = __fadd_rn(s, s_part[v][c][n]);
+            if (GATED) u = __fadd_rn(u, s_part[v][c + 8][n]);
         }
-        s = __fmul_rn(__fmul_rn(s, sigmoid(s)), u);
+        if (GATED) {
+            if (p.y) {
+                store_one(p.y + (r0 + n) * 2 * cols + oc, s);
+                store_one(p.y + (r0 + n) * 2 * cols + cols + oc, u);
+            }
+            s = __fmul_rn(__fmul_rn(s, sigmoid(s)), u);
+        }
+        store_one(static_cast<OUT *>(p.out) + (r0 + n) * cols + oc, s);
     }
-    store_one(static_cast<OUT *>(p.out) + (r0 + n) * cols + oc, s);
+}
+
+template <bool GATED, typename OUT, int NC>
+pmn_status launch_few_of(const void *a, int64_t lda, const void *b, const Args &p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)((p.n + (GATED ? 7 : 15)) / (GATED ? 8 : 16)),
+                    (unsigned)std::min<int64_t>(p.rows, p.rows / (8 * NC) + p.groups));
+    few_rows_kernel<GATED, OUT, NC><<<grid, FEW_THREADS, 0, s>>>(static_cast<const uint16_t *>(a), lda,
+                                                                  static_cast<const uint16_t *>(b), p);
+    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 template <bool GATED, typename OUT>
-pmn_status launch_few(const void *a, int64_t lda, const void *b, const Args &p, cudaStream_t s)
+pmn_status launch_few(int chunks, const void *a, int64_t lda, const void *b, const Args &p, cudaStream_t s)
 {
-    const dim3 grid((unsigned)((p.n + (GATED ? 7 : 15)) / (GATED ? 8 : 16)),
-                    (unsigned)std::min<int64_t>(p.rows, p.rows / 8 + p.groups));
-    few_rows_kernel<GATED, OUT><<<grid, FEW_THREADS, 0, s>>>(static_cast<const uint16_t *>(a), lda,
-                                                              static_cast<const uint16_t *>(b), p);
-    return cudaGetLastError() == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+    return chunks == 1 ? launch_few_of<GATED, OUT, 1>(a, lda, b, p, s) : launch_few_of<GATED, OUT, 2>(a, lda, b, p, s);
 }
 
 // ====================================================================== host
@@ -921,9 +938,10 @@ pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k
     return tiles >= LIMIT / 2 ? PMN_ERR_UNSUPPORTED : PMN_OK;
 }
 
-// Whether the kernel for a few rows serves a call.  f 1536, k 4096, it and the tiles, us: one expert, one and
-// eight rows 12 and 25, 16 rows 16 and 25, 32 rows 27 and 25; 24 experts, 8 rows 37 and 47, 32 rows 68 and 69.
-bool few(int64_t rows) { return rows <= 16; }
+// Chunks of eight rows that a CTA of the kernel for a few rows takes, 0 where the tiles serve a call.  f 1536, k 4096,
+// gated, us for one chunk, two, and the tiles: one expert, 8 rows 8.4, 10.4, 21; 16 rows 9.6, 11.1, 21; 32 rows 16.4, 11.8,
+// 21; 48 rows 23, 20, 21; 64 rows 29, 21, 21.  Eight experts, 32 rows 37, 43, 46; 24 experts, 32 rows 91, 109, 95.
+int few(int64_t rows, int64_t groups) { return rows > 32 ? 0 : rows > 16 && rows > 8 * groups ? 2 : 1; }
 
 // Maps of the token rows [rows, k].
 bool token_maps(Maps &maps, const void *a, int64_t rows, int64_t k, int64_t lda)
@@ -988,8 +1006,9 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
     if (m == 0) return PMN_OK;
     if (!a || !b || !out || !offsets || out == a || out == b) return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
-    if (!b_transposed && few(m))
-        return out_kind == PMN_OUT_F32 ? launch_few<false, float>(a, lda, b, args, s) : launch_few<false, uint16_t>(a, lda, b, args, s);
+    if (const int chunks = b_transposed ? 0 : few(m, num_groups))
+        return out_kind == PMN_OUT_F32 ? launch_few<false, float>(chunks, a, lda, b, args, s)
+                                       : launch_few<false, uint16_t>(chunks, a, lda, b, args, s);
     if (!token_maps(maps, a, m, k, lda) || !(b_transposed ? weight_map(&maps.w, b, num_groups, k, n, 64)
                                                           : weight_map(&maps.w, b, num_groups, n, k, 128)) ||
         !piece_map(&maps.out, out, 1, m, n, out_kind, 0, 16, 128))
@@ -1012,7 +1031,8 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
         return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
                     pmn_wait_limit_ns()};
-    if (few(total_rows)) return launch_few<true, uint16_t>(a, lda, b, args, reinterpret_cast<cudaStream_t>(stream));
+    if (const int chunks = few(total_rows, num_experts))
+        return launch_few<true, uint16_t>(chunks, a, lda, b, args, reinterpret_cast<cudaStream_t>(stream));
     // 16 gate rows, the 16 up rows of the same columns, the next 16 gate rows, ..
     const uint64_t dims[5] = {(uint64_t)k, 16, 2, (uint64_t)f / 16, (uint64_t)num_experts};
     const uint64_t str[4] = {(uint64_t)k * 2, (uint64_t)f * k * 2, (uint64_t)k * 32, (uint64_t)f * k * 4};

@@ -43,7 +43,7 @@ def strided(t):
 
 
 SEGMENTS = [  # rows, offsets
-    (1, [0, 1]), (7, [0, 0, 7, 7]), (16, [0, 1, 1, 10, 13, 15]), (17, [0, 17]), (33, [0, 32, 33]), (300, [3, 3, 40, 296]), (513, [0, 513]), (777, [0, 256, 257, 770]),
+    (1, [0, 1]), (7, [0, 0, 7, 7]), (16, [0, 1, 1, 10, 13, 15]), (17, [0, 17]), (24, [0, 24]), (29, [0, 13, 29]), (31, [1, 2, 9, 9, 31]), (32, [0, 3, 21, 32]), (32, [0, 32]), (33, [0, 32, 33]), (300, [3, 3, 40, 296]), (513, [0, 513]), (777, [0, 256, 257, 770]),
     (640, [0, 31, 62, 95, 129, 130, 130, 131, 400, 640]), (1100, [5, 1029, 1100]),
 ]
 
@@ -160,7 +160,7 @@ def test_gated_projection_and_its_backward(pmn, rows, offsets, f, k):
     assert pmn.get_device_error() == 0
 
 
-@pytest.mark.parametrize("rows", [13, 50])
+@pytest.mark.parametrize("rows", [13, 24, 50])
 def test_gates_far_from_zero(pmn, rows):
     """gate, up and dH given as they are by one-hot products.  The sigmoid's 2^-148 below the normal range reaches h times
     gate and up, which may be large; a product of two that is itself subnormal adds 2^-149 times the third."""
