@@ -790,8 +790,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
 #pragma unroll
     for (int j = 0; j < NC; ++j) xr[j] = x + (r0 + min(8 * j + r, m - 1)) * ldx;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float acc[NC][4] = {};
-    // (the same passes for all lanes of a warp, which multiply together)
+    float sum[NC][4] = {};
+    // (the same passes for all lanes of a warp, which multiply together; a pass's sums are added to those before
+    // it rounded to nearest, where the tensor core would truncate)
     for (int64_t kw = 32 * FEW_UNROLL * warp; kw < p.k; kw += 32 * FEW_UNROLL * WARPS) {
         uint4 a[FEW_UNROLL], b[FEW_UNROLL], c[FEW_UNROLL][NC];
 #pragma unroll
@@ -805,6 +806,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
                 c[i][j] = on && 8 * j + r < m ? __ldg(reinterpret_cast<const uint4 *>(xr[j] + k)) : zero;
         }
         __syncwarp();
+        float acc[NC][4] = {};
 #pragma unroll
         for (int i = 0; i < FEW_UNROLL; ++i)
 #pragma unroll
@@ -812,13 +814,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
                 mma_m16n8k16(acc[j], a[i].x, b[i].x, a[i].y, b[i].y, c[i][j].x, c[i][j].y);
                 mma_m16n8k16(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, c[i][j].z, c[i][j].w);
             }
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum[j][v] = __fadd_rn(sum[j][v], acc[j][v]);
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        s_part[warp][r][8 * j + 2 * q] = acc[j][0];
-        s_part[warp][r][8 * j + 2 * q + 1] = acc[j][1];
-        s_part[warp][r + 8][8 * j + 2 * q] = acc[j][2];
-        s_part[warp][r + 8][8 * j + 2 * q + 1] = acc[j][3];
+        s_part[warp][r][8 * j + 2 * q] = sum[j][0];
+        s_part[warp][r][8 * j + 2 * q + 1] = sum[j][1];
+        s_part[warp][r + 8][8 * j + 2 * q] = sum[j][2];
+        s_part[warp][r + 8][8 * j + 2 * q + 1] = sum[j][3];
     }
     __syncthreads();
     constexpr int OUTS = GATED ? 8 : 16;

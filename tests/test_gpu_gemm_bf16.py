@@ -84,7 +84,7 @@ def test_sums_over_rows(pmn, rows, offsets, m, n, out):
     assert pmn.get_device_error() == 0
 
 
-@pytest.mark.parametrize("form,K", [("rows", 8200), ("transposed", 4096), ("sums", 16384), ("sums", 1025), ("sums", 511)])
+@pytest.mark.parametrize("form,K", [("rows", 8200), ("one", 32776), ("few", 8200), ("transposed", 4096), ("sums", 16384), ("sums", 1025), ("sums", 511)])
 def test_long_sums_keep_float32(pmn, form, K):
     """Positive terms, so that S is the sum itself: the tensor core's 32 additions of a run of 512 truncate (2 u each, with
     those inside an addition 34), the runs' sums are rounded (u each)."""
@@ -98,9 +98,10 @@ def test_long_sums_keep_float32(pmn, form, K):
         got = pmn.grouped_gemm_bf16(a, b, gpu_offsets([0, K]), pmn.GROUP_K)[0]
         want = f64(a).T @ f64(b)
     else:
-        a, b = positive(40, K), positive(1, 264, K)
+        rows = {"one": 1, "few": 30}.get(form, 40)
+        a, b = positive(rows, K), positive(1, 264, K)
         w = b.transpose(1, 2).contiguous() if form == "transposed" else b
-        got = pmn.grouped_gemm_bf16(a, w, gpu_offsets([0, 40]), pmn.GROUP_M, b_transposed=form == "transposed", out_dtype=torch.float32)
+        got = pmn.grouped_gemm_bf16(a, w, gpu_offsets([0, rows]), pmn.GROUP_M, b_transposed=form == "transposed", out_dtype=torch.float32)
         want = f64(a) @ f64(b)[0].T
     assert (np.abs(f64(got) - want) <= (2 * 34 + -(-K // 512)) * U * want).all()
     assert pmn.get_device_error() == 0
