@@ -481,10 +481,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 sb[h][4 * s + j] = u4_word(vb, s);
                             }
                         }
-                    if (c == RAW_STEPS - 2 || k + c + 2 >= q.k1) {  // the slot has been read
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
-                    }
                     const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + C::SF_COL0, first = stage;
                     if (!wait(bar_empty + 8 * stage, phase ^ 1)) break;
                     tc_fence_after();
@@ -501,6 +497,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
+                        // The slot's rows may be overwritten once they are in registers, which only the stores that
+                        // have used them show: an arrival does not wait for loads before it.
+                        if (c == RAW_STEPS - 2 || k + c + 2 >= q.k1) mbar_arrive(bar_raw_empty + 8 * slot);
                         mbar_arrive(bar_full + 8 * first);
                         if (two) mbar_arrive(bar_full + 8 * stage);
                     }

@@ -321,13 +321,14 @@ def test_captured_and_replayed_with_other_rows(pmn):
             assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("which", ["rows", "transposed", "sums", "gated", "gated_backward"])
+@pytest.mark.parametrize("which", ["rows", "rows_f32", "transposed", "sums", "gated", "gated_backward"])
 def test_a_call_that_runs_out_of_time_says_so(pmn, which):
     """with no time to wait a call either is right or latches the timeout, and the next one is right"""
     gen = torch.Generator(device="cuda").manual_seed(6)
     off = gpu_offsets([0, 300, 300, 333, 900])
     a, b, w, w2, y = bf16(gen, 900, 640), bf16(gen, 900, 256), bf16(gen, 4, 512, 640), bf16(gen, 4, 640, 256), bf16(gen, 900, 512)
     call = {"rows": lambda: pmn.grouped_gemm_bf16(a, w, off, pmn.GROUP_M),
+            "rows_f32": lambda: pmn.grouped_gemm_bf16(a, w, off, pmn.GROUP_M, out_dtype=torch.float32),
             "transposed": lambda: pmn.grouped_gemm_bf16(a, w2, off, pmn.GROUP_M, b_transposed=True),
             "sums": lambda: pmn.grouped_gemm_bf16(a, b, off, pmn.GROUP_K),
             "gated": lambda: torch.cat(pmn.w1_gemm_swiglu_bf16(a, w, off, want_y=True), 1),

@@ -245,6 +245,21 @@ def test_a_call_that_runs_out_of_time_says_so(pmn, rows):
     assert torch.equal(pmn.matvec_nvfp4(x, w, off), want) and pmn.get_device_error() == 0
 
 
+@pytest.mark.parametrize("experts,rows,n,k", [(2, 52, 4096, 3584), (1, 104, 1536, 4096), (16, 8, 1040, 3584), (2, 52, 272, 8192)])
+def test_scales_of_every_step_are_its_own(pmn, experts, rows, n, k):
+    """each 256 of K under a scale of its own, many calls: every sum is exact, so a scale taken from another step shows"""
+    step = np.arange(k // 16) // 16
+    w = (np.full((experts, n, k // 2), 0x22, dtype=np.uint8),
+         np.broadcast_to(((1 + step % 14) << 3).astype(np.uint8), (experts, n, k // 16)), np.ones(experts, dtype=np.float32))
+    w, x = cuda(*w), torch.ones((experts * rows, k), device="cuda").bfloat16()
+    off = torch.arange(experts + 1, dtype=torch.int32, device="cuda") * rows
+    want = 16 * (2.0 ** (step % 14 - 6)).sum()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(150):
+        wrong += (pmn.matvec_nvfp4(x, w, off, out_dtype=torch.float32) != want).sum()
+    assert wrong.item() == 0 and pmn.get_device_error() == 0
+
+
 def test_the_same_bits_every_time(pmn):
     """tiles that CTAs share are joined in the order of K, whoever comes last"""
     rng = np.random.default_rng(11)
