@@ -152,7 +152,8 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
             for (int j = 0; j < NV; ++j) {
                 const float b = EXACT || lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
 #pragma unroll
-                for (int t = 0; t < T; ++t) v[t][j] = __fadd_rn(v[t][j], b);
+                for (int t = 0; t < T; ++t)  // (a token behind the last has no logits to be chosen by: -inf plus inf is a NaN)
+                    if (t == 0 || token + t * step < p.tokens) v[t][j] = __fadd_rn(v[t][j], b);
             }
         }
 #pragma unroll
