@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t order_key(float v)
 __device__ __forceinline__ float warp_max(float v)
 {
     float m;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
 }
 
