@@ -58,3 +58,29 @@ def test_a_bias_of_infinity_or_nan(pmn, tokens, experts, kind):
         want = routing64.gates(l.astype(np.float64), chosen, "softmax", True)
         assert (np.abs(r.gates.cpu().numpy() - want) <= (64 + 4 * np.abs(l).max()) * U * want).all()
     assert pmn.get_device_error() == 0
+
+
+@pytest.mark.parametrize("tokens", [2, 64, 256, 257, 1000])
+@pytest.mark.parametrize("experts,k", [(3, 2), (60, 8), (384, 8), (384, 32), (700, 32), (1024, 32)])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_nan_before_infinity_before_numbers(pmn, tokens, experts, k, many, kind):
+    """NaN of either sign and both infinities in every row; many: so many equals that they cannot be packed to a lane each"""
+    rng = np.random.default_rng(tokens + experts + k)
+    l = (rng.standard_normal((tokens, experts)) * 2).astype(np.float32)
+    share = 0.3 if many else 1.5 / experts
+    for v in (NAN, -NAN, INF, -INF):
+        l[rng.random(l.shape) < share] = v
+    l[0, :3] = INF, NAN, 1.0
+    x = torch.from_numpy(l).to(TYPES[kind]).cuda()
+    r = pmn.route_topk(x, k)
+    check(r, ranked(x.float().cpu().numpy(), k), experts)
+    assert pmn.get_device_error() == 0
+
+
+def test_a_few_rows_by_hand(pmn):
+    x = torch.tensor([[INF, NAN, 1.0, -INF], [1.0, INF, 2.0, INF], [-INF, -INF, NAN, -INF], [INF, -INF, -NAN, NAN]])
+    for tokens in (4, 260):
+        got = pmn.route_topk(x.repeat(tokens // 4, 1).cuda(), 3).experts.cpu().numpy()
+        want = np.array([[1, 0, 2], [1, 3, 2], [2, -1, -1], [2, 3, 0]])
+        assert np.array_equal(ranked(x.numpy(), 3), want) and np.array_equal(got, np.tile(want, (tokens // 4, 1)))
