@@ -774,7 +774,8 @@ PMN_API int64_t pmn_matvec_nvfp4_workspace_bytes(int64_t total_rows, int64_t k);
  *           matter; calls that share one must not overlap.
  * x enters the products as eight 4-bit digits under a scale per 16 values: a value is
  * exact unless it is below 2^-15 of the largest of its 16 (or those below 2^-17 of the
- * row's), and then off by 2^-23 of that (2^-40 of the row's) at most.  Sums in float32.  A
+ * row's), and then off by 2^-23 of that (2^-40 of the row's) at most.  Sums in float32,
+ * truncated as the tensor cores do over 4096 of K at most, whose sums are added rounded.  A
  * row with a NaN or an infinity is multiplied value by value, slowly.
  * Right for any number of rows, and fast for few: an expert's weights are read once
  * per 16 of its rows (per 8 where total_rows <= 8 num_experts).  Two kernels on

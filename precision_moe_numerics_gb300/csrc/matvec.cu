@@ -41,6 +41,11 @@ constexpr int MAX_CHUNK = 16;                    // most rows of x per pass over
 constexpr int BM = 128;                          // weight rows of a tile (gated: 64 gate and the 64 up rows of the same columns)
 constexpr int KSTEP = 256;                       // of K per stage: 128 bytes of codes, 16 scales
 constexpr int A_BYTES = BM * 128;
+// The tensor core truncates each of its additions to float32, an error that grows with their number where terms have one
+// sign (one accumulator for K = 262144: 8.8e-5 of such a sum).  RUN stages, 4096 of K, make a sum, and a tile's sums are
+// added rounded (512 rows of 384 experts, k 1536: 148.2 -> 148.8 us; runs of 2048: 149.6 to 151.7).  Where signs are
+// mixed few bits are lost either way: 3.7e-8 of the norm at k 4096, 5.5e-8 at 16384.
+constexpr int RUN = 16;
 constexpr int RAW_STEPS = 4, RAW_W = 16 * RAW_STEPS;  // scale rows come 64 bytes (four stages) at a time
 constexpr int RAW_A = BM * RAW_W, RAW_BYTES = RAW_A + MAX_CHUNK * RAW_W, RAW_SLOTS = 3;
 constexpr uint32_t TMEM_COLS = 512, SF_COLS = 32;
@@ -423,25 +428,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t abuf = 0, aphase = 0;
         while (!dead && walk.next(p, s_cum, q)) {
             const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(digit_rows(q) >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-            if (!wait(bar_acc_empty + 8 * abuf, aphase ^ 1)) break;
-            const uint32_t d = tm + abuf * NB;
-            for (int k = q.k0; k < q.k1; ++k) {
-                if (!wait(bar_full + 8 * stage, phase)) break;
-                tc_fence_after();
-                const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES;
-                const uint32_t sfa = tm + C::SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
+            for (int run = q.k0; run < q.k1 && !dead; run += RUN) {
+                if (!wait(bar_acc_empty + 8 * abuf, aphase ^ 1)) break;
+                const uint32_t d = tm + abuf * NB;
+                const int end = min(q.k1, run + RUN);
+                for (int k = run; k < end; ++k) {
+                    if (!wait(bar_full + 8 * stage, phase)) break;
+                    tc_fence_after();
+                    const uint32_t a = stages + stage * STAGE_BYTES, b = a + A_BYTES;
+                    const uint32_t sfa = tm + C::SF_COL0 + stage * SF_COLS, sfb = sfa + 16;
 #pragma unroll
-                for (int s = 0; s < 4; ++s)  // 64 of K: 32 bytes of the swizzled rows
-                    mma_nvfp4_by(el, d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2), idesc, sfa + 4 * s,
-                                 sfb + 4 * s, k > q.k0 || s > 0);
-                tc_commit_ct<1>(el, bar_empty + 8 * stage);
-                next_stage();
-            }
-            if (dead) break;
-            tc_commit_ct<1>(el, bar_acc_full + 8 * abuf);
-            if (++abuf == 2) {
-                abuf = 0;
-                aphase ^= 1;
+                    for (int s = 0; s < 4; ++s)  // 64 of K: 32 bytes of the swizzled rows
+                        mma_nvfp4_by(el, d, smem_desc(a + 32 * s, 16, 1024, 2), smem_desc(b + 32 * s, 16, 1024, 2), idesc, sfa + 4 * s,
+                                     sfb + 4 * s, k > run || s > 0);
+                    tc_commit_ct<1>(el, bar_empty + 8 * stage);
+                    next_stage();
+                }
+                if (dead) break;
+                tc_commit_ct<1>(el, bar_acc_full + 8 * abuf);
+                if (++abuf == 2) {
+                    abuf = 0;
+                    aphase ^= 1;
+                }
             }
         }
         if (elect_one()) tc_commit(bar_drain);  // every tcgen05 operation of this warp has completed
@@ -527,31 +535,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                 exponent[t] = meta.x;
                 odd |= meta.y << t;
             }
-            if (wait(bar_acc_full + 8 * abuf, aphase)) {
-                tc_fence_after();
-                const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * NB;
+            auto take = [&](bool more) {  // the next accumulator's sums, added to those before it
+                if (wait(bar_acc_full + 8 * abuf, aphase)) {
+                    tc_fence_after();
+                    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + abuf * NB;
 #pragma unroll
-                for (int t = 0; t < CHUNK; t += 2) {
-                    if (t >= m) break;
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(acc + DIGITS * t, v);
-                    tmem_ld_wait();
+                    for (int t = 0; t < CHUNK; t += 2) {
+                        if (t >= m) break;
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(acc + DIGITS * t, v);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float sum = __uint_as_float(v[8 * u + 7]);
+                        for (int u = 0; u < 2; ++u) {
+                            float sum = __uint_as_float(v[8 * u + 7]);
 #pragma unroll
-                        for (int c = 6; c >= 0; --c) sum = fmaf(sum, 0.125f, __uint_as_float(v[8 * u + c]));
-                        y[t + u] = sum;
+                            for (int c = 6; c >= 0; --c) sum = fmaf(sum, 0.125f, __uint_as_float(v[8 * u + c]));
+                            y[t + u] = more ? __fadd_rn(y[t + u], sum) : sum;
+                        }
                     }
+                    tc_fence_before();
                 }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
-            if (++abuf == 2) {
-                abuf = 0;
-                aphase ^= 1;
-            }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_acc_empty + 8 * abuf);
+                if (++abuf == 2) {
+                    abuf = 0;
+                    aphase ^= 1;
+                }
+            };
+            take(false);
+            for (int k = q.k0 + RUN; k < q.k1; k += RUN) take(true);
             if (q.k1 - q.k0 < p.nks) {
                 // A tile that CTAs first .. last share: each leaves its sums, and the one that
                 // comes last adds them up in the order of K.  A CTA's slot 0 is for a tile that began
