@@ -715,7 +715,8 @@ PMN_API pmn_status pmn_combine_rows_backward(const void *dout, const void *z, in
  * One kernel on `stream`: tiles, or with b [num_groups, n, k] and m <= 32 one that reads the
  * weights straight from memory.  The sums' order depends on that choice, the sizes, the
  * segments and the GPU's SM count alone; the tiles' sums are truncated as the tensor
- * cores do, with PMN_OUT_F32 over 512 of K at most, whose sums are added in float32.
+ * cores do, with PMN_OUT_F32 over 512 of K at most, in bf16 over all of K up to 16384 and over
+ * 4096 of a longer one (GROUP_K: K is the rows of a), whose sums are added in float32.
  */
 PMN_API pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,
                                          int num_groups, int group_mode, int b_transposed, int64_t m, int64_t n,

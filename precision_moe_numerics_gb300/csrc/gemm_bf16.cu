@@ -152,14 +152,20 @@ __device__ __forceinline__ int stages_of(const Tile &ti, const Args &p)
 }
 
 // The tensor core truncates each of its additions to float32, an error that grows with their
-// number (sums over 16384 rows: 1.9e-5 of their norm, where rounded additions have 1.9e-7).  Where the
-// output is float32 too, a tile's sums are therefore made in runs of RUN stages, added up in registers and
-// rounded to nearest: 4.8e-7.  RUN 12: 7.3e-7, RUN 4: 2.5e-7; dw1 of 8192 rows of 24 experts takes 255 us
-// without runs, 274, 280 and 319 with 12, 8 and 4, the rows' products 2 to 5 % more with 8.
-template <int FORM, typename OUT>
+// number (sums over 16384 rows: 1.9e-5 of their norm, where rounded additions have 1.9e-7; sums of one sign lose
+// 1.4 x 2^-24 an addition).  Where the output is float32 too, a tile's sums are therefore made in runs of RUN stages, added
+// up in registers and rounded to nearest: 4.8e-7.  RUN 12: 7.3e-7, RUN 4: 2.5e-7; dw1 of 8192 rows of 24 experts takes
+// 255 us without runs, 274, 280 and 319 with 12, 8 and 4, the rows' products 2 to 5 % more with 8.
+// A bf16 output's rounding, up to 3.9e-3, hides that for as long as K is a layer's width: w1, dx and dh of the training
+// batch are 1.65917e-3, 1.65559e-3 and 1.65926e-3 of the norm off with and without runs of 1024 of K, which take
+// 170 -> 173, 168 -> 171 and 140 -> 186 us.  Sums over rows have no such bound (2^20 of one sign would be off by 5.4e-3
+// before they are rounded): LONG, bf16 outputs of more than LONG_K, has runs of 4096.  (16384 of one sign without
+// lose 8.5e-5; dw1 of 8192 rows in bf16 takes 232 us without runs, 239 with these.)
+constexpr int64_t LONG_K = 16384;
+template <int FORM, typename OUT, bool LONG>
 struct Runs {
-    static constexpr bool split = sizeof(OUT) == 4 && !Form<FORM>::gated && !Form<FORM>::backward;
-    static constexpr int RUN = split ? 8 : 1 << 30;
+    static constexpr bool split = LONG || (sizeof(OUT) == 4 && !Form<FORM>::gated && !Form<FORM>::backward);
+    static constexpr int RUN = LONG ? 64 : split ? 8 : 1 << 30;
 };
 
 // The ring of stages.  A slot holds the weights' 16 KB and the rows: 4 KB of a tile of up to 64,
@@ -254,11 +260,12 @@ __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float
 // Roles: warp 0 loads by TMA, warp 1 of the leader issues the pair's MMAs, warp 2 (SUMS) clears
 // rows that are not the group's, warps 4.. store.  Every wait is bounded: on a timeout an
 // error bit is latched and the CTA winds down.
-template <int FORM, typename OUT>
+template <int FORM, typename OUT, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant__ Maps maps, const Args p)
 {
     using F = Form<FORM>;
-    constexpr int RUN = Runs<FORM, OUT>::RUN;
+    using R = Runs<FORM, OUT, LONG>;
+    constexpr int RUN = R::RUN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw;
     asm volatile("" : "+l"(smem));
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                 ++n;
             };
             const int runs = (stages_of<FORM>(ti, p) + RUN - 1) / RUN;
-            if (!Runs<FORM, OUT>::split || runs <= 1) {
+            if (!R::split || runs <= 1) {
                 const uint32_t acc = take();
                 for (int c = group; c < pieces; c += GROUPS) {
                     float v[CH];
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
                     emit(c, v);
                 }
                 give_back();
-            } else if constexpr (Runs<FORM, OUT>::split) {
+            } else if constexpr (R::split) {
                 constexpr int MOST = TILE / CH / GROUPS;
                 float sum[MOST][CH];
 #pragma unroll
@@ -904,10 +911,10 @@ bool rows_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int
 
 inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <int FORM, typename OUT>
-pmn_status launch(const Maps &maps, const Args &args, cudaStream_t s)
+template <int FORM, typename OUT, bool LONG>
+pmn_status launch_of(const Maps &maps, const Args &args, cudaStream_t s)
 {
-    auto kern = bf16_kernel<FORM, OUT>;
+    auto kern = bf16_kernel<FORM, OUT, LONG>;
     static std::atomic<int> sm_count[MAX_DEVICES];  // of each device this kernel has been set up on
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return PMN_ERR_CUDA;
@@ -930,6 +937,14 @@ pmn_status launch(const Maps &maps, const Args &args, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, args) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+}
+
+template <int FORM, typename OUT>
+pmn_status launch(const Maps &maps, const Args &args, cudaStream_t s)
+{
+    if constexpr (sizeof(OUT) == 2)
+        if ((FORM == SUMS ? args.rows : args.k) > LONG_K) return launch_of<FORM, OUT, true>(maps, args, s);
+    return launch_of<FORM, OUT, false>(maps, args, s);
 }
 
 constexpr int64_t LIMIT = int64_t(1) << 31;
