@@ -590,7 +590,7 @@ PMN_API pmn_status pmn_adamw_step(const pmn_adamw_tensor *tensors, int num_tenso
  * calls above expect of their caller (rows by expert, offsets, the tokens' row
  * numbers and gates), made on the device.  The pages have no counterpart.
  * In these calls and the products below no output may overlap an input or another
- * output; the address of an input is refused.
+ * output, nor may a workspace; the address of an input or of another output is refused.
  */
 
 /* Rows that hold every choice whatever the experts' counts are, each expert's

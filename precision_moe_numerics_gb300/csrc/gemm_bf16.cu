@@ -23,6 +23,7 @@
 #include <cstdint>
 
 #include "../../include/pmn.h"
+#include "args.cuh"
 #include "numerics.cuh"
 #include "sm100.cuh"
 #include "tensormap.cuh"
@@ -909,8 +910,6 @@ bool rows_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int
     return make_map(m, base, 2, dims, st, box);
 }
 
-inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 template <int FORM, typename OUT, bool LONG>
 pmn_status launch_of(const Maps &maps, const Args &args, cudaStream_t s)
 {
@@ -1016,7 +1015,7 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
         if (k == 0)  // sums over no rows
             return cudaMemsetAsync(out, 0, (size_t)num_groups * m * n * (out_kind == PMN_OUT_F32 ? 4 : 2), s) == cudaSuccess
                        ? PMN_OK : PMN_ERR_CUDA;
-        if (!a || !b || out == a || out == b) return PMN_ERR_INVALID_ARG;
+        if (!a || !b || among(out, {a, b, offsets})) return PMN_ERR_INVALID_ARG;
         if (!rows_map(&maps.w, b, n, k, ldb, 64) || !rows_map(&maps.x, a, m, k, lda, 64) ||
             !piece_map(&maps.out, out, num_groups, m, n, out_kind, 1, 16, 128))
             return PMN_ERR_CUDA;
@@ -1025,7 +1024,7 @@ extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const vo
     }
     if (k <= 0 || k % 8 != 0 || lda < k) return PMN_ERR_INVALID_ARG;
     if (m == 0) return PMN_OK;
-    if (!a || !b || !out || !offsets || out == a || out == b) return PMN_ERR_INVALID_ARG;
+    if (!a || !b || !out || !offsets || among(out, {a, b, offsets})) return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_groups, m, 0, n, k, out, nullptr, pmn_wait_limit_ns()};
     if (const int chunks = b_transposed ? 0 : few(m, num_groups))
         return out_kind == PMN_OUT_F32 ? launch_few<false, float>(chunks, a, lda, b, args, s)
@@ -1048,7 +1047,7 @@ extern "C" pmn_status pmn_w1_gemm_swiglu_bf16(const void *a, int64_t lda, const 
     if (f % 16 != 0 || k <= 0 || k % 8 != 0 || lda < k || lda % 8 != 0) return PMN_ERR_INVALID_ARG;
     if (total_rows == 0) return PMN_OK;
     if (!a || !b || !offsets || !out || !aligned(a, 16) || !aligned(b, 16) || !aligned(offsets, 4) || !aligned(out, 16) ||
-        !aligned(y_out, 16) || out == a || out == b || out == y_out || y_out == a || y_out == b)
+        !aligned(y_out, 16) || among(out, {a, b, offsets, y_out}) || among(y_out, {a, b, offsets}))
         return PMN_ERR_INVALID_ARG;
     const Args args{offsets, num_experts, total_rows, 0, f, k, out, static_cast<uint16_t *>(y_out),
                     pmn_wait_limit_ns()};
@@ -1075,7 +1074,7 @@ extern "C" pmn_status pmn_dh_gemm_swiglu_backward_bf16(const void *a, int64_t ld
     if (k <= 0 || k % 8 != 0 || lda < k || lda % 8 != 0) return PMN_ERR_INVALID_ARG;
     if (total_rows == 0) return PMN_OK;
     if (!a || !b || !y || !offsets || !out || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(offsets, 4) ||
-        !aligned(out, 16) || out == a || out == b || out == y)
+        !aligned(out, 16) || among(out, {a, b, y, offsets}))
         return PMN_ERR_INVALID_ARG;
     Maps maps = {};
     if (!token_maps(maps, a, total_rows, k, lda) || !weight_map(&maps.w, b, num_experts, k, f, 64) ||

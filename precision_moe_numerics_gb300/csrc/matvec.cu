@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "../../include/pmn.h"
+#include "args.cuh"
 #include "numerics.cuh"
 #include "sm100.cuh"
 #include "tensormap.cuh"
@@ -659,8 +660,6 @@ bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, uin
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 inline int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
 
 // The workspace's parts, each on a 128-byte boundary.
@@ -768,7 +767,9 @@ extern "C" pmn_status pmn_matvec_nvfp4(const void *x, int64_t ldx, int64_t token
         return PMN_ERR_INVALID_ARG;
     // steps are counted in 32 bits
     if ((total_rows / 8 + num_experts) * (n / 64 + 1) * (k / KSTEP) >= LIMIT) return PMN_ERR_UNSUPPORTED;
-    if (out == x || out == workspace) return PMN_ERR_INVALID_ARG;
+    if (among(out, {x, codes, scales, outer, offsets, row_choice, workspace}) ||
+        among(workspace, {x, codes, scales, outer, offsets, row_choice}))
+        return PMN_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int64_t half_n = swiglu ? n / 2 : n, half = swiglu ? BM / 2 : BM;
     const Args a{static_cast<const uint16_t *>(x), ldx, tokens, codes, scales, outer, offsets, num_experts, total_rows, n, k,

@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "../../include/pmn.h"
+#include "args.cuh"
 #include "numerics.cuh"
 
 using namespace pmn;
@@ -24,8 +25,6 @@ __device__ int g_route_error = 0;
 
 constexpr int MAX_EXPERTS = 1024, MAX_K = 32, MAX_CHOICES = 64;
 constexpr unsigned FULL = 0xFFFFFFFFu;
-
-inline bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // ====================================================================== router
 // Tokens are counted and laid out in chunks, one CTA each: at most MAX_CHUNKS, so that
@@ -877,6 +876,11 @@ extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits
         !aligned(chosen, 4) || !aligned(gates, 4) || !aligned(row_index, 4) || workspace_bytes < ws ||
         (ws > 0 && (!workspace || !aligned(workspace, 16))))
         return PMN_ERR_INVALID_ARG;
+    if (among(chosen, {logits, bias, gates, row_index, row_choice, offsets}) ||
+        among(gates, {logits, bias, row_index, row_choice, offsets}) || among(row_index, {logits, bias, row_choice, offsets}) ||
+        among(row_choice, {logits, bias, offsets}) || among(offsets, {logits, bias}) ||
+        (ws > 0 && among(workspace, {logits, bias, chosen, gates, row_index, row_choice, offsets})))
+        return PMN_ERR_INVALID_ARG;
     int half = 0;
     while ((half ? 2 * half : 1) < k) half = half ? 2 * half : 1;
     RouteArgs a{logits, ldl, bias, tokens, chunk_tokens(tokens), rows, experts, k, half, score, normalize, pad, scale,
@@ -893,7 +897,8 @@ extern "C" pmn_status pmn_route_topk_backward(const void *logits, int64_t ldl, i
         return PMN_ERR_INVALID_ARG;
     if (tokens == 0) return PMN_OK;
     if (!logits || !chosen || !dgates || !dlogits || !aligned(logits, kind_bytes(logits_kind)) ||
-        !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4) || dlogits == logits)
+        !aligned(dlogits, kind_bytes(logits_kind)) || !aligned(chosen, 4) || !aligned(dgates, 4) ||
+        among(dlogits, {logits, chosen, dgates}))
         return PMN_ERR_INVALID_ARG;
     const RouteGradArgs a{logits, ldl, chosen, dgates, tokens, experts, k, score, normalize, scale, dlogits, aligned(dlogits, 16)};
     const unsigned blocks = (unsigned)((tokens + 7) / 8);
@@ -910,7 +915,9 @@ extern "C" pmn_status pmn_dispatch_rows(const void *x, int64_t ldx, int kind, in
     if (!good_rows(tokens, cols, kind, k, rows) || ldx < cols || ldx * kind_bytes(kind) % 16 != 0) return PMN_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return PMN_OK;
     if (!out || !aligned(out, 16) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
-    if (tokens > 0 && (!x || !row_index || !aligned(x, 16) || !aligned(row_index, 4) || out == x)) return PMN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || !row_index || !aligned(x, 16) || !aligned(row_index, 4) || among(out, {x, row_index})))
+        return PMN_ERR_INVALID_ARG;
+    if (among(out, {row_choice})) return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const Split by = Split::of(tokens, vecs);
     const int64_t token_blocks = by.blocks(tokens);
@@ -930,7 +937,7 @@ extern "C" pmn_status pmn_combine_rows(const void *z, int kind, int64_t rows, in
         return PMN_ERR_INVALID_ARG;
     if (tokens == 0 || cols == 0) return PMN_OK;
     if ((rows > 0 && !z) || !row_index || !out || !aligned(z, 16) || !aligned(out, 16) || !aligned(row_index, 4) ||
-        !aligned(gates, 4) || out == z)
+        !aligned(gates, 4) || (rows > 0 && out == z) || among(out, {row_index, gates}))
         return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const Split by = Split::of(tokens, vecs);
@@ -956,7 +963,8 @@ extern "C" pmn_status pmn_combine_rows_backward(const void *dout, const void *z,
     if (tokens > 0 && (!dout || !row_index || !dgates || !aligned(dout, 16) || !aligned(row_index, 4) || !aligned(dgates, 4)))
         return PMN_ERR_INVALID_ARG;
     if (rows > 0 && (!z || !dz || !aligned(z, 16) || !aligned(dz, 16))) return PMN_ERR_INVALID_ARG;
-    if (!aligned(row_choice, 4) || !aligned(gates, 4) || (dz && (dz == z || dz == dout)) || (dgates && dgates == gates))
+    if (!aligned(row_choice, 4) || !aligned(gates, 4) || among(dz, {z, dout, row_choice}) || among(dgates, {gates})) return PMN_ERR_INVALID_ARG;
+    if (tokens > 0 && (among(dz, {row_index, gates, dgates}) || among(dgates, {dout, z, row_index, row_choice})))
         return PMN_ERR_INVALID_ARG;
     const int vecs = (int)(cols * kind_bytes(kind) / 16);
     const int64_t blocks = tokens + (row_choice ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0);
