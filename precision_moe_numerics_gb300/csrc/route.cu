@@ -117,7 +117,7 @@ __device__ __noinline__ int choose_slowly(const uint32_t (&given)[NV], int k, in
 // than k keys -- holds the choice; those few are packed, one to a lane, in the experts' order,
 // and ordered by comparing them all.  (16384 tokens of 384 experts: k rounds over all keys 27 us, k rounds over the
 // few 18, this 17; bound by instructions, 530 of them a token.)
-template <int T, int NV, int KIND, bool EXACT>
+template <int T, int NV, int KIND>
 __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_t step, int lane, uint2 (*few)[32],
                                        int (&expert)[T], float (&gate)[T])
 {
@@ -130,7 +130,7 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                v[t][j] = (EXACT || lane + 32 * j < p.experts) && token + t * step < p.tokens
+                v[t][j] = lane + 32 * j < p.experts && token + t * step < p.tokens
                               ? load_logit<KIND>(p.logits, (token + t * step) * p.ldl + lane + 32 * j) : -INFINITY;
         if (every) {  // the denominator runs over all experts
 #pragma unroll
@@ -149,7 +149,7 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
         if (p.bias) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const float b = EXACT || lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
+                const float b = lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
 #pragma unroll
                 for (int t = 0; t < T; ++t)  // (a token behind the last has no logits to be chosen by: -inf plus inf is a NaN)
                     if (t == 0 || token + t * step < p.tokens) v[t][j] = __fadd_rn(v[t][j], b);
@@ -326,7 +326,7 @@ __device__ void mark_padding(const RouteArgs &p, const Layout &s)
 }
 
 // The tokens of a chunk chosen, T by a warp at a time, and counted.
-template <int T, int NV, int KIND, bool EXACT>
+template <int T, int NV, int KIND>
 __device__ __forceinline__ void choose_chunk(const RouteArgs &p, int64_t t0, int64_t t1, uint2 (*few)[32], int32_t *count)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -335,7 +335,7 @@ __device__ __forceinline__ void choose_chunk(const RouteArgs &p, int64_t t0, int
     for (int64_t t = t0 + warp; t < t1; t += T * warps) {
         int expert[T];
         float gate[T];
-        choose<T, NV, KIND, EXACT>(p, t, warps, lane, few, expert, gate);
+        choose<T, NV, KIND>(p, t, warps, lane, few, expert, gate);
 #pragma unroll
         for (int i = 0; i < T; ++i)
             if (lane < p.k && t + i * warps < t1) {
@@ -347,7 +347,7 @@ __device__ __forceinline__ void choose_chunk(const RouteArgs &p, int64_t t0, int
 }
 
 // One CTA per chunk.
-template <int NV, int KIND, bool EXACT>
+template <int NV, int KIND>
 __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(const RouteArgs p)
 {
     __shared__ int32_t count[MAX_EXPERTS];
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(cons
     __shared__ uint2 few[NV > 16 ? 16 : 32][T][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
-    choose_chunk<T, NV, KIND, EXACT>(p, t0, t1, few[threadIdx.x >> 5], count);
+    choose_chunk<T, NV, KIND>(p, t0, t1, few[threadIdx.x >> 5], count);
     __syncthreads();
     const int pitch = (p.experts + 1) / 2 * 2;
     for (int e = threadIdx.x; e < pitch; e += blockDim.x)
@@ -365,14 +365,14 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_choose_kernel(cons
 // Few tokens: one cluster, whose CTAs read one another's counts.  (384 experts, 64 and 256 tokens, us back to
 // back: 6.0 and 7.9; one CTA 9.7 and the two kernels 11.1.  512 tokens: 11.4 either way.  256 threads a CTA
 // instead of 512: 6.5 and 7.9.)
-template <int NV, int KIND, bool EXACT>
+template <int NV, int KIND>
 __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) route_few_kernel(const RouteArgs p)
 {
     __shared__ Layout s;
     __shared__ int32_t count[MAX_EXPERTS];
     __shared__ uint2 few[NV > 16 ? 16 : 32][1][32];
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
-    choose_chunk<1, NV, KIND, EXACT>(p, t0, t1, few[threadIdx.x >> 5], count);
+    choose_chunk<1, NV, KIND>(p, t0, t1, few[threadIdx.x >> 5], count);
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t counts = (uint32_t)__cvta_generic_to_shared(count);
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs p, in
     mark_padding(p, s);
 }
 
-template <int NV, int KIND, bool EXACT>
+template <int NV, int KIND>
 pmn_status launch_route(RouteArgs &p, cudaStream_t s)
 {
     const int most = NV > 16 ? 512 : 1024;
@@ -466,13 +466,13 @@ pmn_status launch_route(RouteArgs &p, cudaStream_t s)
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, route_few_kernel<NV, KIND, EXACT>, p) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, route_few_kernel<NV, KIND>, p) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
     }
     const int chunks = (int)chunk_count(p.tokens);
     // as many warps as share the chunk's tokens evenly (65536 tokens of 384 experts 67 -> 61 us by this and one CTA per SM)
     const int64_t side = NV > 12 ? 1 : 2, most_warps = most / 32, passes = (p.chunk + side * most_warps - 1) / (side * most_warps);
     const int threads = 32 * (int)((p.chunk + side * passes - 1) / (side * passes));
-    route_choose_kernel<NV, KIND, EXACT><<<chunks, threads, 0, s>>>(p);
+    route_choose_kernel<NV, KIND><<<chunks, threads, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PMN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)chunks);
@@ -489,16 +489,12 @@ pmn_status launch_route(RouteArgs &p, cudaStream_t s)
 template <int KIND>
 pmn_status route_by_experts(RouteArgs &p, cudaStream_t s)
 {
-    // a count of experts that fills the lanes needs no checks
-    if (p.experts == 128) return launch_route<4, KIND, true>(p, s);
-    if (p.experts == 256) return launch_route<8, KIND, true>(p, s);
-    if (p.experts == 384) return launch_route<12, KIND, true>(p, s);
-    if (p.experts <= 64) return launch_route<2, KIND, false>(p, s);
-    if (p.experts <= 128) return launch_route<4, KIND, false>(p, s);
-    if (p.experts <= 256) return launch_route<8, KIND, false>(p, s);
-    if (p.experts <= 384) return launch_route<12, KIND, false>(p, s);
-    if (p.experts <= 512) return launch_route<16, KIND, false>(p, s);
-    return launch_route<32, KIND, false>(p, s);
+    if (p.experts <= 64) return launch_route<2, KIND>(p, s);
+    if (p.experts <= 128) return launch_route<4, KIND>(p, s);
+    if (p.experts <= 256) return launch_route<8, KIND>(p, s);
+    if (p.experts <= 384) return launch_route<12, KIND>(p, s);
+    if (p.experts <= 512) return launch_route<16, KIND>(p, s);
+    return launch_route<32, KIND>(p, s);
 }
 
 __global__ void route_empty_kernel(int32_t *offsets, int experts, int32_t *row_choice, int64_t rows)
