@@ -1115,20 +1115,10 @@ pmn_status check_common(const uint8_t *a, const uint8_t *a_scales, const uint8_t
 }  // namespace
 
 // The library's device error word is read through pmn_get_device_error, which
-// collects each translation unit's word.
-pmn_status pmn_take_gated_device_error(cudaStream_t s, int *bits)
+// collects each translation unit's word: this is where this file's is.
+pmn_status pmn_gated_error_word(int **word)
 {
-    int host = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_gated_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (host != 0 &&
-        (cudaMemcpyToSymbolAsync(g_gated_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-         cudaStreamSynchronize(s) != cudaSuccess))
-        return PMN_ERR_CUDA;
-    *bits = host;
-    return PMN_OK;
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_gated_error) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 extern "C" pmn_status pmn_w1_gemm_swiglu_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,

@@ -1247,34 +1247,73 @@ extern "C" const char *pmn_status_string(pmn_status st)
     }
 }
 
-pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits);  // quantize.cu
-pmn_status pmn_take_route_device_error(cudaStream_t s, int *bits);  // route.cu
-pmn_status pmn_take_bf16_device_error(cudaStream_t s, int *bits);   // gemm_bf16.cu
-pmn_status pmn_take_matvec_device_error(cudaStream_t s, int *bits);  // matvec.cu
+pmn_status pmn_quant_error_word(int **word);   // quantize.cu
+pmn_status pmn_gated_error_word(int **word);   // gated.cu
+pmn_status pmn_route_error_word(int **word);   // route.cu
+pmn_status pmn_bf16_error_word(int **word);    // gemm_bf16.cu
+pmn_status pmn_matvec_error_word(int **word);  // matvec.cu
 pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fos, uint8_t *codes,
                                uint8_t *scales, float *outer, const int32_t *row_end, cudaStream_t s);  // quantize.cu
 
-extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
+namespace {
+
+// Every file's word of latched bits on one device, and where calls of pmn_get_device_error (each in turn has a slot
+// of its own) put what they have taken.
+constexpr int ERROR_SLOTS = 64;
+__device__ int g_taken_errors[ERROR_SLOTS];
+
+struct ErrorWords {
+    static constexpr int N = 6;
+    int *at[N], *taken;
+};
+
+__global__ void take_errors_kernel(const ErrorWords w, int slot)
 {
-    if (!err) return PMN_ERR_INVALID_ARG;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int qbits = 0, rbits = 0, bbits = 0, mbits = 0;
-    if (pmn_take_quant_device_error(s, &qbits) != PMN_OK || pmn_take_route_device_error(s, &rbits) != PMN_OK ||
-        pmn_take_bf16_device_error(s, &bbits) != PMN_OK || pmn_take_matvec_device_error(s, &mbits) != PMN_OK)
-        return PMN_ERR_CUDA;
-    int host = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_pmn_device_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
-        cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return PMN_ERR_CUDA;
-    const int zero = 0;
-    if (host != 0) {
-        if (cudaMemcpyToSymbolAsync(g_pmn_device_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess)
+    int bits = 0;
+    for (int i = 0; i < ErrorWords::N; ++i) bits |= atomicExch(w.at[i], 0);
+    w.taken[slot] = bits;
+}
+
+pmn_status error_words(ErrorWords *w)
+{
+    static std::mutex mu;
+    static ErrorWords known[64];  // of each device that has been asked
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PMN_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    ErrorWords &k = known[dev];
+    if (!k.taken) {
+        int **at = k.at;
+        if (pmn_quant_error_word(at) != PMN_OK || pmn_gated_error_word(at + 1) != PMN_OK || pmn_route_error_word(at + 2) != PMN_OK ||
+            pmn_bf16_error_word(at + 3) != PMN_OK || pmn_matvec_error_word(at + 4) != PMN_OK ||
+            cudaGetSymbolAddress(reinterpret_cast<void **>(at + 5), g_pmn_device_error) != cudaSuccess ||
+            cudaGetSymbolAddress(reinterpret_cast<void **>(&k.taken), g_taken_errors) != cudaSuccess)
             return PMN_ERR_CUDA;
     }
-    *err = host | qbits | rbits | bbits | mbits;
+    *w = k;
+    return PMN_OK;
+}
+
+}  // namespace
+
+// One kernel takes all the words and one copy brings them (a copy of each: 63 us a call).
+extern "C" pmn_status pmn_get_device_error(void *stream, int32_t *err)
+{
+    static std::atomic<unsigned> turn;
+    if (!err) return PMN_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ErrorWords w;
+    if (error_words(&w) != PMN_OK) return PMN_ERR_CUDA;
+    const int slot = (int)(turn.fetch_add(1u) % ERROR_SLOTS);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    cfg.stream = s;
+    int host = 0;
+    if (cudaLaunchKernelEx(&cfg, take_errors_kernel, w, slot) != cudaSuccess ||
+        cudaMemcpyAsync(&host, w.taken + slot, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return PMN_ERR_CUDA;
+    *err = host;
     return PMN_OK;
 }
 

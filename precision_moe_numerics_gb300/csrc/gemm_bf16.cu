@@ -981,19 +981,9 @@ bool weight_map(CUtensorMap *m, const void *b, int groups, int64_t rows, int64_t
 
 }  // namespace
 
-pmn_status pmn_take_bf16_device_error(cudaStream_t s, int *bits)
+pmn_status pmn_bf16_error_word(int **word)
 {
-    int host = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_bf16_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (host != 0 &&
-        (cudaMemcpyToSymbolAsync(g_bf16_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-         cudaStreamSynchronize(s) != cudaSuccess))
-        return PMN_ERR_CUDA;
-    *bits = host;
-    return PMN_OK;
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_bf16_error) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 extern "C" pmn_status pmn_grouped_gemm_bf16(const void *a, int64_t lda, const void *b, int64_t ldb, const int32_t *offsets,

@@ -729,19 +729,9 @@ pmn_status launch(const Args &args, int64_t n, cudaStream_t s)
 
 }  // namespace
 
-pmn_status pmn_take_matvec_device_error(cudaStream_t s, int *bits)
+pmn_status pmn_matvec_error_word(int **word)
 {
-    int host = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_matvec_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (host != 0 &&
-        (cudaMemcpyToSymbolAsync(g_matvec_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-         cudaStreamSynchronize(s) != cudaSuccess))
-        return PMN_ERR_CUDA;
-    *bits = host;
-    return PMN_OK;
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_matvec_error) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 extern "C" int64_t pmn_matvec_nvfp4_workspace_bytes(int64_t total_rows, int64_t k)

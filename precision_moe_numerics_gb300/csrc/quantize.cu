@@ -1554,26 +1554,10 @@ pmn_status pmn_quantize_h_rows(const uint16_t *h, int64_t rows, int cols, int fo
     return launch_rows_bf16(h, rows, cols, fos, codes, scales, outer, row_end, s);
 }
 
-pmn_status pmn_take_gated_device_error(cudaStream_t s, int *bits);  // gated.cu
-
-// Reads and clears the device error bits of this file's kernels and of the gated
-// block's (called by pmn_get_device_error, which adds the GEMMs').
-pmn_status pmn_take_quant_device_error(cudaStream_t s, int *bits)
+// Where this file's kernels latch their error bits (for pmn_get_device_error).
+pmn_status pmn_quant_error_word(int **word)
 {
-    int host = 0, gated = 0;
-    if (pmn_take_gated_device_error(s, &gated) != PMN_OK) return PMN_ERR_CUDA;
-    if (cudaMemcpyFromSymbolAsync(&host, g_pmn_quant_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (host != 0) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbolAsync(g_pmn_quant_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess)
-            return PMN_ERR_CUDA;
-    }
-    *bits = host | gated;
-    return PMN_OK;
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_pmn_quant_error) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 // Device address of the fixed scratch, looked up once per device.

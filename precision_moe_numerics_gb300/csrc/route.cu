@@ -821,19 +821,9 @@ bool good_grid(int64_t blocks) { return blocks < (int64_t(1) << 31); }
 
 }  // namespace
 
-pmn_status pmn_take_route_device_error(cudaStream_t s, int *bits)
+pmn_status pmn_route_error_word(int **word)
 {
-    int host = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_route_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return PMN_ERR_CUDA;
-    if (host != 0 &&
-        (cudaMemcpyToSymbolAsync(g_route_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-         cudaStreamSynchronize(s) != cudaSuccess))
-        return PMN_ERR_CUDA;
-    *bits = host;
-    return PMN_OK;
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_route_error) == cudaSuccess ? PMN_OK : PMN_ERR_CUDA;
 }
 
 extern "C" int64_t pmn_route_rows(int64_t tokens, int experts, int k, int pad)
