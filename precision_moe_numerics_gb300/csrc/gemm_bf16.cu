@@ -9,11 +9,12 @@
 // divided evenly and waste less than 32 of them where a tile with rows on the M side wastes up to
 // 255.  An accumulator column is then a row of the output, 32 lanes of a warp write 32
 // neighbours of it, and the rows behind a segment are simply not stored.
-// What bounds it, f 1536, k 4096: shared memory.  A 64-deep stage of 256 rows takes 605 clocks where
-// its MMAs take 512; forward of 8192 rows of 24 experts 170 us (tensor pipe active 58 %, DRAM 57 %), loads and products
-// alone 158, products alone 121; one expert's 16384 rows with k = n = 4096 at 1.74 PFLOP/s, the backward
-// of 16384 rows 138 us.  Weight gradients write: 1.2 GB of float32 in 254 us where no expert has more
-// than 512 rows.
+// What bounds it, f 1536, k 4096: the stages' loads, whose time does not fall with the tile's width.  A 64-deep stage of
+// 256 rows takes 605 clocks where its MMAs take 512 (one expert's 16384 rows with k = n = 4096: 1.74 PFLOP/s, the
+// backward of 16384 rows 138 us); 24 experts of 512 rows, two tiles of 256 each, take 196 us forward, of 384 rows,
+// two of 192, 199.  8192 ragged rows, whose tiles are some 195 wide, take 170 us (tensor pipe active 58 %,
+// DRAM 57 %; loads and products alone 158, products alone 121).  Float32 weight gradients of the same rows take
+// 278 us, 254 where no expert has more than 512 rows; writing their 1.2 GB alone takes 164.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -724,7 +725,8 @@ __global__ void __launch_bounds__(THREADS, 1) bf16_kernel(const __grid_constant_
 
 // ---------------------------------------------------------------- few rows
 // The forward calls for a handful of rows (single tokens of a serving loop): their time is that of
-// reading the weights, which 256-column tiles would spread over few SMs.  A CTA takes
+// reading the weights, which 256-column tiles would spread over few SMs (one row, f 1536, k 4096: 7.6 us for a floor of
+// 3.7; 1.8 of them are the launch and finding the expert).  A CTA takes
 // 16 weight rows (gated: 8 gate rows and the 8 up rows of the same columns) for up to 8 NC
 // rows of one expert; its warps share K, each lane loads 16 bytes of a weight row at a time, which are
 // the tensor core's operands as they are (mma.sync; what it sees as its K is the lanes'
@@ -959,8 +961,11 @@ pmn_status check_sizes(int groups, int64_t rows, int64_t m, int64_t n, int64_t k
 }
 
 // Chunks of eight rows that a CTA of the kernel for a few rows takes, 0 where the tiles serve a call.  f 1536, k 4096,
-// gated, us for one chunk, two, and the tiles: one expert, 8 rows 8.4, 10.4, 21; 16 rows 9.6, 11.1, 21; 32 rows 16.4, 11.8,
-// 21; 48 rows 23, 20, 21; 64 rows 29, 21, 21.  Eight experts, 32 rows 37, 43, 46; 24 experts, 32 rows 91, 109, 95.
+// gated, us for one chunk, two, and the tiles: one expert, 8 rows 8.0, 10.0, 21; 16 rows 9.1, 10.4, 21; 32 rows 15.3, 11.3,
+// 21; 48 rows 21, 20, 21; 64 rows 25, 20, 21.  Eight experts, 32 rows 35, 41, 44; 24 experts, 32 rows 70, 82, 71.
+// Smaller weights, f 768, k 2048: one expert, 8 rows 4.7, 5.6, 14; 32 rows 6.2, 6.2, 13; 48 rows 7.8, 7.4, 13; eight experts,
+// 32 rows 11.5, 13.0, 14.6, 64 rows 13.2, 12.9, 14.2; 24 experts, 32 rows 21, 24, 26, 64 rows 23, 26, 26: there 64
+// rows would still gain.
 int few(int64_t rows, int64_t groups) { return rows > 32 ? 0 : rows > 16 && rows > 8 * groups ? 2 : 1; }
 
 // Maps of the token rows [rows, k].

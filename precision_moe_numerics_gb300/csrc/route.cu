@@ -4,9 +4,10 @@
 //   pmn_dispatch_rows          token rows -> routed rows
 //   pmn_combine_rows           the weighted sum of each token's routed rows
 //   pmn_combine_rows_backward  its gradients
-// The router is bound by instruction issue (choosing, 16384 tokens of 384 experts 16 us) and latency (placing
-// 15, half of it behind the choosing; up to 256 tokens 6 to 8 in all), the rows by HBM (16384 x 4096 bf16,
-// top-8: 215 us out, 6.2 TB/s, and 190 us back).
+// The router is bound by latency (16384 tokens of 384 experts: choosing 16 us, of which its 8.7 M warp instructions
+// fill the issue slots for 7; placing 15 for 4, half of it behind the choosing; the gradient 7 to 10 for 3; up to 256
+// tokens 6 to 8 in all; 512 and 1024 experts 27 and 45, k 16 and 32 of 384 31 and 93, where the lanes no longer bound
+// the choice), the rows by HBM (16384 x 4096 bf16, top-8: 215 us out, 6.2 TB/s, and 190 us back).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,6 +31,8 @@ constexpr unsigned FULL = 0xFFFFFFFFu;
 // Tokens are counted and laid out in chunks, one CTA each: at most MAX_CHUNKS, so that
 // every CTA of the second kernel can add up the counts of all of them by itself.
 constexpr int MAX_CHUNKS = 152, MIN_CHUNK = 64, SUB = 128;
+constexpr int64_t MAX_TOKENS = 8384512;
+static_assert((MAX_TOKENS + MAX_CHUNKS - 1) / MAX_CHUNKS <= 65535, "a chunk's counts are 16 bits wide");
 constexpr int CLUSTER = 8, FEW_TOKENS = 32 * CLUSTER;  // so few are routed by one cluster, a token per warp
 
 inline int64_t chunk_tokens(int64_t tokens) { return std::max<int64_t>(MIN_CHUNK, (tokens + MAX_CHUNKS - 1) / MAX_CHUNKS); }
@@ -116,7 +119,8 @@ __device__ __noinline__ int choose_slowly(const uint32_t (&given)[NV], int k, in
 // keys bounds the token's k-th largest from below, so what is not less than it -- little more
 // than k keys -- holds the choice; those few are packed, one to a lane, in the experts' order,
 // and ordered by comparing them all.  (16384 tokens of 384 experts: k rounds over all keys 27 us, k rounds over the
-// few 18, this 17; bound by instructions, 530 of them a token.)
+// few 18, this 17; 530 instructions a token, which seven warps a scheduler issue less than half of the time: they wait
+// for the k maxima, each behind the one before.)
 template <int T, int NV, int KIND>
 __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_t step, int lane, uint2 (*few)[32],
                                        int (&expert)[T], float (&gate)[T])
@@ -646,7 +650,10 @@ __device__ __forceinline__ int32_t checked_row(int32_t r, int64_t rows)
 
 // Tokens and 16-byte pieces of their rows over CTAs: `tokens` tokens of short rows in a CTA, one
 // token's row in turns of `threads` pieces, or, where the tokens alone would not fill the GPU,
-// 1 / `parts` of a row (64 tokens, eight rows each of 4096 bf16 columns: 7.0 us -> 4.5).
+// 1 / `parts` of a row (64 tokens, eight rows each of 4096 bf16 columns: 7.0 us -> 4.5).  The sums of 8 bf16 rows a
+// token in whole rows and in parts of 256 pieces: 128 tokens of 7168 columns 6.7 and 3.9 us, 256 tokens of 4096 4.9 and 5.2;
+// 512 tokens of 1536 3.9 and 5.0, of 2048 5.2 either way, of 4096 8.8 and 8.1; 768 tokens of 1536 5.4 and 5.8, of 4096 10.7
+// and 11.6.  1024 CTAs are some seven an SM.
 struct Split {
     int tokens, parts, threads;
     static Split of(int64_t n, int vecs)
@@ -851,7 +858,7 @@ extern "C" pmn_status pmn_route_topk(const void *logits, int64_t ldl, int logits
         (score != PMN_SCORE_SOFTMAX && score != PMN_SCORE_SIGMOID) || (normalize != 0 && normalize != 1))
         return PMN_ERR_INVALID_ARG;
     if (!offsets || (rows > 0 && !row_choice) || !aligned(offsets, 4) || !aligned(row_choice, 4)) return PMN_ERR_INVALID_ARG;
-    if (tokens > 8384512) return PMN_ERR_UNSUPPORTED;  // a chunk's counts are 16 bits wide
+    if (tokens > MAX_TOKENS) return PMN_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (tokens == 0) {
         route_empty_kernel<<<64, 256, 0, s>>>(offsets, experts, row_choice, rows);
