@@ -86,6 +86,9 @@ __device__ __forceinline__ float warp_sum(float v)
 // log(1 / (1 + e^-x)), which keeps its relative precision where the sigmoid vanishes
 __device__ __forceinline__ float log_sigmoid(float x) { return __fsub_rn(fminf(x, 0.0f), log1pf(expf(-fabsf(x)))); }
 
+// 1 / (1 + e^-x); far below zero it is e^x, also where e^-x leaves float32's range.
+__device__ __forceinline__ float score_sigmoid(float x) { return x < -80.0f ? expf(x) : 1.0f / (1.0f + expf(-x)); }
+
 // k experts by k rounds over all keys: many equals, or a large k.
 template <int NV>
 __device__ __noinline__ int choose_slowly(const uint32_t (&given)[NV], int k, int lane)
@@ -233,7 +236,7 @@ __device__ __forceinline__ void choose(const RouteArgs &p, int64_t token, int64_
         if (every) {
             g = expf(l[t] - top[t]) / total[t];
         } else if (!p.normalize) {
-            g = 1.0f / (1.0f + expf(-l[t]));
+            g = score_sigmoid(l[t]);
         } else {
             const float v = p.score == PMN_SCORE_SOFTMAX ? l[t] : expert[t] >= 0 ? log_sigmoid(l[t]) : -INFINITY;
             float m = warp_max(v);
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs
     }
     const float l = e >= 0 ? load_logit<KIND>(p.logits, at + e) : -INFINITY;
     float g = 0.0f, top = -INFINITY, total = 0.0f, sg = 0.0f;
-    if (p.score == PMN_SCORE_SIGMOID) sg = 1.0f / (1.0f + expf(l));  // 1 - sigmoid, without its cancellation
+    if (p.score == PMN_SCORE_SIGMOID) sg = score_sigmoid(-l);  // 1 - sigmoid, without its cancellation
     if (every) {
         for (int c = lane; c < p.experts; c += 32) top = fmaxf(top, load_logit<KIND>(p.logits, at + c));
         top = warp_max(top);
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs
         const float sum = warp_sum(x);
         g = e >= 0 ? x / sum : 0.0f;
     } else {
-        g = e >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        g = e >= 0 ? score_sigmoid(l) : 0.0f;
     }
     const float dot = p.score == PMN_SCORE_SIGMOID && !p.normalize ? 0.0f : warp_sum(__fmul_rn(g, d));
     float grad = __fmul_rn(__fmul_rn(p.scale, g), __fsub_rn(d, dot));
